@@ -403,6 +403,84 @@ bi_status bi_verify_block_static_ws(const void* q, const void* k_cache, const vo
                                     float scale, void* out, float* lse, bi_stream_t stream);
 
 /* ---------------------------------------------------------------------------------
+ * 8-bit paged KV cache  (no counterpart on the pages; decode attention is bound by the
+ * cache's bytes, and these halve them)
+ *
+ *   k_cache, v_cache  uint8 [num_pages, num_kv_heads, BI_PAGE_SIZE, head_dim]: FP8 E4M3
+ *                     codes; 16-byte aligned.
+ *   k_scale, v_scale  uint8 [num_pages, num_kv_heads, BI_PAGE_SIZE]: one E8M0 byte s per
+ *                     token and KV head; 16-byte aligned.
+ *   A row stands for code * 2^(s - 127); s = 255 means a row of NaN.  block_table, seq_lens
+ *   and cu_q as for the bf16 cache.
+ *
+ * bi_kv_append_q8: bi_kv_append into an 8-bit cache.  For each row x (D values of one token
+ *   and KV head): e = the smallest integer >= -64 with max|x| <= 448 * 2^e, s = e + 127,
+ *   code = e4m3(x * 2^-e) rounded to nearest even.  A row with a NaN or an infinity is
+ *   stored as NaN (s = 255, codes 0).  The scale covers one token, so the stored bytes
+ *   depend on that token's row alone: not on its neighbours, on how a prompt was cut into
+ *   calls, or on rejected drafts.  Tokens of no sequence (cu_q[batch] .. total_q-1) are
+ *   ignored.  Arguments otherwise as bi_kv_append. */
+bi_status bi_kv_append_q8(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                          void* k_scale, void* v_scale, int64_t num_pages,
+                          const int32_t* block_table, int64_t max_pages, const int32_t* seq_lens,
+                          const int32_t* cu_q, int64_t batch, int64_t total_q,
+                          int64_t num_kv_heads, int64_t head_dim, int64_t page_size,
+                          bi_stream_t stream);
+
+/* bi_verify_block_q8 / bi_decode_attn_q8 / bi_prefill_attn_q8: bi_verify_block,
+ *   bi_decode_attn and bi_prefill_attn over an 8-bit cache: softmax(scale * q . k) v with k
+ *   and v the values the cache stands for, q bf16, fp32 scores and sums, out bf16, lse fp32.
+ *   Workspace: bi_attn_workspace_size() bytes, as there.  One configuration (chunks of
+ *   BI_ATTN_CHUNK keys; the batch-invariant limit has no effect): a query's bits depend on
+ *   that query, its position and the cache rows at positions 0..pos alone, and are the same
+ *   from all three entry points.
+ *   A key row of NaN makes the queries that see it NaN, and no others.  The value scales that
+ *   one query sees should lie within a factor 2^80 of one another (softmax weights are held
+ *   relative to them).
+ *   bi_verify_block_q8: max_q <= BI_ATTN_MAX_Q and max_q * G <= BI_ATTN_MAX_ROWS
+ *   (G = num_q_heads / num_kv_heads).  bi_prefill_attn_q8: any max_q >= 1, G <= 32. */
+bi_status bi_verify_block_q8(const void* q, const void* k_cache, const void* v_cache,
+                             const void* k_scale, const void* v_scale, int64_t num_pages,
+                             const int32_t* block_table, int64_t max_pages,
+                             const int32_t* seq_lens, const int32_t* cu_q, int64_t batch,
+                             int64_t total_q, int64_t max_q, int64_t max_seq_len,
+                             int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
+                             int64_t page_size, float scale, void* out, float* lse,
+                             void* workspace, size_t workspace_bytes, bi_stream_t stream);
+bi_status bi_decode_attn_q8(const void* q, const void* k_cache, const void* v_cache,
+                            const void* k_scale, const void* v_scale, int64_t num_pages,
+                            const int32_t* block_table, int64_t max_pages,
+                            const int32_t* seq_lens, int64_t batch, int64_t max_seq_len,
+                            int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
+                            int64_t page_size, float scale, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, bi_stream_t stream);
+bi_status bi_prefill_attn_q8(const void* q, const void* k_cache, const void* v_cache,
+                             const void* k_scale, const void* v_scale, int64_t num_pages,
+                             const int32_t* block_table, int64_t max_pages,
+                             const int32_t* seq_lens, const int32_t* cu_q, int64_t batch,
+                             int64_t total_q, int64_t max_q, int64_t max_seq_len,
+                             int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
+                             int64_t page_size, float scale, void* out, float* lse,
+                             void* workspace, size_t workspace_bytes, bi_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * bi_kv_copy_pages -- copies pages inside paged caches: in every plane p,
+ *   page dst[i] := page src[i] for i < n.  (A fork copies the open page of a sequence; a
+ *   compaction moves pages together.)
+ *   planes       host array of num_planes device pointers, 16-byte aligned, each a plane of
+ *                num_pages pages of page_bytes[p] bytes (a multiple of 16; host array): a
+ *                layer's k_cache, v_cache, k_scale or v_scale, of any page type.  The arrays
+ *                are read before the call returns.
+ *   src, dst     int32 [n] (device).  All copies of a call happen at once, in no order: a
+ *                page that is a destination may be named only once, and not as a source.
+ *                (Pages that break this hold bytes of either copy afterwards; others are
+ *                not affected.)  A pair with an index outside [0, num_pages) is skipped and
+ *                sets BI_ERR_DEVICE_ARG. */
+bi_status bi_kv_copy_pages(void* const* planes, const int64_t* page_bytes, int64_t num_planes,
+                           int64_t num_pages, const int32_t* src, const int32_t* dst, int64_t n,
+                           bi_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
  * Device error word
  * bi_device_status synchronises `stream`, reads and clears the current device's error
  * word and returns BI_OK, BI_ERR_TIMEOUT (a bounded wait ran out), BI_ERR_DEVICE_ARG,

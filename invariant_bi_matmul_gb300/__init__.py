@@ -12,7 +12,8 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from contextlib import nullcontext
+from typing import NamedTuple, Optional, Sequence
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("BI_LIBRARY_PATH") or os.path.join(HERE, "libbi.so")
@@ -25,6 +26,7 @@ ATTN_CHUNK = 512
 ATTN_MAX_Q = 8
 ATTN_MAX_ROWS = 32
 STATIC_WS_BYTES = 32 * 1024 * 1024
+LOGPROBS_MAX_TOP = 32
 
 # every function include/bi.h, include/bi_glue.h and include/bi_rowwise.h declare, with
 # its ctypes signature
@@ -60,6 +62,16 @@ SIGNATURES = {
                         _p, _p, _p, _sz, _p], _int),
     "bi_verify_block_static_ws": ([_p, _p, _p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _i64, _i64,
                                    _i64, _i64, _i64, _f32, _p, _p, _p], _int),
+    # 8-bit cache and page copies
+    "bi_kv_append_q8": ([_p, _p, _p, _p, _p, _p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _i64,
+                         _i64, _p], _int),
+    "bi_verify_block_q8": ([_p, _p, _p, _p, _p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _i64,
+                            _i64, _i64, _i64, _i64, _f32, _p, _p, _p, _sz, _p], _int),
+    "bi_prefill_attn_q8": ([_p, _p, _p, _p, _p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _i64,
+                            _i64, _i64, _i64, _i64, _f32, _p, _p, _p, _sz, _p], _int),
+    "bi_decode_attn_q8": ([_p, _p, _p, _p, _p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i64, _i64,
+                           _i64, _f32, _p, _p, _p, _sz, _p], _int),
+    "bi_kv_copy_pages": ([_p, _p, _i64, _i64, _p, _p, _i64, _p], _int),
     "bi_device_status": ([_p], _int),
     "bi_selftest_wait_timeout": ([ctypes.c_uint64, _p], _int),
     "bi_selftest_set_wait_budget": ([ctypes.c_uint64, _p], _int),
@@ -72,6 +84,9 @@ SIGNATURES = {
     # row-wise reductions (include/bi_rowwise.h)
     "bi_log_softmax": ([_p, _i64, _p, _i64, _i64, _i64, _p], _int),
     "bi_mean": ([_p, _i64, _int, _i64, _i64, _p, _p], _int),
+    "bi_token_logprobs": ([_p, _i64, _int, _p, _i64, _i64, _p, _p, _p, _i64, _p, _p, _p], _int),
+    "bi_token_logprobs_backward": ([_p, _i64, _int, _p, _i64, _i64, _p, _p, _p, _p, _p, _i64, _p],
+                                   _int),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -426,6 +441,163 @@ def decode_attn(q, k_cache, v_cache, block_table, seq_lens, max_seq_len: int, sc
     return out, lse
 
 
+# ------------------------------------------------------------------------ 8-bit cache
+
+def _on_current_device(**tensors):
+    """The tensors (None among them is skipped) all live on the current CUDA device, the one
+    the library launches on."""
+    cur = _torch().cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{cur}")
+
+
+def _allocating_for(stream):
+    """A context in which torch allocates for `stream`: memory that this module makes for a
+    call on another stream than the current one is taken from, and goes back to, the pool of
+    the stream that uses it."""
+    if stream is None:
+        return nullcontext()
+    torch = _torch()
+    if isinstance(stream, int):
+        if stream == torch.cuda.current_stream().cuda_stream:
+            return nullcontext()
+        stream = torch.cuda.ExternalStream(stream)
+    return torch.cuda.stream(stream)
+
+
+def _paged_common_q8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens):
+    torch = _torch()
+    _need(k_cache, torch.uint8, "k_cache", 4)
+    _need(v_cache, torch.uint8, "v_cache", 4)
+    _need(k_scale, torch.uint8, "k_scale", 3)
+    _need(v_scale, torch.uint8, "v_scale", 3)
+    _need(block_table, torch.int32, "block_table", 2)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
+            and v_scale.is_contiguous() and block_table.is_contiguous()
+            and seq_lens.is_contiguous()):
+        raise ValueError("caches, scales, block_table and seq_lens must be contiguous")
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache shapes differ")
+    if k_scale.shape != k_cache.shape[:3] or v_scale.shape != k_cache.shape[:3]:
+        raise ValueError("k_scale and v_scale must be [num_pages, Hkv, page]")
+    if block_table.shape[0] != seq_lens.shape[0]:
+        raise ValueError("block_table and seq_lens disagree on the batch")
+    _on_current_device(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                       block_table=block_table, seq_lens=seq_lens)
+    return k_cache.shape
+
+
+def kv_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q,
+                 stream=None):
+    """kv_append into an 8-bit cache: uint8 E4M3 codes [num_pages, Hkv, 64, D] and one E8M0
+    scale byte per token and head [num_pages, Hkv, 64] (include/bi.h has the format)."""
+    torch = _torch()
+    num_pages, hkv, page, d = _paged_common_q8(k_cache, v_cache, k_scale, v_scale, block_table,
+                                               seq_lens)
+    _need(k_new, torch.bfloat16, "k_new", 3)
+    _need(v_new, torch.bfloat16, "v_new", 3)
+    _need(cu_q, torch.int32, "cu_q", 1)
+    if not (k_new.is_contiguous() and v_new.is_contiguous() and cu_q.is_contiguous()):
+        raise ValueError("k_new, v_new and cu_q must be contiguous")
+    B = seq_lens.shape[0]
+    if k_new.shape != v_new.shape or tuple(k_new.shape[1:]) != (hkv, d):
+        raise ValueError("k_new and v_new must be [T, Hkv, D] of the cache's Hkv and D")
+    if cu_q.shape[0] != B + 1:
+        raise ValueError("cu_q must have batch + 1 entries")
+    _on_current_device(k_new=k_new, v_new=v_new, cu_q=cu_q)
+    _check(lib().bi_kv_append_q8(_ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
+                                 _ptr(k_scale), _ptr(v_scale), num_pages, _ptr(block_table),
+                                 block_table.shape[1], _ptr(seq_lens), _ptr(cu_q), B,
+                                 k_new.shape[0], hkv, d, page, _stream(stream)))
+
+
+def _attend_q8(fn, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, max_q,
+               max_seq_len, scale, out, lse, want_lse, workspace, stream):
+    torch = _torch()
+    num_pages, hkv, page, d = _paged_common_q8(k_cache, v_cache, k_scale, v_scale, block_table,
+                                               seq_lens)
+    _need(q, torch.bfloat16, "q", 3)
+    T, hq, dq = q.shape
+    B = seq_lens.shape[0]
+    if dq != d or not q.is_contiguous():
+        raise ValueError("q must be a contiguous [T, Hq, D] of the cache's D")
+    if fn == "bi_decode_attn_q8":
+        if T != B:
+            raise ValueError("q must have one token per sequence")
+    else:
+        _need(cu_q, torch.int32, "cu_q", 1)
+        if cu_q.shape[0] != B + 1 or not cu_q.is_contiguous():
+            raise ValueError("cu_q must be contiguous with batch + 1 entries")
+    with _allocating_for(stream):
+        out, lse = _attn_out(q, out, lse, want_lse)
+        ws, ws_bytes = _workspace(workspace, attn_workspace_size(T, hq, d, max_seq_len), q.device)
+    _on_current_device(q=q, cu_q=cu_q, out=out, lse=lse, workspace=ws)
+    head = (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), num_pages,
+            _ptr(block_table), block_table.shape[1], _ptr(seq_lens))
+    sizes = (B,) if fn == "bi_decode_attn_q8" else (_ptr(cu_q), B, T, int(max_q))
+    _check(getattr(lib(), fn)(*head, *sizes, int(max_seq_len), hq, hkv, d, page, float(scale),
+                              _ptr(out), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)))
+    return out, lse
+
+
+def verify_block_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q,
+                    max_q: int, max_seq_len: int, scale: float, out=None, lse=None,
+                    want_lse=True, workspace=None, stream=None):
+    """verify_block over an 8-bit cache (see kv_append_q8)."""
+    return _attend_q8("bi_verify_block_q8", q, k_cache, v_cache, k_scale, v_scale, block_table,
+                      seq_lens, cu_q, max_q, max_seq_len, scale, out, lse, want_lse, workspace,
+                      stream)
+
+
+def prefill_attn_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q,
+                    max_q: int, max_seq_len: int, scale: float, out=None, lse=None,
+                    want_lse=True, workspace=None, stream=None):
+    """verify_block_q8 for blocks of any width; the same bits for every query."""
+    return _attend_q8("bi_prefill_attn_q8", q, k_cache, v_cache, k_scale, v_scale, block_table,
+                      seq_lens, cu_q, max_q, max_seq_len, scale, out, lse, want_lse, workspace,
+                      stream)
+
+
+def decode_attn_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                   max_seq_len: int, scale: float, out=None, lse=None, want_lse=True,
+                   workspace=None, stream=None):
+    """decode_attn over an 8-bit cache: one new token per sequence, q bf16 [B, Hq, D]."""
+    return _attend_q8("bi_decode_attn_q8", q, k_cache, v_cache, k_scale, v_scale, block_table,
+                      seq_lens, None, 1, max_seq_len, scale, out, lse, want_lse, workspace, stream)
+
+
+def kv_copy_pages(planes: Sequence, src, dst, stream=None) -> None:
+    """Copies page src[i] over page dst[i] (int32 CUDA lists) in every plane: tensors of any
+    page type whose first dimension is the pages (a layer's k_cache, v_cache, k_scale,
+    v_scale).  A destination page is named once, and is not a source of the same call."""
+    torch = _torch()
+    _need(src, torch.int32, "src", 1)
+    _need(dst, torch.int32, "dst", 1)
+    if src.shape != dst.shape or not src.is_contiguous() or not dst.is_contiguous():
+        raise ValueError("src and dst must be contiguous lists of one length")
+    _on_current_device(src=src, dst=dst)
+    planes = list(planes)
+    if not planes:
+        return
+    pages = planes[0].shape[0] if planes[0].dim() else 0
+    if pages < 1:
+        raise ValueError("a plane has no pages")
+    cur = src.device
+    ptrs, sizes = [], []
+    for t in planes:
+        if not t.is_cuda or t.device != cur:
+            raise ValueError("planes must be CUDA tensors on the device of src and dst")
+        if not t.is_contiguous() or t.dim() == 0 or t.shape[0] != pages:
+            raise ValueError("planes must be contiguous with one number of pages")
+        ptrs.append(t.data_ptr())
+        sizes.append(t.numel() // pages * t.element_size())
+    n = len(ptrs)
+    _check(lib().bi_kv_copy_pages((ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes), n,
+                                  pages, _ptr(src), _ptr(dst), src.shape[0], _stream(stream)))
+
+
 # ---------------------------------------------------------------------- device status
 
 def device_status(stream=None) -> int:
@@ -562,4 +734,75 @@ def mean(x, out=None, stream=None):
     dt = BI_BF16 if x.dtype == torch.bfloat16 else BI_F32
     _check(lib().bi_mean(_ptr(x), _row_major_2d(x, "x"), dt, rows, n, _ptr(out),
                          _stream(stream)))
+    return out
+
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs returns: fp32 [rows] each, and [rows, top] (None where top is 0)."""
+    logprobs: object
+    entropy: object
+    lse: object
+    top_logprobs: object
+    top_ids: object
+
+
+def token_logprobs(logits, tokens, top: int = 0, stream=None) -> TokenLogprobs:
+    """Log-probability of each row's token under the softmax of its logits (bf16, fp16 or
+    fp32 [rows, n]; tokens int32 [rows], -1 for none), the row's entropy and log-sum-exp, and
+    the `top` largest entries as log-probabilities and ids (descending; lowest id first among
+    equal ones).  A row's bits do not depend on the other rows."""
+    torch = _torch()
+    dt = _in_dtype(logits, "logits")
+    _need(logits, logits.dtype, "logits", 2)
+    _need(tokens, torch.int32, "tokens", 1)
+    rows, n = logits.shape
+    if tokens.shape[0] != rows or not tokens.is_contiguous():
+        raise ValueError("tokens must be a contiguous int32 [rows] tensor")
+    _on_current_device(logits=logits, tokens=tokens)
+    f32 = dict(dtype=torch.float32, device=logits.device)
+    with _allocating_for(stream):
+        stats = torch.empty(3, rows, **f32)
+        tv = torch.empty(rows, top, **f32) if top else None
+        ti = torch.empty(rows, top, dtype=torch.int32, device=logits.device) if top else None
+    logp, entropy, lse = stats.unbind(0)
+    _check(lib().bi_token_logprobs(_ptr(logits), _row_major_2d(logits, "logits"), dt, _ptr(tokens),
+                                   rows, n, _ptr(logp), _ptr(entropy), _ptr(lse), int(top),
+                                   _ptr(tv), _ptr(ti), _stream(stream)))
+    return TokenLogprobs(logp, entropy, lse, tv, ti)
+
+
+def token_logprobs_backward(logits, tokens, lse, entropy=None, grad_logprobs=None,
+                            grad_entropy=None, out=None, stream=None):
+    """Gradient with respect to the logits (their shape and type) of
+    sum(grad_logprobs * logprobs) + sum(grad_entropy * entropy), from the lse and entropy
+    that token_logprobs gave; out may be logits."""
+    torch = _torch()
+    dt = _in_dtype(logits, "logits")
+    _need(logits, logits.dtype, "logits", 2)
+    rows, n = logits.shape
+    _need(tokens, torch.int32, "tokens", 1)
+    if grad_logprobs is None and grad_entropy is None:
+        raise ValueError("grad_logprobs and grad_entropy are both None")
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("grad_entropy needs entropy")
+    for name, t in (("lse", lse), ("entropy", entropy), ("grad_logprobs", grad_logprobs),
+                    ("grad_entropy", grad_entropy)):
+        if t is not None or name == "lse":
+            _need(t, torch.float32, name, 1)
+            if t.shape[0] != rows or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous fp32 [rows] tensor")
+    if tokens.shape[0] != rows or not tokens.is_contiguous():
+        raise ValueError("tokens must be a contiguous int32 [rows] tensor")
+    if out is None:
+        with _allocating_for(stream):
+            out = torch.empty(rows, n, dtype=logits.dtype, device=logits.device)
+    _need(out, logits.dtype, "out", 2)
+    if tuple(out.shape) != (rows, n):
+        raise ValueError("out must have the shape of logits")
+    _on_current_device(logits=logits, tokens=tokens, lse=lse, entropy=entropy,
+                       grad_logprobs=grad_logprobs, grad_entropy=grad_entropy, out=out)
+    _check(lib().bi_token_logprobs_backward(
+        _ptr(logits), _row_major_2d(logits, "logits"), dt, _ptr(tokens), rows, n, _ptr(lse),
+        _ptr(entropy), _ptr(grad_logprobs), _ptr(grad_entropy), _ptr(out),
+        _row_major_2d(out, "out"), _stream(stream)))
     return out

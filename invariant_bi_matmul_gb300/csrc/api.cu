@@ -578,6 +578,176 @@ BI_EXPORT bi_status bi_decode_attn(const void* q, const void* k_cache, const voi
                          workspace_bytes, stream);
 }
 
+// ===================================================================== 8-bit cache
+
+BI_EXPORT bi_status bi_kv_append_q8(const void* k_new, const void* v_new, void* k_cache,
+                                    void* v_cache, void* k_scale, void* v_scale,
+                                    int64_t num_pages, const int32_t* block_table,
+                                    int64_t max_pages, const int32_t* seq_lens,
+                                    const int32_t* cu_q, int64_t batch, int64_t total_q,
+                                    int64_t num_kv_heads, int64_t head_dim, int64_t page_size,
+                                    bi_stream_t stream) {
+    const char* fn = "bi_kv_append_q8";
+    PagedArgs a{k_cache, v_cache, num_pages, block_table, max_pages, seq_lens, cu_q, batch,
+                total_q, BI_ATTN_MAX_Q, int64_t(max_pages) * BI_PAGE_SIZE, num_kv_heads,
+                num_kv_heads, head_dim};
+    if (batch < 0 || total_q < 0)
+        return fail(BI_ERR_INVALID_ARG, "%s: negative batch or total_q", fn);
+    if (head_dim != 64 && head_dim != 128)
+        return fail(BI_ERR_UNSUPPORTED, "%s: head_dim must be 64 or 128", fn);
+    if (page_size != BI_PAGE_SIZE)
+        return fail(BI_ERR_UNSUPPORTED, "%s: page_size must be %d", fn, BI_PAGE_SIZE);
+    if (num_kv_heads < 1 || num_pages < 1 || max_pages < 1)
+        return fail(BI_ERR_INVALID_ARG, "%s: num_kv_heads, num_pages, max_pages >= 1", fn);
+    if (num_pages > kI32Max || max_pages > kI32Max || batch > kI32Max)
+        return fail(BI_ERR_UNSUPPORTED, "%s: num_pages, max_pages, batch must be < 2^31", fn);
+    if (batch == 0 || total_q == 0) return BI_OK;
+    if (!k_new || !v_new || !k_cache || !v_cache || !k_scale || !v_scale || !block_table ||
+        !seq_lens || !cu_q)
+        return fail(BI_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) ||
+        !aligned(v_cache, 16) || !aligned(k_scale, 16) || !aligned(v_scale, 16) ||
+        !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q, 4))
+        return fail(BI_ERR_UNSUPPORTED, "%s: tensors must be 16-byte aligned", fn);
+    if (total_q > kI32Max / num_kv_heads)
+        return fail(BI_ERR_UNSUPPORTED, "%s: total_q too large", fn);
+    cudaError_t why = cudaSuccess;
+    const DeviceInfo* dev = current_device_info(&why);
+    if (!dev) return cuda_fail(why, fn);
+    cudaError_t e = launch_kv_append_q8(*dev, k_new, v_new, k_cache, v_cache, k_scale, v_scale, a,
+                                        reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, fn);
+    return BI_OK;
+}
+
+namespace {
+
+bi_status run_attention_q8(const char* fn, const void* q, const PagedArgs& a, bool prefill,
+                           const void* k_scale, const void* v_scale, int64_t page_size,
+                           float scale, void* out, float* lse, void* workspace, size_t ws_bytes,
+                           bi_stream_t stream) {
+    // the widths and groups of prefill are checked here: any group of up to MAX_ROWS heads
+    if (prefill && (a.max_q < 1 || a.max_q > kI32Max))
+        return fail(BI_ERR_INVALID_ARG, "%s: max_q must be >= 1", fn);
+    PagedArgs c = a;
+    if (prefill) {
+        if (a.hkv < 1 || a.hq < 1 || a.hq % a.hkv != 0)
+            return fail(BI_ERR_INVALID_ARG, "%s: num_q_heads must be a positive multiple of "
+                                            "num_kv_heads", fn);
+        if (a.hq / a.hkv > BI_ATTN_MAX_ROWS)
+            return fail(BI_ERR_UNSUPPORTED, "%s: num_q_heads/num_kv_heads must be <= %d", fn,
+                        BI_ATTN_MAX_ROWS);
+        if (a.batch > 0 && (a.total_q < a.batch || a.total_q > a.batch * a.max_q))
+            return fail(BI_ERR_INVALID_ARG, "%s: total_q must be in [batch, batch*max_q]", fn);
+        c.max_q = 1;
+        if (a.batch > 0) c.total_q = a.batch;
+    }
+    bi_status s = check_paged(fn, c, page_size, a.cu_q != nullptr);
+    if (s != BI_OK) return s;
+    if (!std::isfinite(scale)) return fail(BI_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+    if (a.batch == 0) return BI_OK;
+    if (a.total_q > kI32Max / a.hq || a.max_pages > kI32Max || a.max_seq_len > kI32Max)
+        return fail(BI_ERR_UNSUPPORTED, "%s: total_q, max_pages or max_seq_len too large", fn);
+    if (!q || !out || !workspace || !k_scale || !v_scale)
+        return fail(BI_ERR_INVALID_ARG, "%s: null q/out/workspace/scale", fn);
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
+        (lse && !aligned(lse, 4)) || !aligned(k_scale, 16) || !aligned(v_scale, 16))
+        return fail(BI_ERR_UNSUPPORTED, "%s: q, out, scales and workspace must be 16-byte aligned",
+                    fn);
+    const size_t need = attn_workspace_bytes(a.total_q, a.hq, a.head_dim, a.max_seq_len);
+    if (ws_bytes < need)
+        return fail(BI_ERR_INVALID_ARG, "%s: workspace too small (%zu < %zu bytes)", fn, ws_bytes,
+                    need);
+    cudaError_t why = cudaSuccess;
+    const DeviceInfo* dev = current_device_info(&why);
+    if (!dev) return cuda_fail(why, fn);
+    cudaError_t e = launch_attention_q8(*dev, q, a, k_scale, v_scale, scale, out, lse, workspace,
+                                        reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, fn);
+    return BI_OK;
+}
+
+}  // namespace
+
+BI_EXPORT bi_status bi_verify_block_q8(const void* q, const void* k_cache, const void* v_cache,
+                                       const void* k_scale, const void* v_scale,
+                                       int64_t num_pages, const int32_t* block_table,
+                                       int64_t max_pages, const int32_t* seq_lens,
+                                       const int32_t* cu_q, int64_t batch, int64_t total_q,
+                                       int64_t max_q, int64_t max_seq_len, int64_t num_q_heads,
+                                       int64_t num_kv_heads, int64_t head_dim, int64_t page_size,
+                                       float scale, void* out, float* lse, void* workspace,
+                                       size_t workspace_bytes, bi_stream_t stream) {
+    const char* fn = "bi_verify_block_q8";
+    if (batch > 0 && !cu_q) return fail(BI_ERR_INVALID_ARG, "%s: null cu_q", fn);
+    PagedArgs a{k_cache, v_cache, num_pages, block_table, max_pages, seq_lens, cu_q, batch,
+                total_q, max_q, max_seq_len, num_q_heads, num_kv_heads, head_dim};
+    return run_attention_q8(fn, q, a, false, k_scale, v_scale, page_size, scale, out, lse,
+                            workspace, workspace_bytes, stream);
+}
+
+BI_EXPORT bi_status bi_prefill_attn_q8(const void* q, const void* k_cache, const void* v_cache,
+                                       const void* k_scale, const void* v_scale,
+                                       int64_t num_pages, const int32_t* block_table,
+                                       int64_t max_pages, const int32_t* seq_lens,
+                                       const int32_t* cu_q, int64_t batch, int64_t total_q,
+                                       int64_t max_q, int64_t max_seq_len, int64_t num_q_heads,
+                                       int64_t num_kv_heads, int64_t head_dim, int64_t page_size,
+                                       float scale, void* out, float* lse, void* workspace,
+                                       size_t workspace_bytes, bi_stream_t stream) {
+    const char* fn = "bi_prefill_attn_q8";
+    if (batch > 0 && !cu_q) return fail(BI_ERR_INVALID_ARG, "%s: null cu_q", fn);
+    PagedArgs a{k_cache, v_cache, num_pages, block_table, max_pages, seq_lens, cu_q, batch,
+                total_q, max_q, max_seq_len, num_q_heads, num_kv_heads, head_dim};
+    return run_attention_q8(fn, q, a, true, k_scale, v_scale, page_size, scale, out, lse,
+                            workspace, workspace_bytes, stream);
+}
+
+BI_EXPORT bi_status bi_decode_attn_q8(const void* q, const void* k_cache, const void* v_cache,
+                                      const void* k_scale, const void* v_scale,
+                                      int64_t num_pages, const int32_t* block_table,
+                                      int64_t max_pages, const int32_t* seq_lens, int64_t batch,
+                                      int64_t max_seq_len, int64_t num_q_heads,
+                                      int64_t num_kv_heads, int64_t head_dim, int64_t page_size,
+                                      float scale, void* out, float* lse, void* workspace,
+                                      size_t workspace_bytes, bi_stream_t stream) {
+    PagedArgs a{k_cache, v_cache, num_pages, block_table, max_pages, seq_lens, nullptr, batch,
+                batch, 1, max_seq_len, num_q_heads, num_kv_heads, head_dim};
+    return run_attention_q8("bi_decode_attn_q8", q, a, false, k_scale, v_scale, page_size, scale,
+                            out, lse, workspace, workspace_bytes, stream);
+}
+
+BI_EXPORT bi_status bi_kv_copy_pages(void* const* planes, const int64_t* page_bytes,
+                                     int64_t num_planes, int64_t num_pages, const int32_t* src,
+                                     const int32_t* dst, int64_t n, bi_stream_t stream) {
+    const char* fn = "bi_kv_copy_pages";
+    if (num_planes < 0 || num_pages < 1 || n < 0)
+        return fail(BI_ERR_INVALID_ARG, "%s: need num_planes >= 0, num_pages >= 1 and n >= 0", fn);
+    if (num_pages > kI32Max || n > kI32Max || num_planes > kI32Max)
+        return fail(BI_ERR_UNSUPPORTED, "%s: num_planes, num_pages and n must be < 2^31", fn);
+    if (num_planes == 0 || n == 0) return BI_OK;
+    if (!planes || !page_bytes || !src || !dst)
+        return fail(BI_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned(src, 4) || !aligned(dst, 4))
+        return fail(BI_ERR_INVALID_ARG, "%s: src and dst not element-aligned", fn);
+    for (int64_t p = 0; p < num_planes; ++p) {
+        if (!planes[p]) return fail(BI_ERR_INVALID_ARG, "%s: null plane", fn);
+        if (page_bytes[p] < 16)
+            return fail(BI_ERR_INVALID_ARG, "%s: page_bytes must be positive", fn);
+        if (page_bytes[p] % 16 != 0 || page_bytes[p] / 16 > kI32Max || !aligned(planes[p], 16))
+            return fail(BI_ERR_UNSUPPORTED,
+                        "%s: planes must be 16-byte aligned with pages of a multiple of 16 bytes",
+                        fn);
+    }
+    cudaError_t why = cudaSuccess;
+    const DeviceInfo* dev = current_device_info(&why);
+    if (!dev) return cuda_fail(why, fn);
+    cudaError_t e = launch_copy_pages(*dev, planes, page_bytes, int(num_planes), int(num_pages),
+                                      src, dst, int(n), reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, fn);
+    return BI_OK;
+}
+
 // ==================================================================== device status
 
 BI_EXPORT bi_status bi_device_status(bi_stream_t stream) {

@@ -172,6 +172,25 @@ cudaError_t launch_prefill(const DeviceInfo& dev, const void* q, const PagedArgs
                            float scale, void* out, float* lse, void* workspace,
                            cudaStream_t stream);
 
+// -------------------------------------- 8-bit cache (kv_q8.cu, attention_q8.cu)
+// The caches in `a` hold e4m3 codes; k_scale and v_scale their E8M0 bytes.
+cudaError_t launch_kv_append_q8(const DeviceInfo& dev, const void* k_new, const void* v_new,
+                                void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                                const PagedArgs& a, cudaStream_t stream);
+
+// Blocks of any width (a.max_q); chunk partials of CHUNK keys, then launch_attn_merge.
+cudaError_t launch_attention_q8(const DeviceInfo& dev, const void* q, const PagedArgs& a,
+                                const void* k_scale, const void* v_scale, float scale, void* out,
+                                float* lse, void* workspace, cudaStream_t stream);
+
+// ------------------------------------------------------------------- pages (pages.cu)
+constexpr int kCopyPlanes = 64;  // planes per launch (kernel parameters)
+
+// In each plane, page dst[i] := page src[i], i < n (device lists); page_bytes % 16 == 0.
+cudaError_t launch_copy_pages(const DeviceInfo& dev, void* const* planes,
+                              const int64_t* page_bytes, int num_planes, int num_pages,
+                              const int32_t* src, const int32_t* dst, int n, cudaStream_t stream);
+
 cudaError_t launch_selftest_wait(const DeviceInfo& dev, unsigned long long timeout_ns,
                                  cudaStream_t stream);
 
