@@ -1048,6 +1048,17 @@ cudaError_t launch_attention_t(const DeviceInfo& dev, const void* q, const Paged
 
 }  // namespace
 
+cudaError_t launch_attn_count_reset(unsigned int* cnt, int n, cudaStream_t stream) {
+    return launch_pdl(attn_count_reset_kernel, dim3((n + 1023) / 1024), dim3(256), 0, stream, cnt,
+                      n);
+}
+
+unsigned int* attn_item_counters(const PagedArgs& a, void* workspace, int chunk_log2) {
+    const int64_t chunks = (a.max_seq_len + (int64_t(1) << chunk_log2) - 1) >> chunk_log2;
+    return reinterpret_cast<unsigned int*>(
+        static_cast<uint8_t*>(workspace) + partials_bytes(a.total_q, a.hq, a.head_dim, chunks));
+}
+
 cudaError_t launch_attn_merge(const PagedArgs& a, void* workspace, int chunk_log2, void* out,
                               float* lse, const unsigned int* cnt, unsigned int* err,
                               cudaStream_t stream) {

@@ -1,9 +1,44 @@
 // attention_q8.cu -- decode / verify / prefill attention over the 8-bit paged KV cache
-// (kv_q8.cu has its format).
+// (kv_q8.cu has its format), causal, for blocks of any width.
 //
-// Simple form: one CTA per (sequence, query tile, KV head, 512-key chunk); each row's scores,
-// weights and weighted values on the CUDA cores, into the chunk partials that the merge of
-// attention.cu combines.
+// Mathematics.  With the codes a_i, b_i of key i, its scales 2^x_i (K) and 2^y_i (V), and a
+// query row q:
+//   t_i = scale * log2(e) * 2^x_i * (q . a_i) + y_i,   p_i = 2^(t_i - m),
+//   sum_i p_i b_i  and  l = sum_i p_i 2^-y_i,   out = sum p b / l
+// -- the V scale rides in the exponent, so the tensor cores see codes only, and the row sum
+// takes it out again (2^-y is exact).  m is a reference maximum of the t_i seen so far.
+//
+// Both products run on the codes as they lie in the cache (tcgen05 kind::f8f6f4, e4m3 x e4m3,
+// fp32 accumulators).  The other operand is split into two e4m3 pieces, so nothing of its
+// precision is lost to 8 bits:
+//   * q * 2^s (s puts the row's largest value in [128, 256)) = hi + lo, each rounded to
+//     nearest: exact for bf16 q down to 2^-9 of the row's largest value, off by at most
+//     2^-18 of it below;
+//   * p = hi + lo / 16: p <= 2^8; hi has four bits, lo the next four, so p is held to
+//     2^-9 of itself (bf16 would hold 2^-8) and to 2^-14 absolute, where the reference
+//     maximum stands for p = 2^6 at least.
+//
+// Reduction of one (query, head) -- a function of its position alone, as in attention.cu:
+// chunks of 512 keys from key 0; a chunk in tiles of 128 keys, ascending; per tile the exact
+// maximum of the row's t, m raised to (maximum - 6) only when the maximum exceeds m + 8 (O and
+// the sums then scaled by 2^(m_old - m_new)); each of 128 threads sums its key of every tile,
+// and the 128 sums are added by a fixed tree; the chunk partials (m, l, o) go through the
+// merge of attention.cu.  A tile that a row does not see changes none of its numbers, and a
+// row's place in the MMA tile, the other rows and the block's width enter nowhere.
+//
+// Orientation.  S^T = K Q^T (M = 128 keys, N = 32 query rows) and O^T = V^T P^T (M = head
+// dim, N = 32 hi + 32 lo rows): the cache is the operand that the tensor core reads 128 rows
+// at a time, whatever the number of query rows, and a softmax thread owns one key, so it does
+// as many exponentials as there are query rows (rounded up to 8, 16 or 32), reads its key's
+// two scale bytes once, and writes its P values as 16-byte pieces.
+//
+// Warps: 0..3 softmax (one key of the tile per thread), 4..7 epilogue (they also split the
+// next item's Q), 8 TMA producer, 9 S issuer (and TMEM owner), 10 P V issuer.  One persistent
+// CTA per SM; work items (sequence, chunk, query tile, KV head) are enumerated on the device.
+// All waits are bounded mbarrier waits; warps never meet in a barrier that one of them may
+// have given up on.
+//
+// Bound by memory: 2 * (D + 1) bytes per key and KV head against 4 * 32 * D operations.
 #include "attn_common.cuh"
 
 #include <cuda_fp8.h>
@@ -11,116 +46,800 @@
 namespace bi {
 namespace {
 
-constexpr int QR = 32;  // query rows of a tile: QR / G tokens times the G heads of a KV head
-constexpr int THREADS = 128;
+constexpr int QR = 32;                    // query rows of a tile
+constexpr int TK = 128;                   // keys of a tile: two pages
+constexpr int TPAGES = TK / PAGE;
+constexpr int NSM = 4;                    // softmax warps 0..3
+constexpr int EPI = 4;                    // first epilogue warp (4..7)
+constexpr int PRODUCER = 8, S_WARP = 9, PV_WARP = 10;
+constexpr int THREADS = 11 * 32;
+constexpr int NSB = 4;                    // S buffers in tensor memory
+constexpr int TMEM_COLS = 256;
+constexpr int S_COL = 0;                  // S buffers: 32 columns each
+constexpr int O_COL = NSB * QR;           // O buffers (by item): 32 hi + 32 lo columns each
+constexpr float kNoMax = -1e30f;          // m before any visible key: every finite t exceeds it
+constexpr float kHeadroom = 6.f;          // a raised m leaves p = 2^6 at the maximum ...
+constexpr float kRaise = 8.f;             // ... and holds until p would exceed 2^8 (e4m3: 448)
+constexpr int MAX_BATCH = BI_ATTN_MAX_BATCH;
 
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
-}
-__device__ __forceinline__ float e8m0_value(uint8_t s) {
-    return s == 255 ? __int_as_float(0x7fc00000) : exp2f(float(int(s) - 127));
-}
-
-template <int D>
-__global__ void __launch_bounds__(THREADS)
-attn_q8_kernel(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ k_cache,
-               const uint8_t* __restrict__ v_cache, const uint8_t* __restrict__ k_scale,
-               const uint8_t* __restrict__ v_scale, const int32_t* __restrict__ block_table,
-               int max_pages, int num_pages, const int32_t* __restrict__ seq_lens,
-               const int32_t* __restrict__ cu_q, int total_q, int max_q, int max_seq_len, int Hq,
-               int Hkv, int tiles, float scale_log2, float* __restrict__ ws_o,
-               float* __restrict__ ws_ml, int maxC, unsigned int* err) {
-    __shared__ float p[CHUNK];
-    __shared__ float sq[D];
-    __shared__ float red[THREADS / 32];
-    pdl_wait();
-    pdl_trigger();
-    const int c = blockIdx.x, h = blockIdx.y / tiles, u = blockIdx.y % tiles, b = blockIdx.z;
-    const int tid = threadIdx.x, G = Hq / Hkv, TQ = QR / G;
-    const SeqInfo si = seq_info(seq_lens, cu_q, b);
-    if (!seq_ok(si, max_q, max_seq_len, total_q)) {
-        if (tid == 0) latch_error(err, kErrDeviceArg);
-        return;
-    }
-    for (int r = 0; r < TQ * G; ++r) {
-        const int j = u * TQ + r / G, hq = h * G + r % G;
-        if (j >= si.qb) break;
-        const int pos = si.L - si.qb + j;
-        if (pos < c * CHUNK) continue;
-        const int n = min(CHUNK, pos + 1 - c * CHUNK);
-        const int64_t row = int64_t(si.t0 + j) * Hq + hq;
-        __syncthreads();
-        for (int d = tid; d < D; d += THREADS) sq[d] = __bfloat162float(q[row * D + d]);
-        __syncthreads();
-        float m = -INFINITY;
-        for (int i = tid; i < n; i += THREADS) {
-            const int key = c * CHUNK + i;
-            const int phys = block_table[int64_t(b) * max_pages + key / PAGE];
-            float s = -INFINITY;
-            if (phys >= 0 && phys < num_pages) {
-                const int64_t at = (int64_t(phys) * Hkv + h) * PAGE + key % PAGE;
-                float dot = 0.f;
-                for (int d = 0; d < D; ++d) dot = fmaf(sq[d], e4m3_value(k_cache[at * D + d]), dot);
-                s = dot * e8m0_value(k_scale[at]) * scale_log2;
-            } else {
-                latch_error(err, kErrDeviceArg);
-            }
-            p[i] = s;
-            m = fmaxf(m, s);
-        }
-        for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, off));
-        if ((tid & 31) == 0) red[tid >> 5] = m;
-        __syncthreads();
-        m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        const float use = m == -INFINITY ? 0.f : m;
-        __syncthreads();
-        float l = 0.f;
-        for (int i = tid; i < n; i += THREADS) {
-            p[i] = exp2f(p[i] - use);
-            l += p[i];
-        }
-        for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(~0u, l, off);
-        if ((tid & 31) == 0) red[tid >> 5] = l;
-        __syncthreads();
-        l = (red[0] + red[1]) + (red[2] + red[3]);
-        const int64_t idx = row * maxC + c;
-        for (int d = tid; d < D; d += THREADS) {
-            float o = 0.f;
-            for (int i = 0; i < n; ++i) {
-                const int key = c * CHUNK + i;
-                const int phys = block_table[int64_t(b) * max_pages + key / PAGE];
-                if (phys < 0 || phys >= num_pages) continue;
-                const int64_t at = (int64_t(phys) * Hkv + h) * PAGE + key % PAGE;
-                o = fmaf(p[i] * e8m0_value(v_scale[at]), e4m3_value(v_cache[at * D + d]), o);
-            }
-            ws_o[idx * D + d] = o;
-        }
-        if (tid == 0) {
-            ws_ml[idx * 2] = m;
-            ws_ml[idx * 2 + 1] = l;
-        }
-    }
-}
+static_assert(CHUNK % TK == 0 && TK == NSM * 32, "a thread per key");
+static_assert(O_COL + 2 * 2 * QR <= TMEM_COLS, "tensor memory columns");
 
 template <int D>
+struct Cfg {
+    static constexpr int NST = D == 64 ? 8 : 5;          // tile stages in the ring
+    static constexpr int PAGE_BYTES = PAGE * D;
+    static constexpr int SIDE_BYTES = TK * D;            // K or V of a tile
+    static constexpr int STAGE_BYTES = 2 * SIDE_BYTES;
+    static constexpr int Q_PIECE = QR * D;               // hi or lo of a Q tile
+    static constexpr int Q_BYTES = 2 * Q_PIECE;
+    static constexpr int P_BYTES = TK * 2 * QR;          // [key][32 hi | 32 lo]
+    static constexpr int Q_OFF = 0;                      // two Q buffers
+    static constexpr int P_OFF = Q_OFF + 2 * Q_BYTES;    // two P buffers
+    static constexpr int RING_OFF = P_OFF + 2 * P_BYTES;
+    static constexpr int SCALE_OFF = RING_OFF + NST * STAGE_BYTES;  // [NST][K 128 | V 128]
+    static constexpr int BAR_OFF = SCALE_OFF + NST * 2 * TK;
+    static constexpr int NBARS = 2 * NST + 2 * NSB + 4 + 4 + 2 + 2 + 1 + 2;
+    static constexpr int XS_OFF = (BAR_OFF + NBARS * 8 + 8 + 15) / 16 * 16;
+    // per item buffer: four warps' row sums and the row maxima; per Q buffer the row factors;
+    // the maxima exchanged between the softmax warps (two buffers), and their flags
+    static constexpr int XS_FLOATS = 2 * (NSM + 1) * QR + 2 * QR + 2 * NSM * QR + 2 * NSM;
+    static constexpr int MISC_OFF = XS_OFF + XS_FLOATS * 4;
+    static constexpr int MISC_INTS = NST + (MAX_BATCH + 1) + 3 * MAX_BATCH + 2 + 1;
+    static constexpr size_t SMEM = 1024 + size_t(MISC_OFF) + MISC_INTS * 4;
+    // K-major and MN-major rows of D bytes: the 128- or 64-byte swizzle, groups of 8 rows
+    static constexpr uint32_t LAYOUT = D == 128 ? 2 : 4;
+    static constexpr uint32_t SBO = 8 * D;
+    static_assert(P_OFF % 1024 == 0 && RING_OFF % 1024 == 0 && STAGE_BYTES % 1024 == 0, "");
+    static_assert(SMEM <= 232448, "shared memory per CTA");
+};
+
+// byte offset of 16-byte piece `ch` of row `row` in a tile of D-byte rows (the TMA patterns
+// SWIZZLE_128B and SWIZZLE_64B)
+template <int ROW>
+__device__ __forceinline__ uint32_t swz_row(int row, int ch) {
+    return ROW == 128 ? uint32_t(row) * 128u + uint32_t((ch ^ (row & 7)) << 4)
+                      : uint32_t(row) * 64u + uint32_t((ch ^ ((row >> 1) & 3)) << 4);
+}
+
+// D[tmem] (+)= A[smem desc] * B[smem desc], 8-bit floats (e4m3 here), 32 of K per instruction
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor for kind::f8f6f4, e4m3 operands, fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n, int a_mn, int b_mn) {
+    return (1u << 4) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
+           (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+
+// Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        ::"r"(smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// RP consecutive columns of this warp's 32 lanes, with the wait.
+__device__ __forceinline__ void tmem_cols(uint32_t ta, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(ta)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store_x8(uint32_t ta, const uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(ta),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_cols(uint32_t ta, uint32_t (&r)[16]) {
+    tmem_load_32x32b_x16_sync(ta, r);
+}
+__device__ __forceinline__ void tmem_cols(uint32_t ta, uint32_t (&r)[32]) {
+    tmem_load_32x32b_x32_sync(ta, r);
+}
+
+// Combines v[r] over the 32 lanes for each of N rows (max, or a sum over a fixed tree: lanes
+// that differ in bit 4, then bit 3, .. bit 0 -- the same for every N).  Every lane gets row
+// lane * N / 32: at each step a lane keeps one half of its rows while it has several.
+template <int N, bool MAX, int OFF = 16>
+__device__ __forceinline__ float combine_lanes(const float (&v)[N], int lane) {
+    auto op = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+    if constexpr (OFF == 0) {
+        return v[0];
+    } else if constexpr (N == 1) {
+        const float w[1] = {op(v[0], __shfl_xor_sync(0xffffffffu, v[0], OFF))};
+        return combine_lanes<1, MAX, OFF / 2>(w, lane);
+    } else {
+        const bool up = (lane & OFF) != 0;
+        float w[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + N / 2], OFF);
+            w[i] = op(up ? v[i + N / 2] : v[i], got);
+        }
+        return combine_lanes<N / 2, MAX, OFF / 2>(w, lane);
+    }
+}
+
+// Two e4m3 codes of (a, b), a in the low byte; and the values they stand for.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 e4m3x2_values(uint32_t c) {
+    return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(c), __NV_E4M3)));
+}
+
+// 2^(s - 127) of an E8M0 byte (255: NaN), and its inverse (255: 1, its row is NaN anyway).
+__device__ __forceinline__ float e8m0(uint32_t s) {
+    return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7fc00000u : s << 23);
+}
+__device__ __forceinline__ float e8m0_inv(uint32_t s) {
+    return s == 255 ? 1.f : e8m0(254 - s);
+}
+
+// A work item: chunk c of the keys for query tile u of sequence b, KV head h.
+struct Item {
+    int b, c, u, h;
+    SeqInfo si;
+    int pos0;    // position of the tile's first token
+    int ntok;    // its tokens
+    int npages;  // pages of the chunk that its last token sees (0: none, the item is empty)
+};
+
+template <int D, int RP>
+__global__ void __launch_bounds__(THREADS, 1)
+attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
+               const __grid_constant__ CUtensorMap tmap_v, const __nv_bfloat16* __restrict__ q,
+               const uint8_t* __restrict__ k_scale, const uint8_t* __restrict__ v_scale,
+               const int32_t* __restrict__ block_table, int max_pages, int num_pages,
+               const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ cu_q, int B,
+               int total_q, int max_q, int max_seq_len, int Hq, int Hkv, float scale_log2,
+               float* __restrict__ ws_o, float* __restrict__ ws_ml, int maxC,
+               unsigned int* __restrict__ cnt, unsigned int* err) {
+    using C = Cfg<D>;
+    constexpr int NST = C::NST;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    uint8_t* sQ = smem + C::Q_OFF;
+    uint8_t* sP = smem + C::P_OFF;
+    uint8_t* sStage = smem + C::RING_OFF;
+    uint8_t* sScale = smem + C::SCALE_OFF;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+    uint64_t* empty = full + NST;
+    uint64_t* s_full = empty + NST;     // scores of tile g in S buffer g % NSB
+    uint64_t* s_empty = s_full + NSB;   // ... read by the softmax warps
+    uint64_t* p_full = s_empty + NSB;   // P of tile g in P buffer g & 1
+    uint64_t* p_empty = p_full + 2;     // P V of tile g has completed (MMA commit)
+    uint64_t* o_full = p_empty + 2;     // item k's O (buffer k & 1) is complete (MMA commit)
+    uint64_t* o_empty = o_full + 2;     // ... and read out by the epilogue warps
+    uint64_t* xs_bar = o_empty + 2;     // item k's row sums and maxima are in xs[k & 1]
+    uint64_t* q_full = xs_bar + 2;      // item k's Q tile and row factors are in buffer k & 1
+    uint64_t* x_bar = q_full + 2;       // the softmax warps' exchange
+    uint64_t* drain = x_bar + 1;        // [2]: S issuer, P V issuer
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+    float* xs = reinterpret_cast<float*>(smem + C::XS_OFF);  // [2][NSM + 1][QR]
+    float* q_fac = xs + 2 * (NSM + 1) * QR;                  // [2][QR]
+    float* x_max = q_fac + 2 * QR;                           // [2][NSM][QR]
+    float* x_flag = x_max + 2 * NSM * QR;                    // [2][NSM]
+    int* stage_valid = reinterpret_cast<int*>(smem + C::MISC_OFF);  // [NST], a bit per page
+    int* prefix = stage_valid + NST;                         // [B + 1]
+    int* seq_len = prefix + MAX_BATCH + 1;
+    int* seq_t0 = seq_len + MAX_BATCH;
+    int* seq_qb = seq_t0 + MAX_BATCH;
+    int* done = seq_qb + MAX_BATCH;                          // [2]: epilogue warps per item
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(done + 2);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = Hq / Hkv;
+    const int TQ = QR / G;  // tokens of a query tile
+
+    if (warp == S_WARP) {
+        tmem_alloc(tmem_slot, TMEM_COLS);
+        tmem_relinquish();
+    }
+    // With item counters the grid before this one is the call's own counter reset, which
+    // waited for everything before it: the inputs are final, and only the counters need the
+    // epilogue's wait (see attention.cu).  Without, this grid waits for the previous one.
+    if (!cnt) {
+        pdl_wait();
+        pdl_trigger();
+    }
+    const unsigned long long wait_ns = wait_budget_ns(err);
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < NSB; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_empty[i], NSM);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&p_full[i], NSM);
+            mbar_init(&p_empty[i], 1);
+            mbar_init(&o_full[i], 1);
+            mbar_init(&o_empty[i], 4);
+            mbar_init(&xs_bar[i], NSM);
+            mbar_init(&q_full[i], 4);
+            mbar_init(&drain[i], 1);
+            done[i] = 0;
+        }
+        mbar_init(x_bar, NSM);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    for (int b = tid; b < B; b += THREADS) {
+        const SeqInfo si = seq_info(seq_lens, cu_q, b);
+        const bool ok = seq_ok(si, max_q, max_seq_len, total_q);
+        if (!ok) latch_error(err, kErrDeviceArg);
+        prefix[b + 1] = ok ? ((si.L + CHUNK - 1) >> CHUNK_LOG2) * ((si.qb + TQ - 1) / TQ) * Hkv : 0;
+        seq_len[b] = si.L;
+        seq_t0[b] = si.t0;
+        seq_qb[b] = si.qb;
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == 0) {  // inclusive scan of prefix[1..B], 32 at a time
+        int carry = 0;
+        for (int base = 0; base < B; base += 32) {
+            const int i = base + lane;
+            int v = i < B ? prefix[i + 1] : 0;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, off);
+                if (lane >= off) v += u;
+            }
+            if (i < B) prefix[i + 1] = v + carry;
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) prefix[0] = 0;
+    }
+    __syncthreads();
+    const int total = prefix[B];
+    const uint32_t tmem_base = *tmem_slot;
+
+    // The item at or after w that this CTA runs next (w is moved past empty ones); false at
+    // the end.
+    auto next_item = [&](int& w, Item& it) {
+        for (; w < total; w += gridDim.x) {
+            int lo = 0, hi = B;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (prefix[mid] <= w) lo = mid; else hi = mid;
+            }
+            it.b = lo;
+            it.si.L = seq_len[lo];
+            it.si.t0 = seq_t0[lo];
+            it.si.qb = seq_qb[lo];
+            const int U = (it.si.qb + TQ - 1) / TQ;
+            const int r = w - prefix[lo];
+            it.h = r % Hkv;
+            const int cu = r / Hkv;
+            it.c = cu / U;
+            it.u = cu - it.c * U;
+            it.ntok = min(TQ, it.si.qb - it.u * TQ);
+            it.pos0 = it.si.L - it.si.qb + it.u * TQ;
+            const int seen = it.pos0 + it.ntok - it.c * CHUNK;  // keys of the chunk it sees
+            it.npages = seen <= 0 ? 0 : min(CHUNK / PAGE, (seen + PAGE - 1) / PAGE);
+            if (it.npages > 0) return true;
+        }
+        return false;
+    };
+    auto give_up = [&]() {
+        if (!*abort_flag) {
+            *abort_flag = 1;
+            latch_error(err, kErrTimeout);
+        }
+    };
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && !mbar_wait_warp(bar, parity, abort_flag, wait_ns)) ok = false;
+        return ok;
+    };
+
+    if (warp == PRODUCER) {
+        // ------------------------------------------------------------------ producer
+        if (lane == 0) {
+            tma_prefetch_desc(&tmap_k);
+            tma_prefetch_desc(&tmap_v);
+        }
+        // blocks of one query tile read K and V once; wider ones read them again from L2
+        const uint64_t policy = max_q <= TQ ? l2_policy_evict_first() : l2_policy_evict_last();
+        uint32_t g = 0;
+        Item it;
+        for (int w = blockIdx.x; ok && next_item(w, it); w += gridDim.x) {
+            const int pidx = it.c * (CHUNK / PAGE) + lane;
+            const int phys_l = lane < it.npages && pidx < max_pages
+                                   ? block_table[int64_t(it.b) * max_pages + pidx]
+                                   : -1;
+            for (int i = 0; i < it.npages; i += TPAGES, ++g) {
+                const int s = int(g % NST);
+                if (!wait(&empty[s], ((g / NST) & 1u) ^ 1u)) break;
+                int phys[TPAGES], valid = 0;
+#pragma unroll
+                for (int k = 0; k < TPAGES; ++k) {
+                    phys[k] = __shfl_sync(0xffffffffu, phys_l, i + k);
+                    const bool there = i + k < it.npages;
+                    const bool v = there && phys[k] >= 0 && phys[k] < num_pages;
+                    if (v) valid |= 1 << k;
+                    if (there && !v && lane == 0) latch_error(err, kErrDeviceArg);
+                }
+                if (elect_one()) {
+                    stage_valid[s] = valid;
+                    uint8_t* st = sStage + s * C::STAGE_BYTES;
+                    if (valid)
+                        mbar_arrive_expect_tx(&full[s], uint32_t(__popc(valid)) *
+                                                            (2 * C::PAGE_BYTES + 2 * PAGE));
+                    else
+                        mbar_arrive(&full[s]);
+#pragma unroll
+                    for (int k = 0; k < TPAGES; ++k) {
+                        if (valid & (1 << k)) {
+                            const int row = (phys[k] * Hkv + it.h) * PAGE;
+                            tma_load_2d_hint(st + k * C::PAGE_BYTES, &tmap_k, &full[s], 0, row,
+                                             policy);
+                            tma_load_2d_hint(st + C::SIDE_BYTES + k * C::PAGE_BYTES, &tmap_v,
+                                             &full[s], 0, row, policy);
+                            uint8_t* sc = sScale + s * 2 * TK + k * PAGE;
+                            bulk_load(sc, k_scale + row, PAGE, &full[s]);
+                            bulk_load(sc + TK, v_scale + row, PAGE, &full[s]);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok) {
+            if (lane == 0) give_up();
+            // copies already issued land before the CTA exits (bounded)
+            for (int k = 1; k <= NST && k <= int(g); ++k) {
+                const uint32_t gg = g - k;
+                mbar_wait(&full[gg % NST], (gg / NST) & 1u, nullptr, 100000000ull);
+            }
+        }
+    } else if (warp == S_WARP) {
+        // ------------------------------------------------- S^T = K (Q_hi + Q_lo)^T
+        constexpr uint32_t idesc = idesc_e4m3(TK, QR, 0, 0);
+        const uint64_t q_desc0 = umma_smem_desc(smem_addr(sQ), 16, C::SBO, C::LAYOUT);
+        const uint64_t k_desc0 = umma_smem_desc(smem_addr(sStage), 16, C::SBO, C::LAYOUT);
+        uint32_t g = 0;
+        int item = 0;
+        Item it;
+        for (int w = blockIdx.x; ok && next_item(w, it); w += gridDim.x, ++item) {
+            const int qbuf = item & 1;
+            if (!wait(&q_full[qbuf], uint32_t(item >> 1) & 1u)) break;
+            for (int i = 0; i < it.npages; i += TPAGES, ++g) {
+                const int s = int(g % NST), sb = int(g % NSB);
+                if (!wait(&full[s], (g / NST) & 1u) ||
+                    !wait(&s_empty[sb], ((g / NSB) & 1u) ^ 1u))
+                    break;
+                tc_fence_after_sync();
+                if (elect_one()) {
+                    const uint64_t k_desc = k_desc0 + uint64_t((s * C::STAGE_BYTES) >> 4);
+                    const uint64_t q_desc = q_desc0 + uint64_t((qbuf * C::Q_BYTES) >> 4);
+                    const uint32_t d = tmem_base + uint32_t(S_COL + sb * QR);
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {  // head dims 32k .. 32k+31: +32 B
+                        tc_mma_f8(d, k_desc + uint64_t(k * 2), q_desc + uint64_t(k * 2), idesc,
+                                  k != 0 ? 1u : 0u);
+                        tc_mma_f8(d, k_desc + uint64_t(k * 2),
+                                  q_desc + uint64_t((C::Q_PIECE >> 4) + k * 2), idesc, 1u);
+                    }
+                    tc_commit(&s_full[sb]);
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok && lane == 0) give_up();
+        if (elect_one()) tc_commit(&drain[0]);
+        __syncwarp();
+        mbar_wait(&drain[0], 0, nullptr, 100000000ull);
+    } else if (warp == PV_WARP) {
+        // ------------------------------------------------- O^T += V^T [P_hi | P_lo]^T
+        constexpr uint32_t idesc = idesc_e4m3(D, 2 * QR, 1, 1);
+        const uint64_t v_desc0 =
+            umma_smem_desc(smem_addr(sStage + C::SIDE_BYTES), 16, C::SBO, C::LAYOUT);
+        const uint64_t p_desc0 = umma_smem_desc(smem_addr(sP), 16, 512, 4);
+        uint32_t g = 0;
+        int item = 0;
+        Item it;
+        for (int w = blockIdx.x; ok && next_item(w, it); w += gridDim.x, ++item) {
+            const int ob = item & 1;
+            // the O buffer of this item was read out for item-2
+            if (!wait(&o_empty[ob], (uint32_t(item >> 1) & 1u) ^ 1u)) break;
+            for (int i = 0; i < it.npages; i += TPAGES, ++g) {
+                const int s = int(g % NST), pb = int(g & 1u);
+                if (!wait(&p_full[pb], (g >> 1) & 1u)) break;
+                tc_fence_after_sync();
+                if (elect_one()) {
+                    const uint64_t v_desc = v_desc0 + uint64_t((s * C::STAGE_BYTES) >> 4);
+                    const uint64_t p_desc = p_desc0 + uint64_t((pb * C::P_BYTES) >> 4);
+                    const uint32_t d = tmem_base + uint32_t(O_COL + ob * 2 * QR);
+#pragma unroll
+                    for (int k = 0; k < TK / 32; ++k)  // keys 32k .. 32k+31
+                        tc_mma_f8(d, v_desc + uint64_t(k * 32 * D / 16),
+                                  p_desc + uint64_t(k * 32 * 2 * QR / 16), idesc,
+                                  (i | k) != 0 ? 1u : 0u);
+                    tc_commit(&p_empty[pb]);
+                    tc_commit(&empty[s]);  // K, V and scales of the tile are no longer read
+                    if (i + TPAGES >= it.npages) tc_commit(&o_full[ob]);
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok && lane == 0) give_up();
+        if (elect_one()) tc_commit(&drain[1]);
+        __syncwarp();
+        mbar_wait(&drain[1], 0, nullptr, 100000000ull);
+    } else if (warp >= EPI) {
+        // ------------------------------------------------- Q split and epilogue
+        const int ew = warp - EPI;  // tensor-memory lane quarter
+        // Q tile of an item: four neighbouring threads split one row.
+        auto split_q = [&](const Item& it, int buf) {
+            constexpr int PER = D / 4;  // elements per thread
+            const int r = ew * 8 + (lane >> 2), part = lane & 3;
+            const int j = r / G;
+            uint4 v[PER / 8];
+#pragma unroll
+            for (int k = 0; k < PER / 8; ++k) v[k] = make_uint4(0, 0, 0, 0);
+            if (j < it.ntok && r < TQ * G) {
+                const __nv_bfloat16* src =
+                    q + (int64_t(it.si.t0 + it.u * TQ + j) * Hq + it.h * G + (r - j * G)) * D +
+                    part * PER;
+#pragma unroll
+                for (int k = 0; k < PER / 8; ++k)
+                    v[k] = *reinterpret_cast<const uint4*>(src + k * 8);
+            }
+            uint32_t amax = 0;  // of bf16 magnitudes, which order as their bits
+#pragma unroll
+            for (int k = 0; k < PER / 8; ++k) {
+                const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    amax = max(amax, max(x[n] & 0x7fffu, (x[n] >> 16) & 0x7fffu));
+            }
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // s = 7 - floor(log2(amax)), held where 2^s and 2^-s are normal
+            const int s = max(-120, min(120, 134 - int(amax >> 7)));
+            const float mul = __uint_as_float(uint32_t(127 + s) << 23);
+            uint8_t* hi = sQ + buf * C::Q_BYTES;
+            uint8_t* lo = hi + C::Q_PIECE;
+#pragma unroll
+            for (int k = 0; k < PER / 16; ++k) {
+                uint32_t h[4], l[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const uint4& src = v[2 * k + (n >> 1)];
+                    const uint32_t x0 = n & 1 ? src.z : src.x, x1 = n & 1 ? src.w : src.y;
+                    float f[4] = {__uint_as_float(x0 << 16) * mul,
+                                  __uint_as_float(x0 & 0xffff0000u) * mul,
+                                  __uint_as_float(x1 << 16) * mul,
+                                  __uint_as_float(x1 & 0xffff0000u) * mul};
+                    const uint32_t c0 = e4m3x2(f[0], f[1]), c1 = e4m3x2(f[2], f[3]);
+                    const float2 b0 = e4m3x2_values(c0), b1 = e4m3x2_values(c1);
+                    h[n] = c0 | (c1 << 16);
+                    l[n] = e4m3x2(f[0] - b0.x, f[1] - b0.y) |
+                           (e4m3x2(f[2] - b1.x, f[3] - b1.y) << 16);
+                }
+                const uint32_t at = swz_row<D>(r, part * (PER / 16) + k);
+                *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+            }
+            // a query with an infinity or NaN scores NaN throughout
+            if (part == 0)
+                q_fac[buf * QR + r] = amax >= 0x7f80u
+                                          ? __int_as_float(0x7fc00000)
+                                          : scale_log2 * __uint_as_float(uint32_t(127 - s) << 23);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[buf]);
+        };
+        int item = 0;
+        bool reset_done = cnt == nullptr;  // griddepcontrol.wait passed
+        Item it, nx;
+        int w = blockIdx.x;
+        bool have = next_item(w, it);
+        if (have) split_q(it, 0);
+        for (; ok && have; ++item) {
+            int wn = w + gridDim.x;
+            const bool more = next_item(wn, nx);
+            // (this buffer's item-1 is complete: its O was waited for)
+            if (more) split_q(nx, (item + 1) & 1);
+            const int ob = item & 1;
+            const uint32_t par = uint32_t(item >> 1) & 1u;
+            if (!wait(&xs_bar[ob], par) || !wait(&o_full[ob], par)) break;
+            tc_fence_after_sync();
+            // row r = lane: its partial's place
+            const int r = lane;
+            const int j = r / G;
+            const bool store = j < it.ntok && r < TQ * G && it.pos0 + j >= it.c * CHUNK;
+            const int64_t idx = (int64_t(it.si.t0 + it.u * TQ + j) * Hq + int64_t(it.h) * G +
+                                 (r - j * G)) * maxC + it.c;
+            uint32_t vh[RP], vl[RP];
+            const uint32_t ta =
+                tmem_base + (uint32_t(32 * ew) << 16) + uint32_t(O_COL + ob * 2 * QR);
+            tmem_cols(ta, vh);
+            tmem_cols(ta + QR, vl);
+            // O^T: lane = head dim (M = 128), or dims 16 ew .. 16 ew + 15 in lanes 0..15 (M = 64)
+            const int d = D == 128 ? ew * 32 + lane : ew * 16 + lane;
+            const bool mine = D == 128 || lane < 16;
+#pragma unroll
+            for (int rr = 0; rr < RP; ++rr) {
+                const bool st = __shfl_sync(0xffffffffu, store ? 1 : 0, rr) != 0;
+                const int64_t at = __shfl_sync(0xffffffffu, idx, rr);
+                if (st && mine)
+                    ws_o[at * D + d] =
+                        fmaf(__uint_as_float(vl[rr]), 0.0625f, __uint_as_float(vh[rr]));
+            }
+            if (ew == 0 && store) {
+                const float* x = xs + ob * ((NSM + 1) * QR);
+                const float l = ((x[r] + x[QR + r]) + x[2 * QR + r]) + x[3 * QR + r];
+                *reinterpret_cast<float2*>(ws_ml + idx * 2) = make_float2(x[NSM * QR + r], l);
+            }
+            tc_fence_before_sync();
+            if (cnt) {
+                // the fourth warp to have stored its part of the item counts it
+                __threadfence();
+                __syncwarp();
+                if (!reset_done) {
+                    pdl_wait();
+                    pdl_trigger();
+                    reset_done = true;
+                }
+                if (lane == 0 && (atomicAdd(&done[ob], 1) & 3) == 3) {
+                    __threadfence();
+                    atomicAdd(cnt + it.b * Hkv + it.h, 1u);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_empty[ob]);
+            it = nx;
+            w = wn;
+            have = more;
+        }
+        if (!ok && lane == 0) give_up();
+        // a CTA with no item (or one that gave up) still waits before it completes
+        if (!reset_done) {
+            pdl_wait();
+            pdl_trigger();
+        }
+    } else {
+        // ------------------------------------------------------------------- softmax
+        const int key = tid;  // this thread's key of every tile
+        const uint32_t lane_base = uint32_t(32 * warp) << 16;
+        uint32_t g = 0, ex = 0;  // tiles, exchanges
+        int item = 0;
+        Item it;
+        float m[RP], l[RP];
+        for (int w = blockIdx.x; ok && next_item(w, it); w += gridDim.x, ++item) {
+            const int ob = item & 1;
+            const uint32_t ipar = uint32_t(item >> 1) & 1u;
+            if (!wait(&q_full[ob], ipar)) break;
+            const float* fac = q_fac + ob * QR;
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+                m[r] = kNoMax;
+                l[r] = 0.f;
+            }
+            for (int i = 0; i < it.npages && ok; i += TPAGES, ++g) {
+                const int s = int(g % NST), sb = int(g % NSB), pb = int(g & 1u);
+                const int kp = it.c * CHUNK + i * PAGE + key;  // this key's position
+                if (!wait(&s_full[sb], (g / NSB) & 1u)) break;
+                tc_fence_after_sync();
+                uint32_t sv[RP];
+                tmem_cols(tmem_base + lane_base + uint32_t(S_COL + sb * QR), sv);
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_empty[sb]);
+                // (landed before its scores were computed: this orders the reads below)
+                if (!wait(&full[s], (g / NST) & 1u)) break;
+                const bool there = (stage_valid[s] >> (key / PAGE)) & 1;
+                const bool live = there && kp < it.si.L;
+                const uint32_t ksc = sScale[s * 2 * TK + key], vsc = sScale[s * 2 * TK + TK + key];
+                const float ka = e8m0(ksc);
+                const float vb = vsc == 255 ? __int_as_float(0x7fc00000) : float(int(vsc) - 127);
+                const float vinv = live ? e8m0_inv(vsc) : 0.f;
+                float t[RP];
+#pragma unroll
+                for (int r = 0; r < RP; r += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(fac + r);
+                    t[r] = fmaf(__uint_as_float(sv[r]) * ka, f.x, vb);
+                    t[r + 1] = fmaf(__uint_as_float(sv[r + 1]) * ka, f.y, vb);
+                    t[r + 2] = fmaf(__uint_as_float(sv[r + 2]) * ka, f.z, vb);
+                    t[r + 3] = fmaf(__uint_as_float(sv[r + 3]) * ka, f.w, vb);
+                }
+                // causal mask: row r (token r / G) sees the key when r / G >= kp - pos0
+                if (!__all_sync(0xffffffffu, live && kp <= it.pos0)) {
+                    const int first = live ? max(0, kp - it.pos0) * G : QR;  // first row seeing it
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) t[r] = r >= first ? t[r] : -INFINITY;
+                }
+                // does any row's maximum exceed its reference by more than 2^8?
+                bool slow = i == 0;
+                if (!slow) {
+                    float over = -INFINITY;
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) over = fmaxf(over, t[r] - m[r]);
+                    const bool any = __any_sync(0xffffffffu, over > kRaise);
+                    float* fl = x_flag + (ex & 1u) * NSM;
+                    if (lane == 0) {
+                        fl[warp] = any ? 1.f : 0.f;
+                        mbar_arrive(x_bar);
+                    }
+                    if (!wait(x_bar, ex & 1u)) break;
+                    const float4 f = *reinterpret_cast<const float4*>(fl);
+                    slow = f.x + f.y + f.z + f.w != 0.f;
+                    ++ex;
+                }
+                if (slow) {
+                    // the tile's maximum of every row, over the four warps
+                    const float mine = combine_lanes<RP, true>(t, lane);
+                    float* xm = x_max + (ex & 1u) * (NSM * QR);
+                    if (lane % (32 / RP) == 0) xm[warp * QR + lane / (32 / RP)] = mine;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(x_bar);
+                    if (!wait(x_bar, ex & 1u)) break;
+                    ++ex;
+                    // O of this warp's lanes may be scaled once P V of the tile before is done
+                    const uint32_t gp = g - 1u;
+                    if (i > 0 && !wait(&p_empty[gp & 1u], (gp >> 1) & 1u)) break;
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int r0 = 0; r0 < RP; r0 += 8) {
+                        float fa[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int r = r0 + k;
+                            const float mt = fmaxf(fmaxf(xm[r], xm[QR + r]),
+                                                   fmaxf(xm[2 * QR + r], xm[3 * QR + r]));
+                            const bool raise = mt > m[r] + kRaise;
+                            const float mn = raise ? mt - kHeadroom : m[r];
+                            fa[k] = raise ? ex2(m[r] - mn) : 1.f;
+                            m[r] = mn;
+                            l[r] *= fa[k];
+                        }
+                        if (i > 0) {
+                            uint32_t o[8];
+                            const uint32_t ta =
+                                tmem_base + lane_base + uint32_t(O_COL + ob * 2 * QR + r0);
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                tmem_cols(ta + half * QR, o);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    o[k] = __float_as_uint(__uint_as_float(o[k]) * fa[k]);
+                                tmem_store_x8(ta + half * QR, o);
+                            }
+                        }
+                    }
+                    tc_fence_before_sync();
+                }
+                // P buffer pb is free once P V of tile g-2 has completed
+                if (!wait(&p_empty[pb], ((g >> 1) & 1u) ^ 1u)) break;
+                uint32_t hi[RP / 4], lo[RP / 4];
+#pragma unroll
+                for (int r = 0; r < RP; r += 4) {
+                    float p[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        p[k] = ex2(t[r + k] - m[r + k]);
+                        l[r + k] = fmaf(p[k], vinv, l[r + k]);
+                    }
+                    const uint32_t c0 = e4m3x2(p[0], p[1]), c1 = e4m3x2(p[2], p[3]);
+                    const float2 b0 = e4m3x2_values(c0), b1 = e4m3x2_values(c1);
+                    hi[r / 4] = c0 | (c1 << 16);
+                    lo[r / 4] = e4m3x2((p[0] - b0.x) * 16.f, (p[1] - b0.y) * 16.f) |
+                                (e4m3x2((p[2] - b1.x) * 16.f, (p[3] - b1.y) * 16.f) << 16);
+                }
+                uint8_t* pbuf = sP + pb * C::P_BYTES;
+                if (RP == 8) {
+                    *reinterpret_cast<uint2*>(pbuf + swz_row<64>(key, 0)) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2*>(pbuf + swz_row<64>(key, 2)) = make_uint2(lo[0], lo[1]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < RP / 16; ++k) {
+                        *reinterpret_cast<uint4*>(pbuf + swz_row<64>(key, k)) =
+                            make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+                        *reinterpret_cast<uint4*>(pbuf + swz_row<64>(key, 2 + k)) =
+                            make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                    }
+                }
+                // V rows past the sequence's end or of an invalid page are zeroed, so that
+                // unwritten codes (NaN) cannot reach O through 0 * v
+                if (!live) {
+                    uint4* vr = reinterpret_cast<uint4*>(sStage + s * C::STAGE_BYTES +
+                                                         C::SIDE_BYTES + key * D);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) vr[k] = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[pb]);
+            }
+            if (!ok) break;
+            // the warp's row sums (and the maxima) for the epilogue, once it has read this
+            // buffer's previous contents (item-2)
+            if (!wait(&o_empty[ob], ipar ^ 1u)) break;
+            float* x = xs + ob * ((NSM + 1) * QR);
+            if (warp == 0 && lane == 0) {
+#pragma unroll
+                for (int r = 0; r < RP; ++r) x[NSM * QR + r] = m[r];
+            }
+            const float sum = combine_lanes<RP, false>(l, lane);
+            if (lane % (32 / RP) == 0) x[warp * QR + lane / (32 / RP)] = sum;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&xs_bar[ob]);
+        }
+        if (!ok && lane == 0) give_up();
+    }
+    // every warp is done with tensor memory and shared memory past this barrier
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == S_WARP) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem_base, TMEM_COLS);
+    }
+}
+
+template <int D, int RP>
 cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a,
                         const void* k_scale, const void* v_scale, float scale, void* out,
                         float* lse, void* workspace, cudaStream_t stream) {
+    using Cf = Cfg<D>;
+    const uint64_t rows = uint64_t(a.num_pages) * uint64_t(a.hkv) * PAGE;
+    CUtensorMap tk, tv;
+    if (!tmap_2d_u8_swizzled(&tk, a.k_cache, D, rows, PAGE) ||
+        !tmap_2d_u8_swizzled(&tv, a.v_cache, D, rows, PAGE))
+        return cudaErrorNotSupported;
+    auto kern = attn_q8_kernel<D, RP>;
+    static bool attr_done[64] = {};
+    if (dev.device >= 0 && dev.device < 64 && !attr_done[dev.device]) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             int(Cf::SMEM));
+        if (e != cudaSuccess) return e;
+        attr_done[dev.device] = true;
+    }
     const int maxC = int((a.max_seq_len + CHUNK - 1) / CHUNK);
+    const int64_t TQ = QR / (a.hq / a.hkv);
+    const int64_t tiles = (a.max_q + TQ - 1) / TQ;
+    const int64_t items_bound = a.batch * int64_t(maxC) * tiles * a.hkv;
+    if (items_bound > 0x7fffffffLL - dev.num_sms) return cudaErrorNotSupported;
+    const int grid = int(items_bound < dev.num_sms ? items_bound : dev.num_sms);
     float* ws_o = static_cast<float*>(workspace);
     float* ws_ml = ws_o + a.total_q * a.hq * int64_t(maxC) * D;
-    const int TQ = QR / int(a.hq / a.hkv);
-    const int tiles = int((a.max_q + TQ - 1) / TQ);
-    if (int64_t(tiles) * a.hkv > 65535) return cudaErrorNotSupported;
+    // one query tile per sequence: the merge of a (sequence, KV head) starts when its chunks
+    // are counted; more: it waits for the whole grid
+    unsigned int* cnt = nullptr;
+    if (tiles == 1) {
+        cnt = attn_item_counters(a, workspace, CHUNK_LOG2);
+        cudaError_t e = launch_attn_count_reset(cnt, int(a.batch * a.hkv), stream);
+        if (e != cudaSuccess) return e;
+    }
     cudaError_t e = launch_pdl(
-        attn_q8_kernel<D>, dim3(maxC, unsigned(tiles * a.hkv), unsigned(a.batch)), dim3(THREADS),
-        0, stream, static_cast<const __nv_bfloat16*>(q), static_cast<const uint8_t*>(a.k_cache),
-        static_cast<const uint8_t*>(a.v_cache), static_cast<const uint8_t*>(k_scale),
+        kern, dim3(grid), dim3(THREADS), Cf::SMEM, stream, tk, tv,
+        static_cast<const __nv_bfloat16*>(q), static_cast<const uint8_t*>(k_scale),
         static_cast<const uint8_t*>(v_scale), a.block_table, int(a.max_pages), int(a.num_pages),
-        a.seq_lens, a.cu_q, int(a.total_q), int(a.max_q), int(a.max_seq_len), int(a.hq),
-        int(a.hkv), tiles, scale * kLog2e, ws_o, ws_ml, maxC, dev.err_word);
+        a.seq_lens, a.cu_q, int(a.batch), int(a.total_q), int(a.max_q), int(a.max_seq_len),
+        int(a.hq), int(a.hkv), scale * kLog2e, ws_o, ws_ml, maxC, cnt, dev.err_word);
     if (e != cudaSuccess) return e;
-    return launch_attn_merge(a, workspace, CHUNK_LOG2, out, lse, nullptr, dev.err_word, stream);
+    return launch_attn_merge(a, workspace, CHUNK_LOG2, out, lse, cnt, dev.err_word, stream);
 }
 
 }  // namespace
@@ -128,9 +847,13 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
 cudaError_t launch_attention_q8(const DeviceInfo& dev, const void* q, const PagedArgs& a,
                                 const void* k_scale, const void* v_scale, float scale, void* out,
                                 float* lse, void* workspace, cudaStream_t stream) {
+    // query rows of the fullest tile
+    const int64_t G = a.hq / a.hkv, TQ = QR / G;
+    const int64_t rows = (a.max_q < TQ ? a.max_q : TQ) * G;
+    auto run = [&](auto f) { return f(dev, q, a, k_scale, v_scale, scale, out, lse, workspace, stream); };
     if (a.head_dim == 64)
-        return launch_q8_t<64>(dev, q, a, k_scale, v_scale, scale, out, lse, workspace, stream);
-    return launch_q8_t<128>(dev, q, a, k_scale, v_scale, scale, out, lse, workspace, stream);
+        return run(rows <= 8 ? launch_q8_t<64, 8> : rows <= 16 ? launch_q8_t<64, 16> : launch_q8_t<64, 32>);
+    return run(rows <= 8 ? launch_q8_t<128, 8> : rows <= 16 ? launch_q8_t<128, 16> : launch_q8_t<128, 32>);
 }
 
 }  // namespace bi

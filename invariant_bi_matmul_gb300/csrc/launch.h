@@ -166,6 +166,11 @@ cudaError_t launch_attn_merge(const PagedArgs& a, void* workspace, int chunk_log
                               float* lse, const unsigned int* cnt, unsigned int* err,
                               cudaStream_t stream);
 
+// The item counters' place in a call's workspace, one per (sequence, KV head), and the kernel
+// that zeroes n of them before the partial kernel (which must be the next launch) counts.
+unsigned int* attn_item_counters(const PagedArgs& a, void* workspace, int chunk_log2);
+cudaError_t launch_attn_count_reset(unsigned int* cnt, int n, cudaStream_t stream);
+
 // Chunked prefill (prefill.cu): blocks of any width, each query reduced exactly as the
 // decode / verify kernels reduce it (invariant chunk length), then the same merge.
 cudaError_t launch_prefill(const DeviceInfo& dev, const void* q, const PagedArgs& a,

@@ -131,6 +131,21 @@ bool tmap_2d_u8(CUtensorMap* out, const void* ptr, uint64_t inner_bytes, uint64_
                          stride_bytes, box_inner, box_outer);
 }
 
+bool tmap_2d_u8_swizzled(CUtensorMap* out, const void* ptr, uint32_t row_bytes, uint64_t outer,
+                         uint32_t box_outer) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || (row_bytes != 64 && row_bytes != 128)) return false;
+    const cuuint64_t dims[2] = {row_bytes, outer};
+    const cuuint64_t strides[1] = {row_bytes};
+    const cuuint32_t box[2] = {row_bytes, box_outer};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool tmap_3d_bf16(CUtensorMap* out, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2,
                   uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1,
                   uint32_t box2) {

@@ -26,6 +26,10 @@ bool tmap_kblocked_bf16(CUtensorMap* out, const void* ptr, uint64_t inner, uint6
 // box_inner bytes x box_outer rows, no swizzle; bytes outside the tensor read as 0.
 bool tmap_2d_u8(CUtensorMap* out, const void* ptr, uint64_t inner_bytes, uint64_t outer,
                 uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer);
+// 2D byte tensor of `outer` contiguous rows of row_bytes (64 or 128), boxes of box_outer whole
+// rows with the shared-memory swizzle of that width.
+bool tmap_2d_u8_swizzled(CUtensorMap* out, const void* ptr, uint32_t row_bytes, uint64_t outer,
+                         uint32_t box_outer);
 // 3D bf16 tensor [d2][d1][d0] with element strides stride1 (between d1 rows) and
 // stride2 (between d2 slabs), boxes box0 x box1 x box2 landing densely in shared memory,
 // 128-byte swizzle; elements outside the tensor read as 0.  No cache.

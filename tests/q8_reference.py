@@ -36,20 +36,28 @@ def cache_values(codes: torch.Tensor, scale: torch.Tensor) -> np.ndarray:
     return code_values(codes) * f[..., None]
 
 
-def attention(q, k, v, table, L, q_len, scale, G):
-    """One sequence's block: q [q_len, Hq, D] (float64), k and v [pages, Hkv, 64, D] values;
-    returns out, lse and A [q_len, Hq, D], the weighted mean of |v|, and S [q_len, Hq], the
-    largest sum of |q k| * scale over the keys seen."""
+def scale_values(scale: torch.Tensor) -> np.ndarray:
+    return 2.0 ** (scale.cpu().numpy().astype(np.float64) - 127)
+
+
+def attention(q, k, v, ys, table, L, q_len, scale, G):
+    """One sequence's block: q [q_len, Hq, D] (float64), k and v [pages, Hkv, 64, D] values, ys
+    [pages, Hkv, 64] the value rows' scales; returns out, lse, A [q_len, Hq, D], the weighted
+    mean of |v|, F [q_len, Hq, D], the largest (weight * value scale) times the sum of the
+    codes' magnitudes |v| / scale, and S [q_len, Hq], the largest sum of |q k| * scale, over
+    the keys seen."""
     n = -(-L // PAGE)
     pages = [int(p) for p in table[:n]]
     Hkv, D = k.shape[1], k.shape[3]
     out = np.zeros(q.shape)
     A = np.zeros(q.shape)
+    F = np.zeros(q.shape)
     lse = np.zeros(q.shape[:2])
     S = np.zeros(q.shape[:2])
     for h in range(Hkv):
         kh = k[pages, h].reshape(-1, D)[:L]
         vh = v[pages, h].reshape(-1, D)[:L]
+        yh = ys[pages, h].reshape(-1)[:L]
         for j in range(q_len):
             pos = L - q_len + j
             for g in range(h * G, (h + 1) * G):
@@ -57,23 +65,27 @@ def attention(q, k, v, table, L, q_len, scale, G):
                 m = s.max()
                 p = np.exp(s - m)
                 w = p / p.sum()
-                out[j, g], A[j, g] = w @ vh[:pos + 1], w @ np.abs(vh[:pos + 1])
+                a = np.abs(vh[:pos + 1])
+                out[j, g], A[j, g] = w @ vh[:pos + 1], w @ a
+                F[j, g] = (w * yh[:pos + 1]).max() * (a / yh[:pos + 1, None]).sum(0)
                 lse[j, g] = m + math.log(p.sum())
                 S[j, g] = (np.abs(kh[:pos + 1]) @ np.abs(q[j, g])).max() * abs(scale)
-    return out, lse, A, S
+    return out, lse, A, F, S
 
 
 def check_attention(out, lse, ref, what=""):
     """Against the 64-bit values, element by element.
-    out: rounding to bf16 moves a value by at most 2^-8 of itself; the softmax weights are
-    held to 2^-9 of themselves (two e4m3 pieces of four bits each) plus, per key, 2^-20 of
-    the largest weight of its chunk (512 keys: 2^-11 in all), either way times |v|: with the
-    fp32 parts (scores, exp2, sums: below 2^-12) less than 2^-8 of the weighted mean of |v|.
+    out: rounding to bf16 moves a value by at most 2^-8 of itself.  A weight times its value
+    scale, p, is held as two e4m3 pieces of four bits each: off by at most 2^-9 of itself,
+    which moves out by at most 2^-9 A, or, where the second piece is below e4m3's normal range
+    (steps of 2^-9, in units of 1/16), by at most 2^-10 / 16 = 2^-14 when the largest p is at
+    least 2^6: 2^-20 of the largest p per unit of a code, at most 2^-20 F in all.  The fp32
+    parts (scores off by 2^-17 S, exp2, sums) stay below 2^-10 A for S up to 2^6.
     lse: fp32 scores off by at most 2^-17 of the largest sum of |q k|, and a few fp32
     roundings of a number of lse's size."""
-    o, l, A, S = ref
+    o, l, A, F, S = ref
     g = out.double().cpu().numpy()
-    bound = 2.0 ** -8 * np.abs(o) + 2.0 ** -8 * A
+    bound = 2.0 ** -8 * np.abs(o) + (2.0 ** -9 + 2.0 ** -10) * A + 2.0 ** -20 * F
     err = np.abs(g - o)
     assert np.isfinite(g).all(), f"{what}: non-finite output"
     worst = np.unravel_index(np.argmax(err - bound), err.shape)

@@ -59,7 +59,8 @@ class Cache:
                         i32(cu, dev))
 
     def values(self):
-        return ref.cache_values(self.k, self.ks), ref.cache_values(self.v, self.vs)
+        return (ref.cache_values(self.k, self.ks), ref.cache_values(self.v, self.vs),
+                ref.scale_values(self.vs))
 
 
 def rows(shape, seed, spread=1.0, std=1.0):
@@ -209,7 +210,7 @@ def test_attention_against_64_bits(dev, case):
     q = rows((T, Hq, D), 90 + case, 0.5)
     forms = (["prefill"] + (["verify"] if max(qs) * Hq // Hkv <= 32 and max(qs) <= 8 else [])
              + (["decode"] if max(qs) == 1 else []))
-    k, v = c.values()
+    kv = c.values()
     outs = []
     for form in forms:
         # rows in front of and behind the block stay as they are
@@ -220,7 +221,7 @@ def test_attention_against_64_bits(dev, case):
         assert bool((lbuf[0] == 5).all() and (lbuf[-1] == 5).all())
         t = 0
         for b, (L, w) in enumerate(zip(lens, qs)):
-            r = ref.attention(q[t:t + w].double().numpy(), k, v, c.table[b].tolist(), L, w,
+            r = ref.attention(q[t:t + w].double().numpy(), *kv, c.table[b].tolist(), L, w,
                               D ** -0.5, Hq // Hkv)
             ref.check_attention(obuf[1 + t:1 + t + w], lbuf[1 + t:1 + t + w], r,
                                 f"{form} sequence {b}")
