@@ -14,13 +14,13 @@
 //   * q * 2^s (s puts the row's largest value in [128, 256)) = hi + lo, each rounded to
 //     nearest: exact for bf16 q down to 2^-9 of the row's largest value, off by at most
 //     2^-18 of it below;
-//   * p = hi + lo / 16: p <= 2^8; hi has four bits, lo the next four, so p is held to
-//     2^-9 of itself (bf16 would hold 2^-8) and to 2^-14 absolute, where the reference
-//     maximum stands for p = 2^6 at least.
+//   * p = hi + lo / 32: p <= 2^8; hi has four bits, lo the next four, so p is held to
+//     2^-9 of itself (bf16 would hold 2^-8) or to 2^-15 absolute, whichever is more; the
+//     largest p of a row is 2^3 at least.
 //
 // Reduction of one (query, head) -- a function of its position alone, as in attention.cu:
 // chunks of 512 keys from key 0; a chunk in tiles of 128 keys, ascending; per tile the exact
-// maximum of the row's t, m raised to (maximum - 6) only when the maximum exceeds m + 8 (O and
+// maximum of the row's t, m raised to (maximum - 3) only when the maximum exceeds m + 8 (O and
 // the sums then scaled by 2^(m_old - m_new)); each of 128 threads sums its key of every tile,
 // and the 128 sums are added by a fixed tree; the chunk partials (m, l, o) go through the
 // merge of attention.cu.  A tile that a row does not see changes none of its numbers, and a
@@ -32,11 +32,12 @@
 // as many exponentials as there are query rows (rounded up to 8, 16 or 32), reads its key's
 // two scale bytes once, and writes its P values as 16-byte pieces.
 //
-// Warps: 0..3 softmax (one key of the tile per thread), 4..7 epilogue (they also split the
-// next item's Q), 8 TMA producer, 9 S issuer (and TMEM owner), 10 P V issuer.  One persistent
-// CTA per SM; work items (sequence, chunk, query tile, KV head) are enumerated on the device.
-// All waits are bounded mbarrier waits; warps never meet in a barrier that one of them may
-// have given up on.
+// Warps: one or two softmax groups of four (one key of the tile per thread; two groups share
+// the query rows), four epilogue warps (they also split the next item's Q), the TMA producer
+// (it also finds the work items and publishes them), the S issuer (and TMEM owner), the P V
+// issuer.  One persistent CTA per SM; work items (sequence, chunk, query tile, KV head) are
+// enumerated on the device.  All waits are bounded; the one barrier that warps meet in, a
+// softmax group's, is left by all of them together.
 //
 // Bound by memory: 2 * (D + 1) bytes per key and KV head against 4 * 32 * D operations.
 #include "attn_common.cuh"
@@ -49,20 +50,23 @@ namespace {
 constexpr int QR = 32;                    // query rows of a tile
 constexpr int TK = 128;                   // keys of a tile: two pages
 constexpr int TPAGES = TK / PAGE;
-constexpr int NSM = 4;                    // softmax warps 0..3
-constexpr int EPI = 4;                    // first epilogue warp (4..7)
-constexpr int PRODUCER = 8, S_WARP = 9, PV_WARP = 10;
-constexpr int THREADS = 11 * 32;
+constexpr int NQ = 4;                     // warps of a softmax group: 32 keys each
+constexpr int NDESC = 16;                 // item descriptors in flight
 constexpr int NSB = 4;                    // S buffers in tensor memory
 constexpr int TMEM_COLS = 256;
 constexpr int S_COL = 0;                  // S buffers: 32 columns each
 constexpr int O_COL = NSB * QR;           // O buffers (by item): 32 hi + 32 lo columns each
 constexpr float kNoMax = -1e30f;          // m before any visible key: every finite t exceeds it
-constexpr float kHeadroom = 6.f;          // a raised m leaves p = 2^6 at the maximum ...
-constexpr float kRaise = 8.f;             // ... and holds until p would exceed 2^8 (e4m3: 448)
+// A raised m leaves p = 2^3 at the maximum and holds until p would exceed 2^8 (the second
+// piece of such a p is at most 8: 8 * kLoScale fits e4m3's 448).  More headroom means fewer
+// raises, which cost an exchange between the group's warps and a rescale of O; less, a finer
+// floor of the small weights (2^-15 absolute against the maximum).
+constexpr float kHeadroom = 3.f;
+constexpr float kRaise = 8.f;
+constexpr float kLoScale = 32.f;          // the second piece of p is held times this
 constexpr int MAX_BATCH = BI_ATTN_MAX_BATCH;
 
-static_assert(CHUNK % TK == 0 && TK == NSM * 32, "a thread per key");
+static_assert(CHUNK % TK == 0 && TK == NQ * 32, "a thread per key");
 static_assert(O_COL + 2 * 2 * QR <= TMEM_COLS, "tensor memory columns");
 
 template <int D>
@@ -79,13 +83,14 @@ struct Cfg {
     static constexpr int RING_OFF = P_OFF + 2 * P_BYTES;
     static constexpr int SCALE_OFF = RING_OFF + NST * STAGE_BYTES;  // [NST][K 128 | V 128]
     static constexpr int BAR_OFF = SCALE_OFF + NST * 2 * TK;
-    static constexpr int NBARS = 2 * NST + 2 * NSB + 4 + 4 + 2 + 2 + 1 + 2;
-    static constexpr int XS_OFF = (BAR_OFF + NBARS * 8 + 8 + 15) / 16 * 16;
+    static constexpr int NBARS = 2 * NST + 2 * NSB + 4 + 4 + 2 + 2 + NDESC + 2;
+    static constexpr int DESC_OFF = (BAR_OFF + NBARS * 8 + 8 + 15) / 16 * 16;
+    static constexpr int XS_OFF = DESC_OFF + NDESC * 32;
     // per item buffer: four warps' row sums and the row maxima; per Q buffer the row factors;
-    // the maxima exchanged between the softmax warps (two buffers), and their flags
-    static constexpr int XS_FLOATS = 2 * (NSM + 1) * QR + 2 * QR + 2 * NSM * QR + 2 * NSM;
+    // the maxima exchanged within the softmax groups
+    static constexpr int XS_FLOATS = 2 * (NQ + 1) * QR + 2 * QR + NQ * QR;
     static constexpr int MISC_OFF = XS_OFF + XS_FLOATS * 4;
-    static constexpr int MISC_INTS = NST + (MAX_BATCH + 1) + 3 * MAX_BATCH + 2 + 1;
+    static constexpr int MISC_INTS = NST + (MAX_BATCH + 1) + 4 + 1;
     static constexpr size_t SMEM = 1024 + size_t(MISC_OFF) + MISC_INTS * 4;
     // K-major and MN-major rows of D bytes: the 128- or 64-byte swizzle, groups of 8 rows
     static constexpr uint32_t LAYOUT = D == 128 ? 2 : 4;
@@ -191,17 +196,40 @@ __device__ __forceinline__ float e8m0_inv(uint32_t s) {
     return s == 255 ? 1.f : e8m0(254 - s);
 }
 
-// A work item: chunk c of the keys for query tile u of sequence b, KV head h.
-struct Item {
-    int b, c, u, h;
-    SeqInfo si;
-    int pos0;    // position of the tile's first token
-    int ntok;    // its tokens
-    int npages;  // pages of the chunk that its last token sees (0: none, the item is empty)
-};
+// True in every thread of a softmax group (named barrier `id`, 128 threads) when `v` is true
+// in one of them.  The group's warps leave their loop only on a common decision taken here,
+// so none is left waiting: a warp whose bounded wait ran out runs on (its later waits return
+// at once) to the next such point.
+__device__ __forceinline__ bool group_or(int id, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(v ? 1u : 0u), "r"(id)
+        : "memory");
+    return r != 0;
+}
 
-template <int D, int RP>
-__global__ void __launch_bounds__(THREADS, 1)
+// A work item as the producer publishes it: chunk c of the keys for one query tile of
+// sequence b, KV head h.
+struct alignas(16) Item {
+    int npages;  // pages of the chunk that the tile's last token sees (0: no more items)
+    int key0;    // first key of the chunk
+    int L;       // the sequence's length
+    int pos0;    // position of the tile's first token
+    int t0;      // its row in q and out
+    int ntok;    // the tile's tokens
+    int h;
+    int b;
+};
+static_assert(sizeof(Item) == 32, "two 16-byte pieces");
+
+// RPW query rows per softmax group, NWG groups (each with its own rows of every tile).
+template <int D, int RPW, int NWG>
+__global__ void __launch_bounds__((NQ * NWG + 7) * 32, 1)
 attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                const __grid_constant__ CUtensorMap tmap_v, const __nv_bfloat16* __restrict__ q,
                const uint8_t* __restrict__ k_scale, const uint8_t* __restrict__ v_scale,
@@ -212,6 +240,10 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                unsigned int* __restrict__ cnt, unsigned int* err) {
     using C = Cfg<D>;
     constexpr int NST = C::NST;
+    constexpr int RP = RPW * NWG;
+    constexpr int EPI = NQ * NWG;  // first epilogue warp (a multiple of 4: its lane quarter is 0)
+    constexpr int PRODUCER = EPI + 4, S_WARP = EPI + 5, PV_WARP = EPI + 6;
+    constexpr int THREADS = (EPI + 7) * 32;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -229,20 +261,17 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
     uint64_t* o_empty = o_full + 2;     // ... and read out by the epilogue warps
     uint64_t* xs_bar = o_empty + 2;     // item k's row sums and maxima are in xs[k & 1]
     uint64_t* q_full = xs_bar + 2;      // item k's Q tile and row factors are in buffer k & 1
-    uint64_t* x_bar = q_full + 2;       // the softmax warps' exchange
-    uint64_t* drain = x_bar + 1;        // [2]: S issuer, P V issuer
+    uint64_t* d_full = q_full + 2;      // item k's descriptor is in items[k % NDESC]
+    uint64_t* drain = d_full + NDESC;   // [2]: S issuer, P V issuer
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
-    float* xs = reinterpret_cast<float*>(smem + C::XS_OFF);  // [2][NSM + 1][QR]
-    float* q_fac = xs + 2 * (NSM + 1) * QR;                  // [2][QR]
-    float* x_max = q_fac + 2 * QR;                           // [2][NSM][QR]
-    float* x_flag = x_max + 2 * NSM * QR;                    // [2][NSM]
+    Item* items = reinterpret_cast<Item*>(smem + C::DESC_OFF);
+    float* xs = reinterpret_cast<float*>(smem + C::XS_OFF);  // [2][NQ + 1][QR]
+    float* q_fac = xs + 2 * (NQ + 1) * QR;                   // [2][QR]
+    float* x_max = q_fac + 2 * QR;                           // [NQ][QR]
     int* stage_valid = reinterpret_cast<int*>(smem + C::MISC_OFF);  // [NST], a bit per page
     int* prefix = stage_valid + NST;                         // [B + 1]
-    int* seq_len = prefix + MAX_BATCH + 1;
-    int* seq_t0 = seq_len + MAX_BATCH;
-    int* seq_qb = seq_t0 + MAX_BATCH;
-    int* done = seq_qb + MAX_BATCH;                          // [2]: epilogue warps per item
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(done + 2);
+    int* done = prefix + MAX_BATCH + 1;                      // [4]: epilogue warps per item
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(done + 4);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = Hq / Hkv;
@@ -267,19 +296,19 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         }
         for (int i = 0; i < NSB; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&s_empty[i], NSM);
+            mbar_init(&s_empty[i], NQ * NWG);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&p_full[i], NSM);
+            mbar_init(&p_full[i], NQ * NWG);
             mbar_init(&p_empty[i], 1);
             mbar_init(&o_full[i], 1);
             mbar_init(&o_empty[i], 4);
-            mbar_init(&xs_bar[i], NSM);
+            mbar_init(&xs_bar[i], NQ * NWG);
             mbar_init(&q_full[i], 4);
             mbar_init(&drain[i], 1);
-            done[i] = 0;
         }
-        mbar_init(x_bar, NSM);
+        for (int i = 0; i < NDESC; ++i) mbar_init(&d_full[i], 1);
+        for (int i = 0; i < 4; ++i) done[i] = 0;
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -288,9 +317,6 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const bool ok = seq_ok(si, max_q, max_seq_len, total_q);
         if (!ok) latch_error(err, kErrDeviceArg);
         prefix[b + 1] = ok ? ((si.L + CHUNK - 1) >> CHUNK_LOG2) * ((si.qb + TQ - 1) / TQ) * Hkv : 0;
-        seq_len[b] = si.L;
-        seq_t0[b] = si.t0;
-        seq_qb[b] = si.qb;
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -311,36 +337,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         if (lane == 0) prefix[0] = 0;
     }
     __syncthreads();
-    const int total = prefix[B];
     const uint32_t tmem_base = *tmem_slot;
 
-    // The item at or after w that this CTA runs next (w is moved past empty ones); false at
-    // the end.
-    auto next_item = [&](int& w, Item& it) {
-        for (; w < total; w += gridDim.x) {
-            int lo = 0, hi = B;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (prefix[mid] <= w) lo = mid; else hi = mid;
-            }
-            it.b = lo;
-            it.si.L = seq_len[lo];
-            it.si.t0 = seq_t0[lo];
-            it.si.qb = seq_qb[lo];
-            const int U = (it.si.qb + TQ - 1) / TQ;
-            const int r = w - prefix[lo];
-            it.h = r % Hkv;
-            const int cu = r / Hkv;
-            it.c = cu / U;
-            it.u = cu - it.c * U;
-            it.ntok = min(TQ, it.si.qb - it.u * TQ);
-            it.pos0 = it.si.L - it.si.qb + it.u * TQ;
-            const int seen = it.pos0 + it.ntok - it.c * CHUNK;  // keys of the chunk it sees
-            it.npages = seen <= 0 ? 0 : min(CHUNK / PAGE, (seen + PAGE - 1) / PAGE);
-            if (it.npages > 0) return true;
-        }
-        return false;
-    };
     auto give_up = [&]() {
         if (!*abort_flag) {
             *abort_flag = 1;
@@ -352,9 +350,65 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         if (ok && !mbar_wait_warp(bar, parity, abort_flag, wait_ns)) ok = false;
         return ok;
     };
+    // the descriptor of item k; npages = 0 after the last one (or when the wait ran out)
+    auto item_at = [&](int k) {
+        Item it;
+        it.npages = 0;
+        if (wait(&d_full[k % NDESC], uint32_t(k / NDESC) & 1u)) {
+            const uint4* src = reinterpret_cast<const uint4*>(&items[k % NDESC]);
+            const uint4 a = src[0], b = src[1];
+            it = Item{int(a.x), int(a.y), int(a.z), int(a.w),
+                      int(b.x), int(b.y), int(b.z), int(b.w)};
+        }
+        return it;
+    };
 
     if (warp == PRODUCER) {
         // ------------------------------------------------------------------ producer
+        // The whole warp runs the loop; one elected lane issues the copies.  It also finds
+        // the items and publishes them one item ahead: item k's slot was last read for item
+        // k - NDESC, and no reader is that far behind (the ring holds the producer at most
+        // NST <= 8 tiles, so as many items, ahead of P V, and P V is at most two items ahead
+        // of the epilogue).
+        static_assert(NST + 4 < NDESC, "descriptors in flight");
+        const int total = prefix[B];
+        int w = blockIdx.x, pub = 0;
+        // publishes the next item of this CTA that is not empty; lane k returns the physical
+        // page of the item's page k
+        auto publish = [&](Item& it, int& phys) {
+            it.npages = 0;
+            phys = -1;
+            for (; w < total && it.npages == 0; w += gridDim.x) {
+                int lo = 0, hi = B;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (prefix[mid] <= w) lo = mid; else hi = mid;
+                }
+                const SeqInfo si = seq_info(seq_lens, cu_q, lo);
+                const int U = (si.qb + TQ - 1) / TQ;
+                const int r = w - prefix[lo];
+                const int cu = r / Hkv;
+                const int c = cu / U, u = cu - c * U;
+                it.b = lo;
+                it.h = r - cu * Hkv;
+                it.L = si.L;
+                it.key0 = c * CHUNK;
+                it.t0 = si.t0 + u * TQ;
+                it.ntok = min(TQ, si.qb - u * TQ);
+                it.pos0 = si.L - si.qb + u * TQ;
+                const int seen = it.pos0 + it.ntok - it.key0;
+                it.npages = seen <= 0 ? 0 : min(CHUNK / PAGE, (seen + PAGE - 1) / PAGE);
+            }
+            if (lane < it.npages) {
+                const int pidx = it.key0 / PAGE + lane;
+                if (pidx < max_pages) phys = block_table[int64_t(it.b) * max_pages + pidx];
+            }
+            if (lane == 0) {
+                items[pub % NDESC] = it;
+                mbar_arrive(&d_full[pub % NDESC]);
+            }
+            ++pub;
+        };
         if (lane == 0) {
             tma_prefetch_desc(&tmap_k);
             tma_prefetch_desc(&tmap_v);
@@ -362,12 +416,11 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // blocks of one query tile read K and V once; wider ones read them again from L2
         const uint64_t policy = max_q <= TQ ? l2_policy_evict_first() : l2_policy_evict_last();
         uint32_t g = 0;
-        Item it;
-        for (int w = blockIdx.x; ok && next_item(w, it); w += gridDim.x) {
-            const int pidx = it.c * (CHUNK / PAGE) + lane;
-            const int phys_l = lane < it.npages && pidx < max_pages
-                                   ? block_table[int64_t(it.b) * max_pages + pidx]
-                                   : -1;
+        Item it, nx;
+        int phys_l, phys_n;
+        publish(it, phys_l);
+        while (ok && it.npages > 0) {
+            publish(nx, phys_n);
             for (int i = 0; i < it.npages; i += TPAGES, ++g) {
                 const int s = int(g % NST);
                 if (!wait(&empty[s], ((g / NST) & 1u) ^ 1u)) break;
@@ -404,6 +457,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
                 __syncwarp();
             }
+            it = nx;
+            phys_l = phys_n;
         }
         if (!ok) {
             if (lane == 0) give_up();
@@ -419,12 +474,12 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const uint64_t q_desc0 = umma_smem_desc(smem_addr(sQ), 16, C::SBO, C::LAYOUT);
         const uint64_t k_desc0 = umma_smem_desc(smem_addr(sStage), 16, C::SBO, C::LAYOUT);
         uint32_t g = 0;
-        int item = 0;
-        Item it;
-        for (int w = blockIdx.x; ok && next_item(w, it); w += gridDim.x, ++item) {
+        for (int item = 0; ok; ++item) {
+            const int npages = item_at(item).npages;
+            if (npages == 0) break;
             const int qbuf = item & 1;
             if (!wait(&q_full[qbuf], uint32_t(item >> 1) & 1u)) break;
-            for (int i = 0; i < it.npages; i += TPAGES, ++g) {
+            for (int i = 0; i < npages; i += TPAGES, ++g) {
                 const int s = int(g % NST), sb = int(g % NSB);
                 if (!wait(&full[s], (g / NST) & 1u) ||
                     !wait(&s_empty[sb], ((g / NSB) & 1u) ^ 1u))
@@ -457,13 +512,13 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             umma_smem_desc(smem_addr(sStage + C::SIDE_BYTES), 16, C::SBO, C::LAYOUT);
         const uint64_t p_desc0 = umma_smem_desc(smem_addr(sP), 16, 512, 4);
         uint32_t g = 0;
-        int item = 0;
-        Item it;
-        for (int w = blockIdx.x; ok && next_item(w, it); w += gridDim.x, ++item) {
+        for (int item = 0; ok; ++item) {
+            const int npages = item_at(item).npages;
+            if (npages == 0) break;
             const int ob = item & 1;
             // the O buffer of this item was read out for item-2
             if (!wait(&o_empty[ob], (uint32_t(item >> 1) & 1u) ^ 1u)) break;
-            for (int i = 0; i < it.npages; i += TPAGES, ++g) {
+            for (int i = 0; i < npages; i += TPAGES, ++g) {
                 const int s = int(g % NST), pb = int(g & 1u);
                 if (!wait(&p_full[pb], (g >> 1) & 1u)) break;
                 tc_fence_after_sync();
@@ -478,7 +533,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                   (i | k) != 0 ? 1u : 0u);
                     tc_commit(&p_empty[pb]);
                     tc_commit(&empty[s]);  // K, V and scales of the tile are no longer read
-                    if (i + TPAGES >= it.npages) tc_commit(&o_full[ob]);
+                    if (i + TPAGES >= npages) tc_commit(&o_full[ob]);
                 }
                 __syncwarp();
             }
@@ -500,8 +555,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             for (int k = 0; k < PER / 8; ++k) v[k] = make_uint4(0, 0, 0, 0);
             if (j < it.ntok && r < TQ * G) {
                 const __nv_bfloat16* src =
-                    q + (int64_t(it.si.t0 + it.u * TQ + j) * Hq + it.h * G + (r - j * G)) * D +
-                    part * PER;
+                    q + (int64_t(it.t0 + j) * Hq + it.h * G + (r - j * G)) * D + part * PER;
 #pragma unroll
                 for (int k = 0; k < PER / 8; ++k)
                     v[k] = *reinterpret_cast<const uint4*>(src + k * 8);
@@ -551,69 +605,80 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[buf]);
         };
-        int item = 0;
         bool reset_done = cnt == nullptr;  // griddepcontrol.wait passed
-        Item it, nx;
-        int w = blockIdx.x;
-        bool have = next_item(w, it);
-        if (have) split_q(it, 0);
-        for (; ok && have; ++item) {
-            int wn = w + gridDim.x;
-            const bool more = next_item(wn, nx);
+        // Item k's stores are counted an item later, when the fence finds them done.  The last
+        // of the four warps counts; done[k & 3] holds no other item's arrivals, since a warp
+        // that counts item k has seen O of item k, so every warp has read O of item k - 2 and
+        // counted item k - 3.
+        auto count = [&](int k, int at) {
+            if (!cnt) return;
+            __threadfence();
+            __syncwarp();
+            if (!reset_done) {
+                pdl_wait();
+                pdl_trigger();
+                reset_done = true;
+            }
+            if (lane == 0 && (atomicAdd(&done[k & 3], 1) & 3) == 3) {
+                __threadfence();
+                atomicAdd(cnt + at, 1u);
+            }
+        };
+        Item it = item_at(0), nx;
+        if (it.npages > 0) split_q(it, 0);
+        int item = 0, prev = -1;
+        for (; ok && it.npages > 0; ++item) {
+            nx = item_at(item + 1);
             // (this buffer's item-1 is complete: its O was waited for)
-            if (more) split_q(nx, (item + 1) & 1);
+            if (nx.npages > 0) split_q(nx, (item + 1) & 1);
+            if (prev >= 0) count(item - 1, prev);
             const int ob = item & 1;
             const uint32_t par = uint32_t(item >> 1) & 1u;
             if (!wait(&xs_bar[ob], par) || !wait(&o_full[ob], par)) break;
             tc_fence_after_sync();
-            // row r = lane: its partial's place
-            const int r = lane;
-            const int j = r / G;
-            const bool store = j < it.ntok && r < TQ * G && it.pos0 + j >= it.c * CHUNK;
-            const int64_t idx = (int64_t(it.si.t0 + it.u * TQ + j) * Hq + int64_t(it.h) * G +
-                                 (r - j * G)) * maxC + it.c;
             uint32_t vh[RP], vl[RP];
             const uint32_t ta =
                 tmem_base + (uint32_t(32 * ew) << 16) + uint32_t(O_COL + ob * 2 * QR);
             tmem_cols(ta, vh);
             tmem_cols(ta + QR, vl);
-            // O^T: lane = head dim (M = 128), or dims 16 ew .. 16 ew + 15 in lanes 0..15 (M = 64)
-            const int d = D == 128 ? ew * 32 + lane : ew * 16 + lane;
-            const bool mine = D == 128 || lane < 16;
-#pragma unroll
-            for (int rr = 0; rr < RP; ++rr) {
-                const bool st = __shfl_sync(0xffffffffu, store ? 1 : 0, rr) != 0;
-                const int64_t at = __shfl_sync(0xffffffffu, idx, rr);
-                if (st && mine)
-                    ws_o[at * D + d] =
-                        fmaf(__uint_as_float(vl[rr]), 0.0625f, __uint_as_float(vh[rr]));
-            }
-            if (ew == 0 && store) {
-                const float* x = xs + ob * ((NSM + 1) * QR);
-                const float l = ((x[r] + x[QR + r]) + x[2 * QR + r]) + x[3 * QR + r];
-                *reinterpret_cast<float2*>(ws_ml + idx * 2) = make_float2(x[NSM * QR + r], l);
-            }
             tc_fence_before_sync();
-            if (cnt) {
-                // the fourth warp to have stored its part of the item counts it
-                __threadfence();
-                __syncwarp();
-                if (!reset_done) {
-                    pdl_wait();
-                    pdl_trigger();
-                    reset_done = true;
-                }
-                if (lane == 0 && (atomicAdd(&done[ob], 1) & 3) == 3) {
-                    __threadfence();
-                    atomicAdd(cnt + it.b * Hkv + it.h, 1u);
+            // rows (token j, head gg) are stored when their token sees the chunk
+            const int rows = it.ntok * G;
+            const int first = max(0, it.key0 - it.pos0) * G;
+            const int c = it.key0 >> CHUNK_LOG2;
+            const int64_t row0 = int64_t(it.t0) * Hq + int64_t(it.h) * G;
+            if (ew == 0) {
+                const int r = lane, j = r / G;
+                if (r < rows && r >= first) {
+                    const float* x = xs + ob * ((NQ + 1) * QR);
+                    const float l = ((x[r] + x[QR + r]) + x[2 * QR + r]) + x[3 * QR + r];
+                    const int64_t idx = (row0 + int64_t(j) * (Hq - G) + r) * maxC + c;
+                    *reinterpret_cast<float2*>(ws_ml + idx * 2) = make_float2(x[NQ * QR + r], l);
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_empty[ob]);
+            // O^T: lane = head dim (M = 128), or dims 16 ew .. 16 ew + 15 in lanes 0..15 (M = 64)
+            const int d = D == 128 ? ew * 32 + lane : ew * 16 + lane;
+            if (D == 128 || lane < 16) {
+                float* dst = ws_o + (row0 * maxC + c) * D + d;
+                const int64_t step = int64_t(maxC) * D, skip = step * (Hq - G);
+                int gg = 0;
+#pragma unroll
+                for (int r = 0; r < RP; ++r) {
+                    if (r < rows && r >= first)
+                        *dst = fmaf(__uint_as_float(vl[r]), 1.f / kLoScale, __uint_as_float(vh[r]));
+                    dst += step;
+                    if (++gg == G) {
+                        gg = 0;
+                        dst += skip;
+                    }
+                }
+            }
+            prev = it.b * Hkv + it.h;
             it = nx;
-            w = wn;
-            have = more;
         }
+        if (ok && prev >= 0) count(item - 1, prev);
         if (!ok && lane == 0) give_up();
         // a CTA with no item (or one that gave up) still waits before it completes
         if (!reset_done) {
@@ -622,43 +687,46 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         }
     } else {
         // ------------------------------------------------------------------- softmax
-        const int key = tid;  // this thread's key of every tile
-        const uint32_t lane_base = uint32_t(32 * warp) << 16;
-        uint32_t g = 0, ex = 0;  // tiles, exchanges
-        int item = 0;
-        Item it;
-        float m[RP], l[RP];
-        for (int w = blockIdx.x; ok && next_item(w, it); w += gridDim.x, ++item) {
+        // Group wg owns query rows wg * RPW .. of every tile; each thread one key.
+        const int wg = warp / NQ, wq = warp % NQ;
+        const int key = wq * 32 + lane;
+        const int row0 = wg * RPW;
+        const uint32_t lane_base = uint32_t(32 * wq) << 16;
+        uint32_t g = 0;
+        float m[RPW], l[RPW];
+        for (int item = 0;; ++item) {
+            const Item it = item_at(item);
             const int ob = item & 1;
             const uint32_t ipar = uint32_t(item >> 1) & 1u;
-            if (!wait(&q_full[ob], ipar)) break;
-            const float* fac = q_fac + ob * QR;
+            if (it.npages > 0) wait(&q_full[ob], ipar);
+            if (!ok && lane == 0) give_up();
+            if (group_or(1 + wg, !ok) || it.npages == 0) break;
+            const float* fac = q_fac + ob * QR + row0;
 #pragma unroll
-            for (int r = 0; r < RP; ++r) {
+            for (int r = 0; r < RPW; ++r) {
                 m[r] = kNoMax;
                 l[r] = 0.f;
             }
-            for (int i = 0; i < it.npages && ok; i += TPAGES, ++g) {
+            bool left = false;
+            for (int i = 0; i < it.npages; i += TPAGES, ++g) {
                 const int s = int(g % NST), sb = int(g % NSB), pb = int(g & 1u);
-                const int kp = it.c * CHUNK + i * PAGE + key;  // this key's position
-                if (!wait(&s_full[sb], (g / NSB) & 1u)) break;
+                const int kp = it.key0 + i * PAGE + key;  // this key's position
+                wait(&full[s], (g / NST) & 1u);
+                const bool live = ((stage_valid[s] >> (key / PAGE)) & 1) && kp < it.L;
+                const uint32_t ksc = sScale[s * 2 * TK + key], vsc = sScale[s * 2 * TK + TK + key];
+                wait(&s_full[sb], (g / NSB) & 1u);
                 tc_fence_after_sync();
-                uint32_t sv[RP];
-                tmem_cols(tmem_base + lane_base + uint32_t(S_COL + sb * QR), sv);
+                uint32_t sv[RPW];
+                tmem_cols(tmem_base + lane_base + uint32_t(S_COL + sb * QR + row0), sv);
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_empty[sb]);
-                // (landed before its scores were computed: this orders the reads below)
-                if (!wait(&full[s], (g / NST) & 1u)) break;
-                const bool there = (stage_valid[s] >> (key / PAGE)) & 1;
-                const bool live = there && kp < it.si.L;
-                const uint32_t ksc = sScale[s * 2 * TK + key], vsc = sScale[s * 2 * TK + TK + key];
                 const float ka = e8m0(ksc);
                 const float vb = vsc == 255 ? __int_as_float(0x7fc00000) : float(int(vsc) - 127);
                 const float vinv = live ? e8m0_inv(vsc) : 0.f;
-                float t[RP];
+                float t[RPW];
 #pragma unroll
-                for (int r = 0; r < RP; r += 4) {
+                for (int r = 0; r < RPW; r += 4) {
                     const float4 f = *reinterpret_cast<const float4*>(fac + r);
                     t[r] = fmaf(__uint_as_float(sv[r]) * ka, f.x, vb);
                     t[r + 1] = fmaf(__uint_as_float(sv[r + 1]) * ka, f.y, vb);
@@ -669,56 +737,59 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 if (!__all_sync(0xffffffffu, live && kp <= it.pos0)) {
                     const int first = live ? max(0, kp - it.pos0) * G : QR;  // first row seeing it
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) t[r] = r >= first ? t[r] : -INFINITY;
+                    for (int r = 0; r < RPW; ++r) t[r] = row0 + r >= first ? t[r] : -INFINITY;
                 }
                 // does any row's maximum exceed its reference by more than 2^8?
                 bool slow = i == 0;
                 if (!slow) {
-                    float over = -INFINITY;
+                    float over[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) over = fmaxf(over, t[r] - m[r]);
-                    const bool any = __any_sync(0xffffffffu, over > kRaise);
-                    float* fl = x_flag + (ex & 1u) * NSM;
-                    if (lane == 0) {
-                        fl[warp] = any ? 1.f : 0.f;
-                        mbar_arrive(x_bar);
-                    }
-                    if (!wait(x_bar, ex & 1u)) break;
-                    const float4 f = *reinterpret_cast<const float4*>(fl);
-                    slow = f.x + f.y + f.z + f.w != 0.f;
-                    ++ex;
+                    for (int r = 0; r < RPW; ++r) over[r & 3] = fmaxf(over[r & 3], t[r] - m[r]);
+                    slow = group_or(1 + wg, !ok || fmaxf(fmaxf(over[0], over[1]),
+                                                         fmaxf(over[2], over[3])) > kRaise);
                 }
                 if (slow) {
                     // the tile's maximum of every row, over the four warps
-                    const float mine = combine_lanes<RP, true>(t, lane);
-                    float* xm = x_max + (ex & 1u) * (NSM * QR);
-                    if (lane % (32 / RP) == 0) xm[warp * QR + lane / (32 / RP)] = mine;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(x_bar);
-                    if (!wait(x_bar, ex & 1u)) break;
-                    ++ex;
+                    const float mine = combine_lanes<RPW, true>(t, lane);
+                    if (lane % (32 / RPW) == 0) x_max[wq * QR + row0 + lane / (32 / RPW)] = mine;
+                    if (!ok && lane == 0) give_up();
+                    if (group_or(1 + wg, !ok)) {
+                        ok = false;
+                        left = true;
+                        break;
+                    }
                     // O of this warp's lanes may be scaled once P V of the tile before is done
                     const uint32_t gp = g - 1u;
-                    if (i > 0 && !wait(&p_empty[gp & 1u], (gp >> 1) & 1u)) break;
+                    if (i > 0) wait(&p_empty[gp & 1u], (gp >> 1) & 1u);
                     tc_fence_after_sync();
 #pragma unroll
-                    for (int r0 = 0; r0 < RP; r0 += 8) {
+                    for (int r0 = 0; r0 < RPW; r0 += 8) {
                         float fa[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int r = r0 + k;
-                            const float mt = fmaxf(fmaxf(xm[r], xm[QR + r]),
-                                                   fmaxf(xm[2 * QR + r], xm[3 * QR + r]));
-                            const bool raise = mt > m[r] + kRaise;
-                            const float mn = raise ? mt - kHeadroom : m[r];
-                            fa[k] = raise ? ex2(m[r] - mn) : 1.f;
-                            m[r] = mn;
-                            l[r] *= fa[k];
+                        for (int k = 0; k < 8; k += 4) {
+                            float4 x = *reinterpret_cast<const float4*>(x_max + row0 + r0 + k);
+#pragma unroll
+                            for (int n = 1; n < NQ; ++n) {
+                                const float4 y = *reinterpret_cast<const float4*>(
+                                    x_max + n * QR + row0 + r0 + k);
+                                x = make_float4(fmaxf(x.x, y.x), fmaxf(x.y, y.y),
+                                                fmaxf(x.z, y.z), fmaxf(x.w, y.w));
+                            }
+                            const float mt[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) {
+                                const int r = r0 + k + n;
+                                const bool raise = mt[n] > m[r] + kRaise;
+                                const float mn = raise ? mt[n] - kHeadroom : m[r];
+                                fa[k + n] = raise ? ex2(m[r] - mn) : 1.f;
+                                m[r] = mn;
+                                l[r] *= fa[k + n];
+                            }
                         }
                         if (i > 0) {
                             uint32_t o[8];
-                            const uint32_t ta =
-                                tmem_base + lane_base + uint32_t(O_COL + ob * 2 * QR + r0);
+                            const uint32_t ta = tmem_base + lane_base +
+                                                uint32_t(O_COL + ob * 2 * QR + row0 + r0);
 #pragma unroll
                             for (int half = 0; half < 2; ++half) {
                                 tmem_cols(ta + half * QR, o);
@@ -731,11 +802,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     }
                     tc_fence_before_sync();
                 }
-                // P buffer pb is free once P V of tile g-2 has completed
-                if (!wait(&p_empty[pb], ((g >> 1) & 1u) ^ 1u)) break;
-                uint32_t hi[RP / 4], lo[RP / 4];
+                uint32_t hi[RPW / 4], lo[RPW / 4];
 #pragma unroll
-                for (int r = 0; r < RP; r += 4) {
+                for (int r = 0; r < RPW; r += 4) {
                     float p[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -745,25 +814,28 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const uint32_t c0 = e4m3x2(p[0], p[1]), c1 = e4m3x2(p[2], p[3]);
                     const float2 b0 = e4m3x2_values(c0), b1 = e4m3x2_values(c1);
                     hi[r / 4] = c0 | (c1 << 16);
-                    lo[r / 4] = e4m3x2((p[0] - b0.x) * 16.f, (p[1] - b0.y) * 16.f) |
-                                (e4m3x2((p[2] - b1.x) * 16.f, (p[3] - b1.y) * 16.f) << 16);
+                    lo[r / 4] = e4m3x2((p[0] - b0.x) * kLoScale, (p[1] - b0.y) * kLoScale) |
+                                (e4m3x2((p[2] - b1.x) * kLoScale, (p[3] - b1.y) * kLoScale) << 16);
                 }
+                // P buffer pb is free once P V of tile g-2 has completed
+                wait(&p_empty[pb], ((g >> 1) & 1u) ^ 1u);
+                if (!ok) continue;  // (to the group's next common decision)
                 uint8_t* pbuf = sP + pb * C::P_BYTES;
-                if (RP == 8) {
-                    *reinterpret_cast<uint2*>(pbuf + swz_row<64>(key, 0)) = make_uint2(hi[0], hi[1]);
-                    *reinterpret_cast<uint2*>(pbuf + swz_row<64>(key, 2)) = make_uint2(lo[0], lo[1]);
+                if (RPW == 8) {
+                    const int at = wg * 8;
+                    *reinterpret_cast<uint2*>(pbuf + swz_row<64>(key, 0) + at) =
+                        make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2*>(pbuf + swz_row<64>(key, 2) + at) =
+                        make_uint2(lo[0], lo[1]);
                 } else {
-#pragma unroll
-                    for (int k = 0; k < RP / 16; ++k) {
-                        *reinterpret_cast<uint4*>(pbuf + swz_row<64>(key, k)) =
-                            make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
-                        *reinterpret_cast<uint4*>(pbuf + swz_row<64>(key, 2 + k)) =
-                            make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
-                    }
+                    *reinterpret_cast<uint4*>(pbuf + swz_row<64>(key, wg)) =
+                        make_uint4(hi[0], hi[1], hi[RPW / 4 - 2], hi[RPW / 4 - 1]);
+                    *reinterpret_cast<uint4*>(pbuf + swz_row<64>(key, 2 + wg)) =
+                        make_uint4(lo[0], lo[1], lo[RPW / 4 - 2], lo[RPW / 4 - 1]);
                 }
                 // V rows past the sequence's end or of an invalid page are zeroed, so that
                 // unwritten codes (NaN) cannot reach O through 0 * v
-                if (!live) {
+                if (wg == 0 && !live) {
                     uint4* vr = reinterpret_cast<uint4*>(sStage + s * C::STAGE_BYTES +
                                                          C::SIDE_BYTES + key * D);
 #pragma unroll
@@ -773,19 +845,21 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[pb]);
             }
-            if (!ok) break;
+            if (left) break;
             // the warp's row sums (and the maxima) for the epilogue, once it has read this
             // buffer's previous contents (item-2)
-            if (!wait(&o_empty[ob], ipar ^ 1u)) break;
-            float* x = xs + ob * ((NSM + 1) * QR);
-            if (warp == 0 && lane == 0) {
+            wait(&o_empty[ob], ipar ^ 1u);
+            float* x = xs + ob * ((NQ + 1) * QR) + row0;
+            const float sum = combine_lanes<RPW, false>(l, lane);
+            if (ok) {
+                if (wq == 0 && lane == 0) {
 #pragma unroll
-                for (int r = 0; r < RP; ++r) x[NSM * QR + r] = m[r];
+                    for (int r = 0; r < RPW; ++r) x[NQ * QR + r] = m[r];
+                }
+                if (lane % (32 / RPW) == 0) x[wq * QR + lane / (32 / RPW)] = sum;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&xs_bar[ob]);
             }
-            const float sum = combine_lanes<RP, false>(l, lane);
-            if (lane % (32 / RP) == 0) x[warp * QR + lane / (32 / RP)] = sum;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&xs_bar[ob]);
         }
         if (!ok && lane == 0) give_up();
     }
@@ -798,7 +872,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
 }
 
-template <int D, int RP>
+template <int D, int RPW, int NWG>
 cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a,
                         const void* k_scale, const void* v_scale, float scale, void* out,
                         float* lse, void* workspace, cudaStream_t stream) {
@@ -808,7 +882,7 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
     if (!tmap_2d_u8_swizzled(&tk, a.k_cache, D, rows, PAGE) ||
         !tmap_2d_u8_swizzled(&tv, a.v_cache, D, rows, PAGE))
         return cudaErrorNotSupported;
-    auto kern = attn_q8_kernel<D, RP>;
+    auto kern = attn_q8_kernel<D, RPW, NWG>;
     static bool attr_done[64] = {};
     if (dev.device >= 0 && dev.device < 64 && !attr_done[dev.device]) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -833,7 +907,7 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
         if (e != cudaSuccess) return e;
     }
     cudaError_t e = launch_pdl(
-        kern, dim3(grid), dim3(THREADS), Cf::SMEM, stream, tk, tv,
+        kern, dim3(grid), dim3((NQ * NWG + 7) * 32), Cf::SMEM, stream, tk, tv,
         static_cast<const __nv_bfloat16*>(q), static_cast<const uint8_t*>(k_scale),
         static_cast<const uint8_t*>(v_scale), a.block_table, int(a.max_pages), int(a.num_pages),
         a.seq_lens, a.cu_q, int(a.batch), int(a.total_q), int(a.max_q), int(a.max_seq_len),
@@ -847,13 +921,19 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
 cudaError_t launch_attention_q8(const DeviceInfo& dev, const void* q, const PagedArgs& a,
                                 const void* k_scale, const void* v_scale, float scale, void* out,
                                 float* lse, void* workspace, cudaStream_t stream) {
-    // query rows of the fullest tile
+    // query rows of the fullest tile: up to 8 in one softmax group, 16 or 32 over two
     const int64_t G = a.hq / a.hkv, TQ = QR / G;
     const int64_t rows = (a.max_q < TQ ? a.max_q : TQ) * G;
-    auto run = [&](auto f) { return f(dev, q, a, k_scale, v_scale, scale, out, lse, workspace, stream); };
+    auto run = [&](auto f) {
+        return f(dev, q, a, k_scale, v_scale, scale, out, lse, workspace, stream);
+    };
     if (a.head_dim == 64)
-        return run(rows <= 8 ? launch_q8_t<64, 8> : rows <= 16 ? launch_q8_t<64, 16> : launch_q8_t<64, 32>);
-    return run(rows <= 8 ? launch_q8_t<128, 8> : rows <= 16 ? launch_q8_t<128, 16> : launch_q8_t<128, 32>);
+        return run(rows <= 8    ? launch_q8_t<64, 8, 1>
+                   : rows <= 16 ? launch_q8_t<64, 8, 2>
+                                : launch_q8_t<64, 16, 2>);
+    return run(rows <= 8    ? launch_q8_t<128, 8, 1>
+               : rows <= 16 ? launch_q8_t<128, 8, 2>
+                            : launch_q8_t<128, 16, 2>);
 }
 
 }  // namespace bi

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import q8_reference as ref
-from tolerance import bits_equal
+from tolerance import bits_equal, check_rows_rel_l2
 
 pytestmark = pytest.mark.gpu
 
@@ -225,6 +225,7 @@ def test_attention_against_64_bits(dev, case):
                               D ** -0.5, Hq // Hkv)
             ref.check_attention(obuf[1 + t:1 + t + w], lbuf[1 + t:1 + t + w], r,
                                 f"{form} sequence {b}")
+            check_rows_rel_l2(obuf[1 + t:1 + t + w], r[0], what=f"{form} sequence {b}")
             t += w
         outs.append((obuf, lbuf))
     for o, l in outs[1:]:
@@ -336,6 +337,7 @@ def test_long_contexts(dev, L, qs):
     out, lse = attend(c, q.to(dev), [L], [qs], D ** -0.5, "verify")
     r = ref.attention(q.double().numpy(), *c.values(), c.table[0].tolist(), L, qs, D ** -0.5, 4)
     ref.check_attention(out, lse, r)
+    check_rows_rel_l2(out, r[0])
 
 
 def test_malformed_sequences_are_skipped(dev):
