@@ -15,29 +15,35 @@
 //     nearest: exact for bf16 q down to 2^-9 of the row's largest value, off by at most
 //     2^-18 of it below;
 //   * p = hi + lo / 32: p <= 2^8; hi has four bits, lo the next four, so p is held to
-//     2^-9 of itself (bf16 would hold 2^-8) or to 2^-15 absolute, whichever is more; the
-//     largest p of a row is 2^3 at least.
+//     2^-9 of itself (bf16 would hold 2^-8) or to 2^-15 absolute (2^-23 of the row's
+//     largest), whichever is more.
 //
 // Reduction of one (query, head) -- a function of its position alone, as in attention.cu:
-// chunks of 512 keys from key 0; a chunk in tiles of 128 keys, ascending; per tile the exact
-// maximum of the row's t, m raised to (maximum - 3) only when the maximum exceeds m + 8 (O and
-// the sums then scaled by 2^(m_old - m_new)); each of 128 threads sums its key of every tile,
-// and the 128 sums are added by a fixed tree; the chunk partials (m, l, o) go through the
-// merge of attention.cu.  A tile that a row does not see changes none of its numbers, and a
+// chunks of 512 keys from key 0; m is the exact maximum of the row's t over the chunk, less 8
+// (so p <= 2^8); a chunk is four tiles of 128 keys, each of 128 threads sums its key of every
+// tile in ascending order, and the 128 sums are added by a fixed tree; the chunk partials
+// (m, l, o) go through the merge of attention.cu.  Keys that a row does not see add +0, and a
 // row's place in the MMA tile, the other rows and the block's width enter nowhere.
+//
+// A softmax thread holds its four t of every row in registers between the maximum and the
+// exponentials, so a chunk needs one exchange between warps and O is never rescaled.  (With a
+// running maximum per tile, every tile cost an exchange, and rows whose maximum kept rising a
+// rescale of O: 299 us where this form takes @@DEC@@ us, 64 ragged sequences of up to 16,388 keys.)
+// K and V have rings of their own: K runs an item ahead of V, so the scores of the next chunk
+// are ready when this one's P is done.
 //
 // Orientation.  S^T = K Q^T (M = 128 keys, N = 32 query rows) and O^T = V^T P^T (M = head
 // dim, N = 32 hi + 32 lo rows): the cache is the operand that the tensor core reads 128 rows
-// at a time, whatever the number of query rows, and a softmax thread owns one key, so it does
-// as many exponentials as there are query rows (rounded up to 8, 16 or 32), reads its key's
-// two scale bytes once, and writes its P values as 16-byte pieces.
+// at a time, whatever the number of query rows, and a softmax thread owns one key of a tile, so
+// it does as many exponentials as there are query rows (rounded up to 8, 16 or 32), reads its
+// key's two scale bytes once, and writes its P values as 8-byte pieces.
 //
-// Warps: one or two softmax groups of four (one key of the tile per thread; two groups share
-// the query rows), four epilogue warps (they also split the next item's Q), the TMA producer
-// (it also finds the work items and publishes them), the S issuer (and TMEM owner), the P V
-// issuer.  One persistent CTA per SM; work items (sequence, chunk, query tile, KV head) are
-// enumerated on the device.  All waits are bounded; the one barrier that warps meet in, a
-// softmax group's, is left by all of them together.
+// Warps: one, two or four softmax groups of four (8 query rows each), four epilogue warps (they
+// also split the Q and fetch the scale bytes of the item after next), the scheduler, a TMA
+// producer for K and one for V, the S issuer (and TMEM owner), the P V issuer.  One persistent
+// CTA per SM; work items (sequence, chunk, query tile, KV head) are enumerated on the device.  All waits
+// are bounded; the one barrier that warps meet in, a softmax group's, is left by all of them
+// together.
 //
 // Bound by memory: 2 * (D + 1) bytes per key and KV head against 4 * 32 * D operations.
 #include "attn_common.cuh"
@@ -51,19 +57,16 @@ constexpr int QR = 32;                    // query rows of a tile
 constexpr int TK = 128;                   // keys of a tile: two pages
 constexpr int TPAGES = TK / PAGE;
 constexpr int NQ = 4;                     // warps of a softmax group: 32 keys each
-constexpr int NDESC = 16;                 // item descriptors in flight
-constexpr int NSB = 4;                    // S buffers in tensor memory
-constexpr int TMEM_COLS = 256;
-constexpr int S_COL = 0;                  // S buffers: 32 columns each
-constexpr int O_COL = NSB * QR;           // O buffers (by item): 32 hi + 32 lo columns each
-constexpr float kNoMax = -1e30f;          // m before any visible key: every finite t exceeds it
-// A raised m leaves p = 2^3 at the maximum and holds until p would exceed 2^8 (the second
-// piece of such a p is at most 8: 8 * kLoScale fits e4m3's 448).  More headroom means fewer
-// raises, which cost an exchange between the group's warps and a rescale of O; less, a finer
-// floor of the small weights (2^-15 absolute against the maximum).
-constexpr float kHeadroom = 3.f;
-constexpr float kRaise = 8.f;
-constexpr float kLoScale = 32.f;          // the second piece of p is held times this
+constexpr int RPW = 8;                    // query rows of a softmax group
+constexpr int NDESC = 64;                 // item descriptors in flight
+constexpr int LEAD = 16;                  // items found ahead of the K copies, at most
+constexpr int NT = CHUNK / TK;            // tiles of a chunk
+constexpr int TMEM_COLS = 512;
+constexpr int S_COL = 0;                  // two S sets (by item) of NT tiles, 32 columns each
+constexpr int O_COL = 2 * NT * QR;          // O buffers (by item): 32 hi + 32 lo columns each
+constexpr float kNoMax = -1e30f;          // m of a row that sees no key of the chunk
+constexpr float kHeadroom = 8.f;          // p = 2^8 at the row's maximum (e4m3 holds 448)
+constexpr float kLoScale = 32.f;          // the second piece of p (at most 8) times this
 constexpr int MAX_BATCH = BI_ATTN_MAX_BATCH;
 
 static_assert(CHUNK % TK == 0 && TK == NQ * 32, "a thread per key");
@@ -71,31 +74,33 @@ static_assert(O_COL + 2 * 2 * QR <= TMEM_COLS, "tensor memory columns");
 
 template <int D>
 struct Cfg {
-    static constexpr int NST = D == 64 ? 8 : 5;          // tile stages in the ring
+    static constexpr int NSLOT = D == 64 ? 10 : 5;       // tiles in the K ring, and in V's
     static constexpr int PAGE_BYTES = PAGE * D;
-    static constexpr int SIDE_BYTES = TK * D;            // K or V of a tile
-    static constexpr int STAGE_BYTES = 2 * SIDE_BYTES;
+    static constexpr int SLOT_BYTES = TK * D;
     static constexpr int Q_PIECE = QR * D;               // hi or lo of a Q tile
     static constexpr int Q_BYTES = 2 * Q_PIECE;
     static constexpr int P_BYTES = TK * 2 * QR;          // [key][32 hi | 32 lo]
     static constexpr int Q_OFF = 0;                      // two Q buffers
-    static constexpr int P_OFF = Q_OFF + 2 * Q_BYTES;    // two P buffers
-    static constexpr int RING_OFF = P_OFF + 2 * P_BYTES;
-    static constexpr int SCALE_OFF = RING_OFF + NST * STAGE_BYTES;  // [NST][K 128 | V 128]
-    static constexpr int BAR_OFF = SCALE_OFF + NST * 2 * TK;
-    static constexpr int NBARS = 2 * NST + 2 * NSB + 4 + 4 + 2 + 2 + NDESC + 2;
+    static constexpr int P_OFF = Q_OFF + 2 * Q_BYTES;
+    static constexpr int RING_OFF = P_OFF + NT * P_BYTES;
+    static constexpr int V_OFF = RING_OFF + NSLOT * SLOT_BYTES;
+    static constexpr int SCALE_OFF = V_OFF + NSLOT * SLOT_BYTES;  // two sets of
+    static constexpr int SCALE_BYTES = NT * 2 * TK;                  // [tile][K 128 | V 128]
+    static constexpr int BAR_OFF = SCALE_OFF + 2 * SCALE_BYTES;
+    static constexpr int NBARS = 4 * NSLOT + 4 + 2 + 4 + 2 + 2 + NDESC + LEAD + 2;
     static constexpr int DESC_OFF = (BAR_OFF + NBARS * 8 + 8 + 15) / 16 * 16;
-    static constexpr int XS_OFF = DESC_OFF + NDESC * 32;
+    static constexpr int XS_OFF = DESC_OFF + NDESC * 64;
     // per item buffer: four warps' row sums and the row maxima; per Q buffer the row factors;
     // the maxima exchanged within the softmax groups
     static constexpr int XS_FLOATS = 2 * (NQ + 1) * QR + 2 * QR + NQ * QR;
     static constexpr int MISC_OFF = XS_OFF + XS_FLOATS * 4;
-    static constexpr int MISC_INTS = NST + (MAX_BATCH + 1) + 4 + 1;
+    static constexpr int MISC_INTS = (MAX_BATCH + 1) + 4 + 1;
     static constexpr size_t SMEM = 1024 + size_t(MISC_OFF) + MISC_INTS * 4;
     // K-major and MN-major rows of D bytes: the 128- or 64-byte swizzle, groups of 8 rows
     static constexpr uint32_t LAYOUT = D == 128 ? 2 : 4;
     static constexpr uint32_t SBO = 8 * D;
-    static_assert(P_OFF % 1024 == 0 && RING_OFF % 1024 == 0 && STAGE_BYTES % 1024 == 0, "");
+    static_assert(P_OFF % 1024 == 0 && RING_OFF % 1024 == 0 && SLOT_BYTES % 1024 == 0, "");
+    static_assert(LEAD + NSLOT + 6 < NDESC, "descriptors in flight (see the scheduler)");
     static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
@@ -124,15 +129,6 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n, int a_mn, int b_
            (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
 }
 
-// Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes).
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-        ::"r"(smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(bar))
-        : "memory");
-}
-
 // RP consecutive columns of this warp's 32 lanes, with the wait.
 __device__ __forceinline__ void tmem_cols(uint32_t ta, uint32_t (&r)[8]) {
     asm volatile(
@@ -143,18 +139,26 @@ __device__ __forceinline__ void tmem_cols(uint32_t ta, uint32_t (&r)[8]) {
         : "r"(ta)
         : "memory");
 }
-__device__ __forceinline__ void tmem_store_x8(uint32_t ta, const uint32_t (&r)[8]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t"
-        "tcgen05.wait::st.sync.aligned;" ::"r"(ta),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-        : "memory");
-}
 __device__ __forceinline__ void tmem_cols(uint32_t ta, uint32_t (&r)[16]) {
     tmem_load_32x32b_x16_sync(ta, r);
 }
-__device__ __forceinline__ void tmem_cols(uint32_t ta, uint32_t (&r)[32]) {
-    tmem_load_32x32b_x32_sync(ta, r);
+// Eight columns of each of a set's four S tiles (QR columns apart), with one wait.
+__device__ __forceinline__ void tmem_tiles(uint32_t ta, uint32_t (&r)[NT][RPW]) {
+    static_assert(NT == 4 && RPW == 8, "four loads of eight columns");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%33];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%34];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24, %25, %26, %27, %28, %29, %30, %31}, [%35];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0][0]), "=r"(r[0][1]), "=r"(r[0][2]), "=r"(r[0][3]), "=r"(r[0][4]), "=r"(r[0][5]),
+          "=r"(r[0][6]), "=r"(r[0][7]), "=r"(r[1][0]), "=r"(r[1][1]), "=r"(r[1][2]), "=r"(r[1][3]),
+          "=r"(r[1][4]), "=r"(r[1][5]), "=r"(r[1][6]), "=r"(r[1][7]), "=r"(r[2][0]), "=r"(r[2][1]),
+          "=r"(r[2][2]), "=r"(r[2][3]), "=r"(r[2][4]), "=r"(r[2][5]), "=r"(r[2][6]), "=r"(r[2][7]),
+          "=r"(r[3][0]), "=r"(r[3][1]), "=r"(r[3][2]), "=r"(r[3][3]), "=r"(r[3][4]), "=r"(r[3][5]),
+          "=r"(r[3][6]), "=r"(r[3][7])
+        : "r"(ta), "r"(ta + QR), "r"(ta + 2 * QR), "r"(ta + 3 * QR)
+        : "memory");
 }
 
 // Combines v[r] over the 32 lanes for each of N rows (max, or a sum over a fixed tree: lanes
@@ -213,7 +217,7 @@ __device__ __forceinline__ bool group_or(int id, bool v) {
     return r != 0;
 }
 
-// A work item as the producer publishes it: chunk c of the keys for one query tile of
+// A work item as the scheduler publishes it: chunk c of the keys for one query tile of
 // sequence b, KV head h.
 struct alignas(16) Item {
     int npages;  // pages of the chunk that the tile's last token sees (0: no more items)
@@ -225,11 +229,17 @@ struct alignas(16) Item {
     int h;
     int b;
 };
-static_assert(sizeof(Item) == 32, "two 16-byte pieces");
+struct alignas(16) ItemSlot {
+    Item it;
+    int phys[CHUNK / PAGE];  // physical pages, -1 for those that are not there or out of range
+};
+static_assert(sizeof(ItemSlot) == 64, "four 16-byte pieces");
 
-// RPW query rows per softmax group, NWG groups (each with its own rows of every tile).
-template <int D, int RPW, int NWG>
-__global__ void __launch_bounds__((NQ * NWG + 7) * 32, 1)
+__device__ __forceinline__ int tiles_of(int npages) { return (npages + TPAGES - 1) / TPAGES; }
+
+// NWG softmax groups of RPW query rows.
+template <int D, int NWG>
+__global__ void __launch_bounds__((NQ * NWG + 9) * 32, 1)
 attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                const __grid_constant__ CUtensorMap tmap_v, const __nv_bfloat16* __restrict__ q,
                const uint8_t* __restrict__ k_scale, const uint8_t* __restrict__ v_scale,
@@ -239,37 +249,41 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                float* __restrict__ ws_o, float* __restrict__ ws_ml, int maxC,
                unsigned int* __restrict__ cnt, unsigned int* err) {
     using C = Cfg<D>;
-    constexpr int NST = C::NST;
+    constexpr int NSLOT = C::NSLOT;
     constexpr int RP = RPW * NWG;
     constexpr int EPI = NQ * NWG;  // first epilogue warp (a multiple of 4: its lane quarter is 0)
-    constexpr int PRODUCER = EPI + 4, S_WARP = EPI + 5, PV_WARP = EPI + 6;
-    constexpr int THREADS = (EPI + 7) * 32;
+    constexpr int SCHED = EPI + 4, K_WARP = EPI + 5, V_WARP = EPI + 6;
+    constexpr int S_WARP = EPI + 7, PV_WARP = EPI + 8;
+    constexpr int THREADS = (EPI + 9) * 32;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
     uint8_t* sQ = smem + C::Q_OFF;
     uint8_t* sP = smem + C::P_OFF;
-    uint8_t* sStage = smem + C::RING_OFF;
+    uint8_t* sK = smem + C::RING_OFF;
+    uint8_t* sV = smem + C::V_OFF;
     uint8_t* sScale = smem + C::SCALE_OFF;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
-    uint64_t* empty = full + NST;
-    uint64_t* s_full = empty + NST;     // scores of tile g in S buffer g % NSB
-    uint64_t* s_empty = s_full + NSB;   // ... read by the softmax warps
-    uint64_t* p_full = s_empty + NSB;   // P of tile g in P buffer g & 1
-    uint64_t* p_empty = p_full + 2;     // P V of tile g has completed (MMA commit)
-    uint64_t* o_full = p_empty + 2;     // item k's O (buffer k & 1) is complete (MMA commit)
+    uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+    uint64_t* k_empty = k_full + NSLOT;
+    uint64_t* v_full = k_empty + NSLOT;
+    uint64_t* v_empty = v_full + NSLOT;
+    uint64_t* s_full = v_empty + NSLOT; // item k's scores are in S set k & 1
+    uint64_t* s_empty = s_full + 2;     // ... and read by the softmax
+    uint64_t* p_full = s_empty + 2;     // item k's P is written
+    uint64_t* p_empty = p_full + 1;     // P V of item k has completed (MMA commit)
+    uint64_t* o_full = p_empty + 1;     // item k's O (buffer k & 1) is complete (MMA commit)
     uint64_t* o_empty = o_full + 2;     // ... and read out by the epilogue warps
     uint64_t* xs_bar = o_empty + 2;     // item k's row sums and maxima are in xs[k & 1]
-    uint64_t* q_full = xs_bar + 2;      // item k's Q tile and row factors are in buffer k & 1
+    uint64_t* q_full = xs_bar + 2;      // item k's Q tile, row factors, scale bytes: set k & 1
     uint64_t* d_full = q_full + 2;      // item k's descriptor is in items[k % NDESC]
-    uint64_t* drain = d_full + NDESC;   // [2]: S issuer, P V issuer
+    uint64_t* d_used = d_full + NDESC;  // the K copies of item k are issued (k % LEAD)
+    uint64_t* drain = d_used + LEAD;    // [2]: S issuer, P V issuer
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
-    Item* items = reinterpret_cast<Item*>(smem + C::DESC_OFF);
+    ItemSlot* items = reinterpret_cast<ItemSlot*>(smem + C::DESC_OFF);
     float* xs = reinterpret_cast<float*>(smem + C::XS_OFF);  // [2][NQ + 1][QR]
     float* q_fac = xs + 2 * (NQ + 1) * QR;                   // [2][QR]
     float* x_max = q_fac + 2 * QR;                           // [NQ][QR]
-    int* stage_valid = reinterpret_cast<int*>(smem + C::MISC_OFF);  // [NST], a bit per page
-    int* prefix = stage_valid + NST;                         // [B + 1]
+    int* prefix = reinterpret_cast<int*>(smem + C::MISC_OFF);  // [B + 1]
     int* done = prefix + MAX_BATCH + 1;                      // [4]: epilogue warps per item
     volatile int* abort_flag = reinterpret_cast<volatile int*>(done + 4);
 
@@ -290,17 +304,19 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
     const unsigned long long wait_ns = wait_budget_ns(err);
     if (tid == 0) {
-        for (int i = 0; i < NST; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+        for (int i = 0; i < NSLOT; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
         }
-        for (int i = 0; i < NSB; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&s_empty[i], NQ * NWG);
         }
+        mbar_init(p_full, NQ * NWG);
+        mbar_init(p_empty, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&p_full[i], NQ * NWG);
-            mbar_init(&p_empty[i], 1);
             mbar_init(&o_full[i], 1);
             mbar_init(&o_empty[i], 4);
             mbar_init(&xs_bar[i], NQ * NWG);
@@ -308,6 +324,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             mbar_init(&drain[i], 1);
         }
         for (int i = 0; i < NDESC; ++i) mbar_init(&d_full[i], 1);
+        for (int i = 0; i < LEAD; ++i) mbar_init(&d_used[i], 1);
         for (int i = 0; i < 4; ++i) done[i] = 0;
         *abort_flag = 0;
         fence_barrier_init();
@@ -350,12 +367,16 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         if (ok && !mbar_wait_warp(bar, parity, abort_flag, wait_ns)) ok = false;
         return ok;
     };
+    // tile g's slot of a ring has landed (flip 0) or is free again (flip 1)
+    auto wait_slot = [&](uint64_t* bars, uint32_t g, uint32_t flip) {
+        return wait(&bars[g % NSLOT], ((g / NSLOT) & 1u) ^ flip);
+    };
     // the descriptor of item k; npages = 0 after the last one (or when the wait ran out)
     auto item_at = [&](int k) {
         Item it;
         it.npages = 0;
         if (wait(&d_full[k % NDESC], uint32_t(k / NDESC) & 1u)) {
-            const uint4* src = reinterpret_cast<const uint4*>(&items[k % NDESC]);
+            const uint4* src = reinterpret_cast<const uint4*>(&items[k % NDESC].it);
             const uint4 a = src[0], b = src[1];
             it = Item{int(a.x), int(a.y), int(a.z), int(a.w),
                       int(b.x), int(b.y), int(b.z), int(b.w)};
@@ -363,21 +384,19 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         return it;
     };
 
-    if (warp == PRODUCER) {
-        // ------------------------------------------------------------------ producer
-        // The whole warp runs the loop; one elected lane issues the copies.  It also finds
-        // the items and publishes them one item ahead: item k's slot was last read for item
-        // k - NDESC, and no reader is that far behind (the ring holds the producer at most
-        // NST <= 8 tiles, so as many items, ahead of P V, and P V is at most two items ahead
-        // of the epilogue).
-        static_assert(NST + 4 < NDESC, "descriptors in flight");
+    if (warp == SCHED) {
+        // ----------------------------------------------------------------- scheduler
+        // Finds this CTA's items and publishes them, at most LEAD ahead of the K copies.  Item
+        // j takes the descriptor of item j - NDESC.  When the K copies of item x are issued,
+        // the scores of item x - NSLOT at least are done, so the softmax has finished the item
+        // three before that, and the epilogue is at most two behind it: no reader is as far
+        // back as NDESC.
         const int total = prefix[B];
-        int w = blockIdx.x, pub = 0;
-        // publishes the next item of this CTA that is not empty; lane k returns the physical
-        // page of the item's page k
-        auto publish = [&](Item& it, int& phys) {
+        int w = blockIdx.x;
+        for (int j = 0;; ++j) {
+            if (!wait(&d_used[j % LEAD], (uint32_t(j / LEAD) & 1u) ^ 1u)) break;
+            Item it;
             it.npages = 0;
-            phys = -1;
             for (; w < total && it.npages == 0; w += gridDim.x) {
                 int lo = 0, hi = B;
                 while (hi - lo > 1) {
@@ -399,96 +418,93 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const int seen = it.pos0 + it.ntok - it.key0;
                 it.npages = seen <= 0 ? 0 : min(CHUNK / PAGE, (seen + PAGE - 1) / PAGE);
             }
-            if (lane < it.npages) {
-                const int pidx = it.key0 / PAGE + lane;
-                if (pidx < max_pages) phys = block_table[int64_t(it.b) * max_pages + pidx];
+            ItemSlot* slot = &items[j % NDESC];
+            if (lane < CHUNK / PAGE) {
+                int phys = -1;
+                if (lane < it.npages) {
+                    const int pidx = it.key0 / PAGE + lane;
+                    if (pidx < max_pages) phys = block_table[int64_t(it.b) * max_pages + pidx];
+                    if (phys < 0 || phys >= num_pages) {
+                        phys = -1;
+                        latch_error(err, kErrDeviceArg);
+                    }
+                }
+                slot->phys[lane] = phys;
             }
-            if (lane == 0) {
-                items[pub % NDESC] = it;
-                mbar_arrive(&d_full[pub % NDESC]);
-            }
-            ++pub;
-        };
-        if (lane == 0) {
-            tma_prefetch_desc(&tmap_k);
-            tma_prefetch_desc(&tmap_v);
+            if (lane == 0) slot->it = it;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&d_full[j % NDESC]);
+            if (it.npages == 0) break;
         }
+        if (!ok && lane == 0) give_up();
+    } else if (warp == K_WARP || warp == V_WARP) {
+        // ----------------------------------------------------------------- producers
+        // One warp copies K, one V: the copies' issue takes about as long as their data.  The
+        // whole warp runs the loop; one elected lane issues.
+        const bool is_k = warp == K_WARP;
+        const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
+        uint64_t* full = is_k ? k_full : v_full;
+        uint64_t* empty = is_k ? k_empty : v_empty;
+        uint8_t* ring = is_k ? sK : sV;
+        if (lane == 0) tma_prefetch_desc(map);
         // blocks of one query tile read K and V once; wider ones read them again from L2
         const uint64_t policy = max_q <= TQ ? l2_policy_evict_first() : l2_policy_evict_last();
         uint32_t g = 0;
-        Item it, nx;
-        int phys_l, phys_n;
-        publish(it, phys_l);
-        while (ok && it.npages > 0) {
-            publish(nx, phys_n);
+        for (int item = 0; ok; ++item) {
+            const Item it = item_at(item);
+            if (it.npages == 0) break;
+            const int phys_l = lane < CHUNK / PAGE ? items[item % NDESC].phys[lane] : -1;
             for (int i = 0; i < it.npages; i += TPAGES, ++g) {
-                const int s = int(g % NST);
-                if (!wait(&empty[s], ((g / NST) & 1u) ^ 1u)) break;
-                int phys[TPAGES], valid = 0;
+                if (!wait_slot(empty, g, 1u)) break;
+                int phys[TPAGES], there = 0;
 #pragma unroll
                 for (int k = 0; k < TPAGES; ++k) {
                     phys[k] = __shfl_sync(0xffffffffu, phys_l, i + k);
-                    const bool there = i + k < it.npages;
-                    const bool v = there && phys[k] >= 0 && phys[k] < num_pages;
-                    if (v) valid |= 1 << k;
-                    if (there && !v && lane == 0) latch_error(err, kErrDeviceArg);
+                    there += phys[k] >= 0 ? 1 : 0;
                 }
                 if (elect_one()) {
-                    stage_valid[s] = valid;
-                    uint8_t* st = sStage + s * C::STAGE_BYTES;
-                    if (valid)
-                        mbar_arrive_expect_tx(&full[s], uint32_t(__popc(valid)) *
-                                                            (2 * C::PAGE_BYTES + 2 * PAGE));
+                    const int slot = int(g % NSLOT);
+                    if (there)
+                        mbar_arrive_expect_tx(&full[slot], uint32_t(there * C::PAGE_BYTES));
                     else
-                        mbar_arrive(&full[s]);
+                        mbar_arrive(&full[slot]);
 #pragma unroll
-                    for (int k = 0; k < TPAGES; ++k) {
-                        if (valid & (1 << k)) {
-                            const int row = (phys[k] * Hkv + it.h) * PAGE;
-                            tma_load_2d_hint(st + k * C::PAGE_BYTES, &tmap_k, &full[s], 0, row,
-                                             policy);
-                            tma_load_2d_hint(st + C::SIDE_BYTES + k * C::PAGE_BYTES, &tmap_v,
-                                             &full[s], 0, row, policy);
-                            uint8_t* sc = sScale + s * 2 * TK + k * PAGE;
-                            bulk_load(sc, k_scale + row, PAGE, &full[s]);
-                            bulk_load(sc + TK, v_scale + row, PAGE, &full[s]);
-                        }
-                    }
+                    for (int k = 0; k < TPAGES; ++k)
+                        if (phys[k] >= 0)
+                            tma_load_2d_hint(ring + slot * C::SLOT_BYTES + k * C::PAGE_BYTES, map,
+                                             &full[slot], 0, (phys[k] * Hkv + it.h) * PAGE, policy);
                 }
                 __syncwarp();
             }
-            it = nx;
-            phys_l = phys_n;
+            if (is_k && lane == 0) mbar_arrive(&d_used[item % LEAD]);
         }
         if (!ok) {
             if (lane == 0) give_up();
             // copies already issued land before the CTA exits (bounded)
-            for (int k = 1; k <= NST && k <= int(g); ++k) {
-                const uint32_t gg = g - k;
-                mbar_wait(&full[gg % NST], (gg / NST) & 1u, nullptr, 100000000ull);
+            for (uint32_t k = 1; k <= NSLOT && k <= g; ++k) {
+                const uint32_t p = g - k;
+                mbar_wait(&full[p % NSLOT], (p / NSLOT) & 1u, nullptr, 100000000ull);
             }
         }
     } else if (warp == S_WARP) {
         // ------------------------------------------------- S^T = K (Q_hi + Q_lo)^T
         constexpr uint32_t idesc = idesc_e4m3(TK, QR, 0, 0);
         const uint64_t q_desc0 = umma_smem_desc(smem_addr(sQ), 16, C::SBO, C::LAYOUT);
-        const uint64_t k_desc0 = umma_smem_desc(smem_addr(sStage), 16, C::SBO, C::LAYOUT);
+        const uint64_t k_desc0 = umma_smem_desc(smem_addr(sK), 16, C::SBO, C::LAYOUT);
         uint32_t g = 0;
         for (int item = 0; ok; ++item) {
-            const int npages = item_at(item).npages;
-            if (npages == 0) break;
-            const int qbuf = item & 1;
-            if (!wait(&q_full[qbuf], uint32_t(item >> 1) & 1u)) break;
-            for (int i = 0; i < npages; i += TPAGES, ++g) {
-                const int s = int(g % NST), sb = int(g % NSB);
-                if (!wait(&full[s], (g / NST) & 1u) ||
-                    !wait(&s_empty[sb], ((g / NSB) & 1u) ^ 1u))
-                    break;
+            const int nt = tiles_of(item_at(item).npages);
+            if (nt == 0) break;
+            const int buf = item & 1;
+            const uint32_t par = uint32_t(item >> 1) & 1u;
+            if (!wait(&q_full[buf], par) || !wait(&s_empty[buf], par ^ 1u)) break;
+            for (int i = 0; i < nt; ++i, ++g) {
+                if (!wait_slot(k_full, g, 0u)) break;
                 tc_fence_after_sync();
                 if (elect_one()) {
-                    const uint64_t k_desc = k_desc0 + uint64_t((s * C::STAGE_BYTES) >> 4);
-                    const uint64_t q_desc = q_desc0 + uint64_t((qbuf * C::Q_BYTES) >> 4);
-                    const uint32_t d = tmem_base + uint32_t(S_COL + sb * QR);
+                    const uint64_t k_desc = k_desc0 + uint64_t(((g % NSLOT) * C::SLOT_BYTES) >> 4);
+                    const uint64_t q_desc = q_desc0 + uint64_t((buf * C::Q_BYTES) >> 4);
+                    const uint32_t d = tmem_base + uint32_t(S_COL + (buf * NT + i) * QR);
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k) {  // head dims 32k .. 32k+31: +32 B
                         tc_mma_f8(d, k_desc + uint64_t(k * 2), q_desc + uint64_t(k * 2), idesc,
@@ -496,7 +512,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         tc_mma_f8(d, k_desc + uint64_t(k * 2),
                                   q_desc + uint64_t((C::Q_PIECE >> 4) + k * 2), idesc, 1u);
                     }
-                    tc_commit(&s_full[sb]);
+                    tc_commit(&k_empty[g % NSLOT]);  // K of the tile is no longer read
+                    if (i == nt - 1) tc_commit(&s_full[buf]);
                 }
                 __syncwarp();
             }
@@ -508,32 +525,34 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
     } else if (warp == PV_WARP) {
         // ------------------------------------------------- O^T += V^T [P_hi | P_lo]^T
         constexpr uint32_t idesc = idesc_e4m3(D, 2 * QR, 1, 1);
-        const uint64_t v_desc0 =
-            umma_smem_desc(smem_addr(sStage + C::SIDE_BYTES), 16, C::SBO, C::LAYOUT);
+        const uint64_t v_desc0 = umma_smem_desc(smem_addr(sV), 16, C::SBO, C::LAYOUT);
         const uint64_t p_desc0 = umma_smem_desc(smem_addr(sP), 16, 512, 4);
         uint32_t g = 0;
         for (int item = 0; ok; ++item) {
-            const int npages = item_at(item).npages;
-            if (npages == 0) break;
+            const int nt = tiles_of(item_at(item).npages);
+            if (nt == 0) break;
             const int ob = item & 1;
             // the O buffer of this item was read out for item-2
-            if (!wait(&o_empty[ob], (uint32_t(item >> 1) & 1u) ^ 1u)) break;
-            for (int i = 0; i < npages; i += TPAGES, ++g) {
-                const int s = int(g % NST), pb = int(g & 1u);
-                if (!wait(&p_full[pb], (g >> 1) & 1u)) break;
+            if (!wait(&o_empty[ob], (uint32_t(item >> 1) & 1u) ^ 1u) ||
+                !wait(p_full, uint32_t(item) & 1u))
+                break;
+            for (int i = 0; i < nt; ++i, ++g) {
+                if (!wait_slot(v_full, g, 0u)) break;
                 tc_fence_after_sync();
                 if (elect_one()) {
-                    const uint64_t v_desc = v_desc0 + uint64_t((s * C::STAGE_BYTES) >> 4);
-                    const uint64_t p_desc = p_desc0 + uint64_t((pb * C::P_BYTES) >> 4);
+                    const uint64_t v_desc = v_desc0 + uint64_t(((g % NSLOT) * C::SLOT_BYTES) >> 4);
+                    const uint64_t p_desc = p_desc0 + uint64_t((i * C::P_BYTES) >> 4);
                     const uint32_t d = tmem_base + uint32_t(O_COL + ob * 2 * QR);
 #pragma unroll
                     for (int k = 0; k < TK / 32; ++k)  // keys 32k .. 32k+31
                         tc_mma_f8(d, v_desc + uint64_t(k * 32 * D / 16),
                                   p_desc + uint64_t(k * 32 * 2 * QR / 16), idesc,
                                   (i | k) != 0 ? 1u : 0u);
-                    tc_commit(&p_empty[pb]);
-                    tc_commit(&empty[s]);  // K, V and scales of the tile are no longer read
-                    if (i + TPAGES >= npages) tc_commit(&o_full[ob]);
+                    tc_commit(&v_empty[g % NSLOT]);
+                    if (i == nt - 1) {
+                        tc_commit(p_empty);
+                        tc_commit(&o_full[ob]);
+                    }
                 }
                 __syncwarp();
             }
@@ -545,103 +564,128 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
     } else if (warp >= EPI) {
         // ------------------------------------------------- Q split and epilogue
         const int ew = warp - EPI;  // tensor-memory lane quarter
-        // Q tile of an item: four neighbouring threads split one row.
-        auto split_q = [&](const Item& it, int buf) {
+        // Scale bytes of item k's keys (a key of each tile per thread), and its Q tile (rows 0
+        // .. RP-1; four neighbouring threads split one row).
+        auto split_q = [&](const Item& it, int k) {
             constexpr int PER = D / 4;  // elements per thread
-            const int r = ew * 8 + (lane >> 2), part = lane & 3;
-            const int j = r / G;
-            uint4 v[PER / 8];
+            const int buf = k & 1;
+            const int key = ew * 32 + lane;
+            uint8_t ksc[NT], vsc[NT];
 #pragma unroll
-            for (int k = 0; k < PER / 8; ++k) v[k] = make_uint4(0, 0, 0, 0);
-            if (j < it.ntok && r < TQ * G) {
-                const __nv_bfloat16* src =
-                    q + (int64_t(it.t0 + j) * Hq + it.h * G + (r - j * G)) * D + part * PER;
-#pragma unroll
-                for (int k = 0; k < PER / 8; ++k)
-                    v[k] = *reinterpret_cast<const uint4*>(src + k * 8);
-            }
-            uint32_t amax = 0;  // of bf16 magnitudes, which order as their bits
-#pragma unroll
-            for (int k = 0; k < PER / 8; ++k) {
-                const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-                    amax = max(amax, max(x[n] & 0x7fffu, (x[n] >> 16) & 0x7fffu));
-            }
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // s = 7 - floor(log2(amax)), held where 2^s and 2^-s are normal
-            const int s = max(-120, min(120, 134 - int(amax >> 7)));
-            const float mul = __uint_as_float(uint32_t(127 + s) << 23);
-            uint8_t* hi = sQ + buf * C::Q_BYTES;
-            uint8_t* lo = hi + C::Q_PIECE;
-#pragma unroll
-            for (int k = 0; k < PER / 16; ++k) {
-                uint32_t h[4], l[4];
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const uint4& src = v[2 * k + (n >> 1)];
-                    const uint32_t x0 = n & 1 ? src.z : src.x, x1 = n & 1 ? src.w : src.y;
-                    float f[4] = {__uint_as_float(x0 << 16) * mul,
-                                  __uint_as_float(x0 & 0xffff0000u) * mul,
-                                  __uint_as_float(x1 << 16) * mul,
-                                  __uint_as_float(x1 & 0xffff0000u) * mul};
-                    const uint32_t c0 = e4m3x2(f[0], f[1]), c1 = e4m3x2(f[2], f[3]);
-                    const float2 b0 = e4m3x2_values(c0), b1 = e4m3x2_values(c1);
-                    h[n] = c0 | (c1 << 16);
-                    l[n] = e4m3x2(f[0] - b0.x, f[1] - b0.y) |
-                           (e4m3x2(f[2] - b1.x, f[3] - b1.y) << 16);
+            for (int i = 0; i < NT; ++i) {
+                const int phys = items[k % NDESC].phys[i * TPAGES + key / PAGE];
+                ksc[i] = vsc[i] = 0;
+                if (phys >= 0) {
+                    const int64_t at = (int64_t(phys) * Hkv + it.h) * PAGE + key % PAGE;
+                    ksc[i] = k_scale[at];
+                    vsc[i] = v_scale[at];
                 }
-                const uint32_t at = swz_row<D>(r, part * (PER / 16) + k);
-                *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
             }
-            // a query with an infinity or NaN scores NaN throughout
-            if (part == 0)
-                q_fac[buf * QR + r] = amax >= 0x7f80u
-                                          ? __int_as_float(0x7fc00000)
-                                          : scale_log2 * __uint_as_float(uint32_t(127 - s) << 23);
-            fence_proxy_async_smem();
+            const int r = ew * 8 + (lane >> 2), part = lane & 3;
+            if (ew * 8 < RP) {
+                const int j = r / G;
+                uint4 v[PER / 8];
+#pragma unroll
+                for (int n = 0; n < PER / 8; ++n) v[n] = make_uint4(0, 0, 0, 0);
+                if (j < it.ntok && r < TQ * G) {
+                    const __nv_bfloat16* src =
+                        q + (int64_t(it.t0 + j) * Hq + it.h * G + (r - j * G)) * D + part * PER;
+#pragma unroll
+                    for (int n = 0; n < PER / 8; ++n)
+                        v[n] = *reinterpret_cast<const uint4*>(src + n * 8);
+                }
+                uint32_t amax = 0;  // of bf16 magnitudes, which order as their bits
+#pragma unroll
+                for (int n = 0; n < PER / 8; ++n) {
+                    const uint32_t x[4] = {v[n].x, v[n].y, v[n].z, v[n].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        amax = max(amax, max(x[e] & 0x7fffu, (x[e] >> 16) & 0x7fffu));
+                }
+                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                // s = 7 - floor(log2(amax)), held where 2^s and 2^-s are normal
+                const int s = max(-120, min(120, 134 - int(amax >> 7)));
+                const float mul = __uint_as_float(uint32_t(127 + s) << 23);
+                uint8_t* hi = sQ + buf * C::Q_BYTES;
+                uint8_t* lo = hi + C::Q_PIECE;
+#pragma unroll
+                for (int n = 0; n < PER / 16; ++n) {
+                    uint32_t h[4], l[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint4& src = v[2 * n + (e >> 1)];
+                        const uint32_t x0 = e & 1 ? src.z : src.x, x1 = e & 1 ? src.w : src.y;
+                        const float f[4] = {__uint_as_float(x0 << 16) * mul,
+                                            __uint_as_float(x0 & 0xffff0000u) * mul,
+                                            __uint_as_float(x1 << 16) * mul,
+                                            __uint_as_float(x1 & 0xffff0000u) * mul};
+                        const uint32_t c0 = e4m3x2(f[0], f[1]), c1 = e4m3x2(f[2], f[3]);
+                        const float2 b0 = e4m3x2_values(c0), b1 = e4m3x2_values(c1);
+                        h[e] = c0 | (c1 << 16);
+                        l[e] = e4m3x2(f[0] - b0.x, f[1] - b0.y) |
+                               (e4m3x2(f[2] - b1.x, f[3] - b1.y) << 16);
+                    }
+                    const uint32_t at = swz_row<D>(r, part * (PER / 16) + n);
+                    *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+                }
+                // a query with an infinity or NaN scores NaN throughout
+                if (part == 0)
+                    q_fac[buf * QR + r] =
+                        amax >= 0x7f80u ? __int_as_float(0x7fc00000)
+                                        : scale_log2 * __uint_as_float(uint32_t(127 - s) << 23);
+                fence_proxy_async_smem();
+            }
+            uint8_t* sc = sScale + buf * C::SCALE_BYTES + key;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                sc[i * 2 * TK] = ksc[i];
+                sc[i * 2 * TK + TK] = vsc[i];
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[buf]);
         };
         bool reset_done = cnt == nullptr;  // griddepcontrol.wait passed
-        // Item k's stores are counted an item later, when the fence finds them done.  The last
-        // of the four warps counts; done[k & 3] holds no other item's arrivals, since a warp
-        // that counts item k has seen O of item k, so every warp has read O of item k - 2 and
-        // counted item k - 3.
+        // Item k's partial is counted by the last of the four warps to have stored its part
+        // (each releases its stores to the CTA; the last one's fence takes them to the GPU).
+        // done[k & 3] holds no other item's arrivals: a warp that counts item k has seen O of
+        // item k, so every warp has read O of item k - 2 and counted item k - 3.
         auto count = [&](int k, int at) {
             if (!cnt) return;
-            __threadfence();
-            __syncwarp();
             if (!reset_done) {
                 pdl_wait();
                 pdl_trigger();
                 reset_done = true;
             }
-            if (lane == 0 && (atomicAdd(&done[k & 3], 1) & 3) == 3) {
-                __threadfence();
-                atomicAdd(cnt + at, 1u);
+            __syncwarp();
+            if (lane == 0) {
+                int before;
+                asm volatile("atom.acq_rel.cta.shared::cta.add.s32 %0, [%1], 1;"
+                             : "=r"(before)
+                             : "r"(smem_addr(&done[k & 3]))
+                             : "memory");
+                if ((before & 3) == 3) {
+                    asm volatile("fence.acq_rel.gpu;" ::: "memory");
+                    atomicAdd(cnt + at, 1u);
+                }
             }
         };
+        // Items k and k + 1 have their Q split before O of item k is waited for; then O of
+        // item k is stored and the Q of item k + 2 split into the buffer that item k's scores
+        // no longer need.
         Item it = item_at(0), nx;
-        if (it.npages > 0) split_q(it, 0);
-        int item = 0, prev = -1;
-        for (; ok && it.npages > 0; ++item) {
-            nx = item_at(item + 1);
-            // (this buffer's item-1 is complete: its O was waited for)
-            if (nx.npages > 0) split_q(nx, (item + 1) & 1);
-            if (prev >= 0) count(item - 1, prev);
+        nx.npages = 0;
+        if (it.npages > 0) {
+            split_q(it, 0);
+            nx = item_at(1);
+            if (nx.npages > 0) split_q(nx, 1);
+        }
+        for (int item = 0; ok && it.npages > 0; ++item) {
             const int ob = item & 1;
             const uint32_t par = uint32_t(item >> 1) & 1u;
             if (!wait(&xs_bar[ob], par) || !wait(&o_full[ob], par)) break;
             tc_fence_after_sync();
-            uint32_t vh[RP], vl[RP];
-            const uint32_t ta =
-                tmem_base + (uint32_t(32 * ew) << 16) + uint32_t(O_COL + ob * 2 * QR);
-            tmem_cols(ta, vh);
-            tmem_cols(ta + QR, vl);
-            tc_fence_before_sync();
             // rows (token j, head gg) are stored when their token sees the chunk
             const int rows = it.ntok * G;
             const int first = max(0, it.key0 - it.pos0) * G;
@@ -656,18 +700,25 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     *reinterpret_cast<float2*>(ws_ml + idx * 2) = make_float2(x[NQ * QR + r], l);
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&o_empty[ob]);
             // O^T: lane = head dim (M = 128), or dims 16 ew .. 16 ew + 15 in lanes 0..15 (M = 64)
             const int d = D == 128 ? ew * 32 + lane : ew * 16 + lane;
-            if (D == 128 || lane < 16) {
-                float* dst = ws_o + (row0 * maxC + c) * D + d;
-                const int64_t step = int64_t(maxC) * D, skip = step * (Hq - G);
-                int gg = 0;
+            const bool mine = D == 128 || lane < 16;
+            float* dst = ws_o + (row0 * maxC + c) * D + d;
+            const int64_t step = int64_t(maxC) * D, skip = step * (Hq - G);
+            int gg = 0;
+            const uint32_t ta =
+                tmem_base + (uint32_t(32 * ew) << 16) + uint32_t(O_COL + ob * 2 * QR);
+            constexpr int PART = RP < 16 ? RP : 16;
 #pragma unroll
-                for (int r = 0; r < RP; ++r) {
-                    if (r < rows && r >= first)
-                        *dst = fmaf(__uint_as_float(vl[r]), 1.f / kLoScale, __uint_as_float(vh[r]));
+            for (int r0 = 0; r0 < RP; r0 += PART) {
+                uint32_t vh[PART], vl[PART];
+                tmem_cols(ta + r0, vh);
+                tmem_cols(ta + QR + r0, vl);
+#pragma unroll
+                for (int k = 0; k < PART; ++k) {
+                    const int r = r0 + k;
+                    if (mine && r < rows && r >= first)
+                        *dst = fmaf(__uint_as_float(vl[k]), 1.f / kLoScale, __uint_as_float(vh[k]));
                     dst += step;
                     if (++gg == G) {
                         gg = 0;
@@ -675,10 +726,18 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     }
                 }
             }
-            prev = it.b * Hkv + it.h;
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_empty[ob]);
+            const int at = it.b * Hkv + it.h;
             it = nx;
+            nx.npages = 0;
+            if (it.npages > 0) {
+                nx = item_at(item + 2);
+                if (nx.npages > 0) split_q(nx, item + 2);
+            }
+            count(item, at);
         }
-        if (ok && prev >= 0) count(item - 1, prev);
         if (!ok && lane == 0) give_up();
         // a CTA with no item (or one that gave up) still waits before it completes
         if (!reset_done) {
@@ -693,123 +752,100 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const int row0 = wg * RPW;
         const uint32_t lane_base = uint32_t(32 * wq) << 16;
         uint32_t g = 0;
-        float m[RPW], l[RPW];
         for (int item = 0;; ++item) {
-            const Item it = item_at(item);
             const int ob = item & 1;
             const uint32_t ipar = uint32_t(item >> 1) & 1u;
+            const Item it = item_at(item);
             if (it.npages > 0) wait(&q_full[ob], ipar);
             if (!ok && lane == 0) give_up();
             if (group_or(1 + wg, !ok) || it.npages == 0) break;
-            const float* fac = q_fac + ob * QR + row0;
+            const int nt = tiles_of(it.npages);
+            float f[RPW];
 #pragma unroll
-            for (int r = 0; r < RPW; ++r) {
-                m[r] = kNoMax;
-                l[r] = 0.f;
+            for (int r = 0; r < RPW; r += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(q_fac + ob * QR + row0 + r);
+                f[r] = x.x;
+                f[r + 1] = x.y;
+                f[r + 2] = x.z;
+                f[r + 3] = x.w;
             }
-            bool left = false;
-            for (int i = 0; i < it.npages; i += TPAGES, ++g) {
-                const int s = int(g % NST), sb = int(g % NSB), pb = int(g & 1u);
-                const int kp = it.key0 + i * PAGE + key;  // this key's position
-                wait(&full[s], (g / NST) & 1u);
-                const bool live = ((stage_valid[s] >> (key / PAGE)) & 1) && kp < it.L;
-                const uint32_t ksc = sScale[s * 2 * TK + key], vsc = sScale[s * 2 * TK + TK + key];
-                wait(&s_full[sb], (g / NSB) & 1u);
-                tc_fence_after_sync();
-                uint32_t sv[RPW];
-                tmem_cols(tmem_base + lane_base + uint32_t(S_COL + sb * QR + row0), sv);
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_empty[sb]);
-                const float ka = e8m0(ksc);
-                const float vb = vsc == 255 ? __int_as_float(0x7fc00000) : float(int(vsc) - 127);
-                const float vinv = live ? e8m0_inv(vsc) : 0.f;
-                float t[RPW];
+            // t of this thread's keys (one of each tile), and each row's maximum
+            const uint8_t* sc = sScale + ob * C::SCALE_BYTES + key;
+            uint32_t ksc[NT], vsc[NT], dead = 0;  // dead: a bit per tile
 #pragma unroll
-                for (int r = 0; r < RPW; r += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(fac + r);
-                    t[r] = fmaf(__uint_as_float(sv[r]) * ka, f.x, vb);
-                    t[r + 1] = fmaf(__uint_as_float(sv[r + 1]) * ka, f.y, vb);
-                    t[r + 2] = fmaf(__uint_as_float(sv[r + 2]) * ka, f.z, vb);
-                    t[r + 3] = fmaf(__uint_as_float(sv[r + 3]) * ka, f.w, vb);
-                }
+            for (int i = 0; i < NT; ++i) {
+                ksc[i] = sc[i * 2 * TK];
+                vsc[i] = sc[i * 2 * TK + TK];
+                const bool live = items[item % NDESC].phys[i * TPAGES + key / PAGE] >= 0 &&
+                                  it.key0 + i * TK + key < it.L;
+                if (!live) dead |= 1u << i;
+            }
+            wait(&s_full[ob], ipar);
+            tc_fence_after_sync();
+            uint32_t sv[NT][RPW];
+            tmem_tiles(tmem_base + lane_base + uint32_t(S_COL + ob * NT * QR + row0), sv);
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[ob]);
+            float t[NT][RPW], mx[RPW];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const float ka = e8m0(ksc[i]);
+                const float vb =
+                    vsc[i] == 255 ? __int_as_float(0x7fc00000) : float(int(vsc[i]) - 127);
+#pragma unroll
+                for (int r = 0; r < RPW; ++r)
+                    t[i][r] = fmaf(__uint_as_float(sv[i][r]) * ka, f[r], vb);
                 // causal mask: row r (token r / G) sees the key when r / G >= kp - pos0
-                if (!__all_sync(0xffffffffu, live && kp <= it.pos0)) {
-                    const int first = live ? max(0, kp - it.pos0) * G : QR;  // first row seeing it
+                const int ahead = it.key0 + i * TK + key - it.pos0;
+                if (!__all_sync(0xffffffffu, ahead <= 0 && !((dead >> i) & 1u))) {
+                    const int first = (dead >> i) & 1u ? QR : max(0, ahead) * G;  // first row seeing it
 #pragma unroll
-                    for (int r = 0; r < RPW; ++r) t[r] = row0 + r >= first ? t[r] : -INFINITY;
+                    for (int r = 0; r < RPW; ++r)
+                        t[i][r] = row0 + r >= first ? t[i][r] : -INFINITY;
                 }
-                // does any row's maximum exceed its reference by more than 2^8?
-                bool slow = i == 0;
-                if (!slow) {
-                    float over[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int r = 0; r < RPW; ++r) over[r & 3] = fmaxf(over[r & 3], t[r] - m[r]);
-                    slow = group_or(1 + wg, !ok || fmaxf(fmaxf(over[0], over[1]),
-                                                         fmaxf(over[2], over[3])) > kRaise);
+                for (int r = 0; r < RPW; ++r) mx[r] = i == 0 ? t[i][r] : fmaxf(mx[r], t[i][r]);
+            }
+            // the rows' maxima over the group's four warps
+            const float mine = combine_lanes<RPW, true>(mx, lane);
+            if (lane % (32 / RPW) == 0) x_max[wq * QR + row0 + lane / (32 / RPW)] = mine;
+            if (!ok && lane == 0) give_up();
+            if (group_or(1 + wg, !ok)) {
+                ok = false;
+                break;
+            }
+            float m[RPW], l[RPW];
+#pragma unroll
+            for (int r = 0; r < RPW; r += 4) {
+                float4 x = *reinterpret_cast<const float4*>(x_max + row0 + r);
+#pragma unroll
+                for (int n = 1; n < NQ; ++n) {
+                    const float4 y = *reinterpret_cast<const float4*>(x_max + n * QR + row0 + r);
+                    x = make_float4(fmaxf(x.x, y.x), fmaxf(x.y, y.y), fmaxf(x.z, y.z),
+                                    fmaxf(x.w, y.w));
                 }
-                if (slow) {
-                    // the tile's maximum of every row, over the four warps
-                    const float mine = combine_lanes<RPW, true>(t, lane);
-                    if (lane % (32 / RPW) == 0) x_max[wq * QR + row0 + lane / (32 / RPW)] = mine;
-                    if (!ok && lane == 0) give_up();
-                    if (group_or(1 + wg, !ok)) {
-                        ok = false;
-                        left = true;
-                        break;
-                    }
-                    // O of this warp's lanes may be scaled once P V of the tile before is done
-                    const uint32_t gp = g - 1u;
-                    if (i > 0) wait(&p_empty[gp & 1u], (gp >> 1) & 1u);
-                    tc_fence_after_sync();
+                m[r] = fmaxf(x.x - kHeadroom, kNoMax);
+                m[r + 1] = fmaxf(x.y - kHeadroom, kNoMax);
+                m[r + 2] = fmaxf(x.z - kHeadroom, kNoMax);
+                m[r + 3] = fmaxf(x.w - kHeadroom, kNoMax);
+            }
 #pragma unroll
-                    for (int r0 = 0; r0 < RPW; r0 += 8) {
-                        float fa[8];
+            for (int r = 0; r < RPW; ++r) l[r] = 0.f;
+            // P's buffers are free once P V of item-1 has completed
+            wait(p_empty, (uint32_t(item) & 1u) ^ 1u);
 #pragma unroll
-                        for (int k = 0; k < 8; k += 4) {
-                            float4 x = *reinterpret_cast<const float4*>(x_max + row0 + r0 + k);
-#pragma unroll
-                            for (int n = 1; n < NQ; ++n) {
-                                const float4 y = *reinterpret_cast<const float4*>(
-                                    x_max + n * QR + row0 + r0 + k);
-                                x = make_float4(fmaxf(x.x, y.x), fmaxf(x.y, y.y),
-                                                fmaxf(x.z, y.z), fmaxf(x.w, y.w));
-                            }
-                            const float mt[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                            for (int n = 0; n < 4; ++n) {
-                                const int r = r0 + k + n;
-                                const bool raise = mt[n] > m[r] + kRaise;
-                                const float mn = raise ? mt[n] - kHeadroom : m[r];
-                                fa[k + n] = raise ? ex2(m[r] - mn) : 1.f;
-                                m[r] = mn;
-                                l[r] *= fa[k + n];
-                            }
-                        }
-                        if (i > 0) {
-                            uint32_t o[8];
-                            const uint32_t ta = tmem_base + lane_base +
-                                                uint32_t(O_COL + ob * 2 * QR + row0 + r0);
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                tmem_cols(ta + half * QR, o);
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    o[k] = __float_as_uint(__uint_as_float(o[k]) * fa[k]);
-                                tmem_store_x8(ta + half * QR, o);
-                            }
-                        }
-                    }
-                    tc_fence_before_sync();
-                }
+            for (int i = 0; i < NT; ++i) {
+                if (i >= nt) continue;
+                const float vi = (dead >> i) & 1u ? 0.f : e8m0_inv(vsc[i]);
                 uint32_t hi[RPW / 4], lo[RPW / 4];
 #pragma unroll
                 for (int r = 0; r < RPW; r += 4) {
                     float p[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        p[k] = ex2(t[r + k] - m[r + k]);
-                        l[r + k] = fmaf(p[k], vinv, l[r + k]);
+                        p[k] = ex2(t[i][r + k] - m[r + k]);
+                        l[r + k] = fmaf(p[k], vi, l[r + k]);
                     }
                     const uint32_t c0 = e4m3x2(p[0], p[1]), c1 = e4m3x2(p[2], p[3]);
                     const float2 b0 = e4m3x2_values(c0), b1 = e4m3x2_values(c1);
@@ -817,41 +853,35 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     lo[r / 4] = e4m3x2((p[0] - b0.x) * kLoScale, (p[1] - b0.y) * kLoScale) |
                                 (e4m3x2((p[2] - b1.x) * kLoScale, (p[3] - b1.y) * kLoScale) << 16);
                 }
-                // P buffer pb is free once P V of tile g-2 has completed
-                wait(&p_empty[pb], ((g >> 1) & 1u) ^ 1u);
                 if (!ok) continue;  // (to the group's next common decision)
-                uint8_t* pbuf = sP + pb * C::P_BYTES;
-                if (RPW == 8) {
-                    const int at = wg * 8;
-                    *reinterpret_cast<uint2*>(pbuf + swz_row<64>(key, 0) + at) =
-                        make_uint2(hi[0], hi[1]);
-                    *reinterpret_cast<uint2*>(pbuf + swz_row<64>(key, 2) + at) =
-                        make_uint2(lo[0], lo[1]);
-                } else {
-                    *reinterpret_cast<uint4*>(pbuf + swz_row<64>(key, wg)) =
-                        make_uint4(hi[0], hi[1], hi[RPW / 4 - 2], hi[RPW / 4 - 1]);
-                    *reinterpret_cast<uint4*>(pbuf + swz_row<64>(key, 2 + wg)) =
-                        make_uint4(lo[0], lo[1], lo[RPW / 4 - 2], lo[RPW / 4 - 1]);
-                }
-                // V rows past the sequence's end or of an invalid page are zeroed, so that
-                // unwritten codes (NaN) cannot reach O through 0 * v
-                if (wg == 0 && !live) {
-                    uint4* vr = reinterpret_cast<uint4*>(sStage + s * C::STAGE_BYTES +
-                                                         C::SIDE_BYTES + key * D);
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) vr[k] = make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[pb]);
+                uint8_t* pbuf = sP + i * C::P_BYTES + (wg & 1) * 8;
+                *reinterpret_cast<uint2*>(pbuf + swz_row<64>(key, wg >> 1)) =
+                    make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2*>(pbuf + swz_row<64>(key, 2 + (wg >> 1))) =
+                    make_uint2(lo[0], lo[1]);
             }
-            if (left) break;
+            // V rows past the sequence's end or of an invalid page are zeroed, so that
+            // unwritten codes (NaN) cannot reach O through 0 * v
+            if (wg == 0 && __any_sync(0xffffffffu, dead != 0)) {
+                for (int i = 0; i < nt; ++i) {
+                    wait_slot(v_full, g + i, 0u);
+                    if (ok && ((dead >> i) & 1u)) {
+                        uint4* vr = reinterpret_cast<uint4*>(
+                            sV + ((g + i) % NSLOT) * C::SLOT_BYTES + key * D);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) vr[k] = make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(p_full);
             // the warp's row sums (and the maxima) for the epilogue, once it has read this
             // buffer's previous contents (item-2)
-            wait(&o_empty[ob], ipar ^ 1u);
-            float* x = xs + ob * ((NQ + 1) * QR) + row0;
             const float sum = combine_lanes<RPW, false>(l, lane);
+            wait(&o_empty[ob], ipar ^ 1u);
             if (ok) {
+                float* x = xs + ob * ((NQ + 1) * QR) + row0;
                 if (wq == 0 && lane == 0) {
 #pragma unroll
                     for (int r = 0; r < RPW; ++r) x[NQ * QR + r] = m[r];
@@ -860,6 +890,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&xs_bar[ob]);
             }
+            g += uint32_t(nt);
         }
         if (!ok && lane == 0) give_up();
     }
@@ -872,7 +903,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
 }
 
-template <int D, int RPW, int NWG>
+template <int D, int NWG>
 cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a,
                         const void* k_scale, const void* v_scale, float scale, void* out,
                         float* lse, void* workspace, cudaStream_t stream) {
@@ -882,7 +913,7 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
     if (!tmap_2d_u8_swizzled(&tk, a.k_cache, D, rows, PAGE) ||
         !tmap_2d_u8_swizzled(&tv, a.v_cache, D, rows, PAGE))
         return cudaErrorNotSupported;
-    auto kern = attn_q8_kernel<D, RPW, NWG>;
+    auto kern = attn_q8_kernel<D, NWG>;
     static bool attr_done[64] = {};
     if (dev.device >= 0 && dev.device < 64 && !attr_done[dev.device]) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -907,7 +938,7 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
         if (e != cudaSuccess) return e;
     }
     cudaError_t e = launch_pdl(
-        kern, dim3(grid), dim3((NQ * NWG + 7) * 32), Cf::SMEM, stream, tk, tv,
+        kern, dim3(grid), dim3((NQ * NWG + 9) * 32), Cf::SMEM, stream, tk, tv,
         static_cast<const __nv_bfloat16*>(q), static_cast<const uint8_t*>(k_scale),
         static_cast<const uint8_t*>(v_scale), a.block_table, int(a.max_pages), int(a.num_pages),
         a.seq_lens, a.cu_q, int(a.batch), int(a.total_q), int(a.max_q), int(a.max_seq_len),
@@ -921,19 +952,19 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
 cudaError_t launch_attention_q8(const DeviceInfo& dev, const void* q, const PagedArgs& a,
                                 const void* k_scale, const void* v_scale, float scale, void* out,
                                 float* lse, void* workspace, cudaStream_t stream) {
-    // query rows of the fullest tile: up to 8 in one softmax group, 16 or 32 over two
+    // a softmax group for each 8 query rows of the fullest tile (one, two or four)
     const int64_t G = a.hq / a.hkv, TQ = QR / G;
     const int64_t rows = (a.max_q < TQ ? a.max_q : TQ) * G;
     auto run = [&](auto f) {
         return f(dev, q, a, k_scale, v_scale, scale, out, lse, workspace, stream);
     };
     if (a.head_dim == 64)
-        return run(rows <= 8    ? launch_q8_t<64, 8, 1>
-                   : rows <= 16 ? launch_q8_t<64, 8, 2>
-                                : launch_q8_t<64, 16, 2>);
-    return run(rows <= 8    ? launch_q8_t<128, 8, 1>
-               : rows <= 16 ? launch_q8_t<128, 8, 2>
-                            : launch_q8_t<128, 16, 2>);
+        return run(rows <= 8    ? launch_q8_t<64, 1>
+                   : rows <= 16 ? launch_q8_t<64, 2>
+                                : launch_q8_t<64, 4>);
+    return run(rows <= 8    ? launch_q8_t<128, 1>
+               : rows <= 16 ? launch_q8_t<128, 2>
+                            : launch_q8_t<128, 4>);
 }
 
 }  // namespace bi

@@ -78,14 +78,14 @@ def check_attention(out, lse, ref, what=""):
     out: rounding to bf16 moves a value by at most 2^-8 of itself.  A weight times its value
     scale, p, is held as two e4m3 pieces of four bits each: off by at most 2^-9 of itself,
     which moves out by at most 2^-9 A, or, where the second piece is below e4m3's normal range
-    (steps of 2^-9, in units of 1/32), by at most 2^-10 / 32 = 2^-15 when the largest p is at
-    least 2^3: 2^-18 of the largest p per unit of a code, at most 2^-18 F in all.  The fp32
+    (steps of 2^-9, in units of 1/32), by at most 2^-10 / 32 = 2^-15 where the chunk's
+    largest p is 2^8: 2^-23 of the largest p per unit of a code, at most 2^-23 F in all.  The fp32
     parts (scores off by 2^-17 S, exp2, sums) stay below 2^-10 A for S up to 2^6.
     lse: fp32 scores off by at most 2^-17 of the largest sum of |q k|, and a few fp32
     roundings of a number of lse's size."""
     o, l, A, F, S = ref
     g = out.double().cpu().numpy()
-    bound = 2.0 ** -8 * np.abs(o) + (2.0 ** -9 + 2.0 ** -10) * A + 2.0 ** -18 * F
+    bound = 2.0 ** -8 * np.abs(o) + (2.0 ** -9 + 2.0 ** -10) * A + 2.0 ** -23 * F
     err = np.abs(g - o)
     assert np.isfinite(g).all(), f"{what}: non-finite output"
     worst = np.unravel_index(np.argmax(err - bound), err.shape)
