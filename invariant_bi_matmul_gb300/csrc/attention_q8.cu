@@ -35,13 +35,13 @@
 // Orientation.  S^T = K Q^T (M = 128 keys, N = 32 query rows) and O^T = V^T P^T (M = head
 // dim, N = 32 hi + 32 lo rows): the cache is the operand that the tensor core reads 128 rows
 // at a time, whatever the number of query rows, and a softmax thread owns one key of a tile, so
-// it does as many exponentials as there are query rows (rounded up to 8, 16 or 32), reads its
-// key's two scale bytes once, and writes its P values as 8-byte pieces.
+// it does as many exponentials as there are query rows (rounded up to 4, 8, 16 or 32), reads its
+// key's two scale bytes once, and writes its P values in pieces of 4 or 8 bytes.
 //
-// Warps: one, two or four softmax groups of four (8 query rows each), four epilogue warps (they
-// also split the Q and fetch the scale bytes of the item after next), the scheduler, a TMA
-// producer for K and one for V, the S issuer (and TMEM owner), the P V issuer.  One persistent
-// CTA per SM; work items (sequence, chunk, query tile, KV head) are enumerated on the device.  All waits
+// Warps: one, two or four softmax groups of four warps (4 or 8 query rows each), four epilogue
+// warps, the scheduler, a TMA producer for K and one for V, the S issuer (and TMEM owner), the
+// P V issuer, the counter, one or two warps that split Q and fetch the scale bytes.  One
+// persistent CTA per SM; work items (sequence, chunk, query tile, KV head) are enumerated on the device.  All waits
 // are bounded; the one barrier that warps meet in, a softmax group's, is left by all of them
 // together.
 //
@@ -57,7 +57,6 @@ constexpr int QR = 32;                    // query rows of a tile
 constexpr int TK = 128;                   // keys of a tile: two pages
 constexpr int TPAGES = TK / PAGE;
 constexpr int NQ = 4;                     // warps of a softmax group: 32 keys each
-constexpr int RPW = 8;                    // query rows of a softmax group
 constexpr int NDESC = 64;                 // item descriptors in flight
 constexpr int LEAD = 16;                  // items found ahead of the K copies, at most
 constexpr int NT = CHUNK / TK;            // tiles of a chunk
@@ -87,14 +86,14 @@ struct Cfg {
     static constexpr int SCALE_OFF = V_OFF + NSLOT * SLOT_BYTES;  // two sets of
     static constexpr int SCALE_BYTES = NT * 2 * TK;                  // [tile][K 128 | V 128]
     static constexpr int BAR_OFF = SCALE_OFF + 2 * SCALE_BYTES;
-    static constexpr int NBARS = 4 * NSLOT + 4 + 2 + 4 + 2 + 2 + NDESC + LEAD + 2;
+    static constexpr int NBARS = 4 * NSLOT + 4 + 2 + 4 + 2 + 2 + 4 + NDESC + LEAD + 2;
     static constexpr int DESC_OFF = (BAR_OFF + NBARS * 8 + 8 + 15) / 16 * 16;
     static constexpr int XS_OFF = DESC_OFF + NDESC * 64;
     // per item buffer: four warps' row sums and the row maxima; per Q buffer the row factors;
     // the maxima exchanged within the softmax groups
     static constexpr int XS_FLOATS = 2 * (NQ + 1) * QR + 2 * QR + NQ * QR;
     static constexpr int MISC_OFF = XS_OFF + XS_FLOATS * 4;
-    static constexpr int MISC_INTS = (MAX_BATCH + 1) + 4 + 1;
+    static constexpr int MISC_INTS = (MAX_BATCH + 1) + 1;
     static constexpr size_t SMEM = 1024 + size_t(MISC_OFF) + MISC_INTS * 4;
     // K-major and MN-major rows of D bytes: the 128- or 64-byte swizzle, groups of 8 rows
     static constexpr uint32_t LAYOUT = D == 128 ? 2 : 4;
@@ -130,6 +129,14 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n, int a_mn, int b_
 }
 
 // RP consecutive columns of this warp's 32 lanes, with the wait.
+__device__ __forceinline__ void tmem_cols(uint32_t ta, uint32_t (&r)[4]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(ta)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_cols(uint32_t ta, uint32_t (&r)[8]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
@@ -142,9 +149,9 @@ __device__ __forceinline__ void tmem_cols(uint32_t ta, uint32_t (&r)[8]) {
 __device__ __forceinline__ void tmem_cols(uint32_t ta, uint32_t (&r)[16]) {
     tmem_load_32x32b_x16_sync(ta, r);
 }
-// Eight columns of each of a set's four S tiles (QR columns apart), with one wait.
-__device__ __forceinline__ void tmem_tiles(uint32_t ta, uint32_t (&r)[NT][RPW]) {
-    static_assert(NT == 4 && RPW == 8, "four loads of eight columns");
+// RPW columns of each of a set's four S tiles (QR columns apart), with one wait.
+__device__ __forceinline__ void tmem_tiles(uint32_t ta, uint32_t (&r)[NT][8]) {
+    static_assert(NT == 4, "four loads");
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%32];\n\t"
         "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%33];\n\t"
@@ -157,6 +164,19 @@ __device__ __forceinline__ void tmem_tiles(uint32_t ta, uint32_t (&r)[NT][RPW]) 
           "=r"(r[2][2]), "=r"(r[2][3]), "=r"(r[2][4]), "=r"(r[2][5]), "=r"(r[2][6]), "=r"(r[2][7]),
           "=r"(r[3][0]), "=r"(r[3][1]), "=r"(r[3][2]), "=r"(r[3][3]), "=r"(r[3][4]), "=r"(r[3][5]),
           "=r"(r[3][6]), "=r"(r[3][7])
+        : "r"(ta), "r"(ta + QR), "r"(ta + 2 * QR), "r"(ta + 3 * QR)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_tiles(uint32_t ta, uint32_t (&r)[NT][4]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%4, %5, %6, %7}, [%17];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%8, %9, %10, %11}, [%18];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%12, %13, %14, %15}, [%19];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0][0]), "=r"(r[0][1]), "=r"(r[0][2]), "=r"(r[0][3]), "=r"(r[1][0]), "=r"(r[1][1]),
+          "=r"(r[1][2]), "=r"(r[1][3]), "=r"(r[2][0]), "=r"(r[2][1]), "=r"(r[2][2]), "=r"(r[2][3]),
+          "=r"(r[3][0]), "=r"(r[3][1]), "=r"(r[3][2]), "=r"(r[3][3])
         : "r"(ta), "r"(ta + QR), "r"(ta + 2 * QR), "r"(ta + 3 * QR)
         : "memory");
 }
@@ -190,6 +210,17 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
 }
 __device__ __forceinline__ float2 e4m3x2_values(uint32_t c) {
     return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(c), __NV_E4M3)));
+}
+
+// The two e4m3 pieces of (a, b), both in [0, 2^8]: hi in the low half of the result, lo (times
+// kLoScale) in the high half.  By way of binary16, whose eleven bits lose 2^-11 of a value.
+__device__ __forceinline__ uint32_t split_p(float a, float b) {
+    const __half2 p = __floats2half2_rn(a, b);
+    const uint32_t hi = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(p), __NV_SATFINITE, __NV_E4M3);
+    const __half2 h(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(hi), __NV_E4M3));
+    const __half2 l = __hmul2(__hsub2(p, h), __float2half2_rn(kLoScale));  // exact
+    const uint32_t lo = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(l), __NV_SATFINITE, __NV_E4M3);
+    return hi | (lo << 16);
 }
 
 // 2^(s - 127) of an E8M0 byte (255: NaN), and its inverse (255: 1, its row is NaN anyway).
@@ -238,8 +269,12 @@ static_assert(sizeof(ItemSlot) == 64, "four 16-byte pieces");
 __device__ __forceinline__ int tiles_of(int npages) { return (npages + TPAGES - 1) / TPAGES; }
 
 // NWG softmax groups of RPW query rows.
-template <int D, int NWG>
-__global__ void __launch_bounds__((NQ * NWG + 9) * 32, 1)
+// softmax, epilogue, scheduler, K, V, S, P V, counter, one or two preparing warps
+template <int NWG>
+constexpr int kWarps = NQ * NWG + 4 + 6 + (NWG == 4 ? 2 : 1);
+
+template <int D, int RPW, int NWG>
+__global__ void __launch_bounds__(kWarps<NWG> * 32, 1)
 attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                const __grid_constant__ CUtensorMap tmap_v, const __nv_bfloat16* __restrict__ q,
                const uint8_t* __restrict__ k_scale, const uint8_t* __restrict__ v_scale,
@@ -253,8 +288,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
     constexpr int RP = RPW * NWG;
     constexpr int EPI = NQ * NWG;  // first epilogue warp (a multiple of 4: its lane quarter is 0)
     constexpr int SCHED = EPI + 4, K_WARP = EPI + 5, V_WARP = EPI + 6;
-    constexpr int S_WARP = EPI + 7, PV_WARP = EPI + 8;
-    constexpr int THREADS = (EPI + 9) * 32;
+    constexpr int S_WARP = EPI + 7, PV_WARP = EPI + 8, COUNTER = EPI + 9, PREP = EPI + 10;
+    constexpr int THREADS = kWarps<NWG> * 32;
+    constexpr int NPREP = kWarps<NWG> - PREP;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -275,7 +311,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
     uint64_t* o_empty = o_full + 2;     // ... and read out by the epilogue warps
     uint64_t* xs_bar = o_empty + 2;     // item k's row sums and maxima are in xs[k & 1]
     uint64_t* q_full = xs_bar + 2;      // item k's Q tile, row factors, scale bytes: set k & 1
-    uint64_t* d_full = q_full + 2;      // item k's descriptor is in items[k % NDESC]
+    uint64_t* st_bar = q_full + 2;      // item k's partials are stored by the epilogue warps
+    uint64_t* c_done = st_bar + 2;      // ... and counted
+    uint64_t* d_full = c_done + 2;      // item k's descriptor is in items[k % NDESC]
     uint64_t* d_used = d_full + NDESC;  // the K copies of item k are issued (k % LEAD)
     uint64_t* drain = d_used + LEAD;    // [2]: S issuer, P V issuer
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
@@ -284,8 +322,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
     float* q_fac = xs + 2 * (NQ + 1) * QR;                   // [2][QR]
     float* x_max = q_fac + 2 * QR;                           // [NQ][QR]
     int* prefix = reinterpret_cast<int*>(smem + C::MISC_OFF);  // [B + 1]
-    int* done = prefix + MAX_BATCH + 1;                      // [4]: epilogue warps per item
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(done + 4);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(prefix + MAX_BATCH + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = Hq / Hkv;
@@ -320,12 +357,13 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             mbar_init(&o_full[i], 1);
             mbar_init(&o_empty[i], 4);
             mbar_init(&xs_bar[i], NQ * NWG);
-            mbar_init(&q_full[i], 4);
+            mbar_init(&q_full[i], NPREP);
+            mbar_init(&st_bar[i], 4);
+            mbar_init(&c_done[i], 1);
             mbar_init(&drain[i], 1);
         }
         for (int i = 0; i < NDESC; ++i) mbar_init(&d_full[i], 1);
         for (int i = 0; i < LEAD; ++i) mbar_init(&d_used[i], 1);
-        for (int i = 0; i < 4; ++i) done[i] = 0;
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -389,8 +427,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // Finds this CTA's items and publishes them, at most LEAD ahead of the K copies.  Item
         // j takes the descriptor of item j - NDESC.  When the K copies of item x are issued,
         // the scores of item x - NSLOT at least are done, so the softmax has finished the item
-        // three before that, and the epilogue is at most two behind it: no reader is as far
-        // back as NDESC.
+        // three before that, the epilogue has read the O of the item two before that one, and
+        // the counter is at most two items behind it: no reader is as far back as NDESC.
         const int total = prefix[B];
         int w = blockIdx.x;
         for (int j = 0;; ++j) {
@@ -561,28 +599,32 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         if (elect_one()) tc_commit(&drain[1]);
         __syncwarp();
         mbar_wait(&drain[1], 0, nullptr, 100000000ull);
-    } else if (warp >= EPI) {
-        // ------------------------------------------------- Q split and epilogue
-        const int ew = warp - EPI;  // tensor-memory lane quarter
-        // Scale bytes of item k's keys (a key of each tile per thread), and its Q tile (rows 0
-        // .. RP-1; four neighbouring threads split one row).
-        auto split_q = [&](const Item& it, int k) {
-            constexpr int PER = D / 4;  // elements per thread
-            const int buf = k & 1;
-            const int key = ew * 32 + lane;
-            uint8_t ksc[NT], vsc[NT];
+    } else if (warp >= PREP) {
+        // ------------------------------------------------- scale bytes and Q of an item
+        // As soon as the softmax has read item k - 2's from the same buffers.
+        const int pw = warp - PREP;
+        for (int item = 0; ok; ++item) {
+            const Item it = item_at(item);
+            if (it.npages == 0) break;
+            const int buf = item & 1;
+            // scale bytes: 16 lanes read a page's 64 as words, K and V
+            uint32_t ks[NT / NPREP], vs[NT / NPREP];
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const int phys = items[k % NDESC].phys[i * TPAGES + key / PAGE];
-                ksc[i] = vsc[i] = 0;
+            for (int n = 0; n < NT / NPREP; ++n) {
+                const int phys = items[item % NDESC].phys[(n * NPREP + pw) * TPAGES + (lane >> 4)];
+                ks[n] = vs[n] = 0;
                 if (phys >= 0) {
-                    const int64_t at = (int64_t(phys) * Hkv + it.h) * PAGE + key % PAGE;
-                    ksc[i] = k_scale[at];
-                    vsc[i] = v_scale[at];
+                    const int64_t at = (int64_t(phys) * Hkv + it.h) * (PAGE / 4) + (lane & 15);
+                    ks[n] = reinterpret_cast<const uint32_t*>(k_scale)[at];
+                    vs[n] = reinterpret_cast<const uint32_t*>(v_scale)[at];
                 }
             }
-            const int r = ew * 8 + (lane >> 2), part = lane & 3;
-            if (ew * 8 < RP) {
+            bool free = false;
+#pragma unroll 1
+            for (int r0 = pw * 8; r0 < RP; r0 += NPREP * 8) {
+                // four neighbouring lanes split one query row
+                constexpr int PER = D / 4;  // elements per lane
+                const int r = r0 + (lane >> 2), part = lane & 3;
                 const int j = r / G;
                 uint4 v[PER / 8];
 #pragma unroll
@@ -607,6 +649,10 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 // s = 7 - floor(log2(amax)), held where 2^s and 2^-s are normal
                 const int s = max(-120, min(120, 134 - int(amax >> 7)));
                 const float mul = __uint_as_float(uint32_t(127 + s) << 23);
+                if (!free) {  // item k-2's scores are read, so its Q is no longer needed
+                    if (!wait(&s_empty[buf], (uint32_t(item >> 1) & 1u) ^ 1u)) break;
+                    free = true;
+                }
                 uint8_t* hi = sQ + buf * C::Q_BYTES;
                 uint8_t* lo = hi + C::Q_PIECE;
 #pragma unroll
@@ -635,77 +681,68 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     q_fac[buf * QR + r] =
                         amax >= 0x7f80u ? __int_as_float(0x7fc00000)
                                         : scale_log2 * __uint_as_float(uint32_t(127 - s) << 23);
-                fence_proxy_async_smem();
             }
-            uint8_t* sc = sScale + buf * C::SCALE_BYTES + key;
+            if (!ok) break;
+            if (!free && !wait(&s_empty[buf], (uint32_t(item >> 1) & 1u) ^ 1u)) break;
+            uint32_t* sc = reinterpret_cast<uint32_t*>(sScale + buf * C::SCALE_BYTES);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                sc[i * 2 * TK] = ksc[i];
-                sc[i * 2 * TK + TK] = vsc[i];
+            for (int n = 0; n < NT / NPREP; ++n) {
+                const int tile = n * NPREP + pw;
+                sc[tile * (2 * TK / 4) + lane] = ks[n];
+                sc[tile * (2 * TK / 4) + TK / 4 + lane] = vs[n];
             }
+            fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[buf]);
-        };
-        bool reset_done = cnt == nullptr;  // griddepcontrol.wait passed
-        // Item k's partial is counted by the last of the four warps to have stored its part
-        // (each releases its stores to the CTA; the last one's fence takes them to the GPU).
-        // done[k & 3] holds no other item's arrivals: a warp that counts item k has seen O of
-        // item k, so every warp has read O of item k - 2 and counted item k - 3.
-        auto count = [&](int k, int at) {
-            if (!cnt) return;
-            if (!reset_done) {
-                pdl_wait();
-                pdl_trigger();
-                reset_done = true;
-            }
-            __syncwarp();
-            if (lane == 0) {
-                int before;
-                asm volatile("atom.acq_rel.cta.shared::cta.add.s32 %0, [%1], 1;"
-                             : "=r"(before)
-                             : "r"(smem_addr(&done[k & 3]))
-                             : "memory");
-                if ((before & 3) == 3) {
-                    asm volatile("fence.acq_rel.gpu;" ::: "memory");
-                    atomicAdd(cnt + at, 1u);
-                }
-            }
-        };
-        // Items k and k + 1 have their Q split before O of item k is waited for; then O of
-        // item k is stored and the Q of item k + 2 split into the buffer that item k's scores
-        // no longer need.
-        Item it = item_at(0), nx;
-        nx.npages = 0;
-        if (it.npages > 0) {
-            split_q(it, 0);
-            nx = item_at(1);
-            if (nx.npages > 0) split_q(nx, 1);
         }
-        for (int item = 0; ok && it.npages > 0; ++item) {
+        if (!ok && lane == 0) give_up();
+    } else if (warp == COUNTER) {
+        // ----------------------------------------------------------------- counter
+        // Counts each stored item for its (sequence, KV head), which the merge waits on: the
+        // epilogue warps release their stores to the CTA, the fence takes them to the GPU.
+        if (cnt) {
+            pdl_wait();  // the counters are zeroed
+            pdl_trigger();
+            for (int item = 0; ok; ++item) {
+                const Item it = item_at(item);
+                if (it.npages == 0) break;
+                if (!wait(&st_bar[item & 1], uint32_t(item >> 1) & 1u)) break;
+                if (lane == 0) {
+                    asm volatile("fence.acq_rel.gpu;" ::: "memory");
+                    atomicAdd(cnt + it.b * Hkv + it.h, 1u);
+                    mbar_arrive(&c_done[item & 1]);
+                }
+                __syncwarp();
+            }
+            if (!ok && lane == 0) give_up();
+        }
+    } else if (warp >= EPI && warp < EPI + 4) {
+        // ------------------------------------------------------------------- epilogue
+        const int ew = warp - EPI;  // tensor-memory lane quarter
+        // O^T: lane = head dim (M = 128), or dims 16 ew .. 16 ew + 15 in lanes 0..15 (M = 64)
+        const int d = D == 128 ? ew * 32 + lane : ew * 16 + lane;
+        const bool mine = D == 128 || lane < 16;
+        for (int item = 0; ok; ++item) {
+            const Item it = item_at(item);
+            if (it.npages == 0) break;
             const int ob = item & 1;
             const uint32_t par = uint32_t(item >> 1) & 1u;
+            // rows (token j, head gg) are stored when their token sees the chunk; row r = lane's
+            // place among the partials, or -1
+            const int j = lane / G;
+            const int c = it.key0 >> CHUNK_LOG2;
+            const bool store = j < it.ntok && lane < TQ * G && it.pos0 + j >= it.key0;
+            const int64_t idx =
+                store ? (int64_t(it.t0 + j) * Hq + int64_t(it.h) * G + (lane - j * G)) * maxC + c
+                      : -1;
             if (!wait(&xs_bar[ob], par) || !wait(&o_full[ob], par)) break;
             tc_fence_after_sync();
-            // rows (token j, head gg) are stored when their token sees the chunk
-            const int rows = it.ntok * G;
-            const int first = max(0, it.key0 - it.pos0) * G;
-            const int c = it.key0 >> CHUNK_LOG2;
-            const int64_t row0 = int64_t(it.t0) * Hq + int64_t(it.h) * G;
-            if (ew == 0) {
-                const int r = lane, j = r / G;
-                if (r < rows && r >= first) {
-                    const float* x = xs + ob * ((NQ + 1) * QR);
-                    const float l = ((x[r] + x[QR + r]) + x[2 * QR + r]) + x[3 * QR + r];
-                    const int64_t idx = (row0 + int64_t(j) * (Hq - G) + r) * maxC + c;
-                    *reinterpret_cast<float2*>(ws_ml + idx * 2) = make_float2(x[NQ * QR + r], l);
-                }
+            if (ew == 0 && store) {
+                const float* x = xs + ob * ((NQ + 1) * QR);
+                const float l =
+                    ((x[lane] + x[QR + lane]) + x[2 * QR + lane]) + x[3 * QR + lane];
+                *reinterpret_cast<float2*>(ws_ml + idx * 2) = make_float2(x[NQ * QR + lane], l);
             }
-            // O^T: lane = head dim (M = 128), or dims 16 ew .. 16 ew + 15 in lanes 0..15 (M = 64)
-            const int d = D == 128 ? ew * 32 + lane : ew * 16 + lane;
-            const bool mine = D == 128 || lane < 16;
-            float* dst = ws_o + (row0 * maxC + c) * D + d;
-            const int64_t step = int64_t(maxC) * D, skip = step * (Hq - G);
-            int gg = 0;
             const uint32_t ta =
                 tmem_base + (uint32_t(32 * ew) << 16) + uint32_t(O_COL + ob * 2 * QR);
             constexpr int PART = RP < 16 ? RP : 16;
@@ -714,36 +751,25 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 uint32_t vh[PART], vl[PART];
                 tmem_cols(ta + r0, vh);
                 tmem_cols(ta + QR + r0, vl);
+                if (r0 + PART == RP) {  // O is read
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_empty[ob]);
+                }
 #pragma unroll
                 for (int k = 0; k < PART; ++k) {
-                    const int r = r0 + k;
-                    if (mine && r < rows && r >= first)
-                        *dst = fmaf(__uint_as_float(vl[k]), 1.f / kLoScale, __uint_as_float(vh[k]));
-                    dst += step;
-                    if (++gg == G) {
-                        gg = 0;
-                        dst += skip;
-                    }
+                    const int64_t at = __shfl_sync(0xffffffffu, idx, r0 + k);
+                    if (at >= 0 && mine)
+                        ws_o[at * D + d] =
+                            fmaf(__uint_as_float(vl[k]), 1.f / kLoScale, __uint_as_float(vh[k]));
                 }
             }
-            tc_fence_before_sync();
+            // (item-2 is counted: the counter never falls a phase of st_bar behind)
+            if (cnt && !wait(&c_done[ob], par ^ 1u)) break;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&o_empty[ob]);
-            const int at = it.b * Hkv + it.h;
-            it = nx;
-            nx.npages = 0;
-            if (it.npages > 0) {
-                nx = item_at(item + 2);
-                if (nx.npages > 0) split_q(nx, item + 2);
-            }
-            count(item, at);
+            if (lane == 0) mbar_arrive(&st_bar[ob]);
         }
         if (!ok && lane == 0) give_up();
-        // a CTA with no item (or one that gave up) still waits before it completes
-        if (!reset_done) {
-            pdl_wait();
-            pdl_trigger();
-        }
     } else {
         // ------------------------------------------------------------------- softmax
         // Group wg owns query rows wg * RPW .. of every tile; each thread one key.
@@ -796,17 +822,22 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
                 for (int r = 0; r < RPW; ++r)
                     t[i][r] = fmaf(__uint_as_float(sv[i][r]) * ka, f[r], vb);
-                // causal mask: row r (token r / G) sees the key when r / G >= kp - pos0
-                const int ahead = it.key0 + i * TK + key - it.pos0;
-                if (!__all_sync(0xffffffffu, ahead <= 0 && !((dead >> i) & 1u))) {
-                    const int first = (dead >> i) & 1u ? QR : max(0, ahead) * G;  // first row seeing it
+            }
+            // causal mask, unless every row sees the whole chunk: row r (token r / G) sees the
+            // key that is `ahead` of the first token when r / G >= ahead
+            if (!__all_sync(0xffffffffu, dead == 0 && it.key0 + CHUNK - 1 <= it.pos0)) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const int ahead = it.key0 + i * TK + key - it.pos0;
+                    const int first = (dead >> i) & 1u ? QR : max(0, ahead) * G;
 #pragma unroll
                     for (int r = 0; r < RPW; ++r)
                         t[i][r] = row0 + r >= first ? t[i][r] : -INFINITY;
                 }
-#pragma unroll
-                for (int r = 0; r < RPW; ++r) mx[r] = i == 0 ? t[i][r] : fmaxf(mx[r], t[i][r]);
             }
+#pragma unroll
+            for (int r = 0; r < RPW; ++r)
+                mx[r] = fmaxf(fmax3(t[0][r], t[1][r], t[2][r]), t[3][r]);
             // the rows' maxima over the group's four warps
             const float mine = combine_lanes<RPW, true>(mx, lane);
             if (lane % (32 / RPW) == 0) x_max[wq * QR + row0 + lane / (32 / RPW)] = mine;
@@ -834,9 +865,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             for (int r = 0; r < RPW; ++r) l[r] = 0.f;
             // P's buffers are free once P V of item-1 has completed
             wait(p_empty, (uint32_t(item) & 1u) ^ 1u);
+            uint8_t* pbuf = sP + (row0 & 15);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                if (i >= nt) continue;
+            for (int i = 0; i < NT; ++i) {  // (tiles past the item's last write zeros)
                 const float vi = (dead >> i) & 1u ? 0.f : e8m0_inv(vsc[i]);
                 uint32_t hi[RPW / 4], lo[RPW / 4];
 #pragma unroll
@@ -847,18 +878,19 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         p[k] = ex2(t[i][r + k] - m[r + k]);
                         l[r + k] = fmaf(p[k], vi, l[r + k]);
                     }
-                    const uint32_t c0 = e4m3x2(p[0], p[1]), c1 = e4m3x2(p[2], p[3]);
-                    const float2 b0 = e4m3x2_values(c0), b1 = e4m3x2_values(c1);
-                    hi[r / 4] = c0 | (c1 << 16);
-                    lo[r / 4] = e4m3x2((p[0] - b0.x) * kLoScale, (p[1] - b0.y) * kLoScale) |
-                                (e4m3x2((p[2] - b1.x) * kLoScale, (p[3] - b1.y) * kLoScale) << 16);
+                    const uint32_t a = split_p(p[0], p[1]), b = split_p(p[2], p[3]);
+                    hi[r / 4] = __byte_perm(a, b, 0x5410);
+                    lo[r / 4] = __byte_perm(a, b, 0x7632);
                 }
-                if (!ok) continue;  // (to the group's next common decision)
-                uint8_t* pbuf = sP + i * C::P_BYTES + (wg & 1) * 8;
-                *reinterpret_cast<uint2*>(pbuf + swz_row<64>(key, wg >> 1)) =
-                    make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2*>(pbuf + swz_row<64>(key, 2 + (wg >> 1))) =
-                    make_uint2(lo[0], lo[1]);
+                uint8_t* ph = pbuf + i * C::P_BYTES + swz_row<64>(key, row0 >> 4);
+                uint8_t* pl = pbuf + i * C::P_BYTES + swz_row<64>(key, 2 + (row0 >> 4));
+                if (RPW == 8) {
+                    *reinterpret_cast<uint2*>(ph) = make_uint2(hi[0], hi[RPW / 4 - 1]);
+                    *reinterpret_cast<uint2*>(pl) = make_uint2(lo[0], lo[RPW / 4 - 1]);
+                } else {
+                    *reinterpret_cast<uint32_t*>(ph) = hi[0];
+                    *reinterpret_cast<uint32_t*>(pl) = lo[0];
+                }
             }
             // V rows past the sequence's end or of an invalid page are zeroed, so that
             // unwritten codes (NaN) cannot reach O through 0 * v
@@ -903,7 +935,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
 }
 
-template <int D, int NWG>
+template <int D, int RPW, int NWG>
 cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a,
                         const void* k_scale, const void* v_scale, float scale, void* out,
                         float* lse, void* workspace, cudaStream_t stream) {
@@ -913,7 +945,7 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
     if (!tmap_2d_u8_swizzled(&tk, a.k_cache, D, rows, PAGE) ||
         !tmap_2d_u8_swizzled(&tv, a.v_cache, D, rows, PAGE))
         return cudaErrorNotSupported;
-    auto kern = attn_q8_kernel<D, NWG>;
+    auto kern = attn_q8_kernel<D, RPW, NWG>;
     static bool attr_done[64] = {};
     if (dev.device >= 0 && dev.device < 64 && !attr_done[dev.device]) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -938,7 +970,7 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
         if (e != cudaSuccess) return e;
     }
     cudaError_t e = launch_pdl(
-        kern, dim3(grid), dim3((NQ * NWG + 9) * 32), Cf::SMEM, stream, tk, tv,
+        kern, dim3(grid), dim3(kWarps<NWG> * 32), Cf::SMEM, stream, tk, tv,
         static_cast<const __nv_bfloat16*>(q), static_cast<const uint8_t*>(k_scale),
         static_cast<const uint8_t*>(v_scale), a.block_table, int(a.max_pages), int(a.num_pages),
         a.seq_lens, a.cu_q, int(a.batch), int(a.total_q), int(a.max_q), int(a.max_seq_len),
@@ -952,19 +984,21 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
 cudaError_t launch_attention_q8(const DeviceInfo& dev, const void* q, const PagedArgs& a,
                                 const void* k_scale, const void* v_scale, float scale, void* out,
                                 float* lse, void* workspace, cudaStream_t stream) {
-    // a softmax group for each 8 query rows of the fullest tile (one, two or four)
+    // softmax groups of four or eight query rows for those of the fullest tile
     const int64_t G = a.hq / a.hkv, TQ = QR / G;
     const int64_t rows = (a.max_q < TQ ? a.max_q : TQ) * G;
     auto run = [&](auto f) {
         return f(dev, q, a, k_scale, v_scale, scale, out, lse, workspace, stream);
     };
     if (a.head_dim == 64)
-        return run(rows <= 8    ? launch_q8_t<64, 1>
-                   : rows <= 16 ? launch_q8_t<64, 2>
-                                : launch_q8_t<64, 4>);
-    return run(rows <= 8    ? launch_q8_t<128, 1>
-               : rows <= 16 ? launch_q8_t<128, 2>
-                            : launch_q8_t<128, 4>);
+        return run(rows <= 4    ? launch_q8_t<64, 4, 1>
+                   : rows <= 8  ? launch_q8_t<64, 4, 2>
+                   : rows <= 16 ? launch_q8_t<64, 8, 2>
+                                : launch_q8_t<64, 8, 4>);
+    return run(rows <= 4    ? launch_q8_t<128, 4, 1>
+               : rows <= 8  ? launch_q8_t<128, 4, 2>
+               : rows <= 16 ? launch_q8_t<128, 8, 2>
+                            : launch_q8_t<128, 8, 4>);
 }
 
 }  // namespace bi
