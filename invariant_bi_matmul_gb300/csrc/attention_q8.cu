@@ -204,14 +204,6 @@ __device__ __forceinline__ float combine_lanes(const float (&v)[N], int lane) {
     }
 }
 
-// Two e4m3 codes of (a, b), a in the low byte; and the values they stand for.
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ float2 e4m3x2_values(uint32_t c) {
-    return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(c), __NV_E4M3)));
-}
-
 // The two e4m3 pieces of (a, b), both in [0, 2^8]: hi in the low half of the result, lo (times
 // kLoScale) in the high half.  By way of binary16, whose eleven bits lose 2^-11 of a value.
 __device__ __forceinline__ uint32_t split_p(float a, float b) {
@@ -220,6 +212,18 @@ __device__ __forceinline__ uint32_t split_p(float a, float b) {
     const __half2 h(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(hi), __NV_E4M3));
     const __half2 l = __hmul2(__hsub2(p, h), __float2half2_rn(kLoScale));  // exact
     const uint32_t lo = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(l), __NV_SATFINITE, __NV_E4M3);
+    return hi | (lo << 16);
+}
+
+// The two e4m3 pieces of two bf16 values times `mul`: hi in the low half of the result, lo in
+// the high half.  Binary16 holds the products (below 2^8) but for bits under 2^-24.
+__device__ __forceinline__ uint32_t split_q(uint32_t x, float mul) {
+    const __half2 p = __floats2half2_rn(__uint_as_float(x << 16) * mul,
+                                        __uint_as_float(x & 0xffff0000u) * mul);
+    const uint32_t hi = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(p), __NV_SATFINITE, __NV_E4M3);
+    const __half2 h(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(hi), __NV_E4M3));
+    const uint32_t lo =
+        __nv_cvt_halfraw2_to_fp8x2(__half2_raw(__hsub2(p, h)), __NV_SATFINITE, __NV_E4M3);
     return hi | (lo << 16);
 }
 
@@ -258,7 +262,7 @@ struct alignas(16) Item {
     int t0;      // its row in q and out
     int ntok;    // the tile's tokens
     int h;
-    int b;
+    int bq;      // 2 * b + the buffer of its Q tile
 };
 struct alignas(16) ItemSlot {
     Item it;
@@ -281,7 +285,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                const int32_t* __restrict__ block_table, int max_pages, int num_pages,
                const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ cu_q, int B,
                int total_q, int max_q, int max_seq_len, int Hq, int Hkv, float scale_log2,
-               float* __restrict__ ws_o, float* __restrict__ ws_ml, int maxC,
+               float* __restrict__ ws_o, float* __restrict__ ws_ml, int maxC, int run,
                unsigned int* __restrict__ cnt, unsigned int* err) {
     using C = Cfg<D>;
     constexpr int NSLOT = C::NSLOT;
@@ -310,7 +314,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
     uint64_t* o_full = p_empty + 1;     // item k's O (buffer k & 1) is complete (MMA commit)
     uint64_t* o_empty = o_full + 2;     // ... and read out by the epilogue warps
     uint64_t* xs_bar = o_empty + 2;     // item k's row sums and maxima are in xs[k & 1]
-    uint64_t* q_full = xs_bar + 2;      // item k's Q tile, row factors, scale bytes: set k & 1
+    uint64_t* q_full = xs_bar + 2;      // item k's scale bytes (set k & 1) and its Q are there
     uint64_t* st_bar = q_full + 2;      // item k's partials are stored by the epilogue warps
     uint64_t* c_done = st_bar + 2;      // ... and counted
     uint64_t* d_full = c_done + 2;      // item k's descriptor is in items[k % NDESC]
@@ -371,7 +375,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const SeqInfo si = seq_info(seq_lens, cu_q, b);
         const bool ok = seq_ok(si, max_q, max_seq_len, total_q);
         if (!ok) latch_error(err, kErrDeviceArg);
-        prefix[b + 1] = ok ? ((si.L + CHUNK - 1) >> CHUNK_LOG2) * ((si.qb + TQ - 1) / TQ) * Hkv : 0;
+        // units: runs of up to `run` chunks of one query tile and KV head
+        const int chunks = (si.L + CHUNK - 1) >> CHUNK_LOG2;
+        prefix[b + 1] = ok ? ((chunks + run - 1) / run) * ((si.qb + TQ - 1) / TQ) * Hkv : 0;
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -429,39 +435,54 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // the scores of item x - NSLOT at least are done, so the softmax has finished the item
         // three before that, the epilogue has read the O of the item two before that one, and
         // the counter is at most two items behind it: no reader is as far back as NDESC.
+        // A unit's chunks follow one another, so they share a Q tile, which is split once.
         const int total = prefix[B];
-        int w = blockIdx.x;
+        int w = blockIdx.x, b = 0, left = 0, qgen = 0, last_t0 = -1, last_h = -1;
+        Item it;
         for (int j = 0;; ++j) {
             if (!wait(&d_used[j % LEAD], (uint32_t(j / LEAD) & 1u) ^ 1u)) break;
-            Item it;
-            it.npages = 0;
-            for (; w < total && it.npages == 0; w += gridDim.x) {
-                int lo = 0, hi = B;
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (prefix[mid] <= w) lo = mid; else hi = mid;
+            if (left > 0) {  // the unit's next chunk
+                it.key0 += CHUNK;
+            } else {         // the next unit that has a chunk its tile sees
+                for (; w < total && left == 0; w += gridDim.x) {
+                    int lo = 0, hi = B;
+                    while (hi - lo > 1) {
+                        const int mid = (lo + hi) >> 1;
+                        if (prefix[mid] <= w) lo = mid; else hi = mid;
+                    }
+                    b = lo;
+                    const SeqInfo si = seq_info(seq_lens, cu_q, lo);
+                    const int U = (si.qb + TQ - 1) / TQ;
+                    const int r = w - prefix[lo];
+                    const int cu = r / Hkv;
+                    const int c = cu / U, u = cu - c * U;
+                    it.h = r - cu * Hkv;
+                    it.L = si.L;
+                    it.key0 = c * run * CHUNK;
+                    it.t0 = si.t0 + u * TQ;
+                    it.ntok = min(TQ, si.qb - u * TQ);
+                    it.pos0 = si.L - si.qb + u * TQ;
+                    const int keys = it.pos0 + it.ntok - it.key0;
+                    left = keys <= 0 ? 0 : min(run, (keys + CHUNK - 1) >> CHUNK_LOG2);
                 }
-                const SeqInfo si = seq_info(seq_lens, cu_q, lo);
-                const int U = (si.qb + TQ - 1) / TQ;
-                const int r = w - prefix[lo];
-                const int cu = r / Hkv;
-                const int c = cu / U, u = cu - c * U;
-                it.b = lo;
-                it.h = r - cu * Hkv;
-                it.L = si.L;
-                it.key0 = c * CHUNK;
-                it.t0 = si.t0 + u * TQ;
-                it.ntok = min(TQ, si.qb - u * TQ);
-                it.pos0 = si.L - si.qb + u * TQ;
-                const int seen = it.pos0 + it.ntok - it.key0;
-                it.npages = seen <= 0 ? 0 : min(CHUNK / PAGE, (seen + PAGE - 1) / PAGE);
+                if (left > 0 && (it.t0 != last_t0 || it.h != last_h)) {
+                    ++qgen;
+                    last_t0 = it.t0;
+                    last_h = it.h;
+                }
+            }
+            it.bq = 2 * b + (qgen & 1);
+            it.npages = 0;
+            if (left > 0) {
+                it.npages = min(CHUNK / PAGE, (it.pos0 + it.ntok - it.key0 + PAGE - 1) / PAGE);
+                --left;
             }
             ItemSlot* slot = &items[j % NDESC];
             if (lane < CHUNK / PAGE) {
                 int phys = -1;
                 if (lane < it.npages) {
                     const int pidx = it.key0 / PAGE + lane;
-                    if (pidx < max_pages) phys = block_table[int64_t(it.b) * max_pages + pidx];
+                    if (pidx < max_pages) phys = block_table[int64_t(b) * max_pages + pidx];
                     if (phys < 0 || phys >= num_pages) {
                         phys = -1;
                         latch_error(err, kErrDeviceArg);
@@ -531,9 +552,10 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const uint64_t k_desc0 = umma_smem_desc(smem_addr(sK), 16, C::SBO, C::LAYOUT);
         uint32_t g = 0;
         for (int item = 0; ok; ++item) {
-            const int nt = tiles_of(item_at(item).npages);
+            const Item it = item_at(item);
+            const int nt = tiles_of(it.npages);
             if (nt == 0) break;
-            const int buf = item & 1;
+            const int buf = item & 1, qbuf = it.bq & 1;
             const uint32_t par = uint32_t(item >> 1) & 1u;
             if (!wait(&q_full[buf], par) || !wait(&s_empty[buf], par ^ 1u)) break;
             for (int i = 0; i < nt; ++i, ++g) {
@@ -541,7 +563,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 tc_fence_after_sync();
                 if (elect_one()) {
                     const uint64_t k_desc = k_desc0 + uint64_t(((g % NSLOT) * C::SLOT_BYTES) >> 4);
-                    const uint64_t q_desc = q_desc0 + uint64_t((buf * C::Q_BYTES) >> 4);
+                    const uint64_t q_desc = q_desc0 + uint64_t((qbuf * C::Q_BYTES) >> 4);
                     const uint32_t d = tmem_base + uint32_t(S_COL + (buf * NT + i) * QR);
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k) {  // head dims 32k .. 32k+31: +32 B
@@ -603,10 +625,11 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // ------------------------------------------------- scale bytes and Q of an item
         // As soon as the softmax has read item k - 2's from the same buffers.
         const int pw = warp - PREP;
+        int last_q = -1;
         for (int item = 0; ok; ++item) {
             const Item it = item_at(item);
             if (it.npages == 0) break;
-            const int buf = item & 1;
+            const int buf = item & 1, qbuf = it.bq & 1;
             // scale bytes: 16 lanes read a page's 64 as words, K and V
             uint32_t ks[NT / NPREP], vs[NT / NPREP];
 #pragma unroll
@@ -620,8 +643,10 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
             }
             bool free = false;
+            const int rows = qbuf != last_q ? RP : 0;  // (else the item before has this Q tile)
+            last_q = qbuf;
 #pragma unroll 1
-            for (int r0 = pw * 8; r0 < RP; r0 += NPREP * 8) {
+            for (int r0 = pw * 8; r0 < rows; r0 += NPREP * 8) {
                 // four neighbouring lanes split one query row
                 constexpr int PER = D / 4;  // elements per lane
                 const int r = r0 + (lane >> 2), part = lane & 3;
@@ -649,11 +674,12 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 // s = 7 - floor(log2(amax)), held where 2^s and 2^-s are normal
                 const int s = max(-120, min(120, 134 - int(amax >> 7)));
                 const float mul = __uint_as_float(uint32_t(127 + s) << 23);
-                if (!free) {  // item k-2's scores are read, so its Q is no longer needed
+                // item k-2's scores are read: the Q before the last, in this buffer, is not needed
+                if (!free) {
                     if (!wait(&s_empty[buf], (uint32_t(item >> 1) & 1u) ^ 1u)) break;
                     free = true;
                 }
-                uint8_t* hi = sQ + buf * C::Q_BYTES;
+                uint8_t* hi = sQ + qbuf * C::Q_BYTES;
                 uint8_t* lo = hi + C::Q_PIECE;
 #pragma unroll
                 for (int n = 0; n < PER / 16; ++n) {
@@ -662,15 +688,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     for (int e = 0; e < 4; ++e) {
                         const uint4& src = v[2 * n + (e >> 1)];
                         const uint32_t x0 = e & 1 ? src.z : src.x, x1 = e & 1 ? src.w : src.y;
-                        const float f[4] = {__uint_as_float(x0 << 16) * mul,
-                                            __uint_as_float(x0 & 0xffff0000u) * mul,
-                                            __uint_as_float(x1 << 16) * mul,
-                                            __uint_as_float(x1 & 0xffff0000u) * mul};
-                        const uint32_t c0 = e4m3x2(f[0], f[1]), c1 = e4m3x2(f[2], f[3]);
-                        const float2 b0 = e4m3x2_values(c0), b1 = e4m3x2_values(c1);
-                        h[e] = c0 | (c1 << 16);
-                        l[e] = e4m3x2(f[0] - b0.x, f[1] - b0.y) |
-                               (e4m3x2(f[2] - b1.x, f[3] - b1.y) << 16);
+                        const uint32_t a = split_q(x0, mul), b = split_q(x1, mul);
+                        h[e] = __byte_perm(a, b, 0x5410);
+                        l[e] = __byte_perm(a, b, 0x7632);
                     }
                     const uint32_t at = swz_row<D>(r, part * (PER / 16) + n);
                     *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
@@ -678,7 +698,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
                 // a query with an infinity or NaN scores NaN throughout
                 if (part == 0)
-                    q_fac[buf * QR + r] =
+                    q_fac[qbuf * QR + r] =
                         amax >= 0x7f80u ? __int_as_float(0x7fc00000)
                                         : scale_log2 * __uint_as_float(uint32_t(127 - s) << 23);
             }
@@ -709,7 +729,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 if (!wait(&st_bar[item & 1], uint32_t(item >> 1) & 1u)) break;
                 if (lane == 0) {
                     asm volatile("fence.acq_rel.gpu;" ::: "memory");
-                    atomicAdd(cnt + it.b * Hkv + it.h, 1u);
+                    atomicAdd(cnt + (it.bq >> 1) * Hkv + it.h, 1u);
                     mbar_arrive(&c_done[item & 1]);
                 }
                 __syncwarp();
@@ -789,7 +809,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             float f[RPW];
 #pragma unroll
             for (int r = 0; r < RPW; r += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(q_fac + ob * QR + row0 + r);
+                const float4 x = *reinterpret_cast<const float4*>(q_fac + (it.bq & 1) * QR + row0 + r);
                 f[r] = x.x;
                 f[r + 1] = x.y;
                 f[r + 2] = x.z;
@@ -959,6 +979,13 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
     const int64_t items_bound = a.batch * int64_t(maxC) * tiles * a.hkv;
     if (items_bound > 0x7fffffffLL - dev.num_sms) return cudaErrorNotSupported;
     const int grid = int(items_bound < dev.num_sms ? items_bound : dev.num_sms);
+    // Chunks of a unit (consecutive items of a CTA with one Q tile, split once): as many as
+    // leave each CTA eight units or more, so that the dealing stays even.  Wide blocks of
+    // 2,048 tokens take @@RUN1@@ us with runs and @@RUN0@@ without.
+    int run = 1;
+    while (run < 8 && a.batch * ((maxC + 2 * run - 1) / (2 * run)) * tiles * a.hkv >=
+                          8 * int64_t(dev.num_sms))
+        run *= 2;
     float* ws_o = static_cast<float*>(workspace);
     float* ws_ml = ws_o + a.total_q * a.hq * int64_t(maxC) * D;
     // one query tile per sequence: the merge of a (sequence, KV head) starts when its chunks
@@ -974,7 +1001,7 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
         static_cast<const __nv_bfloat16*>(q), static_cast<const uint8_t*>(k_scale),
         static_cast<const uint8_t*>(v_scale), a.block_table, int(a.max_pages), int(a.num_pages),
         a.seq_lens, a.cu_q, int(a.batch), int(a.total_q), int(a.max_q), int(a.max_seq_len),
-        int(a.hq), int(a.hkv), scale * kLog2e, ws_o, ws_ml, maxC, cnt, dev.err_word);
+        int(a.hq), int(a.hkv), scale * kLog2e, ws_o, ws_ml, maxC, run, cnt, dev.err_word);
     if (e != cudaSuccess) return e;
     return launch_attn_merge(a, workspace, CHUNK_LOG2, out, lse, cnt, dev.err_word, stream);
 }
