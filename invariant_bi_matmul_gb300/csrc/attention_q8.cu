@@ -63,7 +63,7 @@ constexpr int NT = CHUNK / TK;            // tiles of a chunk
 constexpr int TMEM_COLS = 512;
 constexpr int S_COL = 0;                  // two S sets (by item) of NT tiles, 32 columns each
 constexpr int O_COL = 2 * NT * QR;          // O buffers (by item): 32 hi + 32 lo columns each
-constexpr float kNoMax = -1e30f;          // m of a row that sees no key of the chunk
+constexpr float kHidden = -1e30f;         // t of a key that a row does not see
 constexpr float kHeadroom = 8.f;          // p = 2^8 at the row's maximum (e4m3 holds 448)
 constexpr float kLoScale = 32.f;          // the second piece of p (at most 8) times this
 constexpr int MAX_BATCH = BI_ATTN_MAX_BATCH;
@@ -86,12 +86,12 @@ struct Cfg {
     static constexpr int SCALE_OFF = V_OFF + NSLOT * SLOT_BYTES;  // two sets of
     static constexpr int SCALE_BYTES = NT * 2 * TK;                  // [tile][K 128 | V 128]
     static constexpr int BAR_OFF = SCALE_OFF + 2 * SCALE_BYTES;
-    static constexpr int NBARS = 4 * NSLOT + 4 + 2 + 4 + 2 + 2 + 4 + NDESC + LEAD + 2;
+    static constexpr int NBARS = 4 * NSLOT + 4 + 2 + 4 + 4 + 2 + 4 + NDESC + LEAD + 2;
     static constexpr int DESC_OFF = (BAR_OFF + NBARS * 8 + 8 + 15) / 16 * 16;
     static constexpr int XS_OFF = DESC_OFF + NDESC * 64;
-    // per item buffer: four warps' row sums and the row maxima; per Q buffer the row factors;
-    // the maxima exchanged within the softmax groups
-    static constexpr int XS_FLOATS = 2 * (NQ + 1) * QR + 2 * QR + NQ * QR;
+    // per item (four buffers): four warps' row sums and the row maxima; per Q buffer the row factors;
+    // the maxima exchanged within the softmax groups (two buffers: a warp may be an item ahead)
+    static constexpr int XS_FLOATS = 4 * (NQ + 1) * QR + 2 * QR + 2 * NQ * QR;
     static constexpr int MISC_OFF = XS_OFF + XS_FLOATS * 4;
     static constexpr int MISC_INTS = (MAX_BATCH + 1) + 1;
     static constexpr size_t SMEM = 1024 + size_t(MISC_OFF) + MISC_INTS * 4;
@@ -181,27 +181,62 @@ __device__ __forceinline__ void tmem_tiles(uint32_t ta, uint32_t (&r)[NT][4]) {
         : "memory");
 }
 
-// Combines v[r] over the 32 lanes for each of N rows (max, or a sum over a fixed tree: lanes
-// that differ in bit 4, then bit 3, .. bit 0 -- the same for every N).  Every lane gets row
-// lane * N / 32: at each step a lane keeps one half of its rows while it has several.
-template <int N, bool MAX, int OFF = 16>
-__device__ __forceinline__ float combine_lanes(const float (&v)[N], int lane) {
-    auto op = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+// The sum of v[r] over the 32 lanes for each of N rows, over a fixed tree: lanes that differ in
+// bit 4, then bit 3, .. bit 0 -- the same for every N.  Every lane gets row lane * N / 32: at
+// each step a lane keeps one half of its rows while it has several.
+template <int N, int OFF = 16>
+__device__ __forceinline__ float sum_lanes(const float (&v)[N], int lane) {
     if constexpr (OFF == 0) {
         return v[0];
     } else if constexpr (N == 1) {
-        const float w[1] = {op(v[0], __shfl_xor_sync(0xffffffffu, v[0], OFF))};
-        return combine_lanes<1, MAX, OFF / 2>(w, lane);
+        const float w[1] = {v[0] + __shfl_xor_sync(0xffffffffu, v[0], OFF)};
+        return sum_lanes<1, OFF / 2>(w, lane);
     } else {
         const bool up = (lane & OFF) != 0;
         float w[N / 2];
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
             const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + N / 2], OFF);
-            w[i] = op(up ? v[i + N / 2] : v[i], got);
+            w[i] = (up ? v[i + N / 2] : v[i]) + got;
         }
-        return combine_lanes<N / 2, MAX, OFF / 2>(w, lane);
+        return sum_lanes<N / 2, OFF / 2>(w, lane);
     }
+}
+
+// Two fp32 operations in one instruction, each rounded as its scalar form.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// The largest of 32 lanes' values (a NaN is ignored beside a number).
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 // The two e4m3 pieces of (a, b), both in [0, 2^8]: hi in the low half of the result, lo (times
@@ -313,8 +348,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
     uint64_t* p_empty = p_full + 1;     // P V of item k has completed (MMA commit)
     uint64_t* o_full = p_empty + 1;     // item k's O (buffer k & 1) is complete (MMA commit)
     uint64_t* o_empty = o_full + 2;     // ... and read out by the epilogue warps
-    uint64_t* xs_bar = o_empty + 2;     // item k's row sums and maxima are in xs[k & 1]
-    uint64_t* q_full = xs_bar + 2;      // item k's scale bytes (set k & 1) and its Q are there
+    uint64_t* xs_bar = o_empty + 2;     // item k's row sums and maxima are in xs[k & 3]
+    uint64_t* q_full = xs_bar + 4;      // item k's scale bytes (set k & 1) and its Q are there
     uint64_t* st_bar = q_full + 2;      // item k's partials are stored by the epilogue warps
     uint64_t* c_done = st_bar + 2;      // ... and counted
     uint64_t* d_full = c_done + 2;      // item k's descriptor is in items[k % NDESC]
@@ -322,9 +357,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
     uint64_t* drain = d_used + LEAD;    // [2]: S issuer, P V issuer
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
     ItemSlot* items = reinterpret_cast<ItemSlot*>(smem + C::DESC_OFF);
-    float* xs = reinterpret_cast<float*>(smem + C::XS_OFF);  // [2][NQ + 1][QR]
-    float* q_fac = xs + 2 * (NQ + 1) * QR;                   // [2][QR]
-    float* x_max = q_fac + 2 * QR;                           // [NQ][QR]
+    float* xs = reinterpret_cast<float*>(smem + C::XS_OFF);  // [4][NQ + 1][QR]
+    float* q_fac = xs + 4 * (NQ + 1) * QR;                   // [2][QR]
+    float* x_max = q_fac + 2 * QR;                           // [2][NQ][QR]
     int* prefix = reinterpret_cast<int*>(smem + C::MISC_OFF);  // [B + 1]
     volatile int* abort_flag = reinterpret_cast<volatile int*>(prefix + MAX_BATCH + 1);
 
@@ -360,7 +395,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         for (int i = 0; i < 2; ++i) {
             mbar_init(&o_full[i], 1);
             mbar_init(&o_empty[i], 4);
-            mbar_init(&xs_bar[i], NQ * NWG);
+            mbar_init(&xs_bar[2 * i], NQ * NWG);
+            mbar_init(&xs_bar[2 * i + 1], NQ * NWG);
             mbar_init(&q_full[i], NPREP);
             mbar_init(&st_bar[i], 4);
             mbar_init(&c_done[i], 1);
@@ -755,10 +791,10 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const int64_t idx =
                 store ? (int64_t(it.t0 + j) * Hq + int64_t(it.h) * G + (lane - j * G)) * maxC + c
                       : -1;
-            if (!wait(&xs_bar[ob], par) || !wait(&o_full[ob], par)) break;
+            if (!wait(&xs_bar[item & 3], uint32_t(item >> 2) & 1u) || !wait(&o_full[ob], par)) break;
             tc_fence_after_sync();
             if (ew == 0 && store) {
-                const float* x = xs + ob * ((NQ + 1) * QR);
+                const float* x = xs + (item & 3) * ((NQ + 1) * QR);
                 const float l =
                     ((x[lane] + x[QR + lane]) + x[2 * QR + lane]) + x[3 * QR + lane];
                 *reinterpret_cast<float2*>(ws_ml + idx * 2) = make_float2(x[NQ * QR + lane], l);
@@ -803,17 +839,19 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const uint32_t ipar = uint32_t(item >> 1) & 1u;
             const Item it = item_at(item);
             if (it.npages > 0) wait(&q_full[ob], ipar);
-            if (!ok && lane == 0) give_up();
-            if (group_or(1 + wg, !ok) || it.npages == 0) break;
+            if (it.npages == 0) {  // no more items, or this warp gave up: one barrier either way
+                if (!ok && lane == 0) give_up();
+                if (group_or(1 + wg, !ok)) ok = false;
+                break;
+            }
             const int nt = tiles_of(it.npages);
-            float f[RPW];
+            float2 f[RPW / 2];
 #pragma unroll
             for (int r = 0; r < RPW; r += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(q_fac + (it.bq & 1) * QR + row0 + r);
-                f[r] = x.x;
-                f[r + 1] = x.y;
-                f[r + 2] = x.z;
-                f[r + 3] = x.w;
+                const float4 x =
+                    *reinterpret_cast<const float4*>(q_fac + (it.bq & 1) * QR + row0 + r);
+                f[r / 2] = make_float2(x.x, x.y);
+                f[r / 2 + 1] = make_float2(x.z, x.w);
             }
             // t of this thread's keys (one of each tile), and each row's maximum
             const uint8_t* sc = sScale + ob * C::SCALE_BYTES + key;
@@ -840,8 +878,14 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const float vb =
                     vsc[i] == 255 ? __int_as_float(0x7fc00000) : float(int(vsc[i]) - 127);
 #pragma unroll
-                for (int r = 0; r < RPW; ++r)
-                    t[i][r] = fmaf(__uint_as_float(sv[i][r]) * ka, f[r], vb);
+                for (int r = 0; r < RPW; r += 2) {
+                    const float2 s2 = make_float2(__uint_as_float(sv[i][r]),
+                                                  __uint_as_float(sv[i][r + 1]));
+                    const float2 x = fma2(mul2(s2, make_float2(ka, ka)), f[r / 2],
+                                          make_float2(vb, vb));
+                    t[i][r] = x.x;
+                    t[i][r + 1] = x.y;
+                }
             }
             // causal mask, unless every row sees the whole chunk: row r (token r / G) sees the
             // key that is `ahead` of the first token when r / G >= ahead
@@ -852,16 +896,23 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const int first = (dead >> i) & 1u ? QR : max(0, ahead) * G;
 #pragma unroll
                     for (int r = 0; r < RPW; ++r)
-                        t[i][r] = row0 + r >= first ? t[i][r] : -INFINITY;
+                        t[i][r] = row0 + r >= first ? t[i][r] : kHidden;
                 }
             }
 #pragma unroll
             for (int r = 0; r < RPW; ++r)
                 mx[r] = fmaxf(fmax3(t[0][r], t[1][r], t[2][r]), t[3][r]);
             // the rows' maxima over the group's four warps
-            const float mine = combine_lanes<RPW, true>(mx, lane);
-            if (lane % (32 / RPW) == 0) x_max[wq * QR + row0 + lane / (32 / RPW)] = mine;
-            if (!ok && lane == 0) give_up();
+#pragma unroll
+            for (int r = 0; r < RPW; ++r) mx[r] = warp_max(mx[r]);
+            float* xm = x_max + ob * (NQ * QR) + row0;
+            if (lane == 0) {
+#pragma unroll
+                for (int r = 0; r < RPW; r += 4)
+                    *reinterpret_cast<float4*>(xm + wq * QR + r) =
+                        make_float4(mx[r], mx[r + 1], mx[r + 2], mx[r + 3]);
+                if (!ok) give_up();
+            }
             if (group_or(1 + wg, !ok)) {
                 ok = false;
                 break;
@@ -869,17 +920,14 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             float m[RPW], l[RPW];
 #pragma unroll
             for (int r = 0; r < RPW; r += 4) {
-                float4 x = *reinterpret_cast<const float4*>(x_max + row0 + r);
-#pragma unroll
-                for (int n = 1; n < NQ; ++n) {
-                    const float4 y = *reinterpret_cast<const float4*>(x_max + n * QR + row0 + r);
-                    x = make_float4(fmaxf(x.x, y.x), fmaxf(x.y, y.y), fmaxf(x.z, y.z),
-                                    fmaxf(x.w, y.w));
-                }
-                m[r] = fmaxf(x.x - kHeadroom, kNoMax);
-                m[r + 1] = fmaxf(x.y - kHeadroom, kNoMax);
-                m[r + 2] = fmaxf(x.z - kHeadroom, kNoMax);
-                m[r + 3] = fmaxf(x.w - kHeadroom, kNoMax);
+                const float4 x0 = *reinterpret_cast<const float4*>(xm + 0 * QR + r);
+                const float4 x1 = *reinterpret_cast<const float4*>(xm + 1 * QR + r);
+                const float4 x2 = *reinterpret_cast<const float4*>(xm + 2 * QR + r);
+                const float4 x3 = *reinterpret_cast<const float4*>(xm + 3 * QR + r);
+                m[r] = fmaxf(fmax3(x0.x, x1.x, x2.x), x3.x) - kHeadroom;
+                m[r + 1] = fmaxf(fmax3(x0.y, x1.y, x2.y), x3.y) - kHeadroom;
+                m[r + 2] = fmaxf(fmax3(x0.z, x1.z, x2.z), x3.z) - kHeadroom;
+                m[r + 3] = fmaxf(fmax3(x0.w, x1.w, x2.w), x3.w) - kHeadroom;
             }
 #pragma unroll
             for (int r = 0; r < RPW; ++r) l[r] = 0.f;
@@ -894,9 +942,15 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 for (int r = 0; r < RPW; r += 4) {
                     float p[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        p[k] = ex2(t[i][r + k] - m[r + k]);
-                        l[r + k] = fmaf(p[k], vi, l[r + k]);
+                    for (int k = 0; k < 4; k += 2) {
+                        const float2 e = add2(make_float2(t[i][r + k], t[i][r + k + 1]),
+                                              make_float2(-m[r + k], -m[r + k + 1]));
+                        p[k] = ex2(e.x);
+                        p[k + 1] = ex2(e.y);
+                        const float2 s2 = fma2(make_float2(p[k], p[k + 1]), make_float2(vi, vi),
+                                               make_float2(l[r + k], l[r + k + 1]));
+                        l[r + k] = s2.x;
+                        l[r + k + 1] = s2.y;
                     }
                     const uint32_t a = split_p(p[0], p[1]), b = split_p(p[2], p[3]);
                     hi[r / 4] = __byte_perm(a, b, 0x5410);
@@ -928,19 +982,21 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             fence_proxy_async_smem();
             __syncwarp();
             if (ok && lane == 0) mbar_arrive(p_full);
-            // the warp's row sums (and the maxima) for the epilogue, once it has read this
-            // buffer's previous contents (item-2)
-            const float sum = combine_lanes<RPW, false>(l, lane);
-            wait(&o_empty[ob], ipar ^ 1u);
+            // the warp's row sums (and the maxima) for the epilogue.  The buffer held those of
+            // item-4, and the barrier its phase: P V of item-1 has completed, so that of item-2
+            // has begun, for which the epilogue had read O and the sums of item-4.
+            const float sum = sum_lanes<RPW>(l, lane);
             if (ok) {
-                float* x = xs + ob * ((NQ + 1) * QR) + row0;
+                float* x = xs + (item & 3) * ((NQ + 1) * QR) + row0;
                 if (wq == 0 && lane == 0) {
 #pragma unroll
-                    for (int r = 0; r < RPW; ++r) x[NQ * QR + r] = m[r];
+                    for (int r = 0; r < RPW; r += 4)
+                        *reinterpret_cast<float4*>(x + NQ * QR + r) =
+                            make_float4(m[r], m[r + 1], m[r + 2], m[r + 3]);
                 }
                 if (lane % (32 / RPW) == 0) x[wq * QR + lane / (32 / RPW)] = sum;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&xs_bar[ob]);
+                if (lane == 0) mbar_arrive(&xs_bar[item & 3]);
             }
             g += uint32_t(nt);
         }
@@ -980,10 +1036,13 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
     if (items_bound > 0x7fffffffLL - dev.num_sms) return cudaErrorNotSupported;
     const int grid = int(items_bound < dev.num_sms ? items_bound : dev.num_sms);
     // Chunks of a unit (consecutive items of a CTA with one Q tile, split once): as many as
-    // leave each CTA eight units or more, so that the dealing stays even.  Wide blocks of
-    // 2,048 tokens take @@RUN1@@ us with runs and @@RUN0@@ without.
+    // leave each CTA eight units or more, so that the dealing stays even -- where the items'
+    // turn-around is what binds (64 sequences of 8,196 keys, blocks of 8: 303 us with runs, 330
+    // without; one-token blocks at head_dim 64, 16,388 keys: 205 and 245).  One-token blocks at
+    // head_dim 128 are bound by memory and keep the finer dealing (ragged batch of 64: 231 us
+    // without, 235 to 240 with).
     int run = 1;
-    while (run < 8 && a.batch * ((maxC + 2 * run - 1) / (2 * run)) * tiles * a.hkv >=
+    while (run < 8 && (D == 64 || RPW * NWG > 4) && a.batch * ((maxC + 2 * run - 1) / (2 * run)) * tiles * a.hkv >=
                           8 * int64_t(dev.num_sms))
         run *= 2;
     float* ws_o = static_cast<float*>(workspace);

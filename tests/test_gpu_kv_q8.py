@@ -340,6 +340,39 @@ def test_long_contexts(dev, L, qs):
     check_rows_rel_l2(out, r[0])
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,qs", [(128, 32, 8, 1), (128, 32, 8, 8), (64, 8, 8, 3),
+                                         (128, 16, 4, 4), (64, 8, 8, 1), (128, 8, 8, 7)])
+def test_more_work_items_than_multiprocessors(dev, D, Hq, Hkv, qs):
+    """Batches whose chunks give every multiprocessor many items in turn (the hand-offs between
+    the kernel's warps wrap around many times), with short and long sequences: each sequence's
+    bits alone, and two of them against 64 bits."""
+    g = torch.Generator().manual_seed(qs)
+    B = 96
+    lens = [int(x) for x in torch.randint(qs, 2600, (B,), generator=g)]
+    lens[5], lens[50] = 2561, qs
+    widths = [min(qs, 1 + int(x)) for x in torch.randint(0, 8, (B,), generator=g)]
+    widths[0] = qs
+    c = filled(lens, Hkv, D, dev, seed=65)
+    q = rows((sum(widths), Hq, D), 66).to(dev)
+    forms = ["verify", "prefill"] + (["decode"] if qs == 1 else [])
+    out, lse = attend(c, q, lens, widths, D ** -0.5, forms[0])
+    for form in forms[1:]:
+        o, l = attend(c, q, lens, widths, D ** -0.5, form)
+        assert bits_equal(o, out) and bits_equal(l, lse), form
+    cu = np.concatenate([[0], np.cumsum(widths)])
+    kv = c.values()
+    for b in (0, 5, 50, 95):
+        a, e = int(cu[b]), int(cu[b + 1])
+        o, l = attend(c, q[a:e].contiguous(), [lens[b]], [widths[b]], D ** -0.5, "verify", sel=[b])
+        assert bits_equal(o, out[a:e]) and bits_equal(l, lse[a:e]), b
+    for b in (5, 50):
+        a, e = int(cu[b]), int(cu[b + 1])
+        r = ref.attention(q[a:e].double().cpu().numpy(), *kv, c.table[b].tolist(), lens[b],
+                          widths[b], D ** -0.5, Hq // Hkv)
+        ref.check_attention(out[a:e], lse[a:e], r)
+    assert bi.device_status() == bi.BI_OK
+
+
 def test_malformed_sequences_are_skipped(dev):
     """A bad page, a block wider than max_q and a length over max_seq_len are reported; the
     other sequences' rows are right and the offenders' rows of out are not written past."""
