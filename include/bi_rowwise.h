@@ -64,8 +64,8 @@ bi_status bi_mean(const void* x, int64_t ldx, int x_dtype, int64_t rows, int64_t
  *   top      0 .. min(n, BI_LOGPROBS_MAX_TOP): top_logp, top_ids [rows, top] get the row's
  *            largest entries in descending order as log-probabilities and indices; the
  *            lowest index first among equal entries, NaN below every number.
- *   fp32 sums over a tree that depends on n alone: a row's outputs do not depend on the
- *   number of rows, on the other rows, on top, or on alignment and stride.  A row with a NaN
+ *   fp32 sums over a tree that depends on n and x_dtype alone: a row's outputs do not depend on
+ *   the number of rows, on the other rows, on top, or on alignment and stride.  A row with a NaN
  *   or +inf, or of nothing but -inf, gives NaN (ids are still ranked). */
 #define BI_LOGPROBS_MAX_TOP 32
 bi_status bi_token_logprobs(const void* x, int64_t ldx, int x_dtype, const int32_t* tokens,

@@ -3,21 +3,21 @@
 //
 // Forward.  With m a maximum and d_i = x_i - m:  s = sum exp(d_i),  w = sum exp(d_i) d_i,
 // logp = (x_t - m) - log s,  entropy = log s - w / s.  A row is cut into P parts (P <= 8, of
-// 16,384 elements where that is enough), one CTA each, the CTAs of a row in one cluster:
-//   * the part is copied into shared memory by bulk copies, in four pieces with a barrier each;
-//     thread t takes the 4-element groups t, t + T, ... and finds its maximum as they land;
-//   * s and w against the part's maximum, from shared memory, ascending in the thread, then a
-//     butterfly in each warp and the warps in ascending order;
-//   * the parts' (m, s, w) are combined in ascending order by rank 0, w moved to the common
-//     maximum by w + s (m_p - M).
-// The tree is a function of n alone.  One read of the row; several CTAs share an SM, so one's
-// copy runs under another's arithmetic.  Rows whose parts do not fit in shared memory are read
-// from global memory once per step, with the same arithmetic.
+// 16,384 elements where that is enough):
+//   * thread t of 256 (128 for rows of up to 8,192) takes the part's 16-byte vectors t, t + T,
+//     ..., eight at a time, all eight requested before any is used; against a running maximum
+//     it keeps (m, s, w) in one pass, rescaling when a batch raises the maximum;
+//   * one warp folds the threads' (m, s, w) of a part: each lane its T / 32 in ascending order,
+//     then a butterfly; the parts are folded in ascending order.
+// The tree depends on n and the type alone.  Who runs it does not matter to it: with few rows a
+// cluster has a CTA for each part (the parts meet in rank 0's shared memory), with many a CTA
+// takes a whole row and meets a barrier once per row.  @@FWD@@
 //
-// Top alternatives.  The k-th largest of the T thread maxima bounds the part's k-th largest
-// element from below, so few elements (k, and a handful more) lie at or above it; they are
-// gathered with their indices, ranked by counting, and the parts' first k ranked again by rank
-// 0.  Where ties make them too many, k rounds of a maximum below the last one found.
+// Top alternatives.  The k-th largest of the thread maxima bounds the k-th largest element from
+// below, so few elements (k, and a handful more) lie at or above it; the few threads that hold
+// one look at their vectors again (from L2), the elements are ranked by counting, and rank 0
+// ranks the CTAs' first k.  Where ties make them too many, k rounds of a maximum below the last
+// one found.
 //
 // Backward.  Elementwise from the saved lse and entropy: one read, one write.
 //
@@ -42,9 +42,8 @@ namespace {
 
 constexpr int kMaxParts = 8;
 constexpr int64_t kPart = 16384;       // elements of a part, while eight parts are enough
-constexpr int kPieces = 4;             // bulk copies (and barriers) of a part
+constexpr int kBatch = 8;              // vectors that a thread requests at a time
 constexpr int kList = 512;             // candidates gathered for the top entries
-constexpr size_t kMaxStage = 200 * 1024;  // bytes of a part that is staged in shared memory
 constexpr float kNaN = __builtin_nanf("");
 
 template <int DT>
@@ -56,23 +55,54 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
     return widen16(static_cast<const uint16_t*>(p)[i], DT == BI_F16);
 }
 
-// Elements 4g .. 4g+3 of a row (those past n are -inf); vec: aligned to four elements.
-template <int DT>
-__device__ __forceinline__ void load4(const void* p, int g, int n, bool vec, float (&v)[4]) {
-    if (vec && 4 * g + 4 <= n) {
-        if (DT == BI_F32) {
-            const float4 x = static_cast<const float4*>(p)[g];
-            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-        } else {
-            const uint2 x = static_cast<const uint2*>(p)[g];
-            v[0] = widen16(uint16_t(x.x), DT == BI_F16);
-            v[1] = widen16(uint16_t(x.x >> 16), DT == BI_F16);
-            v[2] = widen16(uint16_t(x.y), DT == BI_F16);
-            v[3] = widen16(uint16_t(x.y >> 16), DT == BI_F16);
-        }
-    } else {
+// Vector g of a row of n elements, as its 16 bytes: elements VE g .. VE g + VE - 1 (only those
+// below n are read).  skew: the row's distance from a 16-byte boundary.  A row off that
+// boundary is read as the two aligned vectors that hold the one wanted (where both lie within
+// the row; its ends element by element).
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ uint4 load_vec(const char* row, uint32_t skew, int g, int n) {
+    constexpr int ES = kSize<DT>, VE = 16 / ES;
+    if (ALIGNED) {
+        if (VE * g + VE <= n) return __ldg(reinterpret_cast<const uint4*>(row) + g);
+    } else if (skew == 0 ? VE * g + VE <= n : g > 0 && VE * (g + 2) <= n) {
+        const uint4* p = reinterpret_cast<const uint4*>(row - skew) + g;
+        const uint4 a = __ldg(p);
+        if (skew == 0) return a;
+        const uint4 b = __ldg(p + 1);
+        // bytes skew .. skew + 15 of (a, b)
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const uint32_t ws = skew >> 2, bits = (skew & 3u) * 8u;
+        uint32_t u[5];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = 4 * g + k < n ? load1<DT>(p, 4 * g + k) : -INFINITY;
+        for (int k = 0; k < 5; ++k)
+            u[k] = ws == 0 ? w[k] : ws == 1 ? w[k + 1] : ws == 2 ? w[k + 2] : w[k + 3 < 8 ? k + 3 : 7];
+        return make_uint4(__funnelshift_r(u[0], u[1], bits), __funnelshift_r(u[1], u[2], bits),
+                          __funnelshift_r(u[2], u[3], bits), __funnelshift_r(u[3], u[4], bits));
+    }
+    uint32_t o[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < VE; ++k) {
+        const int i = VE * g + k;
+        if (i < n) {
+            if (ES == 4)
+                o[k] = reinterpret_cast<const uint32_t*>(row)[i];
+            else
+                o[k >> 1] |= uint32_t(reinterpret_cast<const uint16_t*>(row)[i]) << (16 * (k & 1));
+        }
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Its elements, those from `cnt` on -inf.
+template <int DT>
+__device__ __forceinline__ void widen(const uint4& a, int cnt, float (&v)[16 / kSize<DT>]) {
+    constexpr int VE = 16 / kSize<DT>;
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < VE; ++k) {
+        v[k] = DT == BI_F32 ? __uint_as_float(w[k & 3])
+                            : widen16(uint16_t(w[(k >> 1) & 3] >> (16 * (k & 1))), DT == BI_F16);
+        if (k >= cnt) v[k] = -INFINITY;
     }
 }
 
@@ -89,16 +119,19 @@ __device__ __forceinline__ unsigned long long order_key(float x, int i) {
     return (uint64_t(order(x)) << 32) | uint32_t(0x7fffffff - i);
 }
 
-template <int T, class V, class F>
-__device__ __forceinline__ V block_fold(V v, V* scratch, F f) {
+template <int T>
+__device__ __forceinline__ unsigned long long block_max(unsigned long long v,
+                                                        unsigned long long* scratch) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v = f(v, __shfl_xor_sync(~0u, v, off));
-    __syncthreads();  // scratch may still be read from the last fold
+    for (int off = 16; off > 0; off >>= 1) {
+        const unsigned long long o = __shfl_xor_sync(~0u, v, off);
+        v = o > v ? o : v;
+    }
+    __syncthreads();  // scratch may still be read from the last one
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
     __syncthreads();
     v = scratch[0];
-#pragma unroll
-    for (int w = 1; w < T / 32; ++w) v = f(v, scratch[w]);
+    for (int w = 1; w < T / 32; ++w) v = scratch[w] > v ? scratch[w] : v;
     return v;
 }
 
@@ -117,148 +150,139 @@ struct Stats {
     float m, s, w, bad;  // bad: a NaN among the entries
 };
 
-template <int DT, int T>
+// (m, s, w) of two sets of entries together; -inf with s = w = 0 is none.
+__device__ __forceinline__ void join(Stats& a, const Stats& b) {
+    const float M = fmaxf(a.m, b.m);
+    if (M != -INFINITY) {
+        // (exp is 0 long before -1e4; 0 * -inf is not)
+        const float da = fmaxf(a.m - M, -1e4f), db = fmaxf(b.m - M, -1e4f);
+        const float fa = exp_of(da), fb = exp_of(db);
+        a.w = fmaf(fa, fmaf(a.s, da, a.w), fb * fmaf(b.s, db, b.w));
+        a.s = fmaf(a.s, fa, b.s * fb);
+        a.m = M;
+    }
+    a.bad = fmaxf(a.bad, b.bad);
+}
+
+// `ctas` CTAs (one cluster) per row, each over parts / ctas parts of `part` vectors.
+template <int DT, int T, bool ALIGNED>
 __global__ void __launch_bounds__(T)
 token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __restrict__ tokens,
-                      int n, int part, int parts, bool staged, float* logp, float* entropy,
+                      int n, int part, int parts, int ctas, float* logp, float* entropy,
                       float* lse_out, int top, float* top_logp, int32_t* top_ids,
                       unsigned int* err) {
-    constexpr int ES = kSize<DT>;
-    extern __shared__ __align__(16) uint8_t stage[];
-    __shared__ uint64_t bar[kPieces];
-    __shared__ float red[T / 32];
+    constexpr int ES = kSize<DT>, VE = 16 / ES;
     __shared__ Stats stats[kMaxParts];
+    __shared__ float tm[kMaxParts][T], ts[kMaxParts][T], tw[kMaxParts][T];
     __shared__ unsigned long long list[kList];
     __shared__ unsigned long long best[kMaxParts * BI_LOGPROBS_MAX_TOP];
     __shared__ unsigned long long redk[T / 32];
     __shared__ uint32_t tmax[T];
     __shared__ uint32_t floor_order;
-    __shared__ int found;
-    const int tid = threadIdx.x;
-    const int row = blockIdx.x / parts, rank = blockIdx.x - row * parts;
-    const int e0 = rank * part;                 // (a multiple of 8)
-    const int cnt = max(0, min(part, n - e0));  // elements of this part
-    const char* src = static_cast<const char*>(x) + (int64_t(row) * ldx + e0) * ES;
-    const uint32_t skew = uint32_t(reinterpret_cast<uintptr_t>(src) & 15u);
-    // the part as the threads read it: a copy with the row's own alignment, or the row
-    const void* data = staged ? static_cast<const void*>(stage + skew) : src;
-    const bool vec = (skew & (4 * ES - 1)) == 0;
-    const int groups = (cnt + 3) / 4;
-    // 16-byte units of the part lie at [lo, hi) of the skewed bytes; its first and last bytes
-    // outside them are copied by threads
-    const uint32_t bytes = uint32_t(cnt) * ES;
-    const uint32_t lo = skew ? 16u : 0u, hi = (skew + bytes) & ~15u;
-    const uint32_t units = hi > lo ? (hi - lo) / 16 : 0;
-    const uint32_t per = (units + kPieces - 1) / kPieces;
-    if (tid == 0) {
-        for (int i = 0; i < kPieces; ++i) mbar_init(&bar[i], 1);
-        fence_barrier_init();
-        found = 0;
-    }
-    __syncthreads();
+    __shared__ int found, any_nan;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int row = blockIdx.x / ctas, rank = blockIdx.x - row * ctas;
+    const int mine = parts / ctas, p0 = rank * mine;
+    const char* xr = static_cast<const char*>(x) + int64_t(row) * ldx * ES;
+    const uint32_t skew = ALIGNED ? 0u : uint32_t(reinterpret_cast<uintptr_t>(xr) & 15u);
+    const int vecs = (n + VE - 1) / VE;
     pdl_wait();
     pdl_trigger();
-    if (staged) {
-        if (tid == 0) {
-            for (int i = 0; i < kPieces; ++i) {
-                const uint32_t u0 = min(units, i * per), u1 = min(units, (i + 1) * per);
-                const uint32_t b = (u1 - u0) * 16;
-                if (b) {
-                    mbar_arrive_expect_tx(&bar[i], b);
-                    asm volatile(
-                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
-                        "[%0], [%1], %2, [%3];" ::"r"(smem_addr(stage + lo + u0 * 16)),
-                        "l"(src - skew + lo + u0 * 16), "r"(b), "r"(smem_addr(&bar[i]))
-                        : "memory");
-                } else {
-                    mbar_arrive(&bar[i]);
+    if (tid == 0) found = any_nan = 0;
+    __syncthreads();
+    bool nan = false;
+    for (int p = 0; p < mine; ++p) {
+        const int v1 = min(vecs, (p0 + p + 1) * part);
+        float m = -INFINITY, s = 0.f, w = 0.f;
+        for (int g = (p0 + p) * part + tid; g < v1; g += T * kBatch) {
+            uint4 a[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (g + k * T < v1) a[k] = load_vec<DT, ALIGNED>(xr, skew, g + k * T, n);
+            float bm = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (g + k * T < v1) {
+                    float v[VE];
+                    widen<DT>(a[k], n - (g + k * T) * VE, v);
+#pragma unroll
+                    for (int q = 0; q < VE; q += 2) {
+                        bm = fmax3(bm, v[q], v[q + 1]);
+                        nan |= isnan(v[q]) || isnan(v[q + 1]);
+                    }
+                }
+            }
+            if (bm > m) {
+                if (m != -INFINITY) {
+                    const float d = fmaxf(m - bm, -1e4f), f = exp_of(d);
+                    w = f * fmaf(s, d, w);
+                    s *= f;
+                }
+                m = bm;
+            }
+            const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (g + k * T < v1) {
+                    float v[VE];
+                    widen<DT>(a[k], n - (g + k * T) * VE, v);
+#pragma unroll
+                    for (int q = 0; q < VE; ++q) {
+                        const float d = v[q] - ref;
+                        const float e = exp_of(d);
+                        s = s + e;
+                        w = fmaf(e, fmaxf(d, -1e4f), w);
+                    }
                 }
             }
         }
-        // the edges: elements with a byte outside the units
-        const int head = min(cnt, lo ? int(lo - skew) / ES : 0);
-        const int tail0 = units ? int(hi - skew) / ES : head;
-        for (int i = tid; i < head; i += T) {
-            if (ES == 4)
-                reinterpret_cast<float*>(stage + skew)[i] = reinterpret_cast<const float*>(src)[i];
-            else
-                reinterpret_cast<uint16_t*>(stage + skew)[i] =
-                    reinterpret_cast<const uint16_t*>(src)[i];
-        }
-        for (int i = tail0 + tid; i < cnt; i += T) {
-            if (ES == 4)
-                reinterpret_cast<float*>(stage + skew)[i] = reinterpret_cast<const float*>(src)[i];
-            else
-                reinterpret_cast<uint16_t*>(stage + skew)[i] =
-                    reinterpret_cast<const uint16_t*>(src)[i];
-        }
-        __syncthreads();
+        tm[p][tid] = m;
+        ts[p][tid] = s;
+        tw[p][tid] = w;
     }
-    // the thread's maximum, piece by piece
-    float m = -INFINITY;
-    bool nan = false;
-    int ready = staged ? 0 : cnt;  // elements that have landed
-    bool ok = true;
-    int piece = 0;
-    for (int g = tid; g < groups; g += T) {
-        while (min(4 * g + 4, cnt) > ready) {
-            if (!mbar_wait(&bar[piece], 0, nullptr, wait_budget_ns(err))) ok = false;
-            ++piece;
-            ready = piece == kPieces
-                        ? cnt
-                        : min(cnt, int(lo + min(units, piece * per) * 16 - min(skew, lo)) / ES);
-        }
-        float v[4];
-        load4<DT>(data, g, cnt, vec, v);
+    if (nan) any_nan = 1;
+    __syncthreads();
+    // the parts' sums, a warp each
+    for (int p = warp; p < mine; p += T / 32) {
+        Stats a{tm[p][lane], ts[p][lane], tw[p][lane], any_nan ? 1.f : 0.f};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) nan |= isnan(v[k]);
-        m = fmaxf(fmaxf(m, fmaxf(v[0], v[1])), fmaxf(v[2], v[3]));
-    }
-    if (staged)  // every thread has seen every piece land: all read all of it below
-        for (; piece < kPieces; ++piece)
-            if (!mbar_wait(&bar[piece], 0, nullptr, wait_budget_ns(err))) ok = false;
-    if (!ok) latch_error(err, kErrTimeout);
-    if (top > 0) tmax[tid] = tid < groups ? order(m) : 0u;
-    const float pm =
-        block_fold<T>(m, red, [](float a, float b) { return fmaxf(a, b); });
-    const bool any_nan = __syncthreads_or(nan);
-    // s and w of the part; a part of nothing but -inf has s = 0
-    const float ref = pm == -INFINITY ? 0.f : pm;
-    float s = 0.f, w = 0.f;
-    for (int g = tid; g < groups; g += T) {
-        float v[4];
-        load4<DT>(data, g, cnt, vec, v);
+        for (int i = 1; i < T / 32; ++i)
+            join(a, Stats{tm[p][lane + 32 * i], ts[p][lane + 32 * i], tw[p][lane + 32 * i], 0.f});
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float d = v[k] - ref;
-            const float e = exp_of(d);
-            s = s + e;
-            w = fmaf(e, fmaxf(d, -1e4f), w);  // (exp is 0 long before -1e4; 0 * -inf is not)
+        for (int off = 16; off > 0; off >>= 1) {
+            const Stats b{__shfl_xor_sync(~0u, a.m, off), __shfl_xor_sync(~0u, a.s, off),
+                          __shfl_xor_sync(~0u, a.w, off), 0.f};
+            join(a, b);
         }
+        if (lane == 0) stats[p] = a;
     }
-    auto add = [](float a, float b) { return a + b; };
-    s = block_fold<T>(s, red, add);
-    w = block_fold<T>(w, red, add);
-
     if (top > 0) {
-        // the part's first `top` entries in order, as keys (0 where it has fewer)
+        // this CTA's first `top` entries in order, as keys (0 where it has fewer)
+        const int cnt = max(0, min(n, (p0 + mine) * part * VE) - p0 * part * VE);
         const int want = min(top, cnt);
-        const uint32_t own = tmax[tid];
-        int above = 0;
-        for (int i = 0; i < T; ++i) above += tmax[i] > own || (tmax[i] == own && i < tid) ? 1 : 0;
-        if (above == min(want, T) - 1) floor_order = own;
+        float m = -INFINITY;
+        for (int p = 0; p < mine; ++p) m = fmaxf(m, tm[p][tid]);
+        const uint32_t own = order(m);
+        tmax[tid] = own;
         for (int i = tid; i < BI_LOGPROBS_MAX_TOP; i += T) best[i] = 0ull;
         __syncthreads();
+        int above = 0;
+        for (int i = 0; i < T; ++i) above += tmax[i] > own || (tmax[i] == own && i < tid) ? 1 : 0;
+        if (above == max(want, 1) - 1) floor_order = own;
+        __syncthreads();
         const uint32_t fl = floor_order;
-        if (own >= fl) {
-            for (int g = tid; g < groups; g += T) {
-                float v[4];
-                load4<DT>(data, g, cnt, vec, v);
+        for (int p = 0; p < mine && own >= fl; ++p) {
+            if (order(tm[p][tid]) < fl) continue;
+            const int v1 = min(vecs, (p0 + p + 1) * part);
+#pragma unroll 4
+            for (int g = (p0 + p) * part + tid; g < v1; g += T) {
+                float v[VE];
+                widen<DT>(load_vec<DT, ALIGNED>(xr, skew, g, n), n - g * VE, v);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (4 * g + k < cnt && order(v[k]) >= fl) {
+                for (int q = 0; q < VE; ++q) {
+                    if (g * VE + q < n && order(v[q]) >= fl) {
                         const int at = atomicAdd(&found, 1);
-                        if (at < kList) list[at] = order_key(v[k], e0 + 4 * g + k);
+                        if (at < kList) list[at] = order_key(v[q], g * VE + q);
                     }
                 }
             }
@@ -276,34 +300,32 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
             unsigned long long last = ~0ull;
             for (int k = 0; k < want; ++k) {
                 unsigned long long b = 0;
-                for (int g = tid; g < groups; g += T) {
-                    float v[4];
-                    load4<DT>(data, g, cnt, vec, v);
+                for (int g = p0 * part + tid; g < min(vecs, (p0 + mine) * part); g += T) {
+                    float v[VE];
+                    widen<DT>(load_vec<DT, ALIGNED>(xr, skew, g, n), n - g * VE, v);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const unsigned long long key = order_key(v[q], e0 + 4 * g + q);
-                        if (4 * g + q < cnt && key < last && key > b) b = key;
+                    for (int q = 0; q < VE; ++q) {
+                        const unsigned long long key = order_key(v[q], g * VE + q);
+                        if (g * VE + q < n && key < last && key > b) b = key;
                     }
                 }
-                last = block_fold<T>(b, redk, [](unsigned long long p, unsigned long long q) {
-                    return p > q ? p : q;
-                });
+                last = block_max<T>(b, redk);
                 if (tid == 0) best[k] = last;
             }
         }
-        __syncthreads();
     }
+    __syncthreads();
 
-    // the parts meet in rank 0
-    if (parts > 1) {
-        cluster_sync_all();  // (rank 0 has started, and its list is built)
+    // the CTAs of a row meet in rank 0: one part each, so part r's place is stats[r]
+    if (ctas > 1) {
+        cluster_sync_all();  // (rank 0 has started, and its own entries are written)
         if (rank != 0) {
             if (tid == 0) {
                 const uint32_t a = cluster_map(smem_addr(&stats[rank]), 0);
-                st_cluster_f32(a, pm);
-                st_cluster_f32(a + 4, s);
-                st_cluster_f32(a + 8, w);
-                st_cluster_f32(a + 12, any_nan ? 1.f : 0.f);
+                st_cluster_f32(a, stats[0].m);
+                st_cluster_f32(a + 4, stats[0].s);
+                st_cluster_f32(a + 8, stats[0].w);
+                st_cluster_f32(a + 12, stats[0].bad);
             }
             if (tid < top)
                 st_cluster_b64(cluster_map(smem_addr(&best[rank * top]), 0) + tid * 8, best[tid]);
@@ -311,40 +333,25 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
         cluster_sync_all();
         if (rank != 0) return;
     }
-    if (tid == 0) stats[0] = Stats{pm, s, w, any_nan ? 1.f : 0.f};
-    __syncthreads();
-    float M = stats[0].m;
-    bool bad = stats[0].bad != 0.f;
-    for (int p = 1; p < parts; ++p) {
-        M = fmaxf(M, stats[p].m);
-        bad |= stats[p].bad != 0.f;
-    }
-    float S = 0.f, W = 0.f;
-    for (int p = 0; p < parts; ++p) {
-        const Stats a = stats[p];
-        if (a.m == -INFINITY) continue;  // (a part of nothing but -inf adds nothing)
-        const float d = a.m - M, f = exp_of(d);
-        S = fmaf(a.s, f, S);
-        W = fmaf(f, fmaf(a.s, d, a.w), W);
-    }
-    bad |= !isfinite(M);
-    const float ls = bad ? kNaN : logf(S);
+    Stats a = stats[0];
+    for (int p = 1; p < parts; ++p) join(a, stats[p]);
+    const bool bad = a.bad != 0.f || !isfinite(a.m);
+    const float ls = bad ? kNaN : logf(a.s);
     if (tid == 0) {
         const int t = tokens[row];
         if (t >= 0 && t < n) {
-            const float xt = load1<DT>(static_cast<const char*>(x) + int64_t(row) * ldx * ES, t);
-            logp[row] = (xt - M) - ls;
+            logp[row] = (load1<DT>(xr, t) - a.m) - ls;
         } else if (t == -1) {
             logp[row] = 0.f;
         } else {
             latch_error(err, kErrDeviceArg);
             logp[row] = kNaN;
         }
-        if (entropy) entropy[row] = ls - W / S;
-        if (lse_out) lse_out[row] = M + ls;
+        if (entropy) entropy[row] = ls - a.w / a.s;
+        if (lse_out) lse_out[row] = a.m + ls;
     }
     if (top > 0) {
-        const int total = parts * top;  // part p's keys at best[p * top]
+        const int total = ctas * top;  // rank r's keys at best[r * top]
         for (int i = tid; i < total; i += T) {
             const unsigned long long key = best[i];
             int r = key ? 0 : top;
@@ -352,42 +359,36 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
             if (r < top) {
                 top_ids[int64_t(row) * top + r] = 0x7fffffff - int(uint32_t(key));
                 top_logp[int64_t(row) * top + r] =
-                    (ordered_value(uint32_t(key >> 32)) - M) - ls;
+                    (ordered_value(uint32_t(key >> 32)) - a.m) - ls;
             }
         }
     }
 }
 
-// How a row is cut, from n alone.
+// How a row of n elements is cut: parts, and 16-byte vectors of each.
 struct RowCut {
     int parts, part;
 };
-RowCut row_cut(int64_t n) {
+RowCut row_cut(int64_t n, int ve) {
     RowCut c;
     c.parts = int(std::min<int64_t>(kMaxParts, (n + kPart - 1) / kPart));
-    c.part = int(((n + c.parts - 1) / c.parts + 7) / 8 * 8);
+    const int64_t vecs = (n + ve - 1) / ve;
+    c.part = int((vecs + c.parts - 1) / c.parts);
     return c;
 }
 
-template <int DT, int T>
+template <int DT, int T, bool ALIGNED>
 cudaError_t launch_forward(const DeviceInfo& dev, const void* x, int64_t ldx,
                            const int32_t* tokens, int64_t rows, int64_t n, float* logp,
                            float* entropy, float* lse, int top, float* top_logp,
                            int32_t* top_ids, cudaStream_t stream) {
-    const RowCut c = row_cut(n);
-    const size_t bytes = size_t(c.part) * kSize<DT> + 32;
-    const bool staged = bytes <= kMaxStage;
-    auto kern = token_logprobs_kernel<DT, T>;
-    static bool attr_done[64] = {};
-    if (dev.device >= 0 && dev.device < 64 && !attr_done[dev.device]) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             int(kMaxStage));
-        if (e != cudaSuccess) return e;
-        attr_done[dev.device] = true;
-    }
-    return launch_pdl_cluster(kern, dim3(unsigned(rows * c.parts)), dim3(T), staged ? bytes : 0,
-                              stream, unsigned(c.parts), x, ldx, tokens, int(n), c.part, c.parts,
-                              staged, logp, entropy, lse, top, top_logp, top_ids, dev.err_word);
+    const RowCut c = row_cut(n, 16 / kSize<DT>);
+    // a CTA per part while the rows alone would leave multiprocessors idle (@@MODE@@)
+    const int ctas = rows < 2 * dev.num_sms ? c.parts : 1;
+    return launch_pdl_cluster(token_logprobs_kernel<DT, T, ALIGNED>, dim3(unsigned(rows * ctas)),
+                              dim3(T), 0, stream, unsigned(ctas), x, ldx, tokens, int(n), c.part,
+                              c.parts, ctas, logp, entropy, lse, top, top_logp, top_ids,
+                              dev.err_word);
 }
 
 // ------------------------------------------------------------------------- backward
@@ -531,18 +532,25 @@ BI_EXPORT bi_status bi_token_logprobs(const void* x, int64_t ldx, int x_dtype,
     cudaError_t why = cudaSuccess;
     const DeviceInfo* dev = current_device_info(&why);
     if (!dev) return launched(why, fn);
-    if (rows * row_cut(n).parts > kI32Max)
-        return fail(BI_ERR_UNSUPPORTED, "%s: too many rows", fn);
-    // short rows: CTAs of 128 threads
     auto run = [&](auto f) {
         return launched(f(*dev, x, ldx, tokens, rows, n, logp, entropy, lse, int(top), top_logp,
                           top_ids, reinterpret_cast<cudaStream_t>(stream)),
                         fn);
     };
+    // short rows: CTAs of 128 threads
     const bool small = n <= 8192;
-    if (x_dtype == BI_F32) return run(small ? launch_forward<BI_F32, 128> : launch_forward<BI_F32, 256>);
-    if (x_dtype == BI_F16) return run(small ? launch_forward<BI_F16, 128> : launch_forward<BI_F16, 256>);
-    return run(small ? launch_forward<BI_BF16, 128> : launch_forward<BI_BF16, 256>);
+    const bool al = aligned(x, 16) && ldx * (x_dtype == BI_F32 ? 4 : 2) % 16 == 0;
+    if (x_dtype == BI_F32)
+        return run(al ? (small ? launch_forward<BI_F32, 128, true> : launch_forward<BI_F32, 256, true>)
+                      : (small ? launch_forward<BI_F32, 128, false>
+                               : launch_forward<BI_F32, 256, false>));
+    if (x_dtype == BI_F16)
+        return run(al ? (small ? launch_forward<BI_F16, 128, true> : launch_forward<BI_F16, 256, true>)
+                      : (small ? launch_forward<BI_F16, 128, false>
+                               : launch_forward<BI_F16, 256, false>));
+    return run(al ? (small ? launch_forward<BI_BF16, 128, true> : launch_forward<BI_BF16, 256, true>)
+                  : (small ? launch_forward<BI_BF16, 128, false>
+                           : launch_forward<BI_BF16, 256, false>));
 }
 
 BI_EXPORT bi_status bi_token_logprobs_backward(const void* x, int64_t ldx, int x_dtype,
