@@ -135,34 +135,89 @@ __device__ __forceinline__ unsigned long long block_max(unsigned long long v,
     return v;
 }
 
-// e^d, d <= 0: at most 2 ulp from 2^(d log2 e), whose argument is rounded once.
-__device__ __forceinline__ float exp_of(float d) {
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {  // at most 2 ulp from 2^x; 0 below 2^-126
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d * 1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// e^d, d <= 0 (the argument of 2^ is rounded once)
+__device__ __forceinline__ float exp_of(float d) { return ex2(d * kLog2e); }
+
+// Two fp32 operations in one instruction, each rounded as its scalar form.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// The largest of a whole vector's elements (NaN ignored beside a number; a max is exact in the
+// element's own type).
+template <int DT>
+__device__ __forceinline__ float vec_max(const uint4& a) {
+    if (DT == BI_F32)
+        return fmaxf(fmax3(__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z)),
+                     __uint_as_float(a.w));
+    if (DT == BI_BF16) {
+        auto h = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+        const __nv_bfloat162 m = __hmax2(__hmax2(h(a.x), h(a.y)), __hmax2(h(a.z), h(a.w)));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    auto h = [](uint32_t w) { return *reinterpret_cast<const __half2*>(&w); };
+    const __half2 m = __hmax2(__hmax2(h(a.x), h(a.y)), __hmax2(h(a.z), h(a.w)));
+    return fmaxf(__low2float(m), __high2float(m));
 }
 
 __device__ __forceinline__ void st_cluster_b64(uint32_t addr, unsigned long long v) {
     asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
+// The sums of a set of entries, in powers of two: m their maximum, s = sum 2^u and
+// w = sum 2^u u over u = (x - m) log2 e.  s is NaN where an entry is.
 struct Stats {
-    float m, s, w, bad;  // bad: a NaN among the entries
+    float m, s, w;
 };
+__device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.f : m; }
 
-// (m, s, w) of two sets of entries together; -inf with s = w = 0 is none.
+// Two sets together; m = -inf, s = w = 0 is none.  A set of nothing but NaN and -inf has m = -inf
+// and s = NaN, which stays.
 __device__ __forceinline__ void join(Stats& a, const Stats& b) {
-    const float M = fmaxf(a.m, b.m);
-    if (M != -INFINITY) {
-        // (exp is 0 long before -1e4; 0 * -inf is not)
-        const float da = fmaxf(a.m - M, -1e4f), db = fmaxf(b.m - M, -1e4f);
-        const float fa = exp_of(da), fb = exp_of(db);
-        a.w = fmaf(fa, fmaf(a.s, da, a.w), fb * fmaf(b.s, db, b.w));
-        a.s = fmaf(a.s, fa, b.s * fb);
-        a.m = M;
-    }
-    a.bad = fmaxf(a.bad, b.bad);
+    const float M = fmaxf(a.m, b.m), c = ref_of(M);
+    // (2^u is 0 long before -1e4; 0 * -inf is not)
+    const float da = fmaxf((ref_of(a.m) - c) * kLog2e, -1e4f);
+    const float db = fmaxf((ref_of(b.m) - c) * kLog2e, -1e4f);
+    const float fa = a.m == -INFINITY ? a.s : ex2(da), fb = b.m == -INFINITY ? b.s : ex2(db);
+    a.w = fmaf(fa, fmaf(a.s, da, a.w), fb * fmaf(b.s, db, b.w));
+    a.s = fmaf(a.s, fa, b.s * fb);
+    a.m = M;
 }
+
+constexpr int kGroups = 64;  // groups of threads whose maxima bound the top entries
 
 // `ctas` CTAs (one cluster) per row, each over parts / ctas parts of `part` vectors.
 template <int DT, int T, bool ALIGNED>
@@ -177,9 +232,9 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
     __shared__ unsigned long long list[kList];
     __shared__ unsigned long long best[kMaxParts * BI_LOGPROBS_MAX_TOP];
     __shared__ unsigned long long redk[T / 32];
-    __shared__ uint32_t tmax[T];
+    __shared__ uint32_t gmax[kGroups];
     __shared__ uint32_t floor_order;
-    __shared__ int found, any_nan;
+    __shared__ int found;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row = blockIdx.x / ctas, rank = blockIdx.x - row * ctas;
     const int mine = parts / ctas, p0 = rank * mine;
@@ -188,9 +243,8 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
     const int vecs = (n + VE - 1) / VE;
     pdl_wait();
     pdl_trigger();
-    if (tid == 0) found = any_nan = 0;
+    if (tid == 0) found = 0;
     __syncthreads();
-    bool nan = false;
     for (int p = 0; p < mine; ++p) {
         const int v1 = min(vecs, (p0 + p + 1) * part);
         float m = -INFINITY, s = 0.f, w = 0.f;
@@ -199,59 +253,79 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
 #pragma unroll
             for (int k = 0; k < kBatch; ++k)
                 if (g + k * T < v1) a[k] = load_vec<DT, ALIGNED>(xr, skew, g + k * T, n);
+            const int last = g + (kBatch - 1) * T;
+            const bool whole = last < v1 && last * VE + VE <= n;  // kBatch whole vectors
             float bm = -INFINITY;
+            if (whole) {
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                if (g + k * T < v1) {
-                    float v[VE];
-                    widen<DT>(a[k], n - (g + k * T) * VE, v);
+                for (int k = 0; k < kBatch; ++k) bm = fmaxf(bm, vec_max<DT>(a[k]));
+            } else {
 #pragma unroll
-                    for (int q = 0; q < VE; q += 2) {
-                        bm = fmax3(bm, v[q], v[q + 1]);
-                        nan |= isnan(v[q]) || isnan(v[q + 1]);
+                for (int k = 0; k < kBatch; ++k) {
+                    if (g + k * T < v1) {
+                        float v[VE];
+                        widen<DT>(a[k], n - (g + k * T) * VE, v);
+#pragma unroll
+                        for (int q = 0; q < VE; q += 2) bm = fmax3(bm, v[q], v[q + 1]);
                     }
                 }
             }
             if (bm > m) {
-                if (m != -INFINITY) {
-                    const float d = fmaxf(m - bm, -1e4f), f = exp_of(d);
-                    w = f * fmaf(s, d, w);
-                    s *= f;
-                }
+                const float d = fmaxf((ref_of(m) - ref_of(bm)) * kLog2e, -1e4f);
+                const float f = m == -INFINITY ? s : ex2(d);  // (s is 0 or NaN there)
+                w = f * fmaf(s, d, w);
+                s *= f;
                 m = bm;
             }
-            const float ref = m == -INFINITY ? 0.f : m;
+            const float c = -ref_of(m);
+            // two running sums each, of the even and the odd elements: one instruction for both
+            float2 s2 = make_float2(s, 0.f), w2 = make_float2(w, 0.f);
+            auto take = [&](float x0, float x1) {
+                const float2 u = mul2(add2(make_float2(x0, x1), make_float2(c, c)),
+                                      make_float2(kLog2e, kLog2e));
+                const float2 v = make_float2(fmaxf(u.x, -1e4f), fmaxf(u.y, -1e4f));
+                // (a NaN must reach s, so 2^ takes u itself)
+                const float2 e = make_float2(ex2(u.x), ex2(u.y));
+                s2 = add2(s2, e);
+                w2 = fma2(e, v, w2);
+            };
+            if (whole) {
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                if (g + k * T < v1) {
+                for (int k = 0; k < kBatch; ++k) {
                     float v[VE];
-                    widen<DT>(a[k], n - (g + k * T) * VE, v);
+                    widen<DT>(a[k], VE, v);
 #pragma unroll
-                    for (int q = 0; q < VE; ++q) {
-                        const float d = v[q] - ref;
-                        const float e = exp_of(d);
-                        s = s + e;
-                        w = fmaf(e, fmaxf(d, -1e4f), w);
+                    for (int q = 0; q < VE; q += 2) take(v[q], v[q + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    if (g + k * T < v1) {
+                        float v[VE];
+                        widen<DT>(a[k], n - (g + k * T) * VE, v);
+#pragma unroll
+                        for (int q = 0; q < VE; q += 2) take(v[q], v[q + 1]);
                     }
                 }
             }
+            s = s2.x + s2.y;
+            w = w2.x + w2.y;
         }
         tm[p][tid] = m;
         ts[p][tid] = s;
         tw[p][tid] = w;
     }
-    if (nan) any_nan = 1;
     __syncthreads();
     // the parts' sums, a warp each
     for (int p = warp; p < mine; p += T / 32) {
-        Stats a{tm[p][lane], ts[p][lane], tw[p][lane], any_nan ? 1.f : 0.f};
+        Stats a{tm[p][lane], ts[p][lane], tw[p][lane]};
 #pragma unroll
         for (int i = 1; i < T / 32; ++i)
-            join(a, Stats{tm[p][lane + 32 * i], ts[p][lane + 32 * i], tw[p][lane + 32 * i], 0.f});
+            join(a, Stats{tm[p][lane + 32 * i], ts[p][lane + 32 * i], tw[p][lane + 32 * i]});
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) {
             const Stats b{__shfl_xor_sync(~0u, a.m, off), __shfl_xor_sync(~0u, a.s, off),
-                          __shfl_xor_sync(~0u, a.w, off), 0.f};
+                          __shfl_xor_sync(~0u, a.w, off)};
             join(a, b);
         }
         if (lane == 0) stats[p] = a;
@@ -263,26 +337,51 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
         float m = -INFINITY;
         for (int p = 0; p < mine; ++p) m = fmaxf(m, tm[p][tid]);
         const uint32_t own = order(m);
-        tmax[tid] = own;
+        uint32_t gm = own;
+#pragma unroll
+        for (int off = 1; off < T / kGroups; off <<= 1)
+            gm = max(gm, __shfl_xor_sync(~0u, gm, off));
+        if (tid % (T / kGroups) == 0) gmax[tid / (T / kGroups)] = gm;
         for (int i = tid; i < BI_LOGPROBS_MAX_TOP; i += T) best[i] = 0ull;
         __syncthreads();
-        int above = 0;
-        for (int i = 0; i < T; ++i) above += tmax[i] > own || (tmax[i] == own && i < tid) ? 1 : 0;
-        if (above == max(want, 1) - 1) floor_order = own;
+        if (tid < kGroups) {  // the group maximum that want - 1 others exceed
+            const uint32_t g = gmax[tid];
+            int above = 0;
+#pragma unroll 16
+            for (int i = 0; i < kGroups; ++i) above += gmax[i] > g || (gmax[i] == g && i < tid) ? 1 : 0;
+            if (above == max(want, 1) - 1) floor_order = g;
+        }
         __syncthreads();
         const uint32_t fl = floor_order;
         for (int p = 0; p < mine && own >= fl; ++p) {
             if (order(tm[p][tid]) < fl) continue;
             const int v1 = min(vecs, (p0 + p + 1) * part);
-#pragma unroll 4
-            for (int g = (p0 + p) * part + tid; g < v1; g += T) {
-                float v[VE];
-                widen<DT>(load_vec<DT, ALIGNED>(xr, skew, g, n), n - g * VE, v);
+            for (int g = (p0 + p) * part + tid; g < v1; g += T * kBatch) {
+                uint4 a[kBatch];
 #pragma unroll
-                for (int q = 0; q < VE; ++q) {
-                    if (g * VE + q < n && order(v[q]) >= fl) {
-                        const int at = atomicAdd(&found, 1);
-                        if (at < kList) list[at] = order_key(v[q], g * VE + q);
+                for (int k = 0; k < kBatch; ++k)
+                    if (g + k * T < v1) a[k] = load_vec<DT, ALIGNED>(xr, skew, g + k * T, n);
+#pragma unroll 1
+                for (int k = 0; k < kBatch; ++k) {
+                    // (one vector at a time: a[k] by selection, so that a stays in registers)
+                    uint4 x = a[0];
+#pragma unroll
+                    for (int i = 1; i < kBatch; ++i)
+                        if (i == k) x = a[i];
+                    const int at0 = (g + k * T) * VE;
+                    if (g + k * T >= v1) break;
+                    float v[VE];
+                    widen<DT>(x, n - at0, v);
+                    float vm = v[0];
+#pragma unroll
+                    for (int q = 1; q < VE; ++q) vm = fmaxf(vm, v[q]);
+                    if (order(vm) < fl) continue;
+#pragma unroll
+                    for (int q = 0; q < VE; ++q) {
+                        if (at0 + q < n && order(v[q]) >= fl) {
+                            const int at = atomicAdd(&found, 1);
+                            if (at < kList) list[at] = order_key(v[q], at0 + q);
+                        }
                     }
                 }
             }
@@ -325,7 +424,6 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
                 st_cluster_f32(a, stats[0].m);
                 st_cluster_f32(a + 4, stats[0].s);
                 st_cluster_f32(a + 8, stats[0].w);
-                st_cluster_f32(a + 12, stats[0].bad);
             }
             if (tid < top)
                 st_cluster_b64(cluster_map(smem_addr(&best[rank * top]), 0) + tid * 8, best[tid]);
@@ -335,7 +433,7 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
     }
     Stats a = stats[0];
     for (int p = 1; p < parts; ++p) join(a, stats[p]);
-    const bool bad = a.bad != 0.f || !isfinite(a.m);
+    const bool bad = isnan(a.s) || !isfinite(a.m);
     const float ls = bad ? kNaN : logf(a.s);
     if (tid == 0) {
         const int t = tokens[row];
@@ -347,7 +445,7 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
             latch_error(err, kErrDeviceArg);
             logp[row] = kNaN;
         }
-        if (entropy) entropy[row] = ls - a.w / a.s;
+        if (entropy) entropy[row] = ls - a.w / a.s * kLn2;
         if (lse_out) lse_out[row] = a.m + ls;
     }
     if (top > 0) {
