@@ -4,14 +4,18 @@
 // Forward.  With m a maximum and d_i = x_i - m:  s = sum exp(d_i),  w = sum exp(d_i) d_i,
 // logp = (x_t - m) - log s,  entropy = log s - w / s.  A row is cut into P parts (P <= 8, of
 // 16,384 elements where that is enough):
-//   * thread t of 256 (128 for rows of up to 8,192) takes the part's 16-byte vectors t, t + T,
-//     ..., eight at a time, all eight requested before any is used; against a running maximum
-//     it keeps (m, s, w) in one pass, rescaling when a batch raises the maximum;
+//   * thread t of T (256; 128 for 16-bit types, whose vectors hold twice as much, and for rows
+//     of up to 8,192) takes the part's 16-byte vectors t, t + T, ..., eight at a time, all eight
+//     requested before any is used; against a running maximum it keeps (m, s, w) in one pass,
+//     rescaling when a batch raises the maximum;
 //   * one warp folds the threads' (m, s, w) of a part: each lane its T / 32 in ascending order,
 //     then a butterfly; the parts are folded in ascending order.
 // The tree depends on n and the type alone.  Who runs it does not matter to it: with few rows a
 // cluster has a CTA for each part (the parts meet in rank 0's shared memory), with many a CTA
-// takes a whole row and meets a barrier once per row.  @@FWD@@
+// takes a whole row and meets a barrier once per row.  1024 x 128256 fp32 takes 83 us (6.3 TB/s),
+// 2048 x 128256 bf16 90 us (5.8 TB/s; there the instructions of an element, about ten, bind as
+// much as its two bytes).  Staging the parts in shared memory by bulk copies, with a CTA and its
+// barriers per part, took 170 and 247 us.
 //
 // Top alternatives.  The k-th largest of the thread maxima bounds the k-th largest element from
 // below, so few elements (k, and a handful more) lie at or above it; the few threads that hold
@@ -26,6 +30,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <type_traits>
 
 #include "bi.h"
 #include "bi_rowwise.h"
@@ -48,6 +53,8 @@ constexpr float kNaN = __builtin_nanf("");
 
 template <int DT>
 constexpr int kSize = DT == BI_F32 ? 4 : 2;
+template <int DT>  // -inf, in both halves for 16 bits
+constexpr uint32_t kMinusInf = DT == BI_F32 ? 0xff800000u : DT == BI_F16 ? 0xfc00fc00u : 0xff80ff80u;
 
 template <int DT>
 __device__ __forceinline__ float load1(const void* p, int64_t i) {
@@ -55,54 +62,106 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
     return widen16(static_cast<const uint16_t*>(p)[i], DT == BI_F16);
 }
 
-// Vector g of a row of n elements, as its 16 bytes: elements VE g .. VE g + VE - 1 (only those
-// below n are read).  skew: the row's distance from a 16-byte boundary.  A row off that
-// boundary is read as the two aligned vectors that hold the one wanted (where both lie within
-// the row; its ends element by element).
-template <int DT, bool ALIGNED>
-__device__ __forceinline__ uint4 load_vec(const char* row, uint32_t skew, int g, int n) {
+// Vector g of a row of n elements, as its 16 bytes: elements VE g .. VE g + VE - 1 (those from n
+// on are -inf and not read).  vec: the row starts on a 16-byte boundary.
+template <int DT>
+__device__ __forceinline__ uint4 load_vec(const char* row, bool vec, int g, int n) {
     constexpr int ES = kSize<DT>, VE = 16 / ES;
-    if (ALIGNED) {
-        if (VE * g + VE <= n) return __ldg(reinterpret_cast<const uint4*>(row) + g);
-    } else if (skew == 0 ? VE * g + VE <= n : g > 0 && VE * (g + 2) <= n) {
-        const uint4* p = reinterpret_cast<const uint4*>(row - skew) + g;
-        const uint4 a = __ldg(p);
-        if (skew == 0) return a;
-        const uint4 b = __ldg(p + 1);
-        // bytes skew .. skew + 15 of (a, b)
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        const uint32_t ws = skew >> 2, bits = (skew & 3u) * 8u;
-        uint32_t u[5];
-#pragma unroll
-        for (int k = 0; k < 5; ++k)
-            u[k] = ws == 0 ? w[k] : ws == 1 ? w[k + 1] : ws == 2 ? w[k + 2] : w[k + 3 < 8 ? k + 3 : 7];
-        return make_uint4(__funnelshift_r(u[0], u[1], bits), __funnelshift_r(u[1], u[2], bits),
-                          __funnelshift_r(u[2], u[3], bits), __funnelshift_r(u[3], u[4], bits));
-    }
-    uint32_t o[4] = {0, 0, 0, 0};
+    if (vec && VE * g + VE <= n) return __ldg(reinterpret_cast<const uint4*>(row) + g);
+    uint32_t o[4] = {kMinusInf<DT>, kMinusInf<DT>, kMinusInf<DT>, kMinusInf<DT>};
 #pragma unroll
     for (int k = 0; k < VE; ++k) {
         const int i = VE * g + k;
         if (i < n) {
-            if (ES == 4)
+            if (ES == 4) {
                 o[k] = reinterpret_cast<const uint32_t*>(row)[i];
-            else
-                o[k >> 1] |= uint32_t(reinterpret_cast<const uint16_t*>(row)[i]) << (16 * (k & 1));
+            } else {
+                const uint32_t h = reinterpret_cast<const uint16_t*>(row)[i];
+                o[k >> 1] = k & 1 ? (o[k >> 1] & 0xffffu) | (h << 16) : (o[k >> 1] & 0xffff0000u) | h;
+            }
         }
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Its elements, those from `cnt` on -inf.
+// kBatch vectors g, g + T, ... below v1 (this thread's g = base + tid), -inf from there on; none
+// of them is used before all are requested.  A row off its 16-byte boundary by `skew` bytes is
+// read as aligned vectors: the one that starts in front of the wanted 16 bytes, and its
+// neighbour, which the next lane has read (lane 31 reads it itself).  Vectors at the row's ends,
+// whose aligned ones reach outside it, are read element by element.  All threads of the CTA call
+// it together, with one base and v1.
+template <int DT, int T, bool ALIGNED>
+__device__ __forceinline__ void load_batch(uint4 (&a)[kBatch], const char* row, uint32_t skew,
+                                           int base, int v1, int n) {
+    constexpr int ES = kSize<DT>;
+    const uint4 none = make_uint4(kMinusInf<DT>, kMinusInf<DT>, kMinusInf<DT>, kMinusInf<DT>);
+    if (ALIGNED) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int g = base + k * T + int(threadIdx.x);
+            a[k] = none;
+            if (g < v1) a[k] = load_vec<DT>(row, true, g, n);
+        }
+        return;
+    }
+    const uint4* p = reinterpret_cast<const uint4*>(row - skew);
+    const int lane = threadIdx.x & 31;
+    // aligned vectors lo .. hi - 1 lie within the row
+    const int lo = skew ? 1 : 0, hi = int((int64_t(n) * ES + skew) / 16);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+        const int g = base + k * T + int(threadIdx.x);
+        a[k] = none;
+        if (g < v1 && g >= lo && g < hi) a[k] = __ldg(p + g);
+    }
+    if (skew == 0) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int g = base + k * T + int(threadIdx.x);
+            if (g < v1 && g >= hi) a[k] = load_vec<DT>(row, false, g, n);
+        }
+        return;
+    }
+    const bool one = (skew & 4u) != 0, two = (skew & 8u) != 0;
+    const uint32_t bits = (skew & 3u) * 8u;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+        if (base + k * T >= v1) break;
+        const int g = base + k * T + int(threadIdx.x);
+        uint4 b = make_uint4(
+            __shfl_down_sync(0xffffffffu, a[k].x, 1), __shfl_down_sync(0xffffffffu, a[k].y, 1),
+            __shfl_down_sync(0xffffffffu, a[k].z, 1), __shfl_down_sync(0xffffffffu, a[k].w, 1));
+        const bool inside = g >= lo && g + 1 < hi;
+        // (a neighbour from v1 on belongs to the next part and was not read)
+        if (inside && (lane == 31 || g + 1 >= v1) && g < v1) b = __ldg(p + g + 1);
+        // bytes skew .. skew + 15 of (a, b): whole words by selection, the rest by shifts
+        const uint32_t w0[8] = {a[k].x, a[k].y, a[k].z, a[k].w, b.x, b.y, b.z, b.w};
+        uint32_t w1[7], w2[5];
+#pragma unroll
+        for (int i = 0; i < 7; ++i) w1[i] = one ? w0[i + 1] : w0[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w2[i] = two ? w1[i + 2] : w1[i];
+        const uint4 r = make_uint4(
+            __funnelshift_r(w2[0], w2[1], bits), __funnelshift_r(w2[1], w2[2], bits),
+            __funnelshift_r(w2[2], w2[3], bits), __funnelshift_r(w2[3], w2[4], bits));
+        if (inside)
+            a[k] = r;
+        else if (g < v1)
+            a[k] = load_vec<DT>(row, false, g, n);
+        else
+            a[k] = none;
+    }
+}
+
+// Its elements.
 template <int DT>
-__device__ __forceinline__ void widen(const uint4& a, int cnt, float (&v)[16 / kSize<DT>]) {
+__device__ __forceinline__ void widen(const uint4& a, float (&v)[16 / kSize<DT>]) {
     constexpr int VE = 16 / kSize<DT>;
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int k = 0; k < VE; ++k) {
         v[k] = DT == BI_F32 ? __uint_as_float(w[k & 3])
                             : widen16(uint16_t(w[(k >> 1) & 3] >> (16 * (k & 1))), DT == BI_F16);
-        if (k >= cnt) v[k] = -INFINITY;
     }
 }
 
@@ -221,7 +280,7 @@ constexpr int kGroups = 64;  // groups of threads whose maxima bound the top ent
 
 // `ctas` CTAs (one cluster) per row, each over parts / ctas parts of `part` vectors.
 template <int DT, int T, bool ALIGNED>
-__global__ void __launch_bounds__(T)
+__global__ void __launch_bounds__(T, T == 256 ? 4 : 6)
 token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __restrict__ tokens,
                       int n, int part, int parts, int ctas, float* logp, float* entropy,
                       float* lse_out, int top, float* top_logp, int32_t* top_ids,
@@ -245,77 +304,77 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
     pdl_trigger();
     if (tid == 0) found = 0;
     __syncthreads();
-    for (int p = 0; p < mine; ++p) {
-        const int v1 = min(vecs, (p0 + p + 1) * part);
-        float m = -INFINITY, s = 0.f, w = 0.f;
-        for (int g = (p0 + p) * part + tid; g < v1; g += T * kBatch) {
-            uint4 a[kBatch];
+    const int whole = n / VE;  // vectors that hold no padding
+    auto sums = [&](auto clamp) {
+        bool again = false;
+        for (int p = 0; p < mine; ++p) {
+            const int v0 = (p0 + p) * part, v1 = min(vecs, v0 + part);
+            float m = -INFINITY, s = 0.f, w = 0.f;
+            for (int g = v0; g < v1; g += T * kBatch) {
+                // every thread's vectors are there, and whole
+                const bool full = g + kBatch * T <= min(v1, whole);
+                uint4 a[kBatch];
+                if (ALIGNED && full) {
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (g + k * T < v1) a[k] = load_vec<DT, ALIGNED>(xr, skew, g + k * T, n);
-            const int last = g + (kBatch - 1) * T;
-            const bool whole = last < v1 && last * VE + VE <= n;  // kBatch whole vectors
-            float bm = -INFINITY;
-            if (whole) {
+                    for (int k = 0; k < kBatch; ++k)
+                        a[k] = __ldg(reinterpret_cast<const uint4*>(xr) + g + k * T + tid);
+                } else {
+                    load_batch<DT, T, ALIGNED>(a, xr, skew, g, v1, n);
+                }
+                float bm = vec_max<DT>(a[0]);
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) bm = fmaxf(bm, vec_max<DT>(a[k]));
-            } else {
+                for (int k = 1; k < kBatch; ++k) bm = fmaxf(bm, vec_max<DT>(a[k]));
+                if (bm > m) {
+                    const float d = fmaxf((ref_of(m) - ref_of(bm)) * kLog2e, -1e4f);
+                    const float f = m == -INFINITY ? s : ex2(d);  // (s is 0 or NaN there)
+                    w = f * fmaf(s, d, w);
+                    s *= f;
+                    m = bm;
+                }
+                const float c = -ref_of(m);
+                // two running sums each, of the even and the odd elements: one instruction for both
+                float2 s2 = make_float2(s, 0.f), w2 = make_float2(w, 0.f);
+                auto take = [&](float x0, float x1, bool held) {
+                    const float2 u = mul2(add2(make_float2(x0, x1), make_float2(c, c)),
+                                          make_float2(kLog2e, kLog2e));
+                    const float2 e = make_float2(ex2(u.x), ex2(u.y));
+                    s2 = add2(s2, e);
+                    w2 = fma2(e, held ? make_float2(fmaxf(u.x, -1e4f), fmaxf(u.y, -1e4f)) : u, w2);
+                };
+                if (full && !decltype(clamp)::value) {
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    if (g + k * T < v1) {
+                    for (int k = 0; k < kBatch; ++k) {
                         float v[VE];
-                        widen<DT>(a[k], n - (g + k * T) * VE, v);
+                        widen<DT>(a[k], v);
 #pragma unroll
-                        for (int q = 0; q < VE; q += 2) bm = fmax3(bm, v[q], v[q + 1]);
+                        for (int q = 0; q < VE; q += 2) take(v[q], v[q + 1], false);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        if (g + k * T >= v1) break;  // (no thread has a vector here)
+                        float v[VE];
+                        widen<DT>(a[k], v);
+#pragma unroll
+                        for (int q = 0; q < VE; q += 2) take(v[q], v[q + 1], true);
                     }
                 }
+                s = s2.x + s2.y;
+                w = w2.x + w2.y;
             }
-            if (bm > m) {
-                const float d = fmaxf((ref_of(m) - ref_of(bm)) * kLog2e, -1e4f);
-                const float f = m == -INFINITY ? s : ex2(d);  // (s is 0 or NaN there)
-                w = f * fmaf(s, d, w);
-                s *= f;
-                m = bm;
-            }
-            const float c = -ref_of(m);
-            // two running sums each, of the even and the odd elements: one instruction for both
-            float2 s2 = make_float2(s, 0.f), w2 = make_float2(w, 0.f);
-            auto take = [&](float x0, float x1) {
-                const float2 u = mul2(add2(make_float2(x0, x1), make_float2(c, c)),
-                                      make_float2(kLog2e, kLog2e));
-                const float2 v = make_float2(fmaxf(u.x, -1e4f), fmaxf(u.y, -1e4f));
-                // (a NaN must reach s, so 2^ takes u itself)
-                const float2 e = make_float2(ex2(u.x), ex2(u.y));
-                s2 = add2(s2, e);
-                w2 = fma2(e, v, w2);
-            };
-            if (whole) {
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    float v[VE];
-                    widen<DT>(a[k], VE, v);
-#pragma unroll
-                    for (int q = 0; q < VE; q += 2) take(v[q], v[q + 1]);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    if (g + k * T < v1) {
-                        float v[VE];
-                        widen<DT>(a[k], n - (g + k * T) * VE, v);
-#pragma unroll
-                        for (int q = 0; q < VE; q += 2) take(v[q], v[q + 1]);
-                    }
-                }
-            }
-            s = s2.x + s2.y;
-            w = w2.x + w2.y;
+            tm[p][tid] = m;
+            ts[p][tid] = s;
+            tw[p][tid] = w;
+            again |= isnan(w) && !isnan(s);
         }
-        tm[p][tid] = m;
-        ts[p][tid] = s;
-        tw[p][tid] = w;
+        return again;
+    };
+    // 0 * -inf makes w NaN where an entry is -inf: then the CTA goes over its parts again with u
+    // held above -1e4 in w (2^u is 0 long before), which changes no other term
+    if (__syncthreads_or(sums(std::false_type()))) {
+        sums(std::true_type());
+        __syncthreads();
     }
-    __syncthreads();
     // the parts' sums, a warp each
     for (int p = warp; p < mine; p += T / 32) {
         Stats a{tm[p][lane], ts[p][lane], tw[p][lane]};
@@ -328,7 +387,7 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
                           __shfl_xor_sync(~0u, a.w, off)};
             join(a, b);
         }
-        if (lane == 0) stats[p] = a;
+        if (lane == 0) stats[p0 + p] = a;
     }
     if (top > 0) {
         // this CTA's first `top` entries in order, as keys (0 where it has fewer)
@@ -360,7 +419,7 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
                 uint4 a[kBatch];
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k)
-                    if (g + k * T < v1) a[k] = load_vec<DT, ALIGNED>(xr, skew, g + k * T, n);
+                    if (g + k * T < v1) a[k] = load_vec<DT>(xr, skew == 0, g + k * T, n);
 #pragma unroll 1
                 for (int k = 0; k < kBatch; ++k) {
                     // (one vector at a time: a[k] by selection, so that a stays in registers)
@@ -371,7 +430,7 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
                     const int at0 = (g + k * T) * VE;
                     if (g + k * T >= v1) break;
                     float v[VE];
-                    widen<DT>(x, n - at0, v);
+                    widen<DT>(x, v);
                     float vm = v[0];
 #pragma unroll
                     for (int q = 1; q < VE; ++q) vm = fmaxf(vm, v[q]);
@@ -401,7 +460,7 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
                 unsigned long long b = 0;
                 for (int g = p0 * part + tid; g < min(vecs, (p0 + mine) * part); g += T) {
                     float v[VE];
-                    widen<DT>(load_vec<DT, ALIGNED>(xr, skew, g, n), n - g * VE, v);
+                    widen<DT>(load_vec<DT>(xr, skew == 0, g, n), v);
 #pragma unroll
                     for (int q = 0; q < VE; ++q) {
                         const unsigned long long key = order_key(v[q], g * VE + q);
@@ -415,15 +474,15 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
     }
     __syncthreads();
 
-    // the CTAs of a row meet in rank 0: one part each, so part r's place is stats[r]
+    // the CTAs of a row meet in rank 0
     if (ctas > 1) {
         cluster_sync_all();  // (rank 0 has started, and its own entries are written)
         if (rank != 0) {
-            if (tid == 0) {
-                const uint32_t a = cluster_map(smem_addr(&stats[rank]), 0);
-                st_cluster_f32(a, stats[0].m);
-                st_cluster_f32(a + 4, stats[0].s);
-                st_cluster_f32(a + 8, stats[0].w);
+            if (tid < mine) {
+                const uint32_t a = cluster_map(smem_addr(&stats[p0 + tid]), 0);
+                st_cluster_f32(a, stats[p0 + tid].m);
+                st_cluster_f32(a + 4, stats[p0 + tid].s);
+                st_cluster_f32(a + 8, stats[p0 + tid].w);
             }
             if (tid < top)
                 st_cluster_b64(cluster_map(smem_addr(&best[rank * top]), 0) + tid * 8, best[tid]);
@@ -481,8 +540,14 @@ cudaError_t launch_forward(const DeviceInfo& dev, const void* x, int64_t ldx,
                            float* entropy, float* lse, int top, float* top_logp,
                            int32_t* top_ids, cudaStream_t stream) {
     const RowCut c = row_cut(n, 16 / kSize<DT>);
-    // a CTA per part while the rows alone would leave multiprocessors idle (@@MODE@@)
-    const int ctas = rows < 2 * dev.num_sms ? c.parts : 1;
+    // CTAs per row: one, once the rows give every multiprocessor two; with fewer rows, as many
+    // as do that (up to one per part).  Splitting more rows than that costs more in the cluster's
+    // meeting than a last wave that is not full: 1024 x 128256 fp32 83 us with one CTA a row, 166
+    // with four.
+    int ctas = 1;
+    while (ctas < c.parts && rows * ctas < 2 * int64_t(dev.num_sms)) {
+        do ++ctas; while (c.parts % ctas != 0);
+    }
     return launch_pdl_cluster(token_logprobs_kernel<DT, T, ALIGNED>, dim3(unsigned(rows * ctas)),
                               dim3(T), 0, stream, unsigned(ctas), x, ldx, tokens, int(n), c.part,
                               c.parts, ctas, logp, entropy, lse, top, top_logp, top_ids,
@@ -635,20 +700,14 @@ BI_EXPORT bi_status bi_token_logprobs(const void* x, int64_t ldx, int x_dtype,
                           top_ids, reinterpret_cast<cudaStream_t>(stream)),
                         fn);
     };
-    // short rows: CTAs of 128 threads
-    const bool small = n <= 8192;
     const bool al = aligned(x, 16) && ldx * (x_dtype == BI_F32 ? 4 : 2) % 16 == 0;
+    if (x_dtype == BI_F32 && n > 8192)
+        return run(al ? launch_forward<BI_F32, 256, true> : launch_forward<BI_F32, 256, false>);
     if (x_dtype == BI_F32)
-        return run(al ? (small ? launch_forward<BI_F32, 128, true> : launch_forward<BI_F32, 256, true>)
-                      : (small ? launch_forward<BI_F32, 128, false>
-                               : launch_forward<BI_F32, 256, false>));
+        return run(al ? launch_forward<BI_F32, 128, true> : launch_forward<BI_F32, 128, false>);
     if (x_dtype == BI_F16)
-        return run(al ? (small ? launch_forward<BI_F16, 128, true> : launch_forward<BI_F16, 256, true>)
-                      : (small ? launch_forward<BI_F16, 128, false>
-                               : launch_forward<BI_F16, 256, false>));
-    return run(al ? (small ? launch_forward<BI_BF16, 128, true> : launch_forward<BI_BF16, 256, true>)
-                  : (small ? launch_forward<BI_BF16, 128, false>
-                           : launch_forward<BI_BF16, 256, false>));
+        return run(al ? launch_forward<BI_F16, 128, true> : launch_forward<BI_F16, 128, false>);
+    return run(al ? launch_forward<BI_BF16, 128, true> : launch_forward<BI_BF16, 128, false>);
 }
 
 BI_EXPORT bi_status bi_token_logprobs_backward(const void* x, int64_t ldx, int x_dtype,
