@@ -132,9 +132,10 @@ def _torch():
 
 
 def _stream(stream) -> int:
-    torch = _torch()
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        torch = _torch()
+        # the handle alone: building a torch.cuda.Stream for it takes several microseconds
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -452,6 +453,30 @@ def _on_current_device(**tensors):
             raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{cur}")
 
 
+def _device_of(t) -> int:
+    """The CUDA device of t if that is the current one, else -1."""
+    torch = _torch()
+    if isinstance(t, torch.Tensor) and t.is_cuda:
+        dev = t.get_device()
+        if dev == torch.cuda.current_device():
+            return dev
+    return -1
+
+
+def _all(dev, *tensors) -> bool:
+    """Every (tensor, dtype, ndim) is a contiguous tensor of that kind on CUDA device dev.  The
+    calls below ask this first and look for what is wrong only when it is not so: checking one
+    tensor at a time took longer than the kernels of a small call."""
+    if dev < 0:
+        return False
+    Tensor = _torch().Tensor
+    for t, dtype, ndim in tensors:
+        if not (isinstance(t, Tensor) and t.dtype is dtype and t.dim() == ndim
+                and t.get_device() == dev and t.is_contiguous()):
+            return False
+    return True
+
+
 def _allocating_for(stream):
     """A context in which torch allocates for `stream`: memory that this module makes for a
     call on another stream than the current one is taken from, and goes back to, the pool of
@@ -468,25 +493,26 @@ def _allocating_for(stream):
 
 def _paged_common_q8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens):
     torch = _torch()
-    _need(k_cache, torch.uint8, "k_cache", 4)
-    _need(v_cache, torch.uint8, "v_cache", 4)
-    _need(k_scale, torch.uint8, "k_scale", 3)
-    _need(v_scale, torch.uint8, "v_scale", 3)
-    _need(block_table, torch.int32, "block_table", 2)
-    _need(seq_lens, torch.int32, "seq_lens", 1)
-    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
-            and v_scale.is_contiguous() and block_table.is_contiguous()
-            and seq_lens.is_contiguous()):
+    u8, i32 = torch.uint8, torch.int32
+    if not _all(_device_of(k_cache), (k_cache, u8, 4), (v_cache, u8, 4), (k_scale, u8, 3),
+                (v_scale, u8, 3), (block_table, i32, 2), (seq_lens, i32, 1)):
+        _need(k_cache, u8, "k_cache", 4)
+        _need(v_cache, u8, "v_cache", 4)
+        _need(k_scale, u8, "k_scale", 3)
+        _need(v_scale, u8, "v_scale", 3)
+        _need(block_table, i32, "block_table", 2)
+        _need(seq_lens, i32, "seq_lens", 1)
+        _on_current_device(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                           block_table=block_table, seq_lens=seq_lens)
         raise ValueError("caches, scales, block_table and seq_lens must be contiguous")
-    if k_cache.shape != v_cache.shape:
+    shape = k_cache.shape
+    if shape != v_cache.shape:
         raise ValueError("k_cache and v_cache shapes differ")
-    if k_scale.shape != k_cache.shape[:3] or v_scale.shape != k_cache.shape[:3]:
+    if k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
         raise ValueError("k_scale and v_scale must be [num_pages, Hkv, page]")
     if block_table.shape[0] != seq_lens.shape[0]:
         raise ValueError("block_table and seq_lens disagree on the batch")
-    _on_current_device(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-                       block_table=block_table, seq_lens=seq_lens)
-    return k_cache.shape
+    return shape
 
 
 def kv_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q,
@@ -496,21 +522,24 @@ def kv_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, 
     torch = _torch()
     num_pages, hkv, page, d = _paged_common_q8(k_cache, v_cache, k_scale, v_scale, block_table,
                                                seq_lens)
-    _need(k_new, torch.bfloat16, "k_new", 3)
-    _need(v_new, torch.bfloat16, "v_new", 3)
-    _need(cu_q, torch.int32, "cu_q", 1)
-    if not (k_new.is_contiguous() and v_new.is_contiguous() and cu_q.is_contiguous()):
+    bf16 = torch.bfloat16
+    if not _all(k_cache.get_device(), (k_new, bf16, 3), (v_new, bf16, 3), (cu_q, torch.int32, 1)):
+        _need(k_new, bf16, "k_new", 3)
+        _need(v_new, bf16, "v_new", 3)
+        _need(cu_q, torch.int32, "cu_q", 1)
+        _on_current_device(k_new=k_new, v_new=v_new, cu_q=cu_q)
         raise ValueError("k_new, v_new and cu_q must be contiguous")
     B = seq_lens.shape[0]
-    if k_new.shape != v_new.shape or tuple(k_new.shape[1:]) != (hkv, d):
+    T, h, dn = k_new.shape
+    if k_new.shape != v_new.shape or h != hkv or dn != d:
         raise ValueError("k_new and v_new must be [T, Hkv, D] of the cache's Hkv and D")
     if cu_q.shape[0] != B + 1:
         raise ValueError("cu_q must have batch + 1 entries")
-    _on_current_device(k_new=k_new, v_new=v_new, cu_q=cu_q)
-    _check(lib().bi_kv_append_q8(_ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
-                                 _ptr(k_scale), _ptr(v_scale), num_pages, _ptr(block_table),
-                                 block_table.shape[1], _ptr(seq_lens), _ptr(cu_q), B,
-                                 k_new.shape[0], hkv, d, page, _stream(stream)))
+    _check(lib().bi_kv_append_q8(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(),
+                                 v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                 num_pages, block_table.data_ptr(), block_table.shape[1],
+                                 seq_lens.data_ptr(), cu_q.data_ptr(), B, T, hkv, d, page,
+                                 _stream(stream)))
 
 
 def _attend_q8(fn, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, max_q,
@@ -518,27 +547,44 @@ def _attend_q8(fn, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
     torch = _torch()
     num_pages, hkv, page, d = _paged_common_q8(k_cache, v_cache, k_scale, v_scale, block_table,
                                                seq_lens)
-    _need(q, torch.bfloat16, "q", 3)
+    dev = k_cache.get_device()
+    decode = fn == "bi_decode_attn_q8"
+    if not _all(dev, (q, torch.bfloat16, 3)):
+        _need(q, torch.bfloat16, "q", 3)
+        _on_current_device(q=q)
+        raise ValueError("q must be a contiguous [T, Hq, D] of the cache's D")
     T, hq, dq = q.shape
     B = seq_lens.shape[0]
-    if dq != d or not q.is_contiguous():
+    if dq != d:
         raise ValueError("q must be a contiguous [T, Hq, D] of the cache's D")
-    if fn == "bi_decode_attn_q8":
+    if decode:
         if T != B:
             raise ValueError("q must have one token per sequence")
-    else:
+    elif not _all(dev, (cu_q, torch.int32, 1)) or cu_q.shape[0] != B + 1:
         _need(cu_q, torch.int32, "cu_q", 1)
-        if cu_q.shape[0] != B + 1 or not cu_q.is_contiguous():
-            raise ValueError("cu_q must be contiguous with batch + 1 entries")
+        _on_current_device(cu_q=cu_q)
+        raise ValueError("cu_q must be contiguous with batch + 1 entries")
+    L = lib()
+    if out is not None or lse is not None or workspace is not None:
+        _on_current_device(out=out, lse=lse, workspace=workspace)
+        _attn_out(q, q if out is None else out, lse, False)  # (checks what the caller gave)
     with _allocating_for(stream):
-        out, lse = _attn_out(q, out, lse, want_lse)
-        ws, ws_bytes = _workspace(workspace, attn_workspace_size(T, hq, d, max_seq_len), q.device)
-    _on_current_device(q=q, cu_q=cu_q, out=out, lse=lse, workspace=ws)
-    head = (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), num_pages,
-            _ptr(block_table), block_table.shape[1], _ptr(seq_lens))
-    sizes = (B,) if fn == "bi_decode_attn_q8" else (_ptr(cu_q), B, T, int(max_q))
-    _check(getattr(lib(), fn)(*head, *sizes, int(max_seq_len), hq, hkv, d, page, float(scale),
-                              _ptr(out), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)))
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None and want_lse:
+            lse = torch.empty(T, hq, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            ws_bytes = max(16, L.bi_attn_workspace_size(T, hq, d, int(max_seq_len)))
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        else:
+            ws_bytes = workspace.numel() * workspace.element_size()
+    head = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), num_pages, block_table.data_ptr(), block_table.shape[1],
+            seq_lens.data_ptr())
+    sizes = (B,) if decode else (cu_q.data_ptr(), B, T, int(max_q))
+    _check(getattr(L, fn)(*head, *sizes, int(max_seq_len), hq, hkv, d, page, float(scale),
+                          out.data_ptr(), _ptr(lse), workspace.data_ptr(), ws_bytes,
+                          _stream(stream)))
     return out, lse
 
 
@@ -573,29 +619,28 @@ def kv_copy_pages(planes: Sequence, src, dst, stream=None) -> None:
     page type whose first dimension is the pages (a layer's k_cache, v_cache, k_scale,
     v_scale).  A destination page is named once, and is not a source of the same call."""
     torch = _torch()
-    _need(src, torch.int32, "src", 1)
-    _need(dst, torch.int32, "dst", 1)
-    if src.shape != dst.shape or not src.is_contiguous() or not dst.is_contiguous():
+    dev = _device_of(src)
+    if not _all(dev, (src, torch.int32, 1), (dst, torch.int32, 1)) or src.shape != dst.shape:
+        _need(src, torch.int32, "src", 1)
+        _need(dst, torch.int32, "dst", 1)
+        _on_current_device(src=src, dst=dst)
         raise ValueError("src and dst must be contiguous lists of one length")
-    _on_current_device(src=src, dst=dst)
     planes = list(planes)
     if not planes:
         return
     pages = planes[0].shape[0] if planes[0].dim() else 0
     if pages < 1:
         raise ValueError("a plane has no pages")
-    cur = src.device
-    ptrs, sizes = [], []
     for t in planes:
-        if not t.is_cuda or t.device != cur:
-            raise ValueError("planes must be CUDA tensors on the device of src and dst")
-        if not t.is_contiguous() or t.dim() == 0 or t.shape[0] != pages:
+        if t.get_device() != dev:
+            raise ValueError("planes must be CUDA tensors on the current device")
+        if t.dim() == 0 or t.shape[0] != pages or not t.is_contiguous():
             raise ValueError("planes must be contiguous with one number of pages")
-        ptrs.append(t.data_ptr())
-        sizes.append(t.numel() // pages * t.element_size())
-    n = len(ptrs)
-    _check(lib().bi_kv_copy_pages((ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes), n,
-                                  pages, _ptr(src), _ptr(dst), src.shape[0], _stream(stream)))
+    n = len(planes)
+    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in planes])
+    sizes = (ctypes.c_int64 * n)(*[t.nbytes // pages for t in planes])
+    _check(lib().bi_kv_copy_pages(ptrs, sizes, n, pages, src.data_ptr(), dst.data_ptr(),
+                                  src.shape[0], _stream(stream)))
 
 
 # ---------------------------------------------------------------------- device status
@@ -746,11 +791,8 @@ class TokenLogprobs(NamedTuple):
     top_ids: object
 
 
-def token_logprobs(logits, tokens, top: int = 0, stream=None) -> TokenLogprobs:
-    """Log-probability of each row's token under the softmax of its logits (bf16, fp16 or
-    fp32 [rows, n]; tokens int32 [rows], -1 for none), the row's entropy and log-sum-exp, and
-    the `top` largest entries as log-probabilities and ids (descending; lowest id first among
-    equal ones).  A row's bits do not depend on the other rows."""
+def _logits(logits, tokens):
+    """Checks logits and tokens; returns (dtype code, rows, n, row stride)."""
     torch = _torch()
     dt = _in_dtype(logits, "logits")
     _need(logits, logits.dtype, "logits", 2)
@@ -758,17 +800,30 @@ def token_logprobs(logits, tokens, top: int = 0, stream=None) -> TokenLogprobs:
     rows, n = logits.shape
     if tokens.shape[0] != rows or not tokens.is_contiguous():
         raise ValueError("tokens must be a contiguous int32 [rows] tensor")
-    _on_current_device(logits=logits, tokens=tokens)
-    f32 = dict(dtype=torch.float32, device=logits.device)
+    if _device_of(logits) != tokens.get_device():
+        _on_current_device(logits=logits, tokens=tokens)
+    return dt, rows, n, _row_major_2d(logits, "logits")
+
+
+def token_logprobs(logits, tokens, top: int = 0, stream=None) -> TokenLogprobs:
+    """Log-probability of each row's token under the softmax of its logits (bf16, fp16 or
+    fp32 [rows, n]; tokens int32 [rows], -1 for none), the row's entropy and log-sum-exp, and
+    the `top` largest entries as log-probabilities and ids (descending; lowest id first among
+    equal ones).  A row's bits do not depend on the other rows."""
+    torch = _torch()
+    dt, rows, n, ld = _logits(logits, tokens)
+    if not 0 <= top <= min(n, LOGPROBS_MAX_TOP):
+        raise ValueError(f"top must be in [0, min(n, {LOGPROBS_MAX_TOP})]")
+    dev = logits.device
     with _allocating_for(stream):
-        stats = torch.empty(3, rows, **f32)
-        tv = torch.empty(rows, top, **f32) if top else None
-        ti = torch.empty(rows, top, dtype=torch.int32, device=logits.device) if top else None
-    logp, entropy, lse = stats.unbind(0)
-    _check(lib().bi_token_logprobs(_ptr(logits), _row_major_2d(logits, "logits"), dt, _ptr(tokens),
-                                   rows, n, _ptr(logp), _ptr(entropy), _ptr(lse), int(top),
-                                   _ptr(tv), _ptr(ti), _stream(stream)))
-    return TokenLogprobs(logp, entropy, lse, tv, ti)
+        stats = torch.empty(3, rows, dtype=torch.float32, device=dev)
+        tv = torch.empty(rows, top, dtype=torch.float32, device=dev) if top else None
+        ti = torch.empty(rows, top, dtype=torch.int32, device=dev) if top else None
+    p = stats.data_ptr()
+    _check(lib().bi_token_logprobs(logits.data_ptr(), ld, dt, tokens.data_ptr(), rows, n, p,
+                                   p + 4 * rows, p + 8 * rows, int(top), _ptr(tv), _ptr(ti),
+                                   _stream(stream)))
+    return TokenLogprobs(*stats.unbind(0), tv, ti)
 
 
 def token_logprobs_backward(logits, tokens, lse, entropy=None, grad_logprobs=None,
@@ -777,32 +832,29 @@ def token_logprobs_backward(logits, tokens, lse, entropy=None, grad_logprobs=Non
     sum(grad_logprobs * logprobs) + sum(grad_entropy * entropy), from the lse and entropy
     that token_logprobs gave; out may be logits."""
     torch = _torch()
-    dt = _in_dtype(logits, "logits")
-    _need(logits, logits.dtype, "logits", 2)
-    rows, n = logits.shape
-    _need(tokens, torch.int32, "tokens", 1)
+    dt, rows, n, ld = _logits(logits, tokens)
     if grad_logprobs is None and grad_entropy is None:
         raise ValueError("grad_logprobs and grad_entropy are both None")
     if grad_entropy is not None and entropy is None:
         raise ValueError("grad_entropy needs entropy")
+    cur = logits.get_device()
     for name, t in (("lse", lse), ("entropy", entropy), ("grad_logprobs", grad_logprobs),
                     ("grad_entropy", grad_entropy)):
-        if t is not None or name == "lse":
+        if (t is not None or name == "lse") and not (_all(cur, (t, torch.float32, 1))
+                                                     and t.shape[0] == rows):
             _need(t, torch.float32, name, 1)
-            if t.shape[0] != rows or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous fp32 [rows] tensor")
-    if tokens.shape[0] != rows or not tokens.is_contiguous():
-        raise ValueError("tokens must be a contiguous int32 [rows] tensor")
+            _on_current_device(**{name: t})
+            raise ValueError(f"{name} must be a contiguous fp32 [rows] tensor")
     if out is None:
         with _allocating_for(stream):
             out = torch.empty(rows, n, dtype=logits.dtype, device=logits.device)
-    _need(out, logits.dtype, "out", 2)
-    if tuple(out.shape) != (rows, n):
-        raise ValueError("out must have the shape of logits")
-    _on_current_device(logits=logits, tokens=tokens, lse=lse, entropy=entropy,
-                       grad_logprobs=grad_logprobs, grad_entropy=grad_entropy, out=out)
+    else:
+        _need(out, logits.dtype, "out", 2)
+        _on_current_device(out=out)
+        if tuple(out.shape) != (rows, n):
+            raise ValueError("out must have the shape of logits")
     _check(lib().bi_token_logprobs_backward(
-        _ptr(logits), _row_major_2d(logits, "logits"), dt, _ptr(tokens), rows, n, _ptr(lse),
-        _ptr(entropy), _ptr(grad_logprobs), _ptr(grad_entropy), _ptr(out),
-        _row_major_2d(out, "out"), _stream(stream)))
+        logits.data_ptr(), ld, dt, tokens.data_ptr(), rows, n, lse.data_ptr(), _ptr(entropy),
+        _ptr(grad_logprobs), _ptr(grad_entropy), out.data_ptr(), _row_major_2d(out, "out"),
+        _stream(stream)))
     return out
