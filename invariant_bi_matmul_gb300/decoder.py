@@ -25,6 +25,13 @@ bits do not depend on the block width); ``start`` instead loads synthetic cache 
 small checks against the oracle.  Either way a sequence's context depends only on the
 sequence, never on the batch it runs in.
 
+The caches hold bf16, or with ``kv_cache="q8"`` E4M3 codes and a scale byte per token and head
+(half the bytes attention reads); either way a token's cache bytes and a query's bits depend on
+the sequence alone.  With ``logprobs=True`` the log-probability of every emitted token is kept
+beside the traces (``trace_logprobs``): the same bits whether the token was decoded alone or
+accepted from a verify block.  ``fork`` continues one sequence as several: its full cache pages
+are shared, its open page is copied, and ``compact`` moves the pages in use together.
+
 The traces are batch invariant only while every call is inside the batch-invariant
 limit: matmuls of up to ``max_batch * max_width`` rows and verify blocks of up to
 ``max_width`` tokens.  An ``invariant=True`` decoder (the default) refuses to run a block
@@ -37,9 +44,11 @@ from typing import Callable, List, Optional, Sequence
 
 import torch
 
-from . import (ATTN_MAX_Q, add, argmax, attn_workspace_size, embedding, kv_append, matmul,
-               prefill_attn, rmsnorm, rope, swiglu, verify_block, within_batch_invariant_limit)
+from . import (ATTN_MAX_Q, add, argmax, attn_workspace_size, embedding, kv_append, kv_append_q8,
+               kv_copy_pages, matmul, prefill_attn, prefill_attn_q8, rmsnorm, rope, swiglu,
+               token_logprobs, verify_block, verify_block_q8, within_batch_invariant_limit)
 from .inputs import PAGE_SIZE, DecoderConfig, decoder_context, decoder_first_token, page_permutation
+from .pages import PagePool
 
 Drafter = Callable[[int, List[int], int], List[int]]
 
@@ -51,7 +60,11 @@ class GreedyDecoder:
 
     def __init__(self, cfg: DecoderConfig, weights: dict, max_batch: int, max_len: int,
                  max_width: int = 4, device="cuda", page_seed: int = 0,
-                 invariant: bool = True, prefill_width: int = 0):
+                 invariant: bool = True, prefill_width: int = 0, kv_cache: str = "bf16",
+                 logprobs: bool = False):
+        if kv_cache not in ("bf16", "q8"):
+            raise ValueError("kv_cache must be 'bf16' or 'q8'")
+        self.kv_cache, self.want_logprobs = kv_cache, logprobs
         self.cfg, self.w = cfg, weights
         self.invariant = invariant
         self.dev = torch.device(device)
@@ -63,11 +76,19 @@ class GreedyDecoder:
         # physical pages in a seeded random order, so sequences' pages interleave
         self.block_table = page_permutation(self.num_pages, page_seed).view(
             max_batch, pps).contiguous().to(self.dev)
+        # each slot's pages; all are in use from the start, each by one slot
+        self._layout = self.block_table.tolist()
+        self.tables = [list(t) for t in self._layout]
+        self.pool = PagePool(self.num_pages)
+        self.pool.take([p for t in self.tables for p in t])
         shape = (self.num_pages, c.kv_heads, PAGE_SIZE, c.head_dim)
-        self.k_cache = [torch.zeros(shape, dtype=torch.bfloat16, device=self.dev)
-                        for _ in range(c.layers)]
-        self.v_cache = [torch.zeros(shape, dtype=torch.bfloat16, device=self.dev)
-                        for _ in range(c.layers)]
+        kind = dict(dtype=torch.uint8 if kv_cache == "q8" else torch.bfloat16, device=self.dev)
+        self.k_cache = [torch.zeros(shape, **kind) for _ in range(c.layers)]
+        self.v_cache = [torch.zeros(shape, **kind) for _ in range(c.layers)]
+        scales = c.layers if kv_cache == "q8" else 0
+        self.k_scale = [torch.zeros(shape[:3], **kind) for _ in range(scales)]
+        self.v_scale = [torch.zeros(shape[:3], **kind) for _ in range(scales)]
+        self.planes = self.k_cache + self.v_cache + self.k_scale + self.v_scale
         T = max_batch * self.prefill_width     # activations: the widest block
         Td = max_batch * max_width               # logits: decoding blocks only
         bf = dict(dtype=torch.bfloat16, device=self.dev)
@@ -92,6 +113,75 @@ class GreedyDecoder:
         self.batch = 0
         self.cached: List[int] = []
         self.last: List[int] = []
+        self.token_stats = None                 # token_logprobs of the last decoding block
+        self.trace_logprobs: List[List[float]] = []
+
+    # --------------------------------------------------------------------- cache
+    def _append(self, layer: int, k, v, bt, sl, cq) -> None:
+        if self.kv_cache == "q8":
+            kv_append_q8(k, v, self.k_cache[layer], self.v_cache[layer], self.k_scale[layer],
+                         self.v_scale[layer], bt, sl, cq)
+        else:
+            kv_append(k, v, self.k_cache[layer], self.v_cache[layer], bt, sl, cq)
+
+    def _attend(self, layer: int, q, bt, sl, cq, max_q: int, max_seq_len: int, out) -> None:
+        # blocks wider than a verify block: the chunked-prefill attention (same bits)
+        wide = max_q > ATTN_MAX_Q
+        rest = dict(max_q=max_q, max_seq_len=max_seq_len, scale=self.scale, out=out,
+                    want_lse=False, workspace=self.ws)
+        if self.kv_cache == "q8":
+            attend = prefill_attn_q8 if wide else verify_block_q8
+            attend(q, self.k_cache[layer], self.v_cache[layer], self.k_scale[layer],
+                   self.v_scale[layer], bt, sl, cq, **rest)
+        else:
+            attend = prefill_attn if wide else verify_block
+            attend(q, self.k_cache[layer], self.v_cache[layer], bt, sl, cq, **rest)
+
+    def _set_tables(self, tables: List[List[int]]) -> None:
+        self.tables = [list(t) for t in tables]
+        self.block_table.copy_(torch.tensor(self.tables, dtype=torch.int32))
+
+    def _own_pages(self) -> None:
+        """Back to the first layout: no page shared (what the caches hold is given up)."""
+        if self.tables != self._layout:
+            for t in self.tables:
+                self.pool.release(t)
+            self.pool.take([p for t in self._layout for p in t])
+            self._set_tables(self._layout)
+
+    def _copy(self, copies) -> None:
+        if copies:
+            src, dst = (torch.tensor(x, dtype=torch.int32, device=self.dev) for x in zip(*copies))
+            kv_copy_pages(self.planes, src, dst)
+
+    def fork(self, slot: int, n: int, first_tokens: Optional[Sequence[int]] = None) -> None:
+        """n more sequences, in the next cache slots, that continue from slot `slot`: its full
+        pages shared, its open page copied.  first_tokens: their next inputs (default: the
+        slot's own)."""
+        B = self.batch
+        if not 0 <= slot < B or n < 0 or B + n > self.max_batch:
+            raise ValueError("slot or number of forks out of range")
+        if first_tokens is not None and len(first_tokens) != n:
+            raise ValueError("one first token per fork")
+        copies = []
+        for j in range(B, B + n):
+            self.pool.release(self.tables[j])
+            pages, more = self.pool.fork(self.tables[slot], self.cached[slot])
+            self.tables[j] = pages + self.pool.alloc(len(self._layout[j]) - len(pages))
+            copies += more
+        self._set_tables(self.tables)
+        self._copy(copies)
+        self.batch = B + n
+        self.cached += [self.cached[slot]] * n
+        self.last += list(first_tokens) if first_tokens is not None else [self.last[slot]] * n
+
+    def compact(self) -> int:
+        """Moves the pages in use to the lowest indices; returns how many there are."""
+        tables = [list(t) for t in self.tables]
+        copies = self.pool.compact(tables)
+        self._set_tables(tables)
+        self._copy(copies)
+        return self.num_pages - self.pool.free_pages
 
     # ----------------------------------------------------------------- sequences
     def start(self, seq_ids: Sequence[int], seed: int,
@@ -106,6 +196,7 @@ class GreedyDecoder:
             raise ValueError(f"batch must be in [1, {self.max_batch}]")
         if c.context + self.max_width > self.max_len:
             raise ValueError("max_len leaves no room after the context")
+        self._own_pages()
         if context_fn is None:
             def context_fn(sid, layer):
                 return decoder_context(c, sid, layer, seed, device=self.dev)
@@ -116,9 +207,8 @@ class GreedyDecoder:
                 break
             for layer in range(c.layers):
                 k, v = context_fn(sid, layer)
-                kv_append(k.to(self.dev).contiguous(), v.to(self.dev).contiguous(),
-                          self.k_cache[layer], self.v_cache[layer],
-                          self.block_table[b:b + 1], one, cu)
+                self._append(layer, k.to(self.dev).contiguous(), v.to(self.dev).contiguous(),
+                             self.block_table[b:b + 1], one, cu)
         self.batch = B
         self.cached = [c.context] * B
         self.last = (list(first_tokens) if first_tokens is not None else
@@ -169,12 +259,8 @@ class GreedyDecoder:
             matmul(x, w[p + "wv"], out=self.v[:T])
             rope(q, sl, cq, c.theta)
             rope(k, sl, cq, c.theta)
-            kv_append(k, v, self.k_cache[i], self.v_cache[i], bt, sl, cq)
-            # blocks wider than a verify block: the chunked-prefill kernel (same bits)
-            attend = verify_block if max(q_lens) <= ATTN_MAX_Q else prefill_attn
-            attend(q, self.k_cache[i], self.v_cache[i], bt, sl, cq, max_q=max(q_lens),
-                   max_seq_len=max(lens), scale=self.scale, out=attn, want_lse=False,
-                   workspace=self.ws)
+            self._append(i, k, v, bt, sl, cq)
+            self._attend(i, q, bt, sl, cq, max(q_lens), max(lens), attn)
             matmul(attn.view(T, c.heads * c.head_dim), w[p + "wo"], out=o)
             add(h, o, out=h)
             rmsnorm(h, w[p + "mlp_norm"], c.eps, out=x)
@@ -187,7 +273,10 @@ class GreedyDecoder:
             return None
         rmsnorm(h, w["final_norm"], c.eps, out=x)
         matmul(x, w["lm_head"], out=self.logits[:T])
-        return argmax(self.logits[:T], out=self.tokens[:T])
+        tokens = argmax(self.logits[:T], out=self.tokens[:T])
+        if self.want_logprobs:
+            self.token_stats = token_logprobs(self.logits[:T], tokens)
+        return tokens
 
     # ------------------------------------------------------------------ prefill
     def prefill(self, prompts: Sequence[Sequence[int]], width: Optional[int] = None) -> None:
@@ -201,6 +290,7 @@ class GreedyDecoder:
             raise ValueError("1..max_batch prompts of one length >= 1")
         if not 1 <= width <= self.prefill_width or P - 1 + self.max_width > self.max_len:
             raise ValueError("width or prompt length out of range")
+        self._own_pages()
         self.batch = B
         self.cached = [0] * B
         for s0 in range(0, P - 1, width):
@@ -213,15 +303,18 @@ class GreedyDecoder:
     def snapshot(self):
         """The caches and per-sequence state, to run several decodings from one context."""
         return ([k.clone() for k in self.k_cache], [v.clone() for v in self.v_cache],
-                self.batch, list(self.cached), list(self.last))
+                self.batch, list(self.cached), list(self.last),
+                [x.clone() for x in self.k_scale + self.v_scale], [list(t) for t in self.tables])
 
     def restore(self, snap, batch: Optional[int] = None) -> None:
         """Back to a snapshot, keeping its first `batch` sequences (cache slots)."""
-        ks, vs, B, cached, last = snap
-        for dst, src in zip(self.k_cache, ks):
+        ks, vs, B, cached, last, scales, tables = snap
+        for dst, src in zip(self.planes, ks + vs + scales):
             dst.copy_(src)
-        for dst, src in zip(self.v_cache, vs):
-            dst.copy_(src)
+        if tables != self.tables:
+            self.pool = PagePool(self.num_pages)
+            self.pool.adopt(tables)
+            self._set_tables(tables)
         self.batch = B if batch is None else batch
         if not 1 <= self.batch <= B:
             raise ValueError("batch must be in [1, snapshot batch]")
@@ -233,10 +326,14 @@ class GreedyDecoder:
         """Token-by-token greedy decoding: `steps` tokens per sequence."""
         B = self.batch
         traces: List[List[int]] = [[] for _ in range(B)]
+        self.trace_logprobs = [[] for _ in range(B)]
         for _ in range(steps):
             toks = self.forward(self.last, [1] * B).tolist()
+            logps = self.token_stats.logprobs.tolist() if self.want_logprobs else None
             for b in range(B):
                 traces[b].append(toks[b])
+                if logps:
+                    self.trace_logprobs[b].append(logps[b])
                 self.cached[b] += 1
                 self.last[b] = toks[b]
         return traces
@@ -253,6 +350,7 @@ class GreedyDecoder:
         B = self.batch
         history = [[self.last[b]] for b in range(B)]
         traces: List[List[int]] = [[] for _ in range(B)]
+        self.trace_logprobs = [[] for _ in range(B)]
         blocks = accepted = 0
         while min(len(t) for t in traces) < steps:
             q_lens = [width if len(traces[b]) < steps else 1 for b in range(B)]
@@ -263,10 +361,12 @@ class GreedyDecoder:
                 ids.append(self.last[b])
                 ids.extend(drafts[b])
             greedy = self.forward(ids, q_lens).tolist()
+            logps = self.token_stats.logprobs.tolist() if self.want_logprobs else None
             blocks += 1
             t0 = 0
             for b in range(B):
                 gb = greedy[t0:t0 + q_lens[b]]
+                lb = logps[t0:t0 + q_lens[b]] if logps else []
                 t0 += q_lens[b]
                 n = 0
                 while n < q_lens[b] - 1 and drafts[b][n] == gb[n]:
@@ -274,9 +374,11 @@ class GreedyDecoder:
                 new = drafts[b][:n] + [gb[n]]
                 accepted += n
                 traces[b].extend(new)
+                self.trace_logprobs[b].extend(lb[:n + 1])
                 history[b].extend(new)
                 self.cached[b] += n + 1
                 self.last[b] = gb[n]
+        self.trace_logprobs = [t[:steps] for t in self.trace_logprobs]
         return [t[:steps] for t in traces], blocks, accepted
 
 
