@@ -10,6 +10,7 @@ call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from contextlib import nullcontext
@@ -631,16 +632,19 @@ def kv_copy_pages(planes: Sequence, src, dst, stream=None) -> None:
     pages = planes[0].shape[0] if planes[0].dim() else 0
     if pages < 1:
         raise ValueError("a plane has no pages")
-    for t in planes:
-        if t.get_device() != dev:
-            raise ValueError("planes must be CUDA tensors on the current device")
-        if t.dim() == 0 or t.shape[0] != pages or not t.is_contiguous():
-            raise ValueError("planes must be contiguous with one number of pages")
     n = len(planes)
-    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in planes])
-    sizes = (ctypes.c_int64 * n)(*[t.nbytes // pages for t in planes])
-    _check(lib().bi_kv_copy_pages(ptrs, sizes, n, pages, src.data_ptr(), dst.data_ptr(),
-                                  src.shape[0], _stream(stream)))
+    # (one pass over the planes for what is checked and passed on)
+    found = [(t.get_device(), t.is_contiguous(), t.dim() and t.size(0), t.data_ptr(), t.nbytes)
+             for t in planes]
+    for device, contiguous, first, _, _ in found:
+        if device != dev:
+            raise ValueError("planes must be CUDA tensors on the current device")
+        if not contiguous or first != pages:
+            raise ValueError("planes must be contiguous with one number of pages")
+    ptrs = array.array("Q", [f[3] for f in found])
+    sizes = array.array("q", [f[4] // pages for f in found])
+    _check(lib().bi_kv_copy_pages(ptrs.buffer_info()[0], sizes.buffer_info()[0], n, pages,
+                                  src.data_ptr(), dst.data_ptr(), src.shape[0], _stream(stream)))
 
 
 # ---------------------------------------------------------------------- device status
@@ -816,14 +820,17 @@ def token_logprobs(logits, tokens, top: int = 0, stream=None) -> TokenLogprobs:
         raise ValueError(f"top must be in [0, min(n, {LOGPROBS_MAX_TOP})]")
     dev = logits.device
     with _allocating_for(stream):
-        stats = torch.empty(3, rows, dtype=torch.float32, device=dev)
+        # (three tensors: views of one, made and freed, took 5 us more)
+        f32 = torch.float32
+        logp = torch.empty(rows, dtype=f32, device=dev)
+        entropy = torch.empty(rows, dtype=f32, device=dev)
+        lse = torch.empty(rows, dtype=f32, device=dev)
         tv = torch.empty(rows, top, dtype=torch.float32, device=dev) if top else None
         ti = torch.empty(rows, top, dtype=torch.int32, device=dev) if top else None
-    p = stats.data_ptr()
-    _check(lib().bi_token_logprobs(logits.data_ptr(), ld, dt, tokens.data_ptr(), rows, n, p,
-                                   p + 4 * rows, p + 8 * rows, int(top), _ptr(tv), _ptr(ti),
-                                   _stream(stream)))
-    return TokenLogprobs(*stats.unbind(0), tv, ti)
+    _check(lib().bi_token_logprobs(logits.data_ptr(), ld, dt, tokens.data_ptr(), rows, n,
+                                   logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(), int(top),
+                                   _ptr(tv), _ptr(ti), _stream(stream)))
+    return TokenLogprobs(logp, entropy, lse, tv, ti)
 
 
 def token_logprobs_backward(logits, tokens, lse, entropy=None, grad_logprobs=None,
