@@ -371,42 +371,28 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         tmem_alloc(tmem_slot, TMEM_COLS);
         tmem_relinquish();
     }
+    // every barrier, one per thread (one thread after the other took longer than the rest of the
+    // prologue): arrivals of its phase
+    static_assert(C::NBARS <= THREADS, "a thread per barrier");
+    if (tid < C::NBARS) {
+        uint64_t* bar = k_full + tid;
+        int count = 1;
+        if ((bar >= s_empty && bar < p_empty) || (bar >= xs_bar && bar < q_full)) count = NQ * NWG;
+        if (bar >= o_empty && bar < xs_bar) count = 4;
+        if (bar >= q_full && bar < st_bar) count = NPREP;
+        if (bar >= st_bar && bar < c_done) count = 4;
+        mbar_init(bar, uint32_t(count));
+        fence_barrier_init();
+    }
+    if (tid == 0) *abort_flag = 0;
     // With item counters the grid before this one is the call's own counter reset, which
     // waited for everything before it: the inputs are final, and only the counters need the
-    // epilogue's wait (see attention.cu).  Without, this grid waits for the previous one.
+    // counter's wait (see attention.cu).  Without, this grid waits for the previous one.
     if (!cnt) {
         pdl_wait();
         pdl_trigger();
     }
     const unsigned long long wait_ns = wait_budget_ns(err);
-    if (tid == 0) {
-        for (int i = 0; i < NSLOT; ++i) {
-            mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 1);
-            mbar_init(&v_full[i], 1);
-            mbar_init(&v_empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&s_empty[i], NQ * NWG);
-        }
-        mbar_init(p_full, NQ * NWG);
-        mbar_init(p_empty, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&o_full[i], 1);
-            mbar_init(&o_empty[i], 4);
-            mbar_init(&xs_bar[2 * i], NQ * NWG);
-            mbar_init(&xs_bar[2 * i + 1], NQ * NWG);
-            mbar_init(&q_full[i], NPREP);
-            mbar_init(&st_bar[i], 4);
-            mbar_init(&c_done[i], 1);
-            mbar_init(&drain[i], 1);
-        }
-        for (int i = 0; i < NDESC; ++i) mbar_init(&d_full[i], 1);
-        for (int i = 0; i < LEAD; ++i) mbar_init(&d_used[i], 1);
-        *abort_flag = 0;
-        fence_barrier_init();
-    }
     for (int b = tid; b < B; b += THREADS) {
         const SeqInfo si = seq_info(seq_lens, cu_q, b);
         const bool ok = seq_ok(si, max_q, max_seq_len, total_q);
