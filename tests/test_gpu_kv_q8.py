@@ -407,6 +407,61 @@ def test_rows_behind_the_last_sequence_stay(dev):
     assert bi.device_status() == bi.BI_OK
 
 
+def test_the_largest_batch(dev):
+    """1,024 sequences (the limit) of 1 to 130 tokens: sampled ones equal themselves alone."""
+    g = torch.Generator().manual_seed(3)
+    lens = [int(x) for x in torch.randint(1, 131, (1024,), generator=g)]
+    c = filled(lens, 2, 64, dev, seed=84)
+    q = rows((1024, 8, 64), 85).to(dev)
+    out, lse = attend(c, q, lens, [1] * 1024, 0.125, "decode")
+    for b in (0, 1, 511, 1022, 1023):
+        o, l = attend(c, q[b:b + 1].contiguous(), [lens[b]], [1], 0.125, "decode", sel=[b])
+        assert bits_equal(o[0], out[b]) and bits_equal(l[0], lse[b])
+    assert bi.device_status() == bi.BI_OK
+
+
+def test_caches_past_32_bit_offsets(dev):
+    """K and V caches of more than 2^32 bytes each: a sequence in their last pages gives the bits
+    it gives in small ones."""
+    Hkv, D, L, pages = 8, 128, 300, 70000
+    small = filled([L], Hkv, D, dev, seed=86)
+    big = Cache.__new__(Cache)
+    big.k, big.v = (torch.full((pages, Hkv, 64, D), POISON, dtype=torch.uint8, device=dev)
+                    for _ in range(2))
+    big.ks, big.vs = (torch.full((pages, Hkv, 64), 254, dtype=torch.uint8, device=dev)
+                      for _ in range(2))
+    big.table = i32([[pages - 1, pages - 3, pages - 2, 65536, pages - 4]], dev)
+    big.append(small.k_rows.to(dev), small.v_rows.to(dev), [L], [L])
+    q = rows((8, 32, D), 87).to(dev)
+    want, wlse = attend(small, q, [L], [8], 0.1, "verify")
+    for form in ("verify", "prefill"):
+        o, l = attend(big, q, [L], [8], 0.1, form)
+        assert bits_equal(o, want) and bits_equal(l, wlse)
+    assert bi.device_status() == bi.BI_OK
+
+
+def test_bounded_waits_run_out_and_leave_the_gpu_usable(dev):
+    """With a wait budget far below the call's runtime the kernel's waits run out: the timeout is
+    reported, and the next call with the default budget gives the right bits."""
+    L = 16388
+    c = filled([L], 8, 128, dev, seed=88)
+    q = rows((8, 32, 128), 89).to(dev)
+    want, _ = attend(c, q, [L], [8], 0.1, "verify")
+    assert bi.device_status() == bi.BI_OK
+    bi.selftest_set_wait_budget(1000)
+    try:
+        attend(c, q, [L], [8], 0.1, "verify")
+        assert bi.device_status() == bi.BI_ERR_TIMEOUT
+        attend(c, q, [L], [8], 0.1, "prefill")
+        assert bi.device_status() in (bi.BI_OK, bi.BI_ERR_TIMEOUT)
+    finally:
+        bi.selftest_set_wait_budget(0)
+    for form in ("verify", "prefill"):
+        out, _ = attend(c, q, [L], [8], 0.1, form)
+        assert bits_equal(out, want)
+    assert bi.device_status() == bi.BI_OK
+
+
 def test_empty_batch_and_zero_scale(dev):
     c = filled([70], 2, 64, dev, seed=82)
     q = torch.empty(0, 8, 64, dtype=torch.bfloat16, device=dev)
