@@ -83,8 +83,8 @@ struct Cfg {
     static constexpr int P_OFF = Q_OFF + 2 * Q_BYTES;
     static constexpr int RING_OFF = P_OFF + NT * P_BYTES;
     static constexpr int V_OFF = RING_OFF + NSLOT * SLOT_BYTES;
-    static constexpr int SCALE_OFF = V_OFF + NSLOT * SLOT_BYTES;  // two sets of
-    static constexpr int SCALE_BYTES = NT * 2 * TK;                  // [tile][K 128 | V 128]
+    static constexpr int SCALE_OFF = V_OFF + NSLOT * SLOT_BYTES;  // two sets of scale bytes,
+    static constexpr int SCALE_BYTES = 2 * TK * NT;               // [K | V][key][tile]
     static constexpr int BAR_OFF = SCALE_OFF + 2 * SCALE_BYTES;
     static constexpr int NBARS = 4 * NSLOT + 4 + 2 + 4 + 4 + 2 + 4 + NDESC + LEAD + 2;
     static constexpr int DESC_OFF = (BAR_OFF + NBARS * 8 + 8 + 15) / 16 * 16;
@@ -93,7 +93,7 @@ struct Cfg {
     // the maxima exchanged within the softmax groups (two buffers: a warp may be an item ahead)
     static constexpr int XS_FLOATS = 4 * (NQ + 1) * QR + 2 * QR + 2 * NQ * QR;
     static constexpr int MISC_OFF = XS_OFF + XS_FLOATS * 4;
-    static constexpr int MISC_INTS = (MAX_BATCH + 1) + 1;
+    static constexpr int MISC_INTS = (MAX_BATCH + 1) + 1 + 4;
     static constexpr size_t SMEM = 1024 + size_t(MISC_OFF) + MISC_INTS * 4;
     // K-major and MN-major rows of D bytes: the 128- or 64-byte swizzle, groups of 8 rows
     static constexpr uint32_t LAYOUT = D == 128 ? 2 : 4;
@@ -297,13 +297,13 @@ struct alignas(16) Item {
     int t0;      // its row in q and out
     int ntok;    // the tile's tokens
     int h;
-    int bq;      // 2 * b + the buffer of its Q tile
+    int bq;      // 4 * b + 2 when every row sees every key of the chunk + its Q tile's buffer
 };
 struct alignas(16) ItemSlot {
     Item it;
     int phys[CHUNK / PAGE];  // physical pages, -1 for those that are not there or out of range
 };
-static_assert(sizeof(ItemSlot) == 64, "four 16-byte pieces");
+static_assert(sizeof(ItemSlot) == 64 && CHUNK / PAGE == 8, "four 16-byte pieces");
 
 __device__ __forceinline__ int tiles_of(int npages) { return (npages + TPAGES - 1) / TPAGES; }
 
@@ -361,7 +361,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
     float* q_fac = xs + 4 * (NQ + 1) * QR;                   // [2][QR]
     float* x_max = q_fac + 2 * QR;                           // [2][NQ][QR]
     int* prefix = reinterpret_cast<int*>(smem + C::MISC_OFF);  // [B + 1]
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(prefix + MAX_BATCH + 1);
+    int* scale_odd = prefix + MAX_BATCH + 1;  // [2 sets][2]: a scale byte of 254 or 255 among them
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(scale_odd + 4);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = Hq / Hkv;
@@ -385,6 +386,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
         fence_barrier_init();
     }
     if (tid == 0) *abort_flag = 0;
+    if (tid < 4) scale_odd[tid] = 0;
     // With item counters the grid before this one is the call's own counter reset, which
     // waited for everything before it: the inputs are final, and only the counters need the
     // counter's wait (see attention.cu).  Without, this grid waits for the previous one.
@@ -493,25 +495,26 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     last_h = it.h;
                 }
             }
-            it.bq = 2 * b + (qgen & 1);
+            it.bq = 4 * b + (qgen & 1);
             it.npages = 0;
             if (left > 0) {
                 it.npages = min(CHUNK / PAGE, (it.pos0 + it.ntok - it.key0 + PAGE - 1) / PAGE);
                 --left;
             }
             ItemSlot* slot = &items[j % NDESC];
-            if (lane < CHUNK / PAGE) {
-                int phys = -1;
-                if (lane < it.npages) {
-                    const int pidx = it.key0 / PAGE + lane;
-                    if (pidx < max_pages) phys = block_table[int64_t(b) * max_pages + pidx];
-                    if (phys < 0 || phys >= num_pages) {
-                        phys = -1;
-                        latch_error(err, kErrDeviceArg);
-                    }
+            int phys = -1;
+            if (lane < it.npages) {
+                const int pidx = it.key0 / PAGE + lane;
+                if (pidx < max_pages) phys = block_table[int64_t(b) * max_pages + pidx];
+                if (phys < 0 || phys >= num_pages) {
+                    phys = -1;
+                    latch_error(err, kErrDeviceArg);
                 }
-                slot->phys[lane] = phys;
             }
+            if (lane < CHUNK / PAGE) slot->phys[lane] = phys;
+            if ((__ballot_sync(0xffffffffu, phys >= 0) & 0xffu) == 0xffu &&
+                it.key0 + CHUNK - 1 <= it.pos0)
+                it.bq |= 2;
             if (lane == 0) slot->it = it;
             __syncwarp();
             if (lane == 0) mbar_arrive(&d_full[j % NDESC]);
@@ -652,16 +655,20 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const Item it = item_at(item);
             if (it.npages == 0) break;
             const int buf = item & 1, qbuf = it.bq & 1;
-            // scale bytes: 16 lanes read a page's 64 as words, K and V
-            uint32_t ks[NT / NPREP], vs[NT / NPREP];
+            // scale bytes of page pp of every tile: lanes 0..15 read K's as words, 16..31 V's
+            uint32_t sw[2 / NPREP][NT];
+            uint32_t odd = 0;
 #pragma unroll
-            for (int n = 0; n < NT / NPREP; ++n) {
-                const int phys = items[item % NDESC].phys[(n * NPREP + pw) * TPAGES + (lane >> 4)];
-                ks[n] = vs[n] = 0;
-                if (phys >= 0) {
-                    const int64_t at = (int64_t(phys) * Hkv + it.h) * (PAGE / 4) + (lane & 15);
-                    ks[n] = reinterpret_cast<const uint32_t*>(k_scale)[at];
-                    vs[n] = reinterpret_cast<const uint32_t*>(v_scale)[at];
+            for (int n = 0; n < 2 / NPREP; ++n) {
+                const int pp = NPREP == 2 ? pw : n;
+                const uint32_t* src =
+                    reinterpret_cast<const uint32_t*>(lane < 16 ? k_scale : v_scale);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const int phys = items[item % NDESC].phys[i * TPAGES + pp];
+                    sw[n][i] = 0x7f7f7f7fu;
+                    if (phys >= 0)
+                        sw[n][i] = src[(int64_t(phys) * Hkv + it.h) * (PAGE / 4) + (lane & 15)];
                 }
             }
             bool free = false;
@@ -726,13 +733,26 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
             if (!ok) break;
             if (!free && !wait(&s_empty[buf], (uint32_t(item >> 1) & 1u) ^ 1u)) break;
-            uint32_t* sc = reinterpret_cast<uint32_t*>(sScale + buf * C::SCALE_BYTES);
+            // stored key by key, the tiles' four bytes in one word
 #pragma unroll
-            for (int n = 0; n < NT / NPREP; ++n) {
-                const int tile = n * NPREP + pw;
-                sc[tile * (2 * TK / 4) + lane] = ks[n];
-                sc[tile * (2 * TK / 4) + TK / 4 + lane] = vs[n];
+            for (int n = 0; n < 2 / NPREP; ++n) {
+                const int pp = NPREP == 2 ? pw : n;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {  // a byte of 254 or 255?
+                    const uint32_t z = ~sw[n][i] & 0xfefefefeu;
+                    odd |= (z - 0x01010101u) & ~z & 0x80808080u;
+                }
+                const uint32_t a = __byte_perm(sw[n][0], sw[n][1], 0x5140);
+                const uint32_t b = __byte_perm(sw[n][2], sw[n][3], 0x5140);
+                const uint32_t c = __byte_perm(sw[n][0], sw[n][1], 0x7362);
+                const uint32_t d = __byte_perm(sw[n][2], sw[n][3], 0x7362);
+                *reinterpret_cast<uint4*>(sScale + buf * C::SCALE_BYTES + (lane >> 4) * (TK * NT) +
+                                          (pp * PAGE + (lane & 15) * 4) * NT) =
+                    make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632),
+                               __byte_perm(c, d, 0x5410), __byte_perm(c, d, 0x7632));
             }
+            odd = __any_sync(0xffffffffu, odd != 0) ? 1u : 0u;
+            if (lane == 0) scale_odd[buf * 2 + pw] = int(odd);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[buf]);
@@ -751,7 +771,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 if (!wait(&st_bar[item & 1], uint32_t(item >> 1) & 1u)) break;
                 if (lane == 0) {
                     asm volatile("fence.acq_rel.gpu;" ::: "memory");
-                    atomicAdd(cnt + (it.bq >> 1) * Hkv + it.h, 1u);
+                    atomicAdd(cnt + (it.bq >> 2) * Hkv + it.h, 1u);
                     mbar_arrive(&c_done[item & 1]);
                 }
                 __syncwarp();
@@ -840,16 +860,11 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 f[r / 2 + 1] = make_float2(x.z, x.w);
             }
             // t of this thread's keys (one of each tile), and each row's maximum
-            const uint8_t* sc = sScale + ob * C::SCALE_BYTES + key;
-            uint32_t ksc[NT], vsc[NT], dead = 0;  // dead: a bit per tile
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                ksc[i] = sc[i * 2 * TK];
-                vsc[i] = sc[i * 2 * TK + TK];
-                const bool live = items[item % NDESC].phys[i * TPAGES + key / PAGE] >= 0 &&
-                                  it.key0 + i * TK + key < it.L;
-                if (!live) dead |= 1u << i;
-            }
+            const uint32_t* sc =
+                reinterpret_cast<const uint32_t*>(sScale + ob * C::SCALE_BYTES) + key;
+            const uint32_t kw = sc[0], vw = sc[TK];
+            const bool odd = (scale_odd[ob * 2] | scale_odd[ob * 2 + 1]) != 0;
+            const bool all_seen = (it.bq & 2) != 0;  // every row sees every key
             wait(&s_full[ob], ipar);
             tc_fence_after_sync();
             uint32_t sv[NT][RPW];
@@ -857,29 +872,53 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[ob]);
+            // the scales of this thread's keys: 2^x, y, 2^-y
+            float ka[NT], vb[NT], vinv[NT];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const uint32_t ks = i == 0 ? kw << 23 : i == 1 ? kw << 15 : i == 2 ? kw << 7 : kw >> 1;
+                const uint32_t vs = i == 0 ? vw << 23 : i == 1 ? vw << 15 : i == 2 ? vw << 7 : vw >> 1;
+                ka[i] = __uint_as_float(ks & 0x7f800000u);  // (a byte of 0: 2^-127 scores as 0)
+                // 2^23 + byte, less 2^23 + 127
+                vb[i] = __uint_as_float(__byte_perm(vw, 0x4b000000u, 0x7650 | i)) - 8388735.f;
+                vinv[i] = __uint_as_float(0x7f000000u - (vs & 0x7f800000u));
+            }
+            if (odd) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const uint32_t ks = (kw >> (8 * i)) & 0xffu, vs = (vw >> (8 * i)) & 0xffu;
+                    ka[i] = e8m0(ks);
+                    vb[i] = vs == 255 ? __int_as_float(0x7fc00000) : float(int(vs) - 127);
+                    vinv[i] = e8m0_inv(vs);
+                }
+            }
             float t[NT][RPW], mx[RPW];
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                const float ka = e8m0(ksc[i]);
-                const float vb =
-                    vsc[i] == 255 ? __int_as_float(0x7fc00000) : float(int(vsc[i]) - 127);
 #pragma unroll
                 for (int r = 0; r < RPW; r += 2) {
                     const float2 s2 = make_float2(__uint_as_float(sv[i][r]),
                                                   __uint_as_float(sv[i][r + 1]));
-                    const float2 x = fma2(mul2(s2, make_float2(ka, ka)), f[r / 2],
-                                          make_float2(vb, vb));
+                    const float2 x = fma2(mul2(s2, make_float2(ka[i], ka[i])), f[r / 2],
+                                          make_float2(vb[i], vb[i]));
                     t[i][r] = x.x;
                     t[i][r + 1] = x.y;
                 }
             }
-            // causal mask, unless every row sees the whole chunk: row r (token r / G) sees the
-            // key that is `ahead` of the first token when r / G >= ahead
-            if (!__all_sync(0xffffffffu, dead == 0 && it.key0 + CHUNK - 1 <= it.pos0)) {
+            // causal mask: row r (token r / G) sees the key that is `ahead` of the first token
+            // when r / G >= ahead; none sees a key past the sequence's end or of an invalid page
+            uint32_t dead = 0;  // a bit per tile
+            if (!all_seen) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    const int ahead = it.key0 + i * TK + key - it.pos0;
-                    const int first = (dead >> i) & 1u ? QR : max(0, ahead) * G;
+                    const int kp = it.key0 + i * TK + key, ahead = kp - it.pos0;
+                    const bool live =
+                        items[item % NDESC].phys[i * TPAGES + key / PAGE] >= 0 && kp < it.L;
+                    if (!live) {
+                        dead |= 1u << i;
+                        vinv[i] = 0.f;
+                    }
+                    const int first = live ? max(0, ahead) * G : QR;
 #pragma unroll
                     for (int r = 0; r < RPW; ++r)
                         t[i][r] = row0 + r >= first ? t[i][r] : kHidden;
@@ -922,7 +961,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             uint8_t* pbuf = sP + (row0 & 15);
 #pragma unroll
             for (int i = 0; i < NT; ++i) {  // (tiles past the item's last write zeros)
-                const float vi = (dead >> i) & 1u ? 0.f : e8m0_inv(vsc[i]);
+                const float vi = vinv[i];
                 uint32_t hi[RPW / 4], lo[RPW / 4];
 #pragma unroll
                 for (int r = 0; r < RPW; r += 4) {

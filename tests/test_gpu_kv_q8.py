@@ -316,6 +316,42 @@ def test_attention_of_hard_rows(dev, kind):
     ref.check_attention(out, lse, r, kind)
 
 
+def test_caches_written_by_others(dev):
+    """Any codes and scale bytes the format allows, not only what the append writes: K scales of 0
+    and 1 (scores of nothing), the largest ones, V scales far from each other; rows of NaN (byte
+    255) whose codes are not zero reach the queries that see them and no others."""
+    L, Hkv, D, Hq = 700, 2, 128, 8
+    c = filled([L], Hkv, D, dev, seed=52)
+    g = torch.Generator().manual_seed(53)
+    codes = torch.randint(0, 256, c.k.shape, generator=g, dtype=torch.int32)
+    codes = torch.where((codes & 0x7F) == 0x7F, codes - 1, codes).to(torch.uint8)
+    c.k.copy_(codes.flip(0))
+    c.v.copy_(codes)
+    c.ks.copy_(torch.randint(112, 119, c.ks.shape, generator=g))
+    c.vs.copy_(torch.randint(100, 140, c.vs.shape, generator=g))
+    page = c.table[0].long()
+    c.ks[page[0], :, ::5] = 0
+    c.ks[page[3], 1, 3::7] = 1
+    q = rows((8, Hq, D), 54)
+    out, lse = attend(c, q.to(dev), [L], [8], D ** -0.5, "verify")
+    r = ref.attention(q.double().numpy(), *c.values(), c.table[0].tolist(), L, 8, D ** -0.5, 4)
+    ref.check_attention(out, lse, r)
+    at = (int(page[(L - 3) // 64]), 1, (L - 3) % 64)   # seen by the last three tokens, head 1
+    for scale in (c.ks, c.vs):
+        kept = int(scale[at])
+        scale[at] = 255
+        o, l = attend(c, q.to(dev), [L], [8], D ** -0.5, "verify")
+        assert bool(torch.isnan(o[5:, 4:]).all())
+        assert bits_equal(o[:5], out[:5]) and bits_equal(o[5:, :4].contiguous(),
+                                                         out[5:, :4].contiguous())
+        scale[at] = kept
+    c.vs.fill_(254)
+    c.v.copy_(torch.where(codes.to(dev) < 128, 1, 129))  # +-2^-9 * 2^127 = +-2^118
+    out, lse = attend(c, q.to(dev), [L], [8], D ** -0.5, "verify")
+    r = ref.attention(q.double().numpy(), *c.values(), c.table[0].tolist(), L, 8, D ** -0.5, 4)
+    ref.check_attention(out, lse, r)
+
+
 def test_query_sizes(dev):
     """Queries of zeros, and with elements 2^30 apart."""
     L, Hkv, D, Hq = 100, 1, 64, 4
