@@ -52,7 +52,8 @@ bi_status bi_mean(const void* x, int64_t ldx, int x_dtype, int64_t rows, int64_t
  * sampler reports for the tokens it chose and a trainer recomputes for the same tokens.
  *   x        [rows, n] logits, dtype x_dtype (BI_BF16, BI_F16 or BI_F32), row stride
  *            ldx >= n, aligned to its element size (rows that are 16-byte aligned are read
- *            128 bits at a time; the arithmetic is the same either way).  1 <= n < 2^31.
+ *            128 bits at a time; the arithmetic is the same either way).
+ *            1 <= n <= BI_LOGPROBS_MAX_N.
  *   tokens   int32 [rows]: the scored token of each row.  -1 scores nothing (padding): its
  *            logp is 0.  Any other id outside [0, n) gives NaN and sets BI_ERR_DEVICE_ARG
  *            in the device error word.
@@ -68,6 +69,7 @@ bi_status bi_mean(const void* x, int64_t ldx, int x_dtype, int64_t rows, int64_t
  *   the number of rows, on the other rows, on top, or on alignment and stride.  A row with a NaN
  *   or +inf, or of nothing but -inf, gives NaN (ids are still ranked). */
 #define BI_LOGPROBS_MAX_TOP 32
+#define BI_LOGPROBS_MAX_N (0x7fffffff - 0x3fff) /* 2^31 - 2^14 */
 bi_status bi_token_logprobs(const void* x, int64_t ldx, int x_dtype, const int32_t* tokens,
                             int64_t rows, int64_t n, float* logp, float* entropy, float* lse,
                             int64_t top, float* top_logp, int32_t* top_ids, bi_stream_t stream);

@@ -569,6 +569,8 @@ def _attend_q8(fn, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
     if out is not None or lse is not None or workspace is not None:
         _on_current_device(out=out, lse=lse, workspace=workspace)
         _attn_out(q, q if out is None else out, lse, False)  # (checks what the caller gave)
+        if workspace is not None and not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
     with _allocating_for(stream):
         if out is None:
             out = torch.empty_like(q)

@@ -41,9 +41,9 @@
 // Warps: one, two or four softmax groups of four warps (4 or 8 query rows each), four epilogue
 // warps, the scheduler, a TMA producer for K and one for V, the S issuer (and TMEM owner), the
 // P V issuer, the counter, one or two warps that split Q and fetch the scale bytes.  One
-// persistent CTA per SM; work items (sequence, chunk, query tile, KV head) are enumerated on the device.  All waits
-// are bounded; the one barrier that warps meet in, a softmax group's, is left by all of them
-// together.
+// persistent CTA per SM; work items (sequence, chunk, query tile, KV head) are enumerated on
+// the device.  All waits are bounded; the one barrier that warps meet in, a softmax group's,
+// is left by all of them together.
 //
 // Bound by memory: 2 * (D + 1) bytes per key and KV head against 4 * 32 * D operations.
 #include "attn_common.cuh"
@@ -89,8 +89,9 @@ struct Cfg {
     static constexpr int NBARS = 4 * NSLOT + 4 + 2 + 4 + 4 + 2 + 4 + NDESC + LEAD + 2;
     static constexpr int DESC_OFF = (BAR_OFF + NBARS * 8 + 8 + 15) / 16 * 16;
     static constexpr int XS_OFF = DESC_OFF + NDESC * 64;
-    // per item (four buffers): four warps' row sums and the row maxima; per Q buffer the row factors;
-    // the maxima exchanged within the softmax groups (two buffers: a warp may be an item ahead)
+    // per item (four buffers): four warps' row sums and the row maxima; per Q buffer the row
+    // factors; the maxima exchanged within the softmax groups (two buffers: a warp may be an
+    // item ahead)
     static constexpr int XS_FLOATS = 4 * (NQ + 1) * QR + 2 * QR + 2 * NQ * QR;
     static constexpr int MISC_OFF = XS_OFF + XS_FLOATS * 4;
     static constexpr int MISC_INTS = (MAX_BATCH + 1) + 1 + 4;
@@ -797,7 +798,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const int64_t idx =
                 store ? (int64_t(it.t0 + j) * Hq + int64_t(it.h) * G + (lane - j * G)) * maxC + c
                       : -1;
-            if (!wait(&xs_bar[item & 3], uint32_t(item >> 2) & 1u) || !wait(&o_full[ob], par)) break;
+            if (!wait(&xs_bar[item & 3], uint32_t(item >> 2) & 1u) || !wait(&o_full[ob], par))
+                break;
             tc_fence_after_sync();
             if (ew == 0 && store) {
                 const float* x = xs + (item & 3) * ((NQ + 1) * QR);
@@ -876,8 +878,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             float ka[NT], vb[NT], vinv[NT];
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                const uint32_t ks = i == 0 ? kw << 23 : i == 1 ? kw << 15 : i == 2 ? kw << 7 : kw >> 1;
-                const uint32_t vs = i == 0 ? vw << 23 : i == 1 ? vw << 15 : i == 2 ? vw << 7 : vw >> 1;
+                const int up = 23 - 8 * i;  // byte i to the exponent's place
+                const uint32_t ks = up > 0 ? kw << (up & 31) : kw >> (-up & 31);
+                const uint32_t vs = up > 0 ? vw << (up & 31) : vw >> (-up & 31);
                 ka[i] = __uint_as_float(ks & 0x7f800000u);  // (a byte of 0: 2^-127 scores as 0)
                 // 2^23 + byte, less 2^23 + 127
                 vb[i] = __uint_as_float(__byte_perm(vw, 0x4b000000u, 0x7650 | i)) - 8388735.f;
@@ -1067,8 +1070,8 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
     // head_dim 128 are bound by memory and keep the finer dealing (ragged batch of 64: 231 us
     // without, 235 to 240 with).
     int run = 1;
-    while (run < 8 && (D == 64 || RPW * NWG > 4) && a.batch * ((maxC + 2 * run - 1) / (2 * run)) * tiles * a.hkv >=
-                          8 * int64_t(dev.num_sms))
+    auto units = [&](int r) { return a.batch * ((maxC + r - 1) / r) * tiles * a.hkv; };
+    while (run < 8 && (D == 64 || RPW * NWG > 4) && units(2 * run) >= 8 * int64_t(dev.num_sms))
         run *= 2;
     float* ws_o = static_cast<float*>(workspace);
     float* ws_ml = ws_o + a.total_q * a.hq * int64_t(maxC) * D;

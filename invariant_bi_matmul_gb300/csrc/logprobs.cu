@@ -54,7 +54,9 @@ constexpr float kNaN = __builtin_nanf("");
 template <int DT>
 constexpr int kSize = DT == BI_F32 ? 4 : 2;
 template <int DT>  // -inf, in both halves for 16 bits
-constexpr uint32_t kMinusInf = DT == BI_F32 ? 0xff800000u : DT == BI_F16 ? 0xfc00fc00u : 0xff80ff80u;
+constexpr uint32_t kMinusInf = DT == BI_F32   ? 0xff800000u
+                               : DT == BI_F16 ? 0xfc00fc00u
+                                              : 0xff80ff80u;
 
 template <int DT>
 __device__ __forceinline__ float load1(const void* p, int64_t i) {
@@ -77,7 +79,8 @@ __device__ __forceinline__ uint4 load_vec(const char* row, bool vec, int g, int 
                 o[k] = reinterpret_cast<const uint32_t*>(row)[i];
             } else {
                 const uint32_t h = reinterpret_cast<const uint16_t*>(row)[i];
-                o[k >> 1] = k & 1 ? (o[k >> 1] & 0xffffu) | (h << 16) : (o[k >> 1] & 0xffff0000u) | h;
+                o[k >> 1] = k & 1 ? (o[k >> 1] & 0xffffu) | (h << 16)
+                                  : (o[k >> 1] & 0xffff0000u) | h;
             }
         }
     }
@@ -407,7 +410,8 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
             const uint32_t g = gmax[tid];
             int above = 0;
 #pragma unroll 16
-            for (int i = 0; i < kGroups; ++i) above += gmax[i] > g || (gmax[i] == g && i < tid) ? 1 : 0;
+            for (int i = 0; i < kGroups; ++i)
+                above += gmax[i] > g || (gmax[i] == g && i < tid) ? 1 : 0;
             if (above == max(want, 1) - 1) floor_order = g;
         }
         __syncthreads();
@@ -664,8 +668,10 @@ bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % 
 bi_status check_rows(const char* fn, int dtype, int64_t rows, int64_t n, int64_t ldx) {
     if (dtype != BI_BF16 && dtype != BI_F16 && dtype != BI_F32)
         return fail(BI_ERR_INVALID_ARG, "%s: x_dtype must be BI_BF16, BI_F16 or BI_F32", fn);
-    if (rows < 0 || n < 1 || n > kI32Max - 4)
-        return fail(BI_ERR_INVALID_ARG, "%s: need rows >= 0 and 1 <= n < 2^31", fn);
+    // (indices of a row's padded last vectors stay within 32 bits)
+    if (rows < 0 || n < 1 || n > BI_LOGPROBS_MAX_N)
+        return fail(BI_ERR_INVALID_ARG, "%s: need rows >= 0 and 1 <= n <= %d", fn,
+                    BI_LOGPROBS_MAX_N);
     if (ldx < n) return fail(BI_ERR_INVALID_ARG, "%s: ldx < n", fn);
     if (rows > kI32Max) return fail(BI_ERR_UNSUPPORTED, "%s: too many rows", fn);
     return BI_OK;

@@ -578,3 +578,37 @@ def test_repeats_are_identical(dev):
         o, l = attend(c, q, [3000, 10], [8, 4], 0.1, "verify")
         seen.add(bytes(o.view(torch.int16).cpu().numpy()) + bytes(l.cpu().numpy()))
     assert len(seen) == 1
+
+
+def test_refusals(dev):
+    """Arguments that the binding turns away before anything is launched."""
+    c = filled([70, 3], 2, 64, dev)
+    k, v, ks, vs = c.parts()
+    q = rows((2, 4, 64), 90).to(dev)
+    good = dict(q=q, k_cache=k, v_cache=v, k_scale=ks, v_scale=vs, block_table=c.table,
+                seq_lens=i32([70, 3], dev), max_seq_len=70, scale=0.125)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=dev)
+    bi.decode_attn_q8(**good, workspace=ws)
+    for bad in (dict(q=q.float()), dict(q=q[:1]), dict(q=q[:, :, :32]), dict(q=q.cpu()),
+                dict(k_cache=k[:1]), dict(k_cache=k.float()), dict(k_scale=ks[:, :, :32]),
+                dict(v_scale=vs.transpose(1, 2)), dict(v_cache=v.transpose(0, 1)),
+                dict(block_table=c.table.long()), dict(block_table=c.table[:1]),
+                dict(seq_lens=i32([70, 3, 1], dev)), dict(out=torch.empty_like(q).float()),
+                dict(out=torch.empty(2, 4, 128, dtype=q.dtype, device=dev)[:, :, :64]),
+                dict(lse=torch.empty(2, 3, device=dev)), dict(workspace=ws[::2]),
+                dict(workspace=ws[:1].expand(1 << 20)), dict(workspace=ws[:64]),
+                dict(max_seq_len=1 << 20), dict(scale=float("nan"))):
+        with pytest.raises((ValueError, TypeError, bi.BIError)):
+            bi.decode_attn_q8(**{**good, **bad})
+    cu = i32([0, 1, 2], dev)
+    new = rows((2, 2, 64), 91).to(dev)
+    for bad in ((new.float(), new, cu), (new, new[:1], cu), (new[:, :1], new[:, :1], cu),
+                (new, new, cu[:2]), (new, new, cu.long()), (new.cpu(), new, cu)):
+        with pytest.raises((ValueError, TypeError, bi.BIError)):
+            bi.kv_append_q8(bad[0], bad[1], k, v, ks, vs, c.table, i32([70, 3], dev), bad[2])
+    src = i32([0], dev)
+    for bad in (([k], src, src[:0]), ([k], src.long(), src.long()), ([k.cpu()], src, src),
+                ([k, v[:1]], src, src), ([k.transpose(0, 1)], src, src)):
+        with pytest.raises((ValueError, TypeError, bi.BIError)):
+            bi.kv_copy_pages(*bad)
+    assert bi.device_status() == 0

@@ -36,7 +36,8 @@ def reference(x, tok):
     p = torch.exp(logp)
     H = -torch.where(p > 0, p * logp, torch.zeros_like(p)).sum(-1)
     at = tok.long().clamp(min=0)
-    lp = torch.where(tok >= 0, logp.gather(1, at.unsqueeze(1))[:, 0], torch.zeros(len(tok)).double())
+    lp = torch.where(tok >= 0, logp.gather(1, at.unsqueeze(1))[:, 0],
+                     torch.zeros(len(tok)).double())
     return lp, H, torch.logsumexp(x, -1), logp
 
 
@@ -250,7 +251,8 @@ def test_empty_captured_and_streams(dev):
     graph.replay()
     torch.cuda.synchronize()
     wr, wd = both()
-    assert all(bits_equal(a, b) for a, b in zip(r[:4], wr[:4])) and torch.equal(r.top_ids, wr.top_ids)
+    assert all(bits_equal(a, b) for a, b in zip(r[:4], wr[:4]))
+    assert torch.equal(r.top_ids, wr.top_ids)
     assert bits_equal(d, wd)
     s = torch.cuda.Stream()
     torch.cuda.synchronize()
@@ -271,3 +273,23 @@ def test_many_rows(dev):
     p = torch.softmax(x.double(), -1)
     p[torch.arange(rows), tok.long()] -= 1
     assert (d + p).abs().max() < 2e-5
+
+
+def test_refusals(dev):
+    x, tok = logits(4, 40, torch.float32, 17).to(dev), tokens_of(4, 40, 18).to(dev)
+    one = torch.ones(4, device=dev)
+    for bad in (dict(logits=x.t()), dict(logits=x[0]), dict(logits=x.double()),
+                dict(logits=x[:1].expand(4, 40)), dict(tokens=tok.long()), dict(tokens=tok[:3]),
+                dict(tokens=tok.cpu()), dict(top=41), dict(top=-1)):
+        with pytest.raises((ValueError, TypeError, bi.BIError)):
+            bi.token_logprobs(**{**dict(logits=x, tokens=tok), **bad})
+    r = bi.token_logprobs(x, tok)
+    good = dict(logits=x, tokens=tok, lse=r.lse, entropy=r.entropy, grad_logprobs=one,
+                grad_entropy=one)
+    for bad in (dict(lse=r.lse[:3]), dict(lse=None), dict(entropy=None), dict(lse=r.lse.double()),
+                dict(grad_logprobs=None, grad_entropy=None), dict(out=x.half()),
+                dict(grad_logprobs=torch.ones(8, device=dev)[::2]), dict(out=x[:, :39]),
+                dict(out=x[:1].expand(4, 40)), dict(out=x.cpu())):
+        with pytest.raises((ValueError, TypeError, bi.BIError)):
+            bi.token_logprobs_backward(**{**good, **bad})
+    assert bi.device_status() == 0

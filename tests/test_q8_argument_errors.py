@@ -59,7 +59,8 @@ def attend(L, form, **kw):
     (dict(max_seq_len=257), INVALID), (dict(max_seq_len=0), INVALID), (dict(ws_bytes=16), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(q=P + 2), UNSUPPORTED), (dict(ks=None), INVALID),
     (dict(vs=P + 8), UNSUPPORTED), (dict(ws=P + 8), UNSUPPORTED), (dict(out=None), INVALID),
-    (dict(lse=P + 2), UNSUPPORTED), (dict(k=P + 8), UNSUPPORTED), (dict(batch=1025, total_q=1025), UNSUPPORTED),
+    (dict(lse=P + 2), UNSUPPORTED), (dict(k=P + 8), UNSUPPORTED),
+    (dict(batch=1025, total_q=1025), UNSUPPORTED),
     (dict(hq=264, hkv=8), UNSUPPORTED), (dict(batch=-1), INVALID), (dict(num_pages=0), INVALID),
     (dict(num_pages=1 << 23), UNSUPPORTED), (dict(batch=0, total_q=0, q=None), OK)])
 def test_attention_refusals(L, form, change, want):
@@ -111,6 +112,7 @@ def logprobs(L, **kw):
     (dict(top=1), INVALID), (dict(x=None), INVALID), (dict(tok=None), INVALID),
     (dict(x=P + 2), INVALID), (dict(ti=P + 2, tl=P, top=1), INVALID),
     (dict(n=1 << 31, ldx=1 << 31), INVALID), (dict(rows=1 << 31), UNSUPPORTED),
+    (dict(n=(1 << 31) - (1 << 14) + 1, ldx=1 << 31), INVALID),
     (dict(rows=0, x=None), OK)])
 def test_logprobs_refusals(L, change, want):
     assert logprobs(L, **change) == want
@@ -128,7 +130,8 @@ def backward(L, **kw):
 @pytest.mark.parametrize("change,want", [
     (dict(dt=3), INVALID), (dict(lddx=99), INVALID), (dict(gl=None, gh=None), INVALID),
     (dict(ent=None), INVALID), (dict(dx=P, lddx=104), INVALID), (dict(dx=P + 1), INVALID),
-    (dict(lse=None), INVALID), (dict(rows=0, x=None), OK)])
+    (dict(lse=None), INVALID), (dict(rows=0, x=None), OK),
+    (dict(n=(1 << 31) - (1 << 14) + 1, ldx=1 << 31, lddx=1 << 31), INVALID)])
 def test_backward_refusals(L, change, want):
     assert backward(L, **change) == want
 
