@@ -127,9 +127,15 @@ def _check(status: int) -> None:
         raise BIError(status, msg)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream) -> int:
@@ -456,12 +462,11 @@ def _on_current_device(**tensors):
 
 def _device_of(t) -> int:
     """The CUDA device of t if that is the current one, else -1."""
-    torch = _torch()
-    if isinstance(t, torch.Tensor) and t.is_cuda:
+    try:
         dev = t.get_device()
-        if dev == torch.cuda.current_device():
-            return dev
-    return -1
+    except AttributeError:  # not a tensor
+        return -1
+    return dev if dev >= 0 and dev == _torch()._C._cuda_getDevice() else -1
 
 
 def _all(dev, *tensors) -> bool:
@@ -470,12 +475,22 @@ def _all(dev, *tensors) -> bool:
     tensor at a time took longer than the kernels of a small call."""
     if dev < 0:
         return False
-    Tensor = _torch().Tensor
-    for t, dtype, ndim in tensors:
-        if not (isinstance(t, Tensor) and t.dtype is dtype and t.dim() == ndim
-                and t.get_device() == dev and t.is_contiguous()):
-            return False
+    try:
+        for t, dtype, ndim in tensors:
+            if (t.get_device() != dev or t.dtype is not dtype or t.dim() != ndim
+                    or not t.is_contiguous()):
+                return False
+    except AttributeError:  # not a tensor
+        return False
     return True
+
+
+def _stream_on(stream, dev) -> int:
+    """_stream, for a call on the current device dev."""
+    return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+_HERE = nullcontext()
 
 
 def _allocating_for(stream):
@@ -483,11 +498,11 @@ def _allocating_for(stream):
     call on another stream than the current one is taken from, and goes back to, the pool of
     the stream that uses it."""
     if stream is None:
-        return nullcontext()
+        return _HERE
     torch = _torch()
     if isinstance(stream, int):
         if stream == torch.cuda.current_stream().cuda_stream:
-            return nullcontext()
+            return _HERE
         stream = torch.cuda.ExternalStream(stream)
     return torch.cuda.stream(stream)
 
@@ -495,7 +510,8 @@ def _allocating_for(stream):
 def _paged_common_q8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens):
     torch = _torch()
     u8, i32 = torch.uint8, torch.int32
-    if not _all(_device_of(k_cache), (k_cache, u8, 4), (v_cache, u8, 4), (k_scale, u8, 3),
+    dev = _device_of(k_cache)
+    if not _all(dev, (k_cache, u8, 4), (v_cache, u8, 4), (k_scale, u8, 3),
                 (v_scale, u8, 3), (block_table, i32, 2), (seq_lens, i32, 1)):
         _need(k_cache, u8, "k_cache", 4)
         _need(v_cache, u8, "v_cache", 4)
@@ -509,11 +525,12 @@ def _paged_common_q8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens):
     shape = k_cache.shape
     if shape != v_cache.shape:
         raise ValueError("k_cache and v_cache shapes differ")
-    if k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
+    if not k_scale.shape == v_scale.shape == shape[:3]:
         raise ValueError("k_scale and v_scale must be [num_pages, Hkv, page]")
-    if block_table.shape[0] != seq_lens.shape[0]:
+    batch, max_pages = block_table.shape
+    if seq_lens.shape[0] != batch:
         raise ValueError("block_table and seq_lens disagree on the batch")
-    return shape
+    return dev, batch, max_pages, *shape
 
 
 def kv_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q,
@@ -521,41 +538,39 @@ def kv_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, 
     """kv_append into an 8-bit cache: uint8 E4M3 codes [num_pages, Hkv, 64, D] and one E8M0
     scale byte per token and head [num_pages, Hkv, 64] (include/bi.h has the format)."""
     torch = _torch()
-    num_pages, hkv, page, d = _paged_common_q8(k_cache, v_cache, k_scale, v_scale, block_table,
-                                               seq_lens)
+    dev, B, max_pages, num_pages, hkv, page, d = _paged_common_q8(
+        k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
     bf16 = torch.bfloat16
-    if not _all(k_cache.get_device(), (k_new, bf16, 3), (v_new, bf16, 3), (cu_q, torch.int32, 1)):
+    if not _all(dev, (k_new, bf16, 3), (v_new, bf16, 3), (cu_q, torch.int32, 1)):
         _need(k_new, bf16, "k_new", 3)
         _need(v_new, bf16, "v_new", 3)
         _need(cu_q, torch.int32, "cu_q", 1)
         _on_current_device(k_new=k_new, v_new=v_new, cu_q=cu_q)
         raise ValueError("k_new, v_new and cu_q must be contiguous")
-    B = seq_lens.shape[0]
-    T, h, dn = k_new.shape
-    if k_new.shape != v_new.shape or h != hkv or dn != d:
+    shape = k_new.shape
+    T, h, dn = shape
+    if v_new.shape != shape or h != hkv or dn != d:
         raise ValueError("k_new and v_new must be [T, Hkv, D] of the cache's Hkv and D")
     if cu_q.shape[0] != B + 1:
         raise ValueError("cu_q must have batch + 1 entries")
     _check(lib().bi_kv_append_q8(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(),
                                  v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                 num_pages, block_table.data_ptr(), block_table.shape[1],
+                                 num_pages, block_table.data_ptr(), max_pages,
                                  seq_lens.data_ptr(), cu_q.data_ptr(), B, T, hkv, d, page,
-                                 _stream(stream)))
+                                 _stream_on(stream, dev)))
 
 
 def _attend_q8(fn, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, max_q,
                max_seq_len, scale, out, lse, want_lse, workspace, stream):
     torch = _torch()
-    num_pages, hkv, page, d = _paged_common_q8(k_cache, v_cache, k_scale, v_scale, block_table,
-                                               seq_lens)
-    dev = k_cache.get_device()
+    dev, B, max_pages, num_pages, hkv, page, d = _paged_common_q8(
+        k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
     decode = fn == "bi_decode_attn_q8"
     if not _all(dev, (q, torch.bfloat16, 3)):
         _need(q, torch.bfloat16, "q", 3)
         _on_current_device(q=q)
         raise ValueError("q must be a contiguous [T, Hq, D] of the cache's D")
     T, hq, dq = q.shape
-    B = seq_lens.shape[0]
     if dq != d:
         raise ValueError("q must be a contiguous [T, Hq, D] of the cache's D")
     if decode:
@@ -582,12 +597,12 @@ def _attend_q8(fn, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
         else:
             ws_bytes = workspace.numel() * workspace.element_size()
     head = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), num_pages, block_table.data_ptr(), block_table.shape[1],
+            v_scale.data_ptr(), num_pages, block_table.data_ptr(), max_pages,
             seq_lens.data_ptr())
     sizes = (B,) if decode else (cu_q.data_ptr(), B, T, int(max_q))
     _check(getattr(L, fn)(*head, *sizes, int(max_seq_len), hq, hkv, d, page, float(scale),
                           out.data_ptr(), _ptr(lse), workspace.data_ptr(), ws_bytes,
-                          _stream(stream)))
+                          _stream_on(stream, dev)))
     return out, lse
 
 
@@ -644,7 +659,8 @@ def kv_copy_pages(planes: Sequence, src, dst, stream=None) -> None:
     ptrs = array.array("Q", map(Tensor.data_ptr, planes))
     sizes = array.array("q", [t.nbytes // pages for t in planes])
     _check(lib().bi_kv_copy_pages(ptrs.buffer_info()[0], sizes.buffer_info()[0], n, pages,
-                                  src.data_ptr(), dst.data_ptr(), src.shape[0], _stream(stream)))
+                                  src.data_ptr(), dst.data_ptr(), src.shape[0],
+                                  _stream_on(stream, dev)))
 
 
 # ---------------------------------------------------------------------- device status
@@ -796,17 +812,19 @@ class TokenLogprobs(NamedTuple):
 
 
 def _logits(logits, tokens):
-    """Checks logits and tokens; returns (dtype code, rows, n, row stride)."""
+    """Checks logits and tokens; returns (device, dtype code, rows, n, row stride)."""
     torch = _torch()
-    dt = _in_dtype(logits, "logits")
-    _need(logits, logits.dtype, "logits", 2)
-    _need(tokens, torch.int32, "tokens", 1)
-    rows, n = logits.shape
-    if tokens.shape[0] != rows or not tokens.is_contiguous():
-        raise ValueError("tokens must be a contiguous int32 [rows] tensor")
-    if _device_of(logits) != tokens.get_device():
+    dev = _device_of(logits)
+    if not _all(dev, (tokens, torch.int32, 1)) or logits.dim() != 2:
+        _need(logits, logits.dtype, "logits", 2)
+        _need(tokens, torch.int32, "tokens", 1)
         _on_current_device(logits=logits, tokens=tokens)
-    return dt, rows, n, _row_major_2d(logits, "logits")
+        raise ValueError("tokens must be a contiguous int32 [rows] tensor")
+    dt = _in_dtype(logits, "logits")
+    rows, n = logits.shape
+    if tokens.shape[0] != rows:
+        raise ValueError("tokens must be a contiguous int32 [rows] tensor")
+    return dev, dt, rows, n, _row_major_2d(logits, "logits")
 
 
 def token_logprobs(logits, tokens, top: int = 0, stream=None) -> TokenLogprobs:
@@ -815,7 +833,7 @@ def token_logprobs(logits, tokens, top: int = 0, stream=None) -> TokenLogprobs:
     the `top` largest entries as log-probabilities and ids (descending; lowest id first among
     equal ones).  A row's bits do not depend on the other rows."""
     torch = _torch()
-    dt, rows, n, ld = _logits(logits, tokens)
+    cur, dt, rows, n, ld = _logits(logits, tokens)
     if not 0 <= top <= min(n, LOGPROBS_MAX_TOP):
         raise ValueError(f"top must be in [0, min(n, {LOGPROBS_MAX_TOP})]")
     dev = logits.device
@@ -825,11 +843,11 @@ def token_logprobs(logits, tokens, top: int = 0, stream=None) -> TokenLogprobs:
         logp = torch.empty(rows, dtype=f32, device=dev)
         entropy = torch.empty(rows, dtype=f32, device=dev)
         lse = torch.empty(rows, dtype=f32, device=dev)
-        tv = torch.empty(rows, top, dtype=torch.float32, device=dev) if top else None
+        tv = torch.empty(rows, top, dtype=f32, device=dev) if top else None
         ti = torch.empty(rows, top, dtype=torch.int32, device=dev) if top else None
     _check(lib().bi_token_logprobs(logits.data_ptr(), ld, dt, tokens.data_ptr(), rows, n,
                                    logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(), int(top),
-                                   _ptr(tv), _ptr(ti), _stream(stream)))
+                                   _ptr(tv), _ptr(ti), _stream_on(stream, cur)))
     return TokenLogprobs(logp, entropy, lse, tv, ti)
 
 
@@ -839,19 +857,23 @@ def token_logprobs_backward(logits, tokens, lse, entropy=None, grad_logprobs=Non
     sum(grad_logprobs * logprobs) + sum(grad_entropy * entropy), from the lse and entropy
     that token_logprobs gave; out may be logits."""
     torch = _torch()
-    dt, rows, n, ld = _logits(logits, tokens)
+    cur, dt, rows, n, ld = _logits(logits, tokens)
     if grad_logprobs is None and grad_entropy is None:
         raise ValueError("grad_logprobs and grad_entropy are both None")
     if grad_entropy is not None and entropy is None:
         raise ValueError("grad_entropy needs entropy")
-    cur = logits.get_device()
-    for name, t in (("lse", lse), ("entropy", entropy), ("grad_logprobs", grad_logprobs),
-                    ("grad_entropy", grad_entropy)):
-        if (t is not None or name == "lse") and not (_all(cur, (t, torch.float32, 1))
-                                                     and t.shape[0] == rows):
-            _need(t, torch.float32, name, 1)
+    f32 = torch.float32
+    given = [(name, t) for name, t in (("lse", lse), ("entropy", entropy),
+                                       ("grad_logprobs", grad_logprobs),
+                                       ("grad_entropy", grad_entropy))
+             if t is not None or name == "lse"]
+    if not _all(cur, *[(t, f32, 1) for _, t in given]) or any(t.shape[0] != rows
+                                                              for _, t in given):
+        for name, t in given:
+            _need(t, f32, name, 1)
             _on_current_device(**{name: t})
-            raise ValueError(f"{name} must be a contiguous fp32 [rows] tensor")
+            if t.shape[0] != rows or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous fp32 [rows] tensor")
     if out is None:
         with _allocating_for(stream):
             out = torch.empty(rows, n, dtype=logits.dtype, device=logits.device)
@@ -863,5 +885,5 @@ def token_logprobs_backward(logits, tokens, lse, entropy=None, grad_logprobs=Non
     _check(lib().bi_token_logprobs_backward(
         logits.data_ptr(), ld, dt, tokens.data_ptr(), rows, n, lse.data_ptr(), _ptr(entropy),
         _ptr(grad_logprobs), _ptr(grad_entropy), out.data_ptr(), _row_major_2d(out, "out"),
-        _stream(stream)))
+        _stream_on(stream, cur)))
     return out
