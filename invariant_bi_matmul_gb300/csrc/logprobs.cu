@@ -18,9 +18,9 @@
 // barriers per part, took 170 and 247 us.
 //
 // Top alternatives.  The k-th largest of the thread maxima bounds the k-th largest element from
-// below, so few elements (k, and a handful more) lie at or above it; the few threads that hold
-// one look at their vectors again (from L2), the elements are ranked by counting, and rank 0
-// ranks the CTAs' first k.  Where ties make them too many, k rounds of a maximum below the last
+// below, so few elements (k, and a handful more) lie at or above it; all threads look again at
+// the vectors of the few that hold one (each at its own, 1024 x 128256 fp32 with 20 took 133
+// us), the elements are ranked by counting, and rank 0 ranks the CTAs' first k.  Where ties make them too many, k rounds of a maximum below the last
 // one found.
 //
 // Backward.  Elementwise from the saved lse and entropy: one read, one write.
@@ -282,8 +282,11 @@ __device__ __forceinline__ void join(Stats& a, const Stats& b) {
 constexpr int kGroups = 64;  // groups of threads whose maxima bound the top entries
 
 // `ctas` CTAs (one cluster) per row, each over parts / ctas parts of `part` vectors.
+// CTAs per multiprocessor: seven of 128 threads (1024 x 100001 bf16, unaligned, 63 us; six 69,
+// where 1024 rows are two waves), four of 256; three where unaligned, or registers spill (fp32 96
+// us, 106 with four).
 template <int DT, int T, bool ALIGNED>
-__global__ void __launch_bounds__(T, T == 256 ? 4 : 6)
+__global__ void __launch_bounds__(T, T == 128 ? 7 : ALIGNED ? 4 : 3)
 token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __restrict__ tokens,
                       int n, int part, int parts, int ctas, float* logp, float* entropy,
                       float* lse_out, int top, float* top_logp, int32_t* top_ids,
@@ -296,7 +299,8 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
     __shared__ unsigned long long redk[T / 32];
     __shared__ uint32_t gmax[kGroups];
     __shared__ uint32_t floor_order;
-    __shared__ int found;
+    __shared__ int found, holding;
+    __shared__ uint16_t holders[kMaxParts * T];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row = blockIdx.x / ctas, rank = blockIdx.x - row * ctas;
     const int mine = parts / ctas, p0 = rank * mine;
@@ -305,7 +309,7 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
     const int vecs = (n + VE - 1) / VE;
     pdl_wait();
     pdl_trigger();
-    if (tid == 0) found = 0;
+    if (tid == 0) found = holding = 0;
     __syncthreads();
     const int whole = n / VE;  // vectors that hold no padding
     auto sums = [&](auto clamp) {
@@ -416,35 +420,42 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
         }
         __syncthreads();
         const uint32_t fl = floor_order;
-        for (int p = 0; p < mine && own >= fl; ++p) {
-            if (order(tm[p][tid]) < fl) continue;
-            const int v1 = min(vecs, (p0 + p + 1) * part);
-            for (int g = (p0 + p) * part + tid; g < v1; g += T * kBatch) {
-                uint4 a[kBatch];
+        // the threads, by part, whose maximum reaches the floor; all threads look at their vectors
+        for (int p = 0; p < mine; ++p)
+            if (order(tm[p][tid]) >= fl) holders[atomicAdd(&holding, 1)] = uint16_t(p * T + tid);
+        __syncthreads();
+        const int each = (part + T - 1) / T, looks = holding * each;
+        for (int base = tid; base < looks; base += T * kBatch) {
+            uint4 a[kBatch];
+            int at[kBatch];  // the vectors, -1: none
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k)
-                    if (g + k * T < v1) a[k] = load_vec<DT>(xr, skew == 0, g + k * T, n);
-#pragma unroll 1
-                for (int k = 0; k < kBatch; ++k) {
-                    // (one vector at a time: a[k] by selection, so that a stays in registers)
-                    uint4 x = a[0];
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = base + k * T, h = i / each;
+                at[k] = -1;
+                if (i < looks) {
+                    const int p = holders[h] / T;
+                    const int g = (p0 + p) * part + holders[h] % T + (i - h * each) * T;
+                    if (g < min(vecs, (p0 + p + 1) * part)) {
+                        at[k] = g;
+                        a[k] = load_vec<DT>(xr, skew == 0, g, n);
+                    }
+                }
+            }
 #pragma unroll
-                    for (int i = 1; i < kBatch; ++i)
-                        if (i == k) x = a[i];
-                    const int at0 = (g + k * T) * VE;
-                    if (g + k * T >= v1) break;
-                    float v[VE];
-                    widen<DT>(x, v);
-                    float vm = v[0];
+            for (int k = 0; k < kBatch; ++k) {
+                if (at[k] < 0) continue;
+                float v[VE];
+                widen<DT>(a[k], v);
+                float vm = v[0];
 #pragma unroll
-                    for (int q = 1; q < VE; ++q) vm = fmaxf(vm, v[q]);
-                    if (order(vm) < fl) continue;
+                for (int q = 1; q < VE; ++q) vm = fmaxf(vm, v[q]);
+                if (order(vm) < fl) continue;
 #pragma unroll
-                    for (int q = 0; q < VE; ++q) {
-                        if (at0 + q < n && order(v[q]) >= fl) {
-                            const int at = atomicAdd(&found, 1);
-                            if (at < kList) list[at] = order_key(v[q], at0 + q);
-                        }
+                for (int q = 0; q < VE; ++q) {
+                    const int i = at[k] * VE + q;
+                    if (i < n && order(v[q]) >= fl) {
+                        const int to = atomicAdd(&found, 1);
+                        if (to < kList) list[to] = order_key(v[q], i);
                     }
                 }
             }
