@@ -866,11 +866,14 @@ attn_merge_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restric
 }
 
 // One warp per row, eight rows per CTA: the same tree, its eight ranges folded one after
-// another (throughput: many rows, e.g. a prefill block).  UNR (>= the rows' chunk count)
-// sizes the register window that holds a row's partials: the smaller it is, the more CTAs
-// share an SM and the more rows' loads are in flight (it changes no arithmetic).
+// another (throughput: many rows, e.g. a prefill block).  Lane c holds chunk c's (m, l) and
+// works out its two weights, which the fold takes from it by shuffles; the partials pass
+// through a window of up to nine, so that four CTAs or more share an SM and the loads of one
+// row hide behind the folds of others.  UNR: at least the rows' chunk count.  Bound by
+// memory: (D + 2) * 4 bytes per chunk.  (With the ranges' sums and all 17 partials of a row
+// in 167 registers, one CTA per SM: 16,384 rows of 17 chunks 75 us.)
 template <int D, int UNR>
-__global__ void __launch_bounds__(MERGE_WARPS * 32)
+__global__ void __launch_bounds__(MERGE_WARPS * 32, 4)
 attn_merge_rows_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ cu_q,
                        int B, int total_q, int max_q, int max_seq_len, int Hq, int Hkv,
                        const float* ws_o, const float* ws_ml, int maxC, int chunk_log2,
@@ -900,50 +903,73 @@ attn_merge_rows_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __re
     const int64_t base = (int64_t(t) * Hq + hq) * maxC;
     // the host picks UNR >= maxC >= nC for every valid row
     if (nC > UNR) return;
-    float M8[MERGE_WARPS], L8[MERGE_WARPS], acc8[MERGE_WARPS][PER];
-    // every partial of the row in one round trip, then each range folded from the
-    // registers with merge_fold's arithmetic (max first, then the weighted sums in
-    // ascending chunk order)
-    float v[UNR][PER];
-    float2 ml[UNR];
+    constexpr int WIN = UNR < 9 ? UNR : 9;
+    static_assert(UNR <= 32, "a lane per chunk");
+    float v[WIN][PER];
+    auto load = [&](int c0) {  // at L2, as merge_fold loads
 #pragma unroll
-    for (int c = 0; c < UNR; ++c) {
-        if (c < nC) {  // at L2, as merge_fold loads
-            ml[c] = __ldcg(reinterpret_cast<const float2*>(ws_ml + (base + c) * 2));
-            const float* src = ws_o + (base + c) * D + lane * PER;
+        for (int u = 0; u < WIN; ++u) {
+            if (c0 + u >= nC) break;
+            const float* src = ws_o + (base + c0 + u) * D + lane * PER;
             if (PER == 4) {
                 const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-                v[c][0] = f.x; v[c][1 % PER] = f.y; v[c][2 % PER] = f.z; v[c][3 % PER] = f.w;
+                v[u][0] = f.x; v[u][1 % PER] = f.y; v[u][2 % PER] = f.z; v[u][3 % PER] = f.w;
             } else {
                 const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-                v[c][0] = f.x; v[c][1 % PER] = f.y;
+                v[u][0] = f.x; v[u][1 % PER] = f.y;
+            }
+        }
+    };
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < nC) ml = __ldcg(reinterpret_cast<const float2*>(ws_ml + (base + lane) * 2));
+    load(0);
+    // the range [c0, c1) of chunk `lane`, its maximum and the row's
+    int rg = 0;
+#pragma unroll
+    for (int w = 1; w < MERGE_WARPS; ++w)
+        if (lane >= w * nC / MERGE_WARPS) rg = w;
+    const int c0 = rg * nC / MERGE_WARPS, c1 = (rg + 1) * nC / MERGE_WARPS;
+    float Mw = -INFINITY, M = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < UNR; ++c) {
+        const float m = __shfl_sync(0xffffffffu, ml.x, c);
+        if (c >= c0 && c < c1) Mw = fmaxf(Mw, m);
+        M = fmaxf(M, m);
+    }
+    const float in_range = exp2f(ml.x - Mw), of_range = exp2f(Mw - M);
+    const uint32_t last = __ballot_sync(0xffffffffu, lane < nC && lane == c1 - 1);
+    // merge_fold's and merge_combine's arithmetic: the ranges' sums in ascending chunk order,
+    // then their sum in ascending range order (an empty range adds 0)
+    float Ls = 0.f, Lw = 0.f, o[PER], acc[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) o[i] = acc[i] = 0.f;
+#pragma unroll
+    for (int b0 = 0; b0 < UNR; b0 += WIN) {
+        if (b0 > 0) load(b0);
+#pragma unroll
+        for (int u = 0; u < WIN; ++u) {
+            const int c = b0 + u;
+            if (c >= UNR || c >= nC) break;
+            const float wgt = __shfl_sync(0xffffffffu, in_range, c);
+            Lw = Lw + wgt * __shfl_sync(0xffffffffu, ml.y, c);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) acc[i] = acc[i] + wgt * v[u][i];
+            if ((last >> c) & 1u) {
+                const float wr = __shfl_sync(0xffffffffu, of_range, c);
+                Ls = Ls + wr * Lw;
+                Lw = 0.f;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    o[i] = o[i] + wr * acc[i];
+                    acc[i] = 0.f;
+                }
             }
         }
     }
+    __nv_bfloat16* dst = out + (int64_t(t) * Hq + hq) * D + lane * PER;
 #pragma unroll
-    for (int w = 0; w < MERGE_WARPS; ++w) {
-        const int c0 = w * nC / MERGE_WARPS, c1 = (w + 1) * nC / MERGE_WARPS;
-        float Mw = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < UNR; ++c)
-            if (c >= c0 && c < c1) Mw = fmaxf(Mw, ml[c].x);
-        float Lw = 0.f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) acc8[w][i] = 0.f;
-#pragma unroll
-        for (int c = 0; c < UNR; ++c) {
-            if (c >= c0 && c < c1) {
-                const float wgt = exp2f(ml[c].x - Mw);
-                Lw = Lw + wgt * ml[c].y;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) acc8[w][i] = acc8[w][i] + wgt * v[c][i];
-            }
-        }
-        M8[w] = Mw;
-        L8[w] = Lw;
-    }
-    merge_combine<D>(M8, L8, [&](int w, int i) { return acc8[w][i]; }, lane,
-                     out + (int64_t(t) * Hq + hq) * D, lse ? lse + int64_t(t) * Hq + hq : nullptr);
+    for (int i = 0; i < PER; ++i) dst[i] = __float2bfloat16_rn(o[i] / Ls);
+    if (lse && lane == 0) lse[int64_t(t) * Hq + hq] = (M + log2f(Ls)) * kLn2;
 }
 
 // ------------------------------------------------------------------ KV-append kernel
