@@ -1065,10 +1065,10 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
     const int grid = int(items_bound < dev.num_sms ? items_bound : dev.num_sms);
     // Chunks of a unit (consecutive items of a CTA with one Q tile, split once): as many as
     // leave each CTA eight units or more, so that the dealing stays even -- where the items'
-    // turn-around is what binds (64 sequences of 8,196 keys, blocks of 8: 303 us with runs, 330
-    // without; one-token blocks at head_dim 64, 16,388 keys: 205 and 245).  One-token blocks at
-    // head_dim 128 are bound by memory and keep the finer dealing (ragged batch of 64: 231 us
-    // without, 235 to 240 with).
+    // turn-around is what binds (64 sequences of 8,196 keys, blocks of 8: 245 us with runs, 276
+    // without; one-token blocks at head_dim 64, 16,388 keys: 178 and 194; 512 tokens after 65,028:
+    // 1.56 ms and 1.96).  One-token blocks at head_dim 128 are bound by memory and keep the finer
+    // dealing (ragged batch of 64: 230 us without, 246 with).
     int run = 1;
     auto units = [&](int r) { return a.batch * ((maxC + r - 1) / r) * tiles * a.hkv; };
     while (run < 8 && (D == 64 || RPW * NWG > 4) && units(2 * run) >= 8 * int64_t(dev.num_sms))
@@ -1076,10 +1076,11 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
     float* ws_o = static_cast<float*>(workspace);
     float* ws_ml = ws_o + a.total_q * a.hq * int64_t(maxC) * D;
     // The merge of a (sequence, KV head) may start when its chunks are counted, beside the chunks
-    // of others: 64 sequences of 8,196 keys, blocks of 8, 309 us with counts and 341 without.
-    // With few query rows there is little to merge and the counters' reset costs a launch (one
-    // sequence of 16,388 keys 15.7 us with, 15.0 without; 64 at head_dim 64 204 and 189), and the
-    // tiles of a wide block are not counted apart: there the merge waits for the whole grid.
+    // of others: 64 sequences of 8,196 keys, blocks of 8, 245 us with counts and 280 without; two
+    // of 65,540 keys 65.9 and 67.8.  The counters' reset costs a launch, which a call of few items
+    // does not earn back (one of 65,540 keys 39.5 and 38.2).  With few query rows there is little
+    // to merge (64 at head_dim 64 205 with and 178 without), and the tiles of a wide block are not
+    // counted apart: there the merge waits for the whole grid.
     unsigned int* cnt = nullptr;
     if (tiles == 1 && RPW * NWG > 4) {
         cnt = attn_item_counters(a, workspace, CHUNK_LOG2);
