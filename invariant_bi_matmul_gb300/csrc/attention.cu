@@ -655,7 +655,10 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
 // --------------------------------------------------------------------- merge kernel
 
 constexpr int MERGE_WARPS = 8;    // chunk ranges of the merge tree
-constexpr int64_t kMergeRowsMin = 4096;  // rows from which a warp per row merges
+// rows from which a warp per row merges: 2,048 rows of 3 chunks (64 one-token sequences of
+// 1,028 keys over the 8-bit cache, the whole call) 32.8 us, 37.3 with a CTA per row; 512 rows of
+// 17 chunks 48.0 and 47.3
+constexpr int64_t kMergeRowsMin = 1024;
 constexpr int MERGE_UNROLL = 17;  // partials requested per round trip (136 chunks in 8)
 
 // The merge tree of one (token, query head) row with nC = pos/chunk + 1 chunk partials:
@@ -665,15 +668,15 @@ constexpr int MERGE_UNROLL = 17;  // partials requested per round trip (136 chun
 // exactly these two functions, so they give the same bits.
 
 // Fold chunks [c0, c1) of the row at `base` (lane holds dims lane*PER ..): range max Mw,
-// weighted sum Lw and weighted o sums acc.
-template <int D>
+// weighted sum Lw and weighted o sums acc.  UNR: partials requested per round trip.
+template <int D, int UNR>
 __device__ __forceinline__ void merge_fold(const float* __restrict__ ws_o,
                                            const float* __restrict__ ws_ml, int64_t base, int c0,
                                            int c1, int lane, float& Mw, float& Lw,
                                            float (&acc)[D / 32]) {
     constexpr int PER = D / 32;
-    // The first MERGE_UNROLL partials of the range are requested before anything else
-    // (for ranges up to MERGE_UNROLL chunks: all of them, in one global round trip).
+    // The first UNR partials of the range are requested before anything else
+    // (for ranges up to UNR chunks: all of them, in one global round trip).
     // loads at L2 (ld.global.cg): the partial kernel may still be running, and this SM's
     // L1 may hold a neighbouring row's line from before that row was complete
     auto load = [&](int c, float (&v)[PER], float2& ml) {
@@ -687,18 +690,18 @@ __device__ __forceinline__ void merge_fold(const float* __restrict__ ws_o,
             v[0] = f.x; v[1 % PER] = f.y;
         }
     };
-    float v[MERGE_UNROLL][PER];
-    float2 ml[MERGE_UNROLL];
+    float v[UNR][PER];
+    float2 ml[UNR];
 #pragma unroll
-    for (int u = 0; u < MERGE_UNROLL; ++u)
+    for (int u = 0; u < UNR; ++u)
         if (c0 + u < c1) load(c0 + u, v[u], ml[u]);
 
     // range max (exact in any order): from the registers when the whole range was loaded
     // above, else lanes stride over the chunks and a butterfly combines them
     Mw = -INFINITY;
-    if (c1 - c0 <= MERGE_UNROLL) {
+    if (c1 - c0 <= UNR) {
 #pragma unroll
-        for (int u = 0; u < MERGE_UNROLL; ++u)
+        for (int u = 0; u < UNR; ++u)
             if (c0 + u < c1) Mw = fmaxf(Mw, ml[u].x);
     } else {
         for (int c = c0 + lane; c < c1; c += 32) Mw = fmaxf(Mw, __ldcg(ws_ml + (base + c) * 2));
@@ -710,14 +713,14 @@ __device__ __forceinline__ void merge_fold(const float* __restrict__ ws_o,
     Lw = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-    for (int c = c0; c < c1; c += MERGE_UNROLL) {
+    for (int c = c0; c < c1; c += UNR) {
         if (c > c0) {
 #pragma unroll
-            for (int u = 0; u < MERGE_UNROLL; ++u)  // issue the loads of the next chunks first
+            for (int u = 0; u < UNR; ++u)  // issue the loads of the next chunks first
                 if (c + u < c1) load(c + u, v[u], ml[u]);
         }
 #pragma unroll
-        for (int u = 0; u < MERGE_UNROLL; ++u) {  // then fold them in ascending chunk order
+        for (int u = 0; u < UNR; ++u) {  // then fold them in ascending chunk order
             if (c + u < c1) {
                 const float wgt = exp2f(ml[u].x - Mw);
                 Lw = Lw + wgt * ml[u].y;
@@ -811,7 +814,7 @@ __global__ void __launch_bounds__(256) attn_count_reset_kernel(unsigned int* cnt
 }
 
 // One CTA per row: warp w folds range w (latency: a few rows, long contexts).
-template <int D>
+template <int D, int UNR>
 __global__ void __launch_bounds__(MERGE_WARPS * 32)
 attn_merge_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ cu_q, int B,
                   int total_q, int max_q, int max_seq_len, int Hq, int Hkv,
@@ -845,7 +848,7 @@ attn_merge_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restric
     const int nC = (pos >> chunk_log2) + 1;
     const int64_t base = (int64_t(t) * Hq + hq) * maxC;
     float Mw, Lw, acc[PER];
-    merge_fold<D>(ws_o, ws_ml, base, warp * nC / MERGE_WARPS, (warp + 1) * nC / MERGE_WARPS,
+    merge_fold<D, UNR>(ws_o, ws_ml, base, warp * nC / MERGE_WARPS, (warp + 1) * nC / MERGE_WARPS,
                   lane, Mw, Lw, acc);
     if (lane == 0) {
         sM[warp] = Mw;
@@ -1093,11 +1096,16 @@ cudaError_t launch_attn_merge(const PagedArgs& a, void* workspace, int chunk_log
     const float* ws_o = static_cast<const float*>(workspace);
     const float* ws_ml = ws_o + a.total_q * a.hq * int64_t(maxC) * a.head_dim;
     const int64_t rows = a.total_q * a.hq;
-    // few rows or long rows: a CTA per row, its eight ranges in parallel; many rows of at
-    // most MERGE_UNROLL chunks: a warp per row, all its partials loaded at once (both run
-    // the same tree, so the choice does not change any bit)
+    // few rows or long rows: a CTA per row, its eight ranges in parallel (ranges of up to 5
+    // chunks: a window of 5, in 57 registers instead of 128 -- 64 ragged one-token sequences of
+    // up to 16,388 keys over the 8-bit cache 218 us, 227 with the window of 17); many rows of at
+    // most MERGE_UNROLL chunks: a warp per row (all run the same tree, so the choice does not
+    // change any bit)
     if (rows < kMergeRowsMin || maxC > MERGE_UNROLL) {
-        auto kern = a.head_dim == 64 ? attn_merge_kernel<64> : attn_merge_kernel<128>;
+        const bool few = maxC <= 5 * MERGE_WARPS;
+        auto kern = a.head_dim == 64
+                        ? (few ? attn_merge_kernel<64, 5> : attn_merge_kernel<64, MERGE_UNROLL>)
+                        : (few ? attn_merge_kernel<128, 5> : attn_merge_kernel<128, MERGE_UNROLL>);
         return launch_pdl(kern, dim3(unsigned(rows)), dim3(MERGE_WARPS * 32), 0, stream,
                           a.seq_lens, a.cu_q, int(a.batch), int(a.total_q), int(a.max_q),
                           int(a.max_seq_len), int(a.hq), int(a.hkv), ws_o, ws_ml, maxC,
