@@ -653,8 +653,9 @@ def kv_copy_pages(planes: Sequence, src, dst, stream=None) -> None:
     # (each question to all planes in one go: a loop over them took 4 us longer for 32)
     if any(d != dev for d in map(Tensor.get_device, planes)):
         raise ValueError("planes must be CUDA tensors on the current device")
-    if not all(map(Tensor.is_contiguous, planes)) or any(
-            not t.dim() or t.size(0) != pages for t in planes):
+    # (shape[0]: size(0) takes twice as long)
+    if not all(map(Tensor.is_contiguous, planes)) or min(map(Tensor.dim, planes)) < 1 or [
+            t.shape[0] for t in planes].count(pages) != n:
         raise ValueError("planes must be contiguous with one number of pages")
     ptrs = array.array("Q", map(Tensor.data_ptr, planes))
     sizes = array.array("q", [t.nbytes // pages for t in planes])
@@ -841,8 +842,7 @@ def token_logprobs(logits, tokens, top: int = 0, stream=None) -> TokenLogprobs:
         # (three tensors: views of one, made and freed, took 5 us more)
         f32 = torch.float32
         logp = torch.empty(rows, dtype=f32, device=dev)
-        entropy = torch.empty(rows, dtype=f32, device=dev)
-        lse = torch.empty(rows, dtype=f32, device=dev)
+        entropy, lse = torch.empty_like(logp), torch.empty_like(logp)
         tv = torch.empty(rows, top, dtype=f32, device=dev) if top else None
         ti = torch.empty(rows, top, dtype=torch.int32, device=dev) if top else None
     _check(lib().bi_token_logprobs(logits.data_ptr(), ld, dt, tokens.data_ptr(), rows, n,
