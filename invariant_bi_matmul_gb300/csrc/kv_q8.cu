@@ -14,9 +14,11 @@
 // One thread per 16-byte piece of a K row and of the V row beside it; the D/8 threads of a
 // row are neighbours in a warp and combine their maxima by shuffles; a CTA takes consecutive
 // tokens of one head, so the codes and scale bytes it writes lie together in the page.  Reads 4
-// bytes and writes 2 + 2/D per element pair: 8,192 tokens of 8 heads of 128 take 12.3 us (4.1
-// TB/s; 2.2 us of it are what the smallest call takes).  Taking the heads of a token together
-// took 12.5 us (scattered single scale bytes), two and four rows per thread 13.4 and 14.2.
+// bytes and writes 2 + 2/D per element pair: 8,192 tokens of 8 heads of 128 take 10.9 us (4.6
+// TB/s; 2.2 us of it are what the smallest call takes).  The rows are read once, with streaming
+// loads, which leave the L2 to the codes (12.2 us without them).  Slower before that: the heads of
+// a token together (12.9 to 12.3, scattered single scale bytes), two and four rows per thread
+// (13.4 and 14.2), CTAs of 512 (12.7).
 #include "attn_common.cuh"
 
 #include <cuda_fp8.h>
@@ -24,7 +26,7 @@
 namespace bi {
 namespace {
 
-constexpr int APPEND_THREADS = 256;
+constexpr int APPEND_THREADS = 128;
 constexpr int kMinExp = -64;  // the smallest scale exponent (a row of zeros has it)
 
 // Largest magnitude of eight bf16 values, as a bf16 bit pattern (magnitudes order as their
@@ -73,8 +75,8 @@ kv_append_q8_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v
     uint4 k = make_uint4(0, 0, 0, 0), v = k;
     if (live) {
         const int64_t src = (int64_t(t) * Hkv + h) * LPR + ch;
-        k = k_new[src];
-        v = v_new[src];
+        k = __ldcs(k_new + src);
+        v = __ldcs(v_new + src);
     }
     // the row's place, found while the loads are under way; -1: nowhere
     int64_t dst = -1;
