@@ -437,6 +437,9 @@ bi_status bi_kv_append_q8(const void* k_new, const void* v_new, void* k_cache, v
  *   A key row of NaN makes the queries that see it NaN, and no others.  The value scales that
  *   one query sees should lie within a factor 2^80 of one another (softmax weights are held
  *   relative to them).
+ *   Scores scale * q . k may have any finite size.  From 2^23 on fp32 cannot hold one and the
+ *   exponent of a value scale together: keys of equal score then weigh in inverse proportion
+ *   to their value scales.
  *   bi_verify_block_q8: max_q <= BI_ATTN_MAX_Q and max_q * G <= BI_ATTN_MAX_ROWS
  *   (G = num_q_heads / num_kv_heads).  bi_prefill_attn_q8: any max_q >= 1, G <= 32. */
 bi_status bi_verify_block_q8(const void* q, const void* k_cache, const void* v_cache,

@@ -22,8 +22,8 @@
 // chunks of 512 keys from key 0; m is the exact maximum of the row's t over the chunk, less 8
 // (so p <= 2^8); a chunk is four tiles of 128 keys, each of 128 threads sums its key of every
 // tile in ascending order, and the 128 sums are added by a fixed tree; the chunk partials
-// (m, l, o) go through the merge of attention.cu.  Keys that a row does not see add +0, and a
-// row's place in the MMA tile, the other rows and the block's width enter nowhere.
+// (m, l, o) go through the merge of attention.cu.  Keys that a row does not see have t = -inf and
+// add +0, and a row's place in the MMA tile, the other rows and the block's width enter nowhere.
 //
 // A softmax thread holds its four t of every row in registers between the maximum and the
 // exponentials, so a chunk needs one exchange between warps and O is never rescaled.  (With a
@@ -67,7 +67,7 @@ constexpr int NT = CHUNK / TK;            // tiles of a chunk
 constexpr int TMEM_COLS = 512;
 constexpr int S_COL = 0;                  // two S sets (by item) of NT tiles, 32 columns each
 constexpr int O_COL = 2 * NT * QR;          // O buffers (by item): 32 hi + 32 lo columns each
-constexpr float kHidden = -1e30f;         // t of a key that a row does not see
+constexpr float kNoKey = -1e30f;          // m of a chunk of which a row sees no key
 constexpr float kHeadroom = 8.f;          // p = 2^8 at the row's maximum (e4m3 holds 448)
 constexpr float kLoScale = 32.f;          // the second piece of p (at most 8) times this
 constexpr int MAX_BATCH = BI_ATTN_MAX_BATCH;
@@ -928,7 +928,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const int first = live ? max(0, ahead) * G : QR;
 #pragma unroll
                     for (int r = 0; r < RPW; ++r)
-                        t[i][r] = row0 + r >= first ? t[i][r] : kHidden;
+                        t[i][r] = row0 + r >= first ? t[i][r] : -INFINITY;
                 }
             }
 #pragma unroll
@@ -956,11 +956,15 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const float4 x1 = *reinterpret_cast<const float4*>(xm + 1 * QR + r);
                 const float4 x2 = *reinterpret_cast<const float4*>(xm + 2 * QR + r);
                 const float4 x3 = *reinterpret_cast<const float4*>(xm + 3 * QR + r);
-                m[r] = fmaxf(fmax3(x0.x, x1.x, x2.x), x3.x) - kHeadroom;
-                m[r + 1] = fmaxf(fmax3(x0.y, x1.y, x2.y), x3.y) - kHeadroom;
-                m[r + 2] = fmaxf(fmax3(x0.z, x1.z, x2.z), x3.z) - kHeadroom;
-                m[r + 3] = fmaxf(fmax3(x0.w, x1.w, x2.w), x3.w) - kHeadroom;
+                m[r] = fmaxf(fmax3(x0.x, x1.x, x2.x), x3.x);
+                m[r + 1] = fmaxf(fmax3(x0.y, x1.y, x2.y), x3.y);
+                m[r + 2] = fmaxf(fmax3(x0.z, x1.z, x2.z), x3.z);
+                m[r + 3] = fmaxf(fmax3(x0.w, x1.w, x2.w), x3.w);
             }
+            // a row that sees no key here (its p are 0: -inf less any number) has no maximum
+#pragma unroll
+            for (int r = 0; r < RPW; ++r)
+                m[r] = m[r] == -INFINITY ? kNoKey : m[r] - kHeadroom;
 #pragma unroll
             for (int r = 0; r < RPW; ++r) l[r] = 0.f;
             // P's buffers are free once P V of item-1 has completed
