@@ -67,6 +67,7 @@ constexpr int NT = CHUNK / TK;            // tiles of a chunk
 constexpr int TMEM_COLS = 512;
 constexpr int S_COL = 0;                  // two S sets (by item) of NT tiles, 32 columns each
 constexpr int O_COL = 2 * NT * QR;          // O buffers (by item): 32 hi + 32 lo columns each
+constexpr uint32_t kOddScale = 224;       // scale bytes from here on take the longer way
 constexpr float kNoKey = -1e30f;          // m of a chunk of which a row sees no key
 constexpr float kHeadroom = 8.f;          // p = 2^8 at the row's maximum (e4m3 holds 448)
 constexpr float kLoScale = 32.f;          // the second piece of p (at most 8) times this
@@ -366,7 +367,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
     float* q_fac = xs + 4 * (NQ + 1) * QR;                   // [2][QR]
     float* x_max = q_fac + 2 * QR;                           // [2][NQ][QR]
     int* prefix = reinterpret_cast<int*>(smem + C::MISC_OFF);  // [B + 1]
-    int* scale_odd = prefix + MAX_BATCH + 1;  // [2 sets][2]: a scale byte of 254 or 255 among them
+    int* scale_odd = prefix + MAX_BATCH + 1;  // [2 sets][2]: a scale byte from kOddScale on
     volatile int* abort_flag = reinterpret_cast<volatile int*>(scale_odd + 4);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -743,10 +744,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             for (int n = 0; n < 2 / NPREP; ++n) {
                 const int pp = NPREP == 2 ? pw : n;
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {  // a byte of 254 or 255?
-                    const uint32_t z = ~sw[n][i] & 0xfefefefeu;
-                    odd |= (z - 0x01010101u) & ~z & 0x80808080u;
-                }
+                for (int i = 0; i < NT; ++i)  // a byte from kOddScale on?
+                    odd |= sw[n][i] & (sw[n][i] << 1) & (sw[n][i] << 2) & 0x80808080u;
                 const uint32_t a = __byte_perm(sw[n][0], sw[n][1], 0x5140);
                 const uint32_t b = __byte_perm(sw[n][2], sw[n][3], 0x5140);
                 const uint32_t c = __byte_perm(sw[n][0], sw[n][1], 0x7362);
@@ -891,11 +890,15 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 vinv[i] = __uint_as_float(0x7f000000u - (vs & 0x7f800000u));
             }
             if (odd) {
+                // Products of codes are below 2^24: times a key scale below 2^97 they are finite.
+                // With a larger one t is formed as 2^24 * (t * 2^-24), whose factors are finite
+                // where t is, and whose rounding is the same.
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     const uint32_t ks = (kw >> (8 * i)) & 0xffu, vs = (vw >> (8 * i)) & 0xffu;
-                    ka[i] = e8m0(ks);
-                    vb[i] = vs == 255 ? __int_as_float(0x7fc00000) : float(int(vs) - 127);
+                    const float part = ks >= kOddScale ? 0x1p-24f : 1.f;
+                    ka[i] = e8m0(ks) * part;
+                    vb[i] = vs == 255 ? __int_as_float(0x7fc00000) : float(int(vs) - 127) * part;
                     vinv[i] = e8m0_inv(vs);
                 }
             }
@@ -910,6 +913,14 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                           make_float2(vb[i], vb[i]));
                     t[i][r] = x.x;
                     t[i][r + 1] = x.y;
+                }
+            }
+            if (odd) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const float whole = ((kw >> (8 * i)) & 0xffu) >= kOddScale ? 0x1p24f : 1.f;
+#pragma unroll
+                    for (int r = 0; r < RPW; ++r) t[i][r] *= whole;
                 }
             }
             // causal mask: row r (token r / G) sees the key that is `ahead` of the first token
