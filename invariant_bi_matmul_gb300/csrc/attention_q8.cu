@@ -884,7 +884,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const int up = 23 - 8 * i;  // byte i to the exponent's place
                 const uint32_t ks = up > 0 ? kw << (up & 31) : kw >> (-up & 31);
                 const uint32_t vs = up > 0 ? vw << (up & 31) : vw >> (-up & 31);
-                ka[i] = __uint_as_float(ks & 0x7f800000u);  // (a byte of 0: 2^-127 scores as 0)
+                // (a byte of 0 is 2^-127)
+                ka[i] = __uint_as_float(max(ks & 0x7f800000u, 0x00400000u));
                 // 2^23 + byte, less 2^23 + 127
                 vb[i] = __uint_as_float(__byte_perm(vw, 0x4b000000u, 0x7650 | i)) - 8388735.f;
                 vinv[i] = __uint_as_float(0x7f000000u - (vs & 0x7f800000u));

@@ -63,6 +63,31 @@ def test_large_keys_at_right_angles_to_large_queries(dev):  # noqa: F811
     against_64_bits(c, q.bfloat16(), out, lse, L, 0.5)
 
 
+def test_hidden_scale_bytes_change_no_bit(dev):  # noqa: F811
+    """Key scale bytes of 0 stand for 2^-127 whatever the bytes beside them are, hidden ones
+    among them: large queries see the same keys, bit for bit, with NaN, huge or small rows at
+    later positions of the same chunk, and the values of the definition."""
+    L, Hkv, D, Hq = 300, 2, 128, 8
+    c = filled([L], Hkv, D, dev, seed=9, k=(signs((L, Hkv, D), 10) * 448).bfloat16(),
+               v=rows((L, Hkv, D), 11))
+    page = c.table[0].long()
+    for p in page.tolist():
+        c.ks[p] = 0
+        c.ks[p, :, 1::4] = 3
+        c.vs[p] = c.vs[p].clamp(max=200)           # (unwritten slots too)
+    q = (signs((4, Hq, D), 12) * sizes((4, Hq, D), 13) * 2.0 ** 117).bfloat16()
+    last = (int(page[(L - 1) // 64]), slice(None), (L - 1) % 64)
+    got = {}
+    for byte in (0, 3, 100, 223, 224, 230, 253, 254, 255):
+        c.ks[last] = byte
+        out, lse = attend(c, q.to(dev), [L], [4], 0.25, "verify")
+        got[byte] = out[:3].clone(), lse[:3].clone()
+        if byte == 0:
+            against_64_bits(c, q, out, lse, L, 0.25)
+    for byte, (o, l) in got.items():
+        assert bits_equal(o, got[0][0]) and bits_equal(l, got[0][1]), byte
+
+
 def test_bits_beside_hidden_large_rows(dev):  # noqa: F811
     """Ordinary queries and keys beside later rows of every large scale keep their bits, and so
     do single tokens of a sequence whose keys are large."""
