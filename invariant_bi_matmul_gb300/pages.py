@@ -105,6 +105,8 @@ class PagePool:
         pages from the number in use upwards are free afterwards."""
         used: Dict[int, int] = {}
         for t in tables:
+            if len(set(t)) != len(t) or any(not 0 <= p < self.num_pages for p in t):
+                raise ValueError("a sequence's pages must be in range and named once")
             for p in t:
                 used[p] = used.get(p, 0) + 1
         if any(used.get(p, 0) != c for p, c in enumerate(self._count)):
