@@ -1000,9 +1000,10 @@ kv_append_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_ne
     const int b = lo;
     const int L = seq_lens[b];
     const int t0 = cu_q[b];
-    const int qb = cu_q[b + 1] - t0;
-    if (t < t0 || t >= t0 + qb) return;  // token of no sequence (cu_q[0] > 0)
-    if (qb > L || L > max_pages * PAGE || t0 + qb > total_q) {
+    const int qb = int(uint32_t(cu_q[b + 1]) - uint32_t(t0));
+    if (t < t0 || t >= cu_q[b + 1]) return;  // token of no sequence (cu_q[0] > 0)
+    // (qb < 1 here: the difference of the offsets passed 2^31)
+    if (qb < 1 || qb > L || int64_t(L) > int64_t(max_pages) * PAGE || t0 + qb > total_q) {
         latch_error(err, kErrDeviceArg);
         return;
     }

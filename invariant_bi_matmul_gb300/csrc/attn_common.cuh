@@ -44,7 +44,7 @@ __device__ __forceinline__ SeqInfo seq_info(const int32_t* seq_lens, const int32
     s.L = seq_lens[b];
     if (cu_q) {
         s.t0 = cu_q[b];
-        s.qb = cu_q[b + 1] - s.t0;
+        s.qb = int(uint32_t(cu_q[b + 1]) - uint32_t(s.t0));  // (wraps: seq_ok takes any value)
     } else {
         s.t0 = b;
         s.qb = 1;
@@ -53,8 +53,9 @@ __device__ __forceinline__ SeqInfo seq_info(const int32_t* seq_lens, const int32
 }
 
 __device__ __forceinline__ bool seq_ok(const SeqInfo& s, int max_q, int max_seq_len, int total_q) {
+    // (no sum of two offsets, which could pass 2^31: a block that ends in total_q or before)
     return s.L >= 1 && s.L <= max_seq_len && s.qb >= 1 && s.qb <= max_q && s.qb <= s.L &&
-           s.t0 >= 0 && s.t0 + s.qb <= total_q;
+           s.t0 >= 0 && s.t0 <= total_q - s.qb;
 }
 
 }  // namespace bi

@@ -88,9 +88,11 @@ kv_append_q8_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v
     const int b = lo;
     const int L = seq_lens[b];
     const int t0 = cu_q[b];
-    const int qb = cu_q[b + 1] - t0;
-    if (live && t >= t0 && t < t0 + qb) {  // (else a token of no sequence: padding)
-        if (qb > L || int64_t(L) > int64_t(max_pages) * PAGE || t0 < 0 || t0 + qb > total_q) {
+    const int t1 = cu_q[b + 1];
+    if (live && t >= t0 && t < t1) {  // (else a token of no sequence: padding)
+        // (t0 <= t < t1: their difference passes 2^31 where t0 is negative only)
+        const int qb = int(uint32_t(t1) - uint32_t(t0));
+        if (t0 < 0 || qb > L || int64_t(L) > int64_t(max_pages) * PAGE || t1 > total_q) {
             latch_error(err, kErrDeviceArg);
         } else {
             const int pos = L - qb + (t - t0);
