@@ -82,6 +82,8 @@ bi_status bi_token_logprobs(const void* x, int64_t ldx, int x_dtype, const int32
  *            may be NULL when g_entropy is.
  *   A token of -1 has no g_logp term; one outside [0, n) neither, and sets
  *   BI_ERR_DEVICE_ARG.
+ *   A row without a g_logp term, or with one of 0, and with g_entropy NULL or 0 gets zeros,
+ *   whatever its logits, lse and entropy are (padding may hold NaN).
  *   dx       [rows, n] of x's dtype (fp32 arithmetic, rounded once to nearest even), row
  *            stride lddx >= n; may be x itself (lddx == ldx). */
 bi_status bi_token_logprobs_backward(const void* x, int64_t ldx, int x_dtype,

@@ -574,12 +574,14 @@ cudaError_t launch_forward(const DeviceInfo& dev, const void* x, int64_t ldx,
 constexpr int GT = 256;  // threads of a gradient CTA
 constexpr int GV = 4;    // 16-byte vectors per thread
 
+// zero: 0, or the largest bit pattern where no gradient comes in and none goes out, from a NaN
+// either (p is a number from 0 up, or NaN).
 template <int DT>
 __device__ __forceinline__ float gradient_of(float x, int i, int t, float gl, float ge, float ls,
-                                             float H) {
+                                             float H, uint32_t zero) {
     const float lp = x - ls;
     const float p = exp_of(lp);
-    const float d = p == 0.f ? 0.f : -p * fmaf(ge, lp + H, gl);
+    const float d = __float_as_uint(p) <= zero ? 0.f : -p * fmaf(ge, lp + H, gl);
     return i == t ? d + gl : d;
 }
 
@@ -605,8 +607,9 @@ token_logprobs_backward_kernel(const void* x, int64_t ldx, const int32_t* __rest
     const float gl = g_logp && t >= 0 && t < n ? g_logp[r] : 0.f;
     const float ge = g_entropy ? g_entropy[r] : 0.f;
     const float ls = lse[r], H = entropy ? entropy[r] : 0.f;
+    const uint32_t zero = gl == 0.f && ge == 0.f ? ~0u : 0u;
     auto one = [&](int i) {
-        const float d = gradient_of<DT>(load1<DT>(xr, i), i, t, gl, ge, ls, H);
+        const float d = gradient_of<DT>(load1<DT>(xr, i), i, t, gl, ge, ls, H, zero);
         if (DT == BI_F32)
             reinterpret_cast<float*>(dr)[i] = d;
         else
@@ -639,13 +642,14 @@ token_logprobs_backward_kernel(const void* x, int64_t ldx, const int32_t* __rest
         for (int q = 0; q < 4; ++q) {
             if (DT == BI_F32) {
                 o[q] = __float_as_uint(
-                    gradient_of<DT>(__uint_as_float(w[q]), i + q, t, gl, ge, ls, H));
+                    gradient_of<DT>(__uint_as_float(w[q]), i + q, t, gl, ge, ls, H, zero));
             } else {
                 constexpr bool F16 = DT == BI_F16;
                 o[q] = pack16x2(
-                    gradient_of<DT>(widen16(uint16_t(w[q]), F16), i + 2 * q, t, gl, ge, ls, H),
+                    gradient_of<DT>(widen16(uint16_t(w[q]), F16), i + 2 * q, t, gl, ge, ls, H,
+                                    zero),
                     gradient_of<DT>(widen16(uint16_t(w[q] >> 16), F16), i + 2 * q + 1, t, gl, ge,
-                                    ls, H),
+                                    ls, H, zero),
                     F16);
             }
         }
