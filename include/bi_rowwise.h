@@ -66,7 +66,8 @@ bi_status bi_mean(const void* x, int64_t ldx, int x_dtype, int64_t rows, int64_t
  *            largest entries in descending order as log-probabilities and indices; the
  *            lowest index first among equal entries, NaN below every number.
  *   fp32 sums over a tree that depends on n and x_dtype alone: a row's outputs do not depend on
- *   the number of rows, on the other rows, on top, or on alignment and stride.  A row with a NaN
+ *   the number of rows, on the other rows, on top, or on alignment and stride.  No sum has more
+ *   than 264 terms in a row, so s is within 2^-15 of itself at any n.  A row with a NaN
  *   or +inf, or of nothing but -inf, gives NaN (ids are still ranked). */
 #define BI_LOGPROBS_MAX_TOP 32
 #define BI_LOGPROBS_MAX_N (0x7fffffff - 0x3fff) /* 2^31 - 2^14 */

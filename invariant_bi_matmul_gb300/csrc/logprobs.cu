@@ -8,6 +8,9 @@
 //     of up to 8,192) takes the part's 16-byte vectors t, t + T, ..., eight at a time, all eight
 //     requested before any is used; against a running maximum it keeps (m, s, w) in one pass,
 //     rescaling when a batch raises the maximum;
+//   * in rows of more than 524,288 elements it starts anew after every eight batches and adds
+//     the groups pairwise, so that no sum has more than 264 terms in a row, whatever n is (with
+//     running sums all along, log s of equal entries was off by 8e-4 at n = 2^27);
 //   * one warp folds the threads' (m, s, w) of a part: each lane its T / 32 in ascending order,
 //     then a butterfly; the parts are folded in ascending order.
 // The tree depends on n and the type alone.  Who runs it does not matter to it: with few rows a
@@ -19,9 +22,9 @@
 //
 // Top alternatives.  The k-th largest of the thread maxima bounds the k-th largest element from
 // below, so few elements (k, and a handful more) lie at or above it; all threads look again at
-// the vectors of the few that hold one (each at its own, 1024 x 128256 fp32 with 20 took 133
-// us), the elements are ranked by counting, and rank 0 ranks the CTAs' first k.  Where ties make them too many, k rounds of a maximum below the last
-// one found.
+// the vectors of the few that hold one (each at its own, 1024 x 128256 fp32 with 20 took 133 us),
+// the elements are ranked by counting, and rank 0 ranks the CTAs' first k.  Where ties make them
+// too many, k rounds of a maximum below the last one found.
 //
 // Backward.  Elementwise from the saved lse and entropy: one read, one write.
 //
@@ -48,6 +51,8 @@ namespace {
 constexpr int kMaxParts = 8;
 constexpr int64_t kPart = 16384;       // elements of a part, while eight parts are enough
 constexpr int kBatch = 8;              // vectors that a thread requests at a time
+constexpr int kFold = 8;               // batches that a thread sums before it starts anew
+constexpr int kLevels = 13;            // of pairwise sums: 2^12 groups at the longest row
 constexpr int kList = 512;             // candidates gathered for the top entries
 constexpr float kNaN = __builtin_nanf("");
 
@@ -285,7 +290,8 @@ constexpr int kGroups = 64;  // groups of threads whose maxima bound the top ent
 // CTAs per multiprocessor: seven of 128 threads (1024 x 100001 bf16, unaligned, 63 us; six 69,
 // where 1024 rows are two waves), four of 256; three where unaligned, or registers spill (fp32 96
 // us, 106 with four).
-template <int DT, int T, bool ALIGNED>
+// LONG: a part has more than kFold batches.
+template <int DT, int T, bool ALIGNED, bool LONG>
 __global__ void __launch_bounds__(T, T == 128 ? 7 : ALIGNED ? 4 : 3)
 token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __restrict__ tokens,
                       int n, int part, int parts, int ctas, float* logp, float* entropy,
@@ -317,6 +323,9 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
         for (int p = 0; p < mine; ++p) {
             const int v0 = (p0 + p) * part, v1 = min(vecs, v0 + part);
             float m = -INFINITY, s = 0.f, w = 0.f;
+            Stats level[LONG ? kLevels : 1];  // sums of 2^l groups, for each bit l of `groups`
+            uint32_t groups = 0;
+            int batch = 0;
             for (int g = v0; g < v1; g += T * kBatch) {
                 // every thread's vectors are there, and whole
                 const bool full = g + kBatch * T <= min(v1, whole);
@@ -368,6 +377,23 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
                 }
                 s = s2.x + s2.y;
                 w = w2.x + w2.y;
+                if (LONG && (++batch % kFold == 0 || g + T * kBatch >= v1)) {
+                    Stats a{m, s, w};
+                    int l = 0;
+                    for (; (groups >> l) & 1u; ++l) join(a, level[l]);
+                    level[l] = a;
+                    ++groups;
+                    m = -INFINITY;
+                    s = w = 0.f;
+                }
+            }
+            if (LONG) {
+                Stats a{m, s, w};  // (none, and that of a part without vectors)
+                for (int l = 0; l < kLevels; ++l)
+                    if ((groups >> l) & 1u) join(a, level[l]);
+                m = a.m;
+                s = a.s;
+                w = a.w;
             }
             tm[p][tid] = m;
             ts[p][tid] = s;
@@ -563,10 +589,13 @@ cudaError_t launch_forward(const DeviceInfo& dev, const void* x, int64_t ldx,
     while (ctas < c.parts && rows * ctas < 2 * int64_t(dev.num_sms)) {
         do ++ctas; while (c.parts % ctas != 0);
     }
-    return launch_pdl_cluster(token_logprobs_kernel<DT, T, ALIGNED>, dim3(unsigned(rows * ctas)),
-                              dim3(T), 0, stream, unsigned(ctas), x, ldx, tokens, int(n), c.part,
-                              c.parts, ctas, logp, entropy, lse, top, top_logp, top_ids,
-                              dev.err_word);
+    auto kern = token_logprobs_kernel<DT, T, ALIGNED, false>;
+    if constexpr (DT != BI_F32 || T == 256) {  // (fp32 rows for 128 threads are short)
+        if (c.part > kFold * T * kBatch) kern = token_logprobs_kernel<DT, T, ALIGNED, true>;
+    }
+    return launch_pdl_cluster(kern, dim3(unsigned(rows * ctas)), dim3(T), 0, stream,
+                              unsigned(ctas), x, ldx, tokens, int(n), c.part, c.parts, ctas, logp,
+                              entropy, lse, top, top_logp, top_ids, dev.err_word);
 }
 
 // ------------------------------------------------------------------------- backward
