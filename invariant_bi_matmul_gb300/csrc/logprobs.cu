@@ -275,9 +275,9 @@ __device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.f :
 // and s = NaN, which stays.
 __device__ __forceinline__ void join(Stats& a, const Stats& b) {
     const float M = fmaxf(a.m, b.m), c = ref_of(M);
-    // (2^u is 0 long before -1e4; 0 * -inf is not)
-    const float da = fmaxf((ref_of(a.m) - c) * kLog2e, -1e4f);
-    const float db = fmaxf((ref_of(b.m) - c) * kLog2e, -1e4f);
+    // (2^u is 0 long before -1e4; 0 * -inf is not, nor is 0 * +inf: none beside the lowest value)
+    const float da = a.m == -INFINITY ? 0.f : fmaxf((a.m - c) * kLog2e, -1e4f);
+    const float db = b.m == -INFINITY ? 0.f : fmaxf((b.m - c) * kLog2e, -1e4f);
     const float fa = a.m == -INFINITY ? a.s : ex2(da), fb = b.m == -INFINITY ? b.s : ex2(db);
     a.w = fmaf(fa, fmaf(a.s, da, a.w), fb * fmaf(b.s, db, b.w));
     a.s = fmaf(a.s, fa, b.s * fb);
@@ -341,7 +341,7 @@ token_logprobs_kernel(const void* __restrict__ x, int64_t ldx, const int32_t* __
 #pragma unroll
                 for (int k = 1; k < kBatch; ++k) bm = fmaxf(bm, vec_max<DT>(a[k]));
                 if (bm > m) {
-                    const float d = fmaxf((ref_of(m) - ref_of(bm)) * kLog2e, -1e4f);
+                    const float d = m == -INFINITY ? 0.f : fmaxf((m - bm) * kLog2e, -1e4f);
                     const float f = m == -INFINITY ? s : ex2(d);  // (s is 0 or NaN there)
                     w = f * fmaf(s, d, w);
                     s *= f;
