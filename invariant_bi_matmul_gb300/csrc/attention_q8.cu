@@ -104,7 +104,17 @@ struct Cfg {
     // K-major and MN-major rows of D bytes: the 128- or 64-byte swizzle, groups of 8 rows
     static constexpr uint32_t LAYOUT = D == 128 ? 2 : 4;
     static constexpr uint32_t SBO = 8 * D;
-    static_assert(P_OFF % 1024 == 0 && RING_OFF % 1024 == 0 && SLOT_BYTES % 1024 == 0, "");
+    // swizzled tiles start on their pattern's boundary, what is read and written 16 bytes at a
+    // time (scale bytes, descriptors, row factors, sums and maxima) and the barriers on theirs
+    static_assert(Q_OFF % 1024 == 0 && Q_PIECE % 1024 == 0 && P_OFF % 1024 == 0 &&
+                      P_BYTES % 1024 == 0 && RING_OFF % 1024 == 0 && V_OFF % 1024 == 0 &&
+                      SLOT_BYTES % 1024 == 0 && PAGE_BYTES % 1024 == 0,
+                  "tiles");
+    static_assert(SCALE_OFF % 16 == 0 && SCALE_BYTES % 16 == 0 && TK * NT % 16 == 0 &&
+                      BAR_OFF % 8 == 0 && DESC_OFF % 16 == 0 && XS_OFF % 16 == 0 &&
+                      (NQ + 1) * QR % 4 == 0 && QR % 4 == 0 && MISC_OFF % 4 == 0,
+                  "regions");
+    static_assert(DESC_OFF >= BAR_OFF + NBARS * 8 + 4, "the tensor memory's address fits");
     static_assert(LEAD + NSLOT + 6 < NDESC, "descriptors in flight (see the scheduler)");
     static_assert(SMEM <= 232448, "shared memory per CTA");
 };
