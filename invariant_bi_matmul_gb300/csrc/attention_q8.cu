@@ -68,7 +68,7 @@ constexpr int TMEM_COLS = 512;
 constexpr int S_COL = 0;                  // two S sets (by item) of NT tiles, 32 columns each
 constexpr int O_COL = 2 * NT * QR;          // O buffers (by item): 32 hi + 32 lo columns each
 constexpr uint32_t kOddScale = 224;       // scale bytes from here on take the longer way
-constexpr float kNoKey = -1e30f;          // m of a chunk of which a row sees no key
+constexpr float kLowest = -3.402823466e38f;  // the maximum, where a row sees no key of a chunk
 constexpr float kHeadroom = 8.f;          // p = 2^8 at the row's maximum (e4m3 holds 448)
 constexpr float kLoScale = 32.f;          // the second piece of p (at most 8) times this
 constexpr int MAX_BATCH = BI_ATTN_MAX_BATCH;
@@ -978,15 +978,11 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const float4 x1 = *reinterpret_cast<const float4*>(xm + 1 * QR + r);
                 const float4 x2 = *reinterpret_cast<const float4*>(xm + 2 * QR + r);
                 const float4 x3 = *reinterpret_cast<const float4*>(xm + 3 * QR + r);
-                m[r] = fmaxf(fmax3(x0.x, x1.x, x2.x), x3.x);
-                m[r + 1] = fmaxf(fmax3(x0.y, x1.y, x2.y), x3.y);
-                m[r + 2] = fmaxf(fmax3(x0.z, x1.z, x2.z), x3.z);
-                m[r + 3] = fmaxf(fmax3(x0.w, x1.w, x2.w), x3.w);
+                m[r] = fmax3(fmax3(x0.x, x1.x, x2.x), x3.x, kLowest) - kHeadroom;
+                m[r + 1] = fmax3(fmax3(x0.y, x1.y, x2.y), x3.y, kLowest) - kHeadroom;
+                m[r + 2] = fmax3(fmax3(x0.z, x1.z, x2.z), x3.z, kLowest) - kHeadroom;
+                m[r + 3] = fmax3(fmax3(x0.w, x1.w, x2.w), x3.w, kLowest) - kHeadroom;
             }
-            // a row that sees no key here (its p are 0: -inf less any number) has no maximum
-#pragma unroll
-            for (int r = 0; r < RPW; ++r)
-                m[r] = m[r] == -INFINITY ? kNoKey : m[r] - kHeadroom;
 #pragma unroll
             for (int r = 0; r < RPW; ++r) l[r] = 0.f;
             // P's buffers are free once P V of item-1 has completed
