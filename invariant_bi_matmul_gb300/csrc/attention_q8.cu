@@ -888,50 +888,49 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_k,
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[ob]);
             // the scales of this thread's keys: 2^x, y, 2^-y
-            float ka[NT], vb[NT], vinv[NT];
+            float ka[NT], vb[NT], vinv[NT], t[NT][RPW], mx[RPW];
+            auto score = [&](int i, int r) {
+                const float2 s2 = make_float2(__uint_as_float(sv[i][r]),
+                                              __uint_as_float(sv[i][r + 1]));
+                return fma2(mul2(s2, make_float2(ka[i], ka[i])), f[r / 2],
+                            make_float2(vb[i], vb[i]));
+            };
+            if (!odd) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const int up = 23 - 8 * i;  // byte i to the exponent's place
-                const uint32_t ks = up > 0 ? kw << (up & 31) : kw >> (-up & 31);
-                const uint32_t vs = up > 0 ? vw << (up & 31) : vw >> (-up & 31);
-                // (a byte of 0 is 2^-127)
-                ka[i] = __uint_as_float(max(ks & 0x7f800000u, 0x00400000u));
-                // 2^23 + byte, less 2^23 + 127
-                vb[i] = __uint_as_float(__byte_perm(vw, 0x4b000000u, 0x7650 | i)) - 8388735.f;
-                vinv[i] = __uint_as_float(0x7f000000u - (vs & 0x7f800000u));
-            }
-            if (odd) {
+                for (int i = 0; i < NT; ++i) {
+                    const int up = 23 - 8 * i;  // byte i to the exponent's place
+                    const uint32_t ks = up > 0 ? kw << (up & 31) : kw >> (-up & 31);
+                    const uint32_t vs = up > 0 ? vw << (up & 31) : vw >> (-up & 31);
+                    // (a byte of 0 is 2^-127)
+                    ka[i] = __uint_as_float(max(ks & 0x7f800000u, 0x00400000u));
+                    // 2^23 + byte, less 2^23 + 127
+                    vb[i] = __uint_as_float(__byte_perm(vw, 0x4b000000u, 0x7650 | i)) - 8388735.f;
+                    vinv[i] = __uint_as_float(0x7f000000u - (vs & 0x7f800000u));
+#pragma unroll
+                    for (int r = 0; r < RPW; r += 2) {
+                        const float2 x = score(i, r);
+                        t[i][r] = x.x;
+                        t[i][r + 1] = x.y;
+                    }
+                }
+            } else {
                 // Products of codes are below 2^24: times a key scale below 2^97 they are finite.
                 // With a larger one t is formed as 2^24 * (t * 2^-24), whose factors are finite
                 // where t is, and whose rounding is the same.
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     const uint32_t ks = (kw >> (8 * i)) & 0xffu, vs = (vw >> (8 * i)) & 0xffu;
-                    const float part = ks >= kOddScale ? 0x1p-24f : 1.f;
-                    ka[i] = e8m0(ks) * part;
-                    vb[i] = vs == 255 ? __int_as_float(0x7fc00000) : float(int(vs) - 127) * part;
+                    const bool big = ks >= kOddScale;
+                    ka[i] = e8m0(ks) * (big ? 0x1p-24f : 1.f);
+                    vb[i] = vs == 255 ? __int_as_float(0x7fc00000)
+                                      : float(int(vs) - 127) * (big ? 0x1p-24f : 1.f);
                     vinv[i] = e8m0_inv(vs);
-                }
-            }
-            float t[NT][RPW], mx[RPW];
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-#pragma unroll
-                for (int r = 0; r < RPW; r += 2) {
-                    const float2 s2 = make_float2(__uint_as_float(sv[i][r]),
-                                                  __uint_as_float(sv[i][r + 1]));
-                    const float2 x = fma2(mul2(s2, make_float2(ka[i], ka[i])), f[r / 2],
-                                          make_float2(vb[i], vb[i]));
-                    t[i][r] = x.x;
-                    t[i][r + 1] = x.y;
-                }
-            }
-            if (odd) {
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const float whole = ((kw >> (8 * i)) & 0xffu) >= kOddScale ? 0x1p24f : 1.f;
-#pragma unroll
-                    for (int r = 0; r < RPW; ++r) t[i][r] *= whole;
+                    for (int r = 0; r < RPW; r += 2) {
+                        const float2 x = score(i, r);
+                        t[i][r] = x.x * (big ? 0x1p24f : 1.f);
+                        t[i][r + 1] = x.y * (big ? 0x1p24f : 1.f);
+                    }
                 }
             }
             // causal mask: row r (token r / G) sees the key that is `ahead` of the first token
