@@ -410,8 +410,9 @@ bi_status bi_verify_block_static_ws(const void* q, const void* k_cache, const vo
  *                     codes; 16-byte aligned.
  *   k_scale, v_scale  uint8 [num_pages, num_kv_heads, BI_PAGE_SIZE]: one E8M0 byte s per
  *                     token and KV head; 16-byte aligned.
- *   A row stands for code * 2^(s - 127); s = 255 means a row of NaN.  block_table, seq_lens
- *   and cu_q as for the bf16 cache.
+ *   A row stands for code * 2^(s - 127); s = 255 means a row of NaN, whatever its codes.  Codes
+ *   of rows that hold a token are numbers (0x7f and 0xff, E4M3's NaN, are not used).
+ *   block_table, seq_lens and cu_q as for the bf16 cache.
  *
  * bi_kv_append_q8: bi_kv_append into an 8-bit cache.  For each row x (D values of one token
  *   and KV head): e = the smallest integer >= -64 with max|x| <= 448 * 2^e, s = e + 127,
@@ -436,7 +437,8 @@ bi_status bi_kv_append_q8(const void* k_new, const void* v_new, void* k_cache, v
  *   from all three entry points.
  *   A key row of NaN makes the queries that see it NaN, and no others.  The value scales that
  *   one query sees should lie within a factor 2^80 of one another (softmax weights are held
- *   relative to them).
+ *   relative to them), and be 2^-96 or more (their inverses are summed; the append writes
+ *   2^-64 and more).
  *   Scores scale * q . k may have any finite size.  From 2^23 on fp32 cannot hold one and the
  *   exponent of a value scale together: keys of equal score then weigh in inverse proportion
  *   to their value scales.

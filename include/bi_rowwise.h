@@ -77,7 +77,8 @@ bi_status bi_token_logprobs(const void* x, int64_t ldx, int x_dtype, const int32
 
 /* Gradient of sum_r g_logp[r] * logp[r] + g_entropy[r] * entropy[r] with respect to x:
  *   dx[r, i] = g_logp[r] * ([i == tokens[r]] - p_i) - g_entropy[r] * p_i * (log p_i + entropy[r]),
- *   p_i = exp(x_i - lse[r]); an entry with p_i = 0 gets 0 (plus g_logp at the token).
+ *   p_i = exp(x_i - lse[r]); an entry with p_i = 0 gets 0 (plus g_logp at the token).  The
+ *   fp32 lse is off by up to 2^-24 of itself, which p_i takes over as a factor.
  *   lse, entropy  fp32 [rows], as bi_token_logprobs gave them.
  *   g_logp, g_entropy  fp32 [rows]; either may be NULL (a gradient of 0), not both; entropy
  *            may be NULL when g_entropy is.

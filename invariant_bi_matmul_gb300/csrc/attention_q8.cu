@@ -11,12 +11,12 @@
 // Both products run on the codes as they lie in the cache (tcgen05 kind::f8f6f4, e4m3 x e4m3,
 // fp32 accumulators).  The other operand is split into two e4m3 pieces, so nothing of its
 // precision is lost to 8 bits:
-//   * q * 2^s (s puts the row's largest value in [128, 256)) = hi + lo, each rounded to
-//     nearest: exact for bf16 q down to 2^-9 of the row's largest value, off by at most
-//     2^-18 of it below;
-//   * p = hi + lo / 32: p <= 2^8; hi has four bits, lo the next four, so p is held to
-//     2^-9 of itself (bf16 would hold 2^-8) or to 2^-15 absolute (2^-23 of the row's
-//     largest), whichever is more.
+//   * q * 2^s (s puts the row's largest value in [128, 256) where that is 2^-113 or more) =
+//     hi + lo, each rounded to nearest: exact for bf16 q down to 2^-9 of the row's largest
+//     value, off by at most 2^-17 of it below (2^-10 beside 128);
+//   * p = hi + lo / 32: p <= 2^8, rounded to binary16 first; hi has four bits, lo the next
+//     four, so p is held to 2^-9 + 2^-11 of itself (bf16 would hold 2^-8) or, in place of the
+//     2^-9, to 2^-15 absolute (2^-23 of the row's largest), whichever is more.
 //
 // Reduction of one (query, head) -- a function of its position alone, as in attention.cu:
 // chunks of 512 keys from key 0; m is the exact maximum of the row's t over the chunk, less 8
@@ -47,9 +47,10 @@
 //
 // Bound by memory: 2 * (D + 1) bytes per key and KV head against 4 * 32 * D operations.  One query
 // row per KV group of four: eight sequences of 65,540 keys 165 us (97% of the copy rate), 64 ragged
-// ones of up to 16,388 220 us (98%), one of 1,028 9.4 us (launches, one chunk's chain, the merge).
-// 32 query rows: 64 of 8,196 keys 245 us (66%: 4.1 us an item where one row takes 3.2, and a merge
-// of 145 MB), one of 65,540 39.5 us (51%: seven rounds of items).
+// ones of up to 16,388 220 us (98%), one of 1,028 9.6 us (launches, one chunk's chain, the merge).
+// 32 query rows: 64 of 8,196 keys 240 us (67%: 4 us an item where one row takes 3.2, and a merge
+// of 145 MB), one of 65,540 38.8 us (51%: seven rounds of items).  The two instances of 32 rows
+// have 28 warps at 72 registers and spill 40 bytes.
 #include "attn_common.cuh"
 
 #include <cuda_fp8.h>
