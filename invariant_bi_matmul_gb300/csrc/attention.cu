@@ -660,6 +660,13 @@ constexpr int MERGE_WARPS = 8;    // chunk ranges of the merge tree
 // 17 chunks 48.0 and 47.3
 constexpr int64_t kMergeRowsMin = 1024;
 constexpr int MERGE_UNROLL = 17;  // partials requested per round trip (136 chunks in 8)
+// A merge that waits on item counts runs beside the partial kernel.  At head_dim 64 that kernel
+// leaves room for several merge CTAs on its SM, and their polling slows it down: this much shared
+// memory each leaves one (bf16 cache, 128 one-token sequences of 8,196 keys 624 us, 656 with
+// several; 64 of 8 heads and 16,388 keys 414 and 425).  Calls with few items have a short wait, and
+// the CTA per row does better early there (24 sequences of 1,028 keys 25.3 us, 26.4 with one).
+constexpr int kMergeApart = 40 * 1024;
+constexpr int64_t kMergeApartItems = 2048;
 
 // The merge tree of one (token, query head) row with nC = pos/chunk + 1 chunk partials:
 // range w = [w*nC/8, (w+1)*nC/8) is folded in ascending chunk order (its max first, then
@@ -1107,10 +1114,12 @@ cudaError_t launch_attn_merge(const PagedArgs& a, void* workspace, int chunk_log
         auto kern = a.head_dim == 64
                         ? (few ? attn_merge_kernel<64, 5> : attn_merge_kernel<64, MERGE_UNROLL>)
                         : (few ? attn_merge_kernel<128, 5> : attn_merge_kernel<128, MERGE_UNROLL>);
-        return launch_pdl(kern, dim3(unsigned(rows)), dim3(MERGE_WARPS * 32), 0, stream,
-                          a.seq_lens, a.cu_q, int(a.batch), int(a.total_q), int(a.max_q),
-                          int(a.max_seq_len), int(a.hq), int(a.hkv), ws_o, ws_ml, maxC,
-                          chunk_log2, cnt, static_cast<__nv_bfloat16*>(out), lse, err);
+        const bool apart = cnt && a.batch * a.hkv * int64_t(maxC) >= kMergeApartItems;
+        return launch_pdl(kern, dim3(unsigned(rows)), dim3(MERGE_WARPS * 32),
+                          apart ? kMergeApart : 0, stream, a.seq_lens, a.cu_q, int(a.batch),
+                          int(a.total_q), int(a.max_q), int(a.max_seq_len), int(a.hq), int(a.hkv),
+                          ws_o, ws_ml, maxC, chunk_log2, cnt, static_cast<__nv_bfloat16*>(out),
+                          lse, err);
     }
     auto kern = a.head_dim == 64
                     ? (maxC <= 4 ? attn_merge_rows_kernel<64, 4>
@@ -1120,10 +1129,10 @@ cudaError_t launch_attn_merge(const PagedArgs& a, void* workspace, int chunk_log
                                  : maxC <= 8 ? attn_merge_rows_kernel<128, 8>
                                              : attn_merge_rows_kernel<128, MERGE_UNROLL>);
     return launch_pdl(kern, dim3(unsigned((rows + MERGE_WARPS - 1) / MERGE_WARPS)),
-                      dim3(MERGE_WARPS * 32), 0, stream, a.seq_lens, a.cu_q, int(a.batch),
-                      int(a.total_q), int(a.max_q), int(a.max_seq_len), int(a.hq), int(a.hkv),
-                      ws_o, ws_ml, maxC, chunk_log2, cnt, static_cast<__nv_bfloat16*>(out), lse,
-                      err);
+                      dim3(MERGE_WARPS * 32), cnt ? kMergeApart : 0, stream, a.seq_lens, a.cu_q,
+                      int(a.batch), int(a.total_q), int(a.max_q), int(a.max_seq_len), int(a.hq),
+                      int(a.hkv), ws_o, ws_ml, maxC, chunk_log2, cnt,
+                      static_cast<__nv_bfloat16*>(out), lse, err);
 }
 
 size_t attn_workspace_bytes(int64_t total_q, int64_t hq, int64_t head_dim, int64_t max_seq_len) {
