@@ -403,6 +403,57 @@ bi_status bi_verify_block_static_ws(const void* q, const void* k_cache, const vo
                                     float scale, void* out, float* lse, bi_stream_t stream);
 
 /* ---------------------------------------------------------------------------------
+ * Rotating append  (no counterpart on the pages; one launch in place of bi_rope on the
+ * queries, bi_rope on the keys and the append)
+ *
+ * bi_rope_kv_append: turns a block's queries and keys by their positions and appends its
+ *   keys and values to a bf16 cache; bi_rope_kv_append_q8: to an 8-bit cache (next section).
+ *   q, q_out  bf16 [total_q, num_q_heads, head_dim], k_new, v_new bf16 [total_q,
+ *             num_kv_heads, head_dim]: a token's heads are contiguous, tokens ldq, ldo, ldk,
+ *             ldv elements apart (slices of one projection's output, for instance).  q_out
+ *             may be q (ldo == ldq); otherwise nothing that the call writes may overlap what
+ *             it reads.  k_new and v_new are not changed.
+ *   Pair i < rotary_dim / 2 of a head joins elements i and i + rotary_dim / 2, as in bi_rope,
+ *   and turns by a = pos * w_i; elements from rotary_dim on stay.
+ *     w_i     inv_freq[i] (host array of rotary_dim / 2), or theta^(-2i/rotary_dim) where
+ *             inv_freq is NULL (theta is then ignored where inv_freq is given).
+ *     pos     the token's place in its sequence, as in bi_rope; with num_axes > 0
+ *             positions[axis * ldp + token] (int32 [num_axes, ldp >= total_q], any value)
+ *             where axis is the section that holds pair i: sections (host array of num_axes)
+ *             says how many pairs each axis turns, in order, rotary_dim / 2 in all.  Where
+ *             rows go in the cache does not depend on positions.
+ *   The angle is formed modulo a turn in 64-bit fixed point: it is as exact at position
+ *   2^31 - 1 as at 1 (bi_rope forms pos * w_i in fp32, which is off by 2^-24 of itself, so
+ *   far positions of the two differ).  Turned rows are rounded to bf16 (nearest even), and
+ *   those bf16 rows are what an 8-bit cache quantises, as bi_kv_append_q8 does.
+ *   rotary_dim: a multiple of 16, at most head_dim (64 or 128).
+ *   Tokens of no sequence (in front of cu_q[0], from cu_q[batch] on) are left alone: nothing
+ *   of them is read into a result or written.  A malformed sequence is skipped, and a row
+ *   whose page is out of range is not appended; either sets BI_ERR_DEVICE_ARG.  A token's
+ *   outputs depend on its own rows and positions alone.
+ * ------------------------------------------------------------------------------- */
+bi_status bi_rope_kv_append(const void* q, int64_t ldq, const void* k_new, int64_t ldk,
+                            const void* v_new, int64_t ldv, void* q_out, int64_t ldo,
+                            void* k_cache, void* v_cache, int64_t num_pages,
+                            const int32_t* block_table, int64_t max_pages,
+                            const int32_t* seq_lens, const int32_t* cu_q, int64_t batch,
+                            int64_t total_q, int64_t num_q_heads, int64_t num_kv_heads,
+                            int64_t head_dim, int64_t page_size, double theta,
+                            const double* inv_freq, int64_t rotary_dim, const int32_t* positions,
+                            int64_t ldp, int64_t num_axes, const int64_t* sections,
+                            bi_stream_t stream);
+bi_status bi_rope_kv_append_q8(const void* q, int64_t ldq, const void* k_new, int64_t ldk,
+                               const void* v_new, int64_t ldv, void* q_out, int64_t ldo,
+                               void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                               int64_t num_pages, const int32_t* block_table, int64_t max_pages,
+                               const int32_t* seq_lens, const int32_t* cu_q, int64_t batch,
+                               int64_t total_q, int64_t num_q_heads, int64_t num_kv_heads,
+                               int64_t head_dim, int64_t page_size, double theta,
+                               const double* inv_freq, int64_t rotary_dim,
+                               const int32_t* positions, int64_t ldp, int64_t num_axes,
+                               const int64_t* sections, bi_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
  * 8-bit paged KV cache  (no counterpart on the pages; decode attention is bound by the
  * cache's bytes, and these halve them)
  *

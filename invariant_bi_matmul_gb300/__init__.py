@@ -32,6 +32,7 @@ LOGPROBS_MAX_TOP = 32
 # every function include/bi.h, include/bi_glue.h and include/bi_rowwise.h declare, with
 # its ctypes signature
 _p, _i64, _f32, _sz, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t, ctypes.c_int
+_f64 = ctypes.c_double
 SIGNATURES = {
     "bi_abi_version": ([], _int),
     "bi_status_string": ([_int], ctypes.c_char_p),
@@ -72,6 +73,12 @@ SIGNATURES = {
                             _i64, _i64, _i64, _i64, _f32, _p, _p, _p, _sz, _p], _int),
     "bi_decode_attn_q8": ([_p, _p, _p, _p, _p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i64, _i64,
                            _i64, _f32, _p, _p, _p, _sz, _p], _int),
+    "bi_rope_kv_append": ([_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _i64, _p, _p,
+                           _i64, _i64, _i64, _i64, _i64, _i64, _f64, _p, _i64, _p, _i64, _i64, _p,
+                           _p], _int),
+    "bi_rope_kv_append_q8": ([_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _i64, _p,
+                              _i64, _p, _p, _i64, _i64, _i64, _i64, _i64, _i64, _f64, _p, _i64,
+                              _p, _i64, _i64, _p, _p], _int),
     "bi_kv_copy_pages": ([_p, _p, _i64, _i64, _p, _p, _i64, _p], _int),
     "bi_device_status": ([_p], _int),
     "bi_selftest_wait_timeout": ([ctypes.c_uint64, _p], _int),
@@ -630,6 +637,120 @@ def decode_attn_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
     """decode_attn over an 8-bit cache: one new token per sequence, q bf16 [B, Hq, D]."""
     return _attend_q8("bi_decode_attn_q8", q, k_cache, v_cache, k_scale, v_scale, block_table,
                       seq_lens, None, 1, max_seq_len, scale, out, lse, want_lse, workspace, stream)
+
+
+# -------------------------------------------------------------------- rotating append
+
+def _token_rows(t, dev, d, name):
+    """(tokens, heads, row stride) of a bf16 [T, H, D] tensor on CUDA device dev whose heads are
+    contiguous within a token."""
+    torch = _torch()
+    try:
+        fine = t.get_device() == dev and t.dtype is torch.bfloat16 and t.dim() == 3
+    except AttributeError:
+        fine = False
+    if not fine or dev < 0:
+        _need(t, torch.bfloat16, name, 3)
+        _on_current_device(**{name: t})
+    T, h, dt = t.shape
+    st = t.stride()
+    if dt != d or st[2] != 1 or (st[1] != d and h > 1):
+        raise ValueError(f"{name} must have contiguous heads of the cache's D within a token")
+    return T, h, st[0] if T > 1 else h * d
+
+
+def _rope_kv_append(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                    cu_q, theta, positions, sections, inv_freq, rotary_dim, out, stream):
+    torch = _torch()
+    i32 = torch.int32
+    if k_scale is not None:
+        dev, B, max_pages, num_pages, hkv, page, d = _paged_common_q8(
+            k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
+    else:
+        dev = _device_of(k_cache)
+        num_pages, hkv, page, d = _paged_common(k_cache, v_cache, block_table, seq_lens)
+        _on_current_device(k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+                           seq_lens=seq_lens)
+        B, max_pages = block_table.shape
+        if seq_lens.shape[0] != B:
+            raise ValueError("block_table and seq_lens disagree on the batch")
+    T, hq, ldq = _token_rows(q, dev, d, "q")
+    Tk, hk, ldk = _token_rows(k_new, dev, d, "k_new")
+    Tv, hv, ldv = _token_rows(v_new, dev, d, "v_new")
+    if not T == Tk == Tv or not hk == hv == hkv:
+        raise ValueError("q, k_new and v_new must have one number of tokens, and k_new and v_new "
+                         "the cache's Hkv")
+    if not _all(dev, (cu_q, i32, 1)) or cu_q.shape[0] != B + 1:
+        _need(cu_q, i32, "cu_q", 1)
+        _on_current_device(cu_q=cu_q)
+        raise ValueError("cu_q must be contiguous with batch + 1 entries")
+    rotary_dim = d if rotary_dim is None else int(rotary_dim)
+    freq_ptr = axes_ptr = pos_ptr = None
+    axes = ldp = 0
+    if inv_freq is not None:
+        freq = array.array("d", inv_freq)
+        if 2 * len(freq) != rotary_dim:
+            raise ValueError("inv_freq must have rotary_dim / 2 entries")
+        freq_ptr = freq.buffer_info()[0]
+    if (positions is None) != (sections is None):
+        raise ValueError("positions and sections go together")
+    if positions is not None:
+        if not _all(dev, (positions, i32, 2)):
+            _need(positions, i32, "positions", 2)
+            _on_current_device(positions=positions)
+            raise ValueError("positions must be contiguous")
+        pairs = array.array("q", sections)
+        axes, ldp = positions.shape
+        if len(pairs) != axes or ldp != T or axes < 1:
+            raise ValueError("positions must be [axes, T], with one section per axis")
+        axes_ptr, pos_ptr = pairs.buffer_info()[0], positions.data_ptr()
+    if out is None:
+        with _allocating_for(stream):
+            out = torch.empty(T, hq, d, dtype=torch.bfloat16, device=q.device)
+        ldo = hq * d
+    else:
+        To, ho, ldo = _token_rows(out, dev, d, "out")
+        if (To, ho) != (T, hq):
+            raise ValueError("out must have the shape of q")
+    head = (q.data_ptr(), ldq, k_new.data_ptr(), ldk, v_new.data_ptr(), ldv, out.data_ptr(), ldo,
+            k_cache.data_ptr(), v_cache.data_ptr())
+    tail = (num_pages, block_table.data_ptr(), max_pages, seq_lens.data_ptr(), cu_q.data_ptr(), B,
+            T, hq, hkv, d, page, float(theta), freq_ptr, rotary_dim, pos_ptr, ldp, axes, axes_ptr,
+            _stream_on(stream, dev))
+    if k_scale is None:
+        _check(lib().bi_rope_kv_append(*head, *tail))
+    else:
+        _check(lib().bi_rope_kv_append_q8(*head, k_scale.data_ptr(), v_scale.data_ptr(), *tail))
+    return out
+
+
+def rope_kv_append(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_q,
+                   theta: float = 500000.0, positions=None, sections: Optional[Sequence[int]] = None,
+                   inv_freq: Optional[Sequence[float]] = None, rotary_dim: Optional[int] = None,
+                   out=None, stream=None):
+    """rope on q and k_new and kv_append of the turned keys and the values, in one launch;
+    returns the turned queries (in `out`, which may be q).  q bf16 [T, Hq, D], k_new and v_new
+    bf16 [T, Hkv, D], whose tokens may be strided (slices of one projection's output).
+
+    Pair i of a head turns by pos * inv_freq[i], by default theta ** (-2 i / rotary_dim); pos is
+    the token's place in its sequence or, with `positions` (int32 [axes, T]) and `sections` (pairs
+    per axis, rotary_dim / 2 in all), the position on the axis that pair i belongs to.  Angles
+    are exact at any position (rope forms them in fp32)."""
+    return _rope_kv_append(q, k_new, v_new, k_cache, v_cache, None, None, block_table, seq_lens,
+                           cu_q, theta, positions, sections, inv_freq, rotary_dim, out, stream)
+
+
+def rope_kv_append_q8(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                      cu_q, theta: float = 500000.0, positions=None,
+                      sections: Optional[Sequence[int]] = None,
+                      inv_freq: Optional[Sequence[float]] = None,
+                      rotary_dim: Optional[int] = None, out=None, stream=None):
+    """rope_kv_append into an 8-bit cache (see kv_append_q8)."""
+    if k_scale is None or v_scale is None:
+        raise TypeError("k_scale and v_scale must be torch.Tensors")
+    return _rope_kv_append(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table,
+                           seq_lens, cu_q, theta, positions, sections, inv_freq, rotary_dim, out,
+                           stream)
 
 
 def kv_copy_pages(planes: Sequence, src, dst, stream=None) -> None:
