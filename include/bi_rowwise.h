@@ -1,7 +1,7 @@
 /*
  * bi_rowwise.h -- batch-invariant row-wise reductions beyond RMSNorm, in libbi: the
- * log-softmax of a logits row, the mean of a row, and the log-probabilities of given tokens
- * with entropy, top alternatives and gradient.
+ * log-softmax of a logits row, the mean of a row, the log-probabilities of given tokens
+ * with entropy, top alternatives and gradient, and the verification of drafted tokens.
  *
  * Source: book chapter "Batch-invariant kernels: why temperature-0 decoding is still
  * nondeterministic", Sources (the companion library overrides RMSNorm, matmul, mean and
@@ -93,6 +93,56 @@ bi_status bi_token_logprobs_backward(const void* x, int64_t ldx, int x_dtype,
                                      const float* lse, const float* entropy, const float* g_logp,
                                      const float* g_entropy, void* dx, int64_t lddx,
                                      bi_stream_t stream);
+
+/* Verification of drafted tokens from given random numbers: what a speculative step does with
+ * the logits of its verify block at a temperature.  One row of logits per token of the block, as
+ * bi_verify_block lays blocks out: rows cu_q[b] .. cu_q[b+1]-1 are sequence b's, the first for its
+ * last input and one for each drafted token behind it; the row in front of a drafted token decides
+ * it.  With p = softmax(row / T) of that row and q the distribution that the draft was drawn from:
+ *   - draft j is kept while u_j * q(token_j) < p(token_j);
+ *   - in place of the first that is not, the first token i is emitted for which the sum of
+ *     max(p_k - q_k, 0) over k <= i exceeds u of the whole sum (where p and q are equal
+ *     throughout: of p);
+ *   - behind a block that is kept in full, the first i for which the sum of p_k exceeds u.
+ *   The emitted tokens are distributed as p, whatever the drafts were.
+ *   T = 0 (or below 2^-64): a draft is kept while it is the row's largest entry, and the largest
+ *   entry is emitted at the end, ranked as bi_argmax ranks.
+ *
+ *   logits       [total_q, n], dtype BI_BF16, BI_F16 or BI_F32, row stride ldl >= n, aligned to
+ *                its element size.  1 <= n <= BI_DRAFTS_MAX_N.
+ *   draft_logits [num_drafts, n] of the same dtype, row stride ldd >= n: q = softmax(row / T); or
+ *                NULL: each draft was chosen without chance, q is 1 at the token and 0 elsewhere.
+ *   draft_tokens int32 [num_drafts]: the drafts of all sequences one after the other, a sequence
+ *                of w rows having w - 1.  (Draft j of sequence b is entry cu_q[b] - b + j.)  -1 is
+ *                no draft: the block ends in front of it, with a token drawn from p.  Any other id
+ *                outside [0, n) does the same and sets BI_ERR_DEVICE_ARG.
+ *   uniforms     fp32 [total_q], in [0, 1): row cu_q[b] + j decides draft j, and the sequence's
+ *                last row draws its last token.  (Values outside are taken as the nearest inside
+ *                for a draw, NaN as 0; as they are in the comparison.)
+ *   temperatures fp32 [batch], or NULL: `temperature` for all.  A sequence whose temperature is
+ *                negative, infinite or NaN gets no tokens and sets BI_ERR_DEVICE_ARG.
+ *   cu_q         int32 [batch + 1], cu_q[0] = 0, 1 to max_q rows each, cu_q[batch] <= total_q and
+ *                cu_q[batch] - batch <= num_drafts; else the whole call emits nothing and sets
+ *                BI_ERR_DEVICE_ARG.  Rows behind the last sequence are not read.
+ *   tokens       int32 [batch, max_q]: the kept drafts, then the drawn token, then -1.
+ *   accepted     int32 [batch]: how many drafts were kept.
+ *   logprobs     fp32 [batch, max_q] or NULL: log p of each emitted token (of the softmax at
+ *                temperature 1 where T is 0), 0 behind them.
+ *   A row that the block comes to, target or draft, with a NaN, +inf or nothing but -inf has no
+ *   distribution: the block ends there with a token of -1 and a log-probability of NaN.
+ *   workspace    bi_verify_drafts_workspace_size(total_q, num_drafts, n) bytes (num_drafts 0 where
+ *                draft_logits is NULL), 16-byte aligned, contents scratch.
+ *   Weights are whole numbers of 2^-60, within 2^-30 of themselves, so the drawn token does not
+ *   depend on the order of any sum.  A sequence's outputs depend on its own rows, drafts, uniforms
+ *   and temperature alone: not on the batch, max_q, alignment or strides. */
+#define BI_DRAFTS_MAX_N (1 << 20)
+size_t bi_verify_drafts_workspace_size(int64_t total_q, int64_t num_drafts, int64_t n);
+bi_status bi_verify_drafts(const void* logits, int64_t ldl, const void* draft_logits, int64_t ldd,
+                           int dtype, const int32_t* draft_tokens, int64_t num_drafts,
+                           const float* uniforms, const float* temperatures, float temperature,
+                           const int32_t* cu_q, int64_t batch, int64_t total_q, int64_t max_q,
+                           int64_t n, int32_t* tokens, int32_t* accepted, float* logprobs,
+                           void* workspace, size_t workspace_bytes, bi_stream_t stream);
 
 #ifdef __cplusplus
 }

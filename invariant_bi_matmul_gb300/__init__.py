@@ -93,6 +93,9 @@ SIGNATURES = {
     "bi_log_softmax": ([_p, _i64, _p, _i64, _i64, _i64, _p], _int),
     "bi_mean": ([_p, _i64, _int, _i64, _i64, _p, _p], _int),
     "bi_token_logprobs": ([_p, _i64, _int, _p, _i64, _i64, _p, _p, _p, _i64, _p, _p, _p], _int),
+    "bi_verify_drafts_workspace_size": ([_i64, _i64, _i64], _sz),
+    "bi_verify_drafts": ([_p, _i64, _p, _i64, _int, _p, _i64, _p, _p, _f32, _p, _i64, _i64, _i64,
+                          _i64, _p, _p, _p, _p, _sz, _p], _int),
     "bi_token_logprobs_backward": ([_p, _i64, _int, _p, _i64, _i64, _p, _p, _p, _p, _p, _i64, _p],
                                    _int),
 }
@@ -662,15 +665,18 @@ def _token_rows(t, dev, d, name):
 def _rope_kv_append(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                     cu_q, theta, positions, sections, inv_freq, rotary_dim, out, stream):
     torch = _torch()
-    i32 = torch.int32
+    i32, bf16 = torch.int32, torch.bfloat16
     if k_scale is not None:
         dev, B, max_pages, num_pages, hkv, page, d = _paged_common_q8(
             k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
     else:
         dev = _device_of(k_cache)
-        num_pages, hkv, page, d = _paged_common(k_cache, v_cache, block_table, seq_lens)
-        _on_current_device(k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-                           seq_lens=seq_lens)
+        if not _all(dev, (k_cache, bf16, 4), (v_cache, bf16, 4), (block_table, i32, 2),
+                    (seq_lens, i32, 1)) or k_cache.shape != v_cache.shape:
+            _paged_common(k_cache, v_cache, block_table, seq_lens)
+            _on_current_device(k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+                               seq_lens=seq_lens)
+        num_pages, hkv, page, d = k_cache.shape
         B, max_pages = block_table.shape
         if seq_lens.shape[0] != B:
             raise ValueError("block_table and seq_lens disagree on the batch")
@@ -706,7 +712,7 @@ def _rope_kv_append(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_t
         axes_ptr, pos_ptr = pairs.buffer_info()[0], positions.data_ptr()
     if out is None:
         with _allocating_for(stream):
-            out = torch.empty(T, hq, d, dtype=torch.bfloat16, device=q.device)
+            out = torch.empty((T, hq, d), dtype=bf16, device=q.device)
         ldo = hq * d
     else:
         To, ho, ldo = _token_rows(out, dev, d, "out")
@@ -1008,3 +1014,81 @@ def token_logprobs_backward(logits, tokens, lse, entropy=None, grad_logprobs=Non
         _ptr(grad_logprobs), _ptr(grad_entropy), out.data_ptr(), _row_major_2d(out, "out"),
         _stream_on(stream, cur)))
     return out
+
+
+class VerifiedDrafts(NamedTuple):
+    """What verify_drafts returns: int32 [batch, max_q], int32 [batch], fp32 [batch, max_q]."""
+    tokens: object
+    accepted: object
+    logprobs: object
+
+
+def verify_drafts_workspace_size(total_q: int, num_drafts: int, n: int) -> int:
+    return int(lib().bi_verify_drafts_workspace_size(int(total_q), int(num_drafts), int(n)))
+
+
+def verify_drafts(logits, draft_tokens, uniforms, cu_q, max_q: int, draft_logits=None,
+                  temperature=1.0, workspace=None, stream=None) -> VerifiedDrafts:
+    """Verification of drafted tokens from given uniform numbers (speculative sampling).
+
+    logits (bf16, fp16 or fp32 [T, n]) has a row per token of each sequence's block: its last
+    input, then its drafts; draft_tokens (int32 [T - batch]) the drafts of all sequences one after
+    the other, -1 for none; draft_logits [T - batch, n] what they were drawn from, or None where
+    they were chosen without chance.  A draft is kept while uniforms[t] * q < p of the row in
+    front of it; the first that is not is replaced by a draw from max(p - q, 0), and behind a
+    block kept in full one more token is drawn from p, with the sequence's last uniform.
+    temperature: a float, or fp32 [batch]; 0 keeps and emits the largest entries.
+
+    Returns tokens [batch, max_q] (kept drafts, the drawn token, -1 behind it), accepted [batch]
+    (drafts kept) and the emitted tokens' logprobs [batch, max_q].  include/bi_rowwise.h has the
+    exact definition."""
+    torch = _torch()
+    i32, f32 = torch.int32, torch.float32
+    dev = _device_of(logits)
+    per_row = isinstance(temperature, torch.Tensor)
+    given = [("draft_tokens", draft_tokens, i32), ("uniforms", uniforms, f32), ("cu_q", cu_q, i32)]
+    if per_row:
+        given.append(("temperature", temperature, f32))
+    if not _all(dev, *[(t, dtype, 1) for _, t, dtype in given]) or logits.dim() != 2:
+        _need(logits, getattr(logits, "dtype", None), "logits", 2)
+        _on_current_device(logits=logits)
+        for name, t, dtype in given:
+            _need(t, dtype, name, 1)
+            _on_current_device(**{name: t})
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+    dt = _in_dtype(logits, "logits")
+    T, n = logits.shape
+    B, N = cu_q.shape[0] - 1, draft_tokens.shape[0]
+    if B < 0 or uniforms.shape[0] != T:
+        raise ValueError("cu_q must have batch + 1 entries, and uniforms one per row of logits")
+    if per_row and temperature.shape[0] != B:
+        raise ValueError("temperature must have one entry per sequence")
+    ldl, ldd = _row_major_2d(logits, "logits"), 0
+    if draft_logits is not None:
+        _need(draft_logits, logits.dtype, "draft_logits", 2)
+        _on_current_device(draft_logits=draft_logits)
+        if tuple(draft_logits.shape) != (N, n):
+            raise ValueError("draft_logits must have one row of n entries per drafted token")
+        ldd = _row_major_2d(draft_logits, "draft_logits")
+    L = lib()
+    max_q = int(max_q)
+    if workspace is not None:
+        _on_current_device(workspace=workspace)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    with _allocating_for(stream):
+        device = logits.device
+        tokens = torch.empty((B, max(max_q, 0)), dtype=i32, device=device)
+        logprobs = torch.empty((B, max(max_q, 0)), dtype=f32, device=device)
+        accepted = torch.empty(B, dtype=i32, device=device)
+        if workspace is None:
+            size = L.bi_verify_drafts_workspace_size(T, 0 if draft_logits is None else N, n)
+            workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=device)
+    _check(L.bi_verify_drafts(
+        logits.data_ptr(), ldl, _ptr(draft_logits), ldd, dt, draft_tokens.data_ptr(), N,
+        uniforms.data_ptr(), temperature.data_ptr() if per_row else None,
+        0.0 if per_row else float(temperature), cu_q.data_ptr(), B, T, max_q, n,
+        tokens.data_ptr(), accepted.data_ptr(), logprobs.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_on(stream, dev)))
+    return VerifiedDrafts(tokens, accepted, logprobs)

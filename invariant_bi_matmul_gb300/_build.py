@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(HERE, "libbi.so")
 
 SOURCES = ["api.cu", "rmsnorm.cu", "gemm.cu", "attention.cu", "selftest.cu", "tmap.cu",
            "static_ws.cu", "glue.cu", "rowwise.cu", "f32path.cu", "prefill.cu", "kv_q8.cu",
-           "attention_q8.cu", "pages.cu", "logprobs.cu", "rope_append.cu"]
+           "attention_q8.cu", "pages.cu", "logprobs.cu", "rope_append.cu",
+           "verify_drafts.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
                      f"-I{INCLUDE}", f"-I{CSRC}"]
