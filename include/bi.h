@@ -366,6 +366,55 @@ bi_status bi_prefill_attn(const void* q, const void* k_cache, const void* v_cach
                           void* workspace, size_t workspace_bytes, bi_stream_t stream);
 
 /* ---------------------------------------------------------------------------------
+ * Shaped scores  (no counterpart on the pages): bi_verify_block, bi_decode_attn and
+ * bi_prefill_attn with what models do to their scores before the softmax.  With
+ * x = scale * q[t,h,:] . k_j for token t at position pos, in this order:
+ *   softcap    0: none; else in [2^-20, 2^20]:  x := softcap * tanh(x / softcap).
+ *   slopes     fp32 [num_q_heads] (device) or NULL:  x := x + slopes[h] * (j - pos), a bias
+ *              that falls with distance where the slope is positive.
+ *   window     0: none; else a token sees the keys pos - window + 1 .. pos alone.
+ *   first_key  int32 [total_q] (device; decode: [batch]) or NULL: a token sees no key in
+ *              front of first_key[t] (a document's start in packed documents, for instance;
+ *              negative: no limit).  Both limits hold together with j <= pos.  Where they
+ *              leave nothing, out is 0 and lse -inf.
+ * scale must be in (0, 2^20] where any of them is given.  With none of them the call is the
+ * plain one; with limits alone a token whose limits hide nothing gets the plain call's bits.
+ *
+ * Only the pages that a block's tokens see are read, the others may be gone (any
+ * block-table entry): work follows the window, not the sequence.  Keys and values that no
+ * token of the block (bi_prefill_attn: of the tile of 128 / G tokens) sees are not part of
+ * any sum, whatever they hold; those that one of them sees must be finite, as a value that
+ * is not times a weight of 0 makes the others NaN.
+ * Chunks, merge tree, workspace, limit and invariance as in the plain calls: a query's bits
+ * depend on it, its position, its limits, its head's slope, softcap, scale and the keys and
+ * values it sees, and are the same from all three (inside the batch-invariant limit).
+ * Scores are formed in fp32 (tanh within 2^-22 of itself).
+ * ------------------------------------------------------------------------------- */
+bi_status bi_verify_block_ex(const void* q, const void* k_cache, const void* v_cache,
+                             int64_t num_pages, const int32_t* block_table, int64_t max_pages,
+                             const int32_t* seq_lens, const int32_t* cu_q, int64_t batch,
+                             int64_t total_q, int64_t max_q, int64_t max_seq_len,
+                             int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
+                             int64_t page_size, float scale, float softcap, const float* slopes,
+                             int64_t window, const int32_t* first_key, void* out, float* lse,
+                             void* workspace, size_t workspace_bytes, bi_stream_t stream);
+bi_status bi_decode_attn_ex(const void* q, const void* k_cache, const void* v_cache,
+                            int64_t num_pages, const int32_t* block_table, int64_t max_pages,
+                            const int32_t* seq_lens, int64_t batch, int64_t max_seq_len,
+                            int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
+                            int64_t page_size, float scale, float softcap, const float* slopes,
+                            int64_t window, const int32_t* first_key, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, bi_stream_t stream);
+bi_status bi_prefill_attn_ex(const void* q, const void* k_cache, const void* v_cache,
+                             int64_t num_pages, const int32_t* block_table, int64_t max_pages,
+                             const int32_t* seq_lens, const int32_t* cu_q, int64_t batch,
+                             int64_t total_q, int64_t max_q, int64_t max_seq_len,
+                             int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
+                             int64_t page_size, float scale, float softcap, const float* slopes,
+                             int64_t window, const int32_t* first_key, void* out, float* lse,
+                             void* workspace, size_t workspace_bytes, bi_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
  * bi_verify_block_static_ws -- bi_verify_block without a caller-provided workspace.
  * (No counterpart on the pages; it exists for callers that cannot allocate.)
  *

@@ -62,6 +62,12 @@ SIGNATURES = {
                          _i64, _i64, _f32, _p, _p, _p, _sz, _p], _int),
     "bi_decode_attn": ([_p, _p, _p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i64, _i64, _i64, _f32,
                         _p, _p, _p, _sz, _p], _int),
+    "bi_verify_block_ex": ([_p, _p, _p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _i64, _i64, _i64,
+                            _i64, _i64, _f32, _f32, _p, _i64, _p, _p, _p, _p, _sz, _p], _int),
+    "bi_prefill_attn_ex": ([_p, _p, _p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _i64, _i64, _i64,
+                            _i64, _i64, _f32, _f32, _p, _i64, _p, _p, _p, _p, _sz, _p], _int),
+    "bi_decode_attn_ex": ([_p, _p, _p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i64, _i64, _i64, _f32,
+                           _f32, _p, _i64, _p, _p, _p, _p, _sz, _p], _int),
     "bi_verify_block_static_ws": ([_p, _p, _p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _i64, _i64,
                                    _i64, _i64, _i64, _f32, _p, _p, _p], _int),
     # 8-bit cache and page copies
@@ -378,9 +384,27 @@ def _workspace(workspace, need, device):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _shape(softcap, slopes, window, first_key, hq, T):
+    """The arguments of a call that shapes its scores, None where it does not."""
+    if not softcap and slopes is None and not window and first_key is None:
+        return None
+    torch = _torch()
+    for name, t, dtype, n in (("slopes", slopes, torch.float32, hq),
+                              ("first_key", first_key, torch.int32, T)):
+        if t is not None:
+            _need(t, dtype, name, 1)
+            _on_current_device(**{name: t})
+            if t.shape[0] != n or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous [{n}] tensor")
+    return float(softcap), _ptr(slopes), int(window), _ptr(first_key)
+
+
 def verify_block(q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q: int, max_seq_len: int,
-                 scale: float, out=None, lse=None, want_lse=True, workspace=None, stream=None):
-    """Causal attention of each sequence's new block (q bf16 [T,Hq,D]) over its paged cache."""
+                 scale: float, out=None, lse=None, want_lse=True, workspace=None, stream=None,
+                 softcap: float = 0.0, slopes=None, window: int = 0, first_key=None):
+    """Causal attention of each sequence's new block (q bf16 [T,Hq,D]) over its paged cache.
+    softcap, slopes (fp32 [Hq]), window and first_key (int32 [T]) shape the scores before the
+    softmax and limit the keys that a token sees (include/bi.h, Shaped scores)."""
     torch = _torch()
     num_pages, hkv, page, d = _paged_common(k_cache, v_cache, block_table, seq_lens)
     _need(q, torch.bfloat16, "q", 3)
@@ -390,18 +414,23 @@ def verify_block(q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q: int, m
     T, hq, _ = q.shape
     out, lse = _attn_out(q, out, lse, want_lse)
     ws, ws_bytes = _workspace(workspace, attn_workspace_size(T, hq, d, max_seq_len), q.device)
-    _check(lib().bi_verify_block(_ptr(q), _ptr(k_cache), _ptr(v_cache), num_pages,
-                                 _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
-                                 _ptr(cu_q), seq_lens.shape[0], T, int(max_q), int(max_seq_len),
-                                 hq, hkv, d, page, float(scale), _ptr(out), _ptr(lse), _ptr(ws),
-                                 ws_bytes, _stream(stream)))
+    shape = _shape(softcap, slopes, window, first_key, hq, T)
+    head = (_ptr(q), _ptr(k_cache), _ptr(v_cache), num_pages, _ptr(block_table),
+            block_table.shape[1], _ptr(seq_lens), _ptr(cu_q), seq_lens.shape[0], T, int(max_q),
+            int(max_seq_len), hq, hkv, d, page, float(scale))
+    tail = (_ptr(out), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream))
+    if shape is None:
+        _check(lib().bi_verify_block(*head, *tail))
+    else:
+        _check(lib().bi_verify_block_ex(*head, *shape, *tail))
     return out, lse
 
 
 def prefill_attn(q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q: int, max_seq_len: int,
-                 scale: float, out=None, lse=None, want_lse=True, workspace=None, stream=None):
+                 scale: float, out=None, lse=None, want_lse=True, workspace=None, stream=None,
+                 softcap: float = 0.0, slopes=None, window: int = 0, first_key=None):
     """verify_block for blocks of any width (chunked prefill, prefix caching): every query
-    reduced exactly as verify_block / decode_attn reduce it."""
+    reduced exactly as verify_block / decode_attn reduce it, shaped scores included."""
     torch = _torch()
     num_pages, hkv, page, d = _paged_common(k_cache, v_cache, block_table, seq_lens)
     _need(q, torch.bfloat16, "q", 3)
@@ -411,11 +440,15 @@ def prefill_attn(q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q: int, m
     T, hq, _ = q.shape
     out, lse = _attn_out(q, out, lse, want_lse)
     ws, ws_bytes = _workspace(workspace, attn_workspace_size(T, hq, d, max_seq_len), q.device)
-    _check(lib().bi_prefill_attn(_ptr(q), _ptr(k_cache), _ptr(v_cache), num_pages,
-                                 _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
-                                 _ptr(cu_q), seq_lens.shape[0], T, int(max_q), int(max_seq_len),
-                                 hq, hkv, d, page, float(scale), _ptr(out), _ptr(lse), _ptr(ws),
-                                 ws_bytes, _stream(stream)))
+    shape = _shape(softcap, slopes, window, first_key, hq, T)
+    head = (_ptr(q), _ptr(k_cache), _ptr(v_cache), num_pages, _ptr(block_table),
+            block_table.shape[1], _ptr(seq_lens), _ptr(cu_q), seq_lens.shape[0], T, int(max_q),
+            int(max_seq_len), hq, hkv, d, page, float(scale))
+    tail = (_ptr(out), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream))
+    if shape is None:
+        _check(lib().bi_prefill_attn(*head, *tail))
+    else:
+        _check(lib().bi_prefill_attn_ex(*head, *shape, *tail))
     return out, lse
 
 
@@ -442,8 +475,10 @@ def verify_block_static_ws(q, k_cache, v_cache, block_table, seq_lens, cu_q, max
 
 
 def decode_attn(q, k_cache, v_cache, block_table, seq_lens, max_seq_len: int, scale: float,
-                out=None, lse=None, want_lse=True, workspace=None, stream=None):
-    """One new token per sequence: q bf16 [B,Hq,D]; token b is the last position of b."""
+                out=None, lse=None, want_lse=True, workspace=None, stream=None,
+                softcap: float = 0.0, slopes=None, window: int = 0, first_key=None):
+    """One new token per sequence: q bf16 [B,Hq,D]; token b is the last position of b.
+    Shaped scores as in verify_block (first_key int32 [B])."""
     torch = _torch()
     num_pages, hkv, page, d = _paged_common(k_cache, v_cache, block_table, seq_lens)
     _need(q, torch.bfloat16, "q", 3)
@@ -452,10 +487,15 @@ def decode_attn(q, k_cache, v_cache, block_table, seq_lens, max_seq_len: int, sc
     B, hq, _ = q.shape
     out, lse = _attn_out(q, out, lse, want_lse)
     ws, ws_bytes = _workspace(workspace, attn_workspace_size(B, hq, d, max_seq_len), q.device)
-    _check(lib().bi_decode_attn(_ptr(q), _ptr(k_cache), _ptr(v_cache), num_pages,
-                                _ptr(block_table), block_table.shape[1], _ptr(seq_lens), B,
-                                int(max_seq_len), hq, hkv, d, page, float(scale), _ptr(out),
-                                _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)))
+    shape = _shape(softcap, slopes, window, first_key, hq, B)
+    head = (_ptr(q), _ptr(k_cache), _ptr(v_cache), num_pages, _ptr(block_table),
+            block_table.shape[1], _ptr(seq_lens), B, int(max_seq_len), hq, hkv, d, page,
+            float(scale))
+    tail = (_ptr(out), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream))
+    if shape is None:
+        _check(lib().bi_decode_attn(*head, *tail))
+    else:
+        _check(lib().bi_decode_attn_ex(*head, *shape, *tail))
     return out, lse
 
 

@@ -11,6 +11,7 @@
 #include <mutex>
 #include <string>
 
+#include "attn_common.cuh"
 #include "bi.h"
 #include "launch.h"
 
@@ -446,13 +447,46 @@ bi_status check_paged(const char* fn, const PagedArgs& a, int64_t page_size, boo
     return BI_OK;
 }
 
+// What a call does to its scores, from its arguments (checked by check_paged already).
+bi_status shape_of(const char* fn, const PagedArgs& a, float scale, float softcap,
+                   const float* slopes, int64_t window, const int32_t* first_key, Shape* sh) {
+    if (window < 0) return fail(BI_ERR_INVALID_ARG, "%s: window must be >= 0", fn);
+    if (!(softcap >= 0.0f) || !std::isfinite(softcap))
+        return fail(BI_ERR_INVALID_ARG, "%s: softcap must be finite and >= 0", fn);
+    if (softcap > 0.0f && (softcap < 0x1p-20f || softcap > 0x1p20f))
+        return fail(BI_ERR_UNSUPPORTED, "%s: softcap must be 0 or in [2^-20, 2^20]", fn);
+    if (!aligned(slopes, 4) || !aligned(first_key, 4))
+        return fail(BI_ERR_UNSUPPORTED, "%s: slopes and first_key not element-aligned", fn);
+    // a window as long as the longest sequence hides nothing
+    if (window >= a.max_seq_len) window = 0;
+    *sh = Shape{};
+    if (softcap == 0.0f && !slopes && window == 0 && !first_key) return BI_OK;
+    // (the largest raw score is the largest shaped one)
+    if (!(scale > 0.0f) || scale > 0x1p20f)
+        return fail(BI_ERR_UNSUPPORTED, "%s: scale must be in (0, 2^20] where scores are shaped",
+                    fn);
+    sh->mode = kRange | (softcap > 0.0f ? kCap : 0) | (slopes ? kBias : 0);
+    if (softcap > 0.0f) {
+        sh->cap_in = scale / softcap;
+        sh->cap_log2 = softcap * kLog2e;
+    }
+    sh->slopes = slopes;
+    sh->first_key = first_key;
+    sh->window = int(window);
+    return BI_OK;
+}
+
 bi_status run_attention(const char* fn, const void* q, const PagedArgs& a, int64_t page_size,
                         float scale, void* out, float* lse, void* workspace, size_t ws_bytes,
-                        bi_stream_t stream) {
+                        bi_stream_t stream, float softcap = 0.0f, const float* slopes = nullptr,
+                        int64_t window = 0, const int32_t* first_key = nullptr) {
     init_limit_from_env();
     bi_status s = check_paged(fn, a, page_size, a.cu_q != nullptr);
     if (s != BI_OK) return s;
     if (!std::isfinite(scale)) return fail(BI_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+    Shape shape;
+    s = shape_of(fn, a, scale, softcap, slopes, window, first_key, &shape);
+    if (s != BI_OK) return s;
     if (a.batch == 0) return BI_OK;
     if (!q || !out || !workspace) return fail(BI_ERR_INVALID_ARG, "%s: null q/out/workspace", fn);
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || (lse && !aligned(lse, 4)))
@@ -467,8 +501,9 @@ bi_status run_attention(const char* fn, const void* q, const PagedArgs& a, int64
     // inside the limit (verify width max_q): the fixed chunk length; outside it a chunk
     // length chosen from the call's parallelism
     const int chunk_log2 = attn_chunk_log2(a, ws_bytes, dev->num_sms,
-                                           bi_within_batch_invariant_limit(a.max_q) != 0);
-    cudaError_t e = launch_attention(*dev, q, a, scale, out, lse, workspace, chunk_log2,
+                                           bi_within_batch_invariant_limit(a.max_q) != 0,
+                                           shape.window);
+    cudaError_t e = launch_attention(*dev, q, a, scale, shape, out, lse, workspace, chunk_log2,
                                      reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, fn);
     return BI_OK;
@@ -533,6 +568,38 @@ BI_EXPORT bi_status bi_verify_block(const void* q, const void* k_cache, const vo
                          workspace_bytes, stream);
 }
 
+namespace {
+
+bi_status run_prefill(const char* fn, const void* q, const PagedArgs& a, int64_t page_size,
+                      float scale, void* out, float* lse, void* workspace, size_t ws_bytes,
+                      bi_stream_t stream, float softcap = 0.0f, const float* slopes = nullptr,
+                      int64_t window = 0, const int32_t* first_key = nullptr) {
+    bi_status s = check_paged(fn, a, page_size, true, true);
+    if (s != BI_OK) return s;
+    if (!std::isfinite(scale)) return fail(BI_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+    Shape shape;
+    s = shape_of(fn, a, scale, softcap, slopes, window, first_key, &shape);
+    if (s != BI_OK) return s;
+    if (a.batch == 0) return BI_OK;
+    if (!a.cu_q) return fail(BI_ERR_INVALID_ARG, "%s: null cu_q", fn);
+    if (!q || !out || !workspace) return fail(BI_ERR_INVALID_ARG, "%s: null q/out/workspace", fn);
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || (lse && !aligned(lse, 4)))
+        return fail(BI_ERR_UNSUPPORTED, "%s: q, out and workspace must be 16-byte aligned", fn);
+    const size_t need = attn_workspace_bytes(a.total_q, a.hq, a.head_dim, a.max_seq_len);
+    if (ws_bytes < need)
+        return fail(BI_ERR_INVALID_ARG, "%s: workspace too small (%zu < %zu bytes)", fn,
+                    ws_bytes, need);
+    cudaError_t why = cudaSuccess;
+    const DeviceInfo* dev = current_device_info(&why);
+    if (!dev) return cuda_fail(why, fn);
+    cudaError_t e = launch_prefill(*dev, q, a, scale, shape, out, lse, workspace,
+                                   reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, fn);
+    return BI_OK;
+}
+
+}  // namespace
+
 BI_EXPORT bi_status bi_prefill_attn(const void* q, const void* k_cache, const void* v_cache,
                                     int64_t num_pages, const int32_t* block_table,
                                     int64_t max_pages, const int32_t* seq_lens,
@@ -541,28 +608,58 @@ BI_EXPORT bi_status bi_prefill_attn(const void* q, const void* k_cache, const vo
                                     int64_t num_kv_heads, int64_t head_dim, int64_t page_size,
                                     float scale, void* out, float* lse, void* workspace,
                                     size_t workspace_bytes, bi_stream_t stream) {
-    const char* fn = "bi_prefill_attn";
     PagedArgs a{k_cache, v_cache, num_pages, block_table, max_pages, seq_lens, cu_q, batch,
                 total_q, max_q, max_seq_len, num_q_heads, num_kv_heads, head_dim};
-    bi_status s = check_paged(fn, a, page_size, true, true);
-    if (s != BI_OK) return s;
-    if (!std::isfinite(scale)) return fail(BI_ERR_INVALID_ARG, "%s: scale must be finite", fn);
-    if (a.batch == 0) return BI_OK;
-    if (!cu_q) return fail(BI_ERR_INVALID_ARG, "%s: null cu_q", fn);
-    if (!q || !out || !workspace) return fail(BI_ERR_INVALID_ARG, "%s: null q/out/workspace", fn);
-    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || (lse && !aligned(lse, 4)))
-        return fail(BI_ERR_UNSUPPORTED, "%s: q, out and workspace must be 16-byte aligned", fn);
-    const size_t need = attn_workspace_bytes(a.total_q, a.hq, a.head_dim, a.max_seq_len);
-    if (workspace_bytes < need)
-        return fail(BI_ERR_INVALID_ARG, "%s: workspace too small (%zu < %zu bytes)", fn,
-                    workspace_bytes, need);
-    cudaError_t why = cudaSuccess;
-    const DeviceInfo* dev = current_device_info(&why);
-    if (!dev) return cuda_fail(why, fn);
-    cudaError_t e = launch_prefill(*dev, q, a, scale, out, lse, workspace,
-                                   reinterpret_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail(e, fn);
-    return BI_OK;
+    return run_prefill("bi_prefill_attn", q, a, page_size, scale, out, lse, workspace,
+                       workspace_bytes, stream);
+}
+
+BI_EXPORT bi_status bi_prefill_attn_ex(const void* q, const void* k_cache, const void* v_cache,
+                                       int64_t num_pages, const int32_t* block_table,
+                                       int64_t max_pages, const int32_t* seq_lens,
+                                       const int32_t* cu_q, int64_t batch, int64_t total_q,
+                                       int64_t max_q, int64_t max_seq_len, int64_t num_q_heads,
+                                       int64_t num_kv_heads, int64_t head_dim, int64_t page_size,
+                                       float scale, float softcap, const float* slopes,
+                                       int64_t window, const int32_t* first_key, void* out,
+                                       float* lse, void* workspace, size_t workspace_bytes,
+                                       bi_stream_t stream) {
+    PagedArgs a{k_cache, v_cache, num_pages, block_table, max_pages, seq_lens, cu_q, batch,
+                total_q, max_q, max_seq_len, num_q_heads, num_kv_heads, head_dim};
+    return run_prefill("bi_prefill_attn_ex", q, a, page_size, scale, out, lse, workspace,
+                       workspace_bytes, stream, softcap, slopes, window, first_key);
+}
+
+BI_EXPORT bi_status bi_verify_block_ex(const void* q, const void* k_cache, const void* v_cache,
+                                       int64_t num_pages, const int32_t* block_table,
+                                       int64_t max_pages, const int32_t* seq_lens,
+                                       const int32_t* cu_q, int64_t batch, int64_t total_q,
+                                       int64_t max_q, int64_t max_seq_len, int64_t num_q_heads,
+                                       int64_t num_kv_heads, int64_t head_dim, int64_t page_size,
+                                       float scale, float softcap, const float* slopes,
+                                       int64_t window, const int32_t* first_key, void* out,
+                                       float* lse, void* workspace, size_t workspace_bytes,
+                                       bi_stream_t stream) {
+    if (batch > 0 && !cu_q) return fail(BI_ERR_INVALID_ARG, "bi_verify_block_ex: null cu_q");
+    PagedArgs a{k_cache, v_cache, num_pages, block_table, max_pages, seq_lens, cu_q, batch,
+                total_q, max_q, max_seq_len, num_q_heads, num_kv_heads, head_dim};
+    return run_attention("bi_verify_block_ex", q, a, page_size, scale, out, lse, workspace,
+                         workspace_bytes, stream, softcap, slopes, window, first_key);
+}
+
+BI_EXPORT bi_status bi_decode_attn_ex(const void* q, const void* k_cache, const void* v_cache,
+                                      int64_t num_pages, const int32_t* block_table,
+                                      int64_t max_pages, const int32_t* seq_lens, int64_t batch,
+                                      int64_t max_seq_len, int64_t num_q_heads,
+                                      int64_t num_kv_heads, int64_t head_dim, int64_t page_size,
+                                      float scale, float softcap, const float* slopes,
+                                      int64_t window, const int32_t* first_key, void* out,
+                                      float* lse, void* workspace, size_t workspace_bytes,
+                                      bi_stream_t stream) {
+    PagedArgs a{k_cache, v_cache, num_pages, block_table, max_pages, seq_lens, nullptr, batch,
+                batch, 1, max_seq_len, num_q_heads, num_kv_heads, head_dim};
+    return run_attention("bi_decode_attn_ex", q, a, page_size, scale, out, lse, workspace,
+                         workspace_bytes, stream, softcap, slopes, window, first_key);
 }
 
 BI_EXPORT bi_status bi_decode_attn(const void* q, const void* k_cache, const void* v_cache,

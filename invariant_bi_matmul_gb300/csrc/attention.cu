@@ -92,7 +92,8 @@ struct Cfg {
 
 // ------------------------------------------------------------------- partial kernel
 
-template <int D>
+// MODE: what the call does to its scores (kRange, kCap, kBias of attn_common.cuh; 0: nothing)
+template <int D, int MODE>
 __global__ void __launch_bounds__(THREADS, 1)
 attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v,
@@ -101,7 +102,8 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const int32_t* __restrict__ cu_q, int B, int total_q, int max_q,
                     int max_seq_len, int Hq, int Hkv, float scale_log2,
                     float* __restrict__ ws_o, float* __restrict__ ws_ml, int maxC,
-                    int chunk_log2, unsigned int* __restrict__ cnt, unsigned int* err) {
+                    int chunk_log2, unsigned int* __restrict__ cnt, unsigned int* err,
+                    const Shape sh) {
     using C = Cfg<D>;
     const int chunk = 1 << chunk_log2;         // keys per work item (CHUNK when invariant)
     const int chunk_pages = chunk / PAGE;
@@ -132,6 +134,8 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
     int* seq_t0 = seq_len + MAX_BATCH;
     uint8_t* seq_qb = reinterpret_cast<uint8_t*>(seq_t0 + MAX_BATCH);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(seq_qb + MAX_BATCH);
+    // first key that any of a sequence's tokens sees (a call that shapes its scores)
+    int* seq_lo = reinterpret_cast<int*>(seq_qb + MAX_BATCH) + 4;
     const unsigned long long wait_ns = wait_budget_ns(err);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -172,7 +176,13 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const SeqInfo si = seq_info(seq_lens, cu_q, b);
         const bool ok = seq_ok(si, max_q, max_seq_len, total_q);
         if (!ok) latch_error(err, kErrDeviceArg);
-        prefix[b + 1] = ok ? ((si.L + chunk - 1) >> chunk_log2) * Hkv : 0;
+        int first_chunk = 0;
+        if (MODE && ok) {
+            const int low = block_low(sh, si.t0, si.L - si.qb, si.qb);
+            seq_lo[b] = low;
+            first_chunk = low >> chunk_log2;
+        }
+        prefix[b + 1] = ok ? (((si.L + chunk - 1) >> chunk_log2) - first_chunk) * Hkv : 0;
         seq_len[b] = si.L;
         seq_t0[b] = si.t0;
         seq_qb[b] = uint8_t(ok ? si.qb : 0);  // <= BI_ATTN_MAX_Q
@@ -209,6 +219,11 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const int r = w - prefix[b];
         c = r / Hkv;
         h = r - c * Hkv;
+        if (MODE) c += seq_lo[b] >> chunk_log2;
+    };
+    // first page that an item of chunk c reads
+    auto page_of = [&](int b, int c) {
+        return MODE ? max(c * chunk_pages, seq_lo[b] / PAGE) : c * chunk_pages;
     };
     auto seq_of = [&](int b) {
         SeqInfo si;
@@ -217,8 +232,9 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         si.qb = seq_qb[b];
         return si;
     };
-    auto pages_of = [&](const SeqInfo& si, int c) {
-        return min(chunk_pages, (si.L - c * chunk + PAGE - 1) / PAGE);
+    auto pages_of = [&](const SeqInfo& si, int c, int pg0) {
+        const int n = min(chunk_pages, (si.L - c * chunk + PAGE - 1) / PAGE);
+        return MODE ? n - (pg0 - c * chunk_pages) : n;
     };
     auto give_up = [&]() {
         if (!*abort_flag) {
@@ -247,14 +263,15 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
             int b, c, h;
             decode(w, b, c, h);
-            const int npages = pages_of(seq_of(b), c);
+            const int pg0 = page_of(b, c);
+            const int npages = pages_of(seq_of(b), c, pg0);
             int phys_l = -1;  // lane k: the physical page of page (i & ~31) + k of the item
             for (int i = 0; i < npages; ++i, ++g) {
                 // the item's block-table entries are read 32 at a time, one per lane, before
                 // the wait for a free stage: one load latency per item at the ring's start
                 // instead of one per page
                 if ((i & 31) == 0) {
-                    const int pidx = c * chunk_pages + i + lane;
+                    const int pidx = pg0 + i + lane;
                     phys_l = (i + lane < npages && pidx < max_pages)
                                  ? block_table[int64_t(b) * max_pages + pidx]
                                  : -1;
@@ -341,7 +358,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         for (int w = blockIdx.x; ok && w < total; w += gridDim.x, ++item) {
             int b, c, h;
             decode(w, b, c, h);
-            const int npages = pages_of(seq_of(b), c);
+            const int npages = pages_of(seq_of(b), c, page_of(b, c));
             if (!wait(q_full, uint32_t(item) & 1u)) break;
             for (int i = 0; i < npages; ++i) {
                 const uint32_t gi = g + uint32_t(i);
@@ -500,17 +517,26 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             decode(w, b, c, h);
             const SeqInfo si = seq_of(b);
             const int L = si.L, qb = si.qb;
-            const int npages = pages_of(si, c);
+            const int pg0 = page_of(b, c);
+            const int npages = pages_of(si, c, pg0);
             const int R = qb * G;
             const int pos = r < R ? L - qb + r / G : -1;
             const int ob = item & 1;
+            // the row's first key, the last one of any row's, and the row's slope
+            int low = 0, all_low = 0;
+            float slope_log2 = 0.f;
+            if (MODE) {
+                if (r < R) low = row_low(sh, si.t0 + r / G, pos);
+                all_low = __reduce_max_sync(0xffffffffu, low);
+                if ((MODE & kBias) && r < R) slope_log2 = sh.slopes[h * G + r % G] * kLog2e;
+            }
 
             float m_ref = -INFINITY, l_run = 0.f;
             for (int i = 0; i < npages && ok; ++i) {
                 const uint32_t gi = g + uint32_t(i);
                 const int s = int(gi % NST), sb = int(gi & 1u);
                 const uint32_t par = (gi >> 1) & 1u;
-                const int page0 = c * chunk + i * PAGE;  // first key of the page
+                const int page0 = (pg0 + i) * PAGE;  // first key of the page
                 // the whole page of scores of row r (every lane quarter holds all 64 keys
                 // of the query rows) and this warp's 16-key slice of it, then release the
                 // S buffer
@@ -538,19 +564,44 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 float sl[KSL], m_raw;
                 {
                     float a[PAGE];
-                    if (valid && page0 + PAGE - 1 <= L - qb) {
+                    if (MODE & kBias) {  // (a score's size depends on its place: all are shaped)
+                        float v[PAGE], w[KSL];
+#pragma unroll
+                        for (int k = 0; k < PAGE; ++k) v[k] = __uint_as_float(sa[k]);
+#pragma unroll
+                        for (int k = 0; k < KSL; ++k) w[k] = __uint_as_float(sv[k]);
+                        shape_scores<MODE>(v, sh, scale_log2, slope_log2, float(page0 - pos));
+                        shape_scores<MODE>(w, sh, scale_log2, slope_log2,
+                                           float(page0 + sw * KSL - pos));
+#pragma unroll
+                        for (int k = 0; k < PAGE; ++k) sa[k] = __float_as_uint(v[k]);
+#pragma unroll
+                        for (int k = 0; k < KSL; ++k) sv[k] = __float_as_uint(w[k]);
+                    } else if (MODE & kCap) {  // (its maximum is the maximum's)
+                        float w[KSL];
+#pragma unroll
+                        for (int k = 0; k < KSL; ++k) w[k] = __uint_as_float(sv[k]);
+                        shape_scores<MODE>(w, sh, scale_log2, 0.f, 0.f);
+#pragma unroll
+                        for (int k = 0; k < KSL; ++k) sv[k] = __float_as_uint(w[k]);
+                    }
+                    if (valid && page0 + PAGE - 1 <= L - qb && (!MODE || page0 >= all_low)) {
 #pragma unroll
                         for (int k = 0; k < PAGE; ++k) a[k] = __uint_as_float(sa[k]);
 #pragma unroll
                         for (int k = 0; k < KSL; ++k) sl[k] = __uint_as_float(sv[k]);
                     } else {
                         const int lim = valid ? pos - page0 : -1;  // last visible key, or < 0
+                        const int fst = MODE ? low - page0 : 0;    // first
 #pragma unroll
                         for (int k = 0; k < PAGE; ++k)
-                            a[k] = k <= lim ? __uint_as_float(sa[k]) : -INFINITY;
+                            a[k] = k <= lim && (!MODE || k >= fst) ? __uint_as_float(sa[k])
+                                                                   : -INFINITY;
 #pragma unroll
                         for (int k = 0; k < KSL; ++k)
-                            sl[k] = sw * KSL + k <= lim ? __uint_as_float(sv[k]) : -INFINITY;
+                            sl[k] = sw * KSL + k <= lim && (!MODE || sw * KSL + k >= fst)
+                                        ? __uint_as_float(sv[k])
+                                        : -INFINITY;
                     }
                     float t1[22], t2[8];
 #pragma unroll
@@ -562,7 +613,14 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     m_raw = fmax3(fmax3(t2[0], t2[1], t2[2]), fmax3(t2[3], t2[4], t2[5]),
                                   fmaxf(t2[6], t2[7]));
                 }
-                const float m_page = m_raw * scale_log2;
+                float m_page = m_raw * scale_log2;
+                if (MODE & kBias) {
+                    m_page = m_raw;
+                } else if (MODE & kCap) {
+                    float one[1] = {m_raw};
+                    shape_scores<MODE>(one, sh, scale_log2, 0.f, 0.f);
+                    m_page = m_raw == -INFINITY ? -INFINITY : one[0];
+                }
 
                 // reference max: raised (and O, l rescaled) only when the page max exceeds
                 // it by more than 2^8, so p = exp2(s - m_ref) <= 2^8
@@ -577,7 +635,9 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 {
                     const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
 #pragma unroll
-                    for (int k = 0; k < KSL; ++k) pv[k] = ex2(fmaf(sl[k], scale_log2, -m_use));
+                    for (int k = 0; k < KSL; ++k)
+                        pv[k] = (MODE & (kCap | kBias)) ? ex2(sl[k] - m_use)
+                                                        : ex2(fmaf(sl[k], scale_log2, -m_use));
                 }
                 uint32_t pk[KSL / 2];
 #pragma unroll
@@ -622,6 +682,16 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const int n16 = ((sw + 1) * KSL - r0) * 8;  // 16-byte pieces per box
                     for (int idx = lane; idx < C::BOXES * n16; idx += 32) {
                         const int bx = idx / n16, rem = idx - bx * n16;
+                        *reinterpret_cast<uint4*>(vst + bx * C::BOX_BYTES + r0 * 128 + rem * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                }
+                // ... and so are those in front of the first key that a row sees
+                if (MODE && seq_lo[b] - page0 > sw * KSL) {
+                    const int r0 = sw * KSL, r1 = min(seq_lo[b] - page0, r0 + KSL);
+                    uint8_t* vst = sStage + s * C::STAGE_BYTES + C::PAGE_BYTES;
+                    for (int idx = lane; idx < C::BOXES * (r1 - r0) * 8; idx += 32) {
+                        const int bx = idx / ((r1 - r0) * 8), rem = idx - bx * ((r1 - r0) * 8);
                         *reinterpret_cast<uint4*>(vst + bx * C::BOX_BYTES + r0 * 128 + rem * 16) =
                             make_uint4(0, 0, 0, 0);
                     }
@@ -766,12 +836,20 @@ __device__ __forceinline__ void merge_combine(const float (&Mw)[MERGE_WARPS],
     if (lse_slot && lane == 0) *lse_slot = (M + log2f(L)) * kLn2;
 }
 
+// Where a row's keys start, in a call that shapes its scores.
+struct RowRange {
+    int low;          // the row's first key
+    int first_chunk;  // the first chunk that its sequence's block reads
+};
+
 // Row (token t, query head hq) of the call: its sequence and position, or false when the
 // sequence is malformed or the token belongs to none.
+template <bool RANGED>
 __device__ __forceinline__ bool merge_row(const int32_t* __restrict__ seq_lens,
                                           const int32_t* __restrict__ cu_q, int B, int total_q,
                                           int max_q, int max_seq_len, int t, int& pos, int& bq,
-                                          int& len) {
+                                          int& len, RowRange& rr, const Shape& sh,
+                                          int chunk_log2, bool counted) {
     int b;
     if (cu_q) {
         int lo = 0, hi = B;  // largest b with cu_q[b] <= t
@@ -788,6 +866,12 @@ __device__ __forceinline__ bool merge_row(const int32_t* __restrict__ seq_lens,
     pos = si.L - si.qb + (t - si.t0);
     bq = b;
     len = si.L;
+    if (RANGED) {
+        rr.low = row_low(sh, t, pos);
+        // (the prefill kernels do not count items)
+        rr.first_chunk =
+            counted ? block_low(sh, si.t0, si.L - si.qb, si.qb) >> chunk_log2 : 0;
+    }
     return true;
 }
 
@@ -821,13 +905,13 @@ __global__ void __launch_bounds__(256) attn_count_reset_kernel(unsigned int* cnt
 }
 
 // One CTA per row: warp w folds range w (latency: a few rows, long contexts).
-template <int D, int UNR>
+template <int D, int UNR, bool RANGED>
 __global__ void __launch_bounds__(MERGE_WARPS * 32)
 attn_merge_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ cu_q, int B,
                   int total_q, int max_q, int max_seq_len, int Hq, int Hkv,
                   const float* ws_o, const float* ws_ml, int maxC, int chunk_log2,
                   const unsigned int* cnt, __nv_bfloat16* __restrict__ out,
-                  float* __restrict__ lse, unsigned int* err) {
+                  float* __restrict__ lse, unsigned int* err, const Shape sh) {
     constexpr int PER = D / 32;
     __shared__ float sM[MERGE_WARPS], sL[MERGE_WARPS];
     __shared__ float sO[MERGE_WARPS][D];
@@ -842,18 +926,33 @@ attn_merge_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restric
     const int hq = int(blockIdx.x - unsigned(t) * unsigned(Hq));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int pos, b, L;
-    if (!merge_row(seq_lens, cu_q, B, total_q, max_q, max_seq_len, t, pos, b, L)) return;
+    RowRange rr{0, 0};
+    if (!merge_row<RANGED>(seq_lens, cu_q, B, total_q, max_q, max_seq_len, t, pos, b, L, rr, sh,
+                           chunk_log2, cnt != nullptr))
+        return;
+    if (RANGED && rr.low > pos) {  // it sees nothing
+        if (warp == 0) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                out[(int64_t(t) * Hq + hq) * D + lane * PER + i] = __float2bfloat16_rn(0.f);
+            if (lse && lane == 0) lse[int64_t(t) * Hq + hq] = -INFINITY;
+        }
+        return;
+    }
     if (cnt) {
         if (threadIdx.x == 0) {
-            const unsigned int items = unsigned((L + (1 << chunk_log2) - 1) >> chunk_log2);
+            const unsigned int items =
+                unsigned(((L + (1 << chunk_log2) - 1) >> chunk_log2) - rr.first_chunk);
             s_ready = wait_items(cnt + b * Hkv + hq / (Hq / Hkv), items, wait_budget_ns(err)) ? 1 : 0;
             if (!s_ready) latch_error(err, kErrTimeout);
         }
         __syncthreads();
         if (!s_ready) return;
     }
-    const int nC = (pos >> chunk_log2) + 1;
-    const int64_t base = (int64_t(t) * Hq + hq) * maxC;
+    // (the chunks in front of the row's first key are no part of its tree)
+    const int first = RANGED ? rr.low >> chunk_log2 : 0;
+    const int nC = (pos >> chunk_log2) + 1 - first;
+    const int64_t base = (int64_t(t) * Hq + hq) * maxC + first;
     float Mw, Lw, acc[PER];
     merge_fold<D, UNR>(ws_o, ws_ml, base, warp * nC / MERGE_WARPS, (warp + 1) * nC / MERGE_WARPS,
                   lane, Mw, Lw, acc);
@@ -882,13 +981,13 @@ attn_merge_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restric
 // row hide behind the folds of others.  UNR: at least the rows' chunk count.  Bound by
 // memory: (D + 2) * 4 bytes per chunk.  (With the ranges' sums and all 17 partials of a row
 // in 167 registers, one CTA per SM: 16,384 rows of 17 chunks 75 us.)
-template <int D, int UNR>
+template <int D, int UNR, bool RANGED>
 __global__ void __launch_bounds__(MERGE_WARPS * 32, 4)
 attn_merge_rows_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ cu_q,
                        int B, int total_q, int max_q, int max_seq_len, int Hq, int Hkv,
                        const float* ws_o, const float* ws_ml, int maxC, int chunk_log2,
                        const unsigned int* cnt, __nv_bfloat16* __restrict__ out,
-                       float* __restrict__ lse, unsigned int* err) {
+                       float* __restrict__ lse, unsigned int* err, const Shape sh) {
     constexpr int PER = D / 32;
     if (!cnt) pdl_wait();  // see attn_merge_kernel
     pdl_trigger();
@@ -898,19 +997,34 @@ attn_merge_rows_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __re
     const int t = int(row / Hq);
     const int hq = int(row - int64_t(t) * Hq);
     int pos, b, L;
-    if (!merge_row(seq_lens, cu_q, B, total_q, max_q, max_seq_len, t, pos, b, L)) return;
+    RowRange rr{0, 0};
+    if (!merge_row<RANGED>(seq_lens, cu_q, B, total_q, max_q, max_seq_len, t, pos, b, L, rr, sh,
+                           chunk_log2, cnt != nullptr))
+        return;
+    if (RANGED && rr.low > pos) {  // it sees nothing
+        {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                out[(int64_t(t) * Hq + hq) * D + lane * PER + i] = __float2bfloat16_rn(0.f);
+            if (lse && lane == 0) lse[int64_t(t) * Hq + hq] = -INFINITY;
+        }
+        return;
+    }
     if (cnt) {
         int ready = 1;
         if (lane == 0) {
-            const unsigned int items = unsigned((L + (1 << chunk_log2) - 1) >> chunk_log2);
+            const unsigned int items =
+                unsigned(((L + (1 << chunk_log2) - 1) >> chunk_log2) - rr.first_chunk);
             ready = wait_items(cnt + b * Hkv + hq / (Hq / Hkv), items, wait_budget_ns(err)) ? 1 : 0;
             if (!ready) latch_error(err, kErrTimeout);
         }
         __syncwarp();  // orders lane 0's acquire before the other lanes' loads
         if (!__shfl_sync(0xffffffffu, ready, 0)) return;
     }
-    const int nC = (pos >> chunk_log2) + 1;
-    const int64_t base = (int64_t(t) * Hq + hq) * maxC;
+    // (the chunks in front of the row's first key are no part of its tree)
+    const int first = RANGED ? rr.low >> chunk_log2 : 0;
+    const int nC = (pos >> chunk_log2) + 1 - first;
+    const int64_t base = (int64_t(t) * Hq + hq) * maxC + first;
     // the host picks UNR >= maxC >= nC for every valid row
     if (nC > UNR) return;
     constexpr int WIN = UNR < 9 ? UNR : 9;
@@ -1042,21 +1156,23 @@ size_t workspace_for(int64_t total_q, int64_t hq, int64_t head_dim, int64_t max_
     return partials_bytes(total_q, hq, head_dim, chunks) +
            (size_t(total_q) * size_t(hq) * sizeof(unsigned int) + 15) / 16 * 16;
 }
-template <int D>
+template <int D, int MODE>
 cudaError_t launch_attention_t(const DeviceInfo& dev, const void* q, const PagedArgs& a,
-                               float scale, void* out, float* lse, void* workspace,
-                               int chunk_log2, cudaStream_t stream) {
+                               float scale, const Shape& shape, void* out, float* lse,
+                               void* workspace, int chunk_log2, cudaStream_t stream) {
     using Cf = Cfg<D>;
+    constexpr size_t SMEM = Cf::SMEM + (MODE ? MAX_BATCH * 4 + 16 : 0);  // (and seq_lo)
+    static_assert(SMEM <= 232448, "shared memory per CTA");
     const uint64_t rows = uint64_t(a.num_pages) * uint64_t(a.hkv) * PAGE;
     CUtensorMap tk, tv;
     if (!tmap_2d_bf16(&tk, a.k_cache, D, rows, D, 64, PAGE, 128) ||
         !tmap_2d_bf16(&tv, a.v_cache, D, rows, D, 64, PAGE, 128))
         return cudaErrorNotSupported;
-    auto kern = attn_partial_kernel<D>;
+    auto kern = attn_partial_kernel<D, MODE>;
     static bool attr_done[64] = {};
     if (dev.device >= 0 && dev.device < 64 && !attr_done[dev.device]) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             int(Cf::SMEM));
+                                             int(SMEM));
         if (e != cudaSuccess) return e;
         attr_done[dev.device] = true;
     }
@@ -1075,12 +1191,25 @@ cudaError_t launch_attention_t(const DeviceInfo& dev, const void* q, const Paged
                                stream, cnt, ncnt);
     if (e != cudaSuccess) return e;
     e = launch_pdl(
-        kern, dim3(grid), dim3(THREADS), Cf::SMEM, stream, tk, tv,
+        kern, dim3(grid), dim3(THREADS), SMEM, stream, tk, tv,
         static_cast<const __nv_bfloat16*>(q), a.block_table, int(a.max_pages), int(a.num_pages),
         a.seq_lens, a.cu_q, int(a.batch), int(a.total_q), int(a.max_q), int(a.max_seq_len),
-        int(a.hq), int(a.hkv), scale_log2, ws_o, ws_ml, maxC, chunk_log2, cnt, dev.err_word);
+        int(a.hq), int(a.hkv), scale_log2, ws_o, ws_ml, maxC, chunk_log2, cnt, dev.err_word, shape);
     if (e != cudaSuccess) return e;
-    return launch_attn_merge(a, workspace, chunk_log2, out, lse, cnt, dev.err_word, stream);
+    return launch_attn_merge(a, workspace, chunk_log2, out, lse, cnt, dev.err_word, stream,
+                             shape);
+}
+
+template <int D>
+cudaError_t launch_attention_d(const DeviceInfo& dev, const void* q, const PagedArgs& a,
+                               float scale, const Shape& shape, void* out, float* lse,
+                               void* workspace, int chunk_log2, cudaStream_t stream) {
+    auto run = shape.mode == 0                        ? launch_attention_t<D, 0>
+               : shape.mode == kRange                 ? launch_attention_t<D, kRange>
+               : shape.mode == (kRange | kCap)        ? launch_attention_t<D, kRange | kCap>
+               : shape.mode == (kRange | kBias)       ? launch_attention_t<D, kRange | kBias>
+                                                      : launch_attention_t<D, kRange | kCap | kBias>;
+    return run(dev, q, a, scale, shape, out, lse, workspace, chunk_log2, stream);
 }
 
 }  // namespace
@@ -1096,9 +1225,12 @@ unsigned int* attn_item_counters(const PagedArgs& a, void* workspace, int chunk_
         static_cast<uint8_t*>(workspace) + partials_bytes(a.total_q, a.hq, a.head_dim, chunks));
 }
 
-cudaError_t launch_attn_merge(const PagedArgs& a, void* workspace, int chunk_log2, void* out,
-                              float* lse, const unsigned int* cnt, unsigned int* err,
-                              cudaStream_t stream) {
+namespace {
+
+template <int D, bool RANGED>
+cudaError_t launch_merge_t(const PagedArgs& a, void* workspace, int chunk_log2, void* out,
+                           float* lse, const unsigned int* cnt, unsigned int* err,
+                           cudaStream_t stream, const Shape& shape) {
     const int chunk = 1 << chunk_log2;
     const int maxC = int((a.max_seq_len + chunk - 1) / chunk);
     const float* ws_o = static_cast<const float*>(workspace);
@@ -1111,38 +1243,48 @@ cudaError_t launch_attn_merge(const PagedArgs& a, void* workspace, int chunk_log
     // change any bit)
     if (rows < kMergeRowsMin || maxC > MERGE_UNROLL) {
         const bool few = maxC <= 5 * MERGE_WARPS;
-        auto kern = a.head_dim == 64
-                        ? (few ? attn_merge_kernel<64, 5> : attn_merge_kernel<64, MERGE_UNROLL>)
-                        : (few ? attn_merge_kernel<128, 5> : attn_merge_kernel<128, MERGE_UNROLL>);
+        auto kern = few ? attn_merge_kernel<D, 5, RANGED>
+                        : attn_merge_kernel<D, MERGE_UNROLL, RANGED>;
         const bool apart = cnt && a.batch * a.hkv * int64_t(maxC) >= kMergeApartItems;
         return launch_pdl(kern, dim3(unsigned(rows)), dim3(MERGE_WARPS * 32),
                           apart ? kMergeApart : 0, stream, a.seq_lens, a.cu_q, int(a.batch),
                           int(a.total_q), int(a.max_q), int(a.max_seq_len), int(a.hq), int(a.hkv),
                           ws_o, ws_ml, maxC, chunk_log2, cnt, static_cast<__nv_bfloat16*>(out),
-                          lse, err);
+                          lse, err, shape);
     }
-    auto kern = a.head_dim == 64
-                    ? (maxC <= 4 ? attn_merge_rows_kernel<64, 4>
-                                 : maxC <= 8 ? attn_merge_rows_kernel<64, 8>
-                                             : attn_merge_rows_kernel<64, MERGE_UNROLL>)
-                    : (maxC <= 4 ? attn_merge_rows_kernel<128, 4>
-                                 : maxC <= 8 ? attn_merge_rows_kernel<128, 8>
-                                             : attn_merge_rows_kernel<128, MERGE_UNROLL>);
+    auto kern = maxC <= 4   ? attn_merge_rows_kernel<D, 4, RANGED>
+                : maxC <= 8 ? attn_merge_rows_kernel<D, 8, RANGED>
+                            : attn_merge_rows_kernel<D, MERGE_UNROLL, RANGED>;
     return launch_pdl(kern, dim3(unsigned((rows + MERGE_WARPS - 1) / MERGE_WARPS)),
                       dim3(MERGE_WARPS * 32), cnt ? kMergeApart : 0, stream, a.seq_lens, a.cu_q,
                       int(a.batch), int(a.total_q), int(a.max_q), int(a.max_seq_len), int(a.hq),
                       int(a.hkv), ws_o, ws_ml, maxC, chunk_log2, cnt,
-                      static_cast<__nv_bfloat16*>(out), lse, err);
+                      static_cast<__nv_bfloat16*>(out), lse, err, shape);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_merge(const PagedArgs& a, void* workspace, int chunk_log2, void* out,
+                              float* lse, const unsigned int* cnt, unsigned int* err,
+                              cudaStream_t stream, const Shape& shape) {
+    auto run = a.head_dim == 64
+                   ? (shape.mode ? launch_merge_t<64, true> : launch_merge_t<64, false>)
+                   : (shape.mode ? launch_merge_t<128, true> : launch_merge_t<128, false>);
+    return run(a, workspace, chunk_log2, out, lse, cnt, err, stream, shape);
 }
 
 size_t attn_workspace_bytes(int64_t total_q, int64_t hq, int64_t head_dim, int64_t max_seq_len) {
     return workspace_for(total_q, hq, head_dim, max_seq_len, CHUNK_LOG2);
 }
 
-int attn_chunk_log2(const PagedArgs& a, size_t ws_bytes, int num_sms, bool invariant) {
+int attn_chunk_log2(const PagedArgs& a, size_t ws_bytes, int num_sms, bool invariant,
+                    int64_t window) {
     if (invariant) return CHUNK_LOG2;
+    // (keys that a sequence's block sees)
+    const int64_t len = window > 0 && window + a.max_q < a.max_seq_len ? window + a.max_q
+                                                                       : a.max_seq_len;
     // Non-invariant call: the chunk length that minimises a simple cost in page-times.
-    // Sequences are taken to be max_seq_len long.  Work items are dealt round-robin to
+    // Sequences are taken to be `len` long.  Work items are dealt round-robin to
     // the persistent CTAs, so the busiest CTA runs ceil(items / SMs) of them; in the
     // worst case only one in every (chunks per sequence) of those is a short last chunk.
     // An item costs its pages plus a fixed overhead (pipeline turn-around, ~half a page)
@@ -1158,12 +1300,12 @@ int attn_chunk_log2(const PagedArgs& a, size_t ws_bytes, int num_sms, bool invar
     for (int lg = MAX_CHUNK_LOG2; lg >= MIN_CHUNK_LOG2; --lg) {
         if (workspace_for(a.total_q, a.hq, a.head_dim, a.max_seq_len, lg) > ws_bytes) continue;
         const int64_t chunk = int64_t(1) << lg;
-        const int64_t chunks = (a.max_seq_len + chunk - 1) / chunk;
+        const int64_t chunks = (len + chunk - 1) / chunk;
         const int64_t items = a.batch * a.hkv * chunks;
         const int64_t per_cta = (items + num_sms - 1) / num_sms;
         const int64_t tails = per_cta / chunks;
         const double full_pages = double(chunk / PAGE);
-        const double tail_pages = double((a.max_seq_len - (chunks - 1) * chunk + PAGE - 1) / PAGE);
+        const double tail_pages = double((len - (chunks - 1) * chunk + PAGE - 1) / PAGE);
         const double cost = double(per_cta) * item_ovh + double(per_cta - tails) * full_pages +
                             double(tails) * tail_pages;
         if (best_cost < 0.0 || cost < best_cost) {
@@ -1186,12 +1328,11 @@ cudaError_t launch_kv_append(const DeviceInfo& dev, const void* k_new, const voi
 }
 
 cudaError_t launch_attention(const DeviceInfo& dev, const void* q, const PagedArgs& a,
-                             float scale, void* out, float* lse, void* workspace,
-                             int chunk_log2, cudaStream_t stream) {
+                             float scale, const Shape& shape, void* out, float* lse,
+                             void* workspace, int chunk_log2, cudaStream_t stream) {
     if (chunk_log2 < MIN_CHUNK_LOG2 || chunk_log2 > MAX_CHUNK_LOG2) return cudaErrorNotSupported;
-    if (a.head_dim == 64)
-        return launch_attention_t<64>(dev, q, a, scale, out, lse, workspace, chunk_log2, stream);
-    return launch_attention_t<128>(dev, q, a, scale, out, lse, workspace, chunk_log2, stream);
+    auto run = a.head_dim == 64 ? launch_attention_d<64> : launch_attention_d<128>;
+    return run(dev, q, a, scale, shape, out, lse, workspace, chunk_log2, stream);
 }
 
 }  // namespace bi

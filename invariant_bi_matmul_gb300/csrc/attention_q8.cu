@@ -1120,7 +1120,8 @@ cudaError_t launch_q8_t(const DeviceInfo& dev, const void* q, const PagedArgs& a
         a.seq_lens, a.cu_q, int(a.batch), int(a.total_q), int(a.max_q), int(a.max_seq_len),
         int(a.hq), int(a.hkv), scale * kLog2e, ws_o, ws_ml, maxC, run, cnt, dev.err_word);
     if (e != cudaSuccess) return e;
-    return launch_attn_merge(a, workspace, CHUNK_LOG2, out, lse, cnt, dev.err_word, stream);
+    return launch_attn_merge(a, workspace, CHUNK_LOG2, out, lse, cnt, dev.err_word, stream,
+                             Shape{});
 }
 
 }  // namespace

@@ -142,6 +142,8 @@ struct PagedArgs {
     int64_t head_dim;
 };
 
+struct Shape;  // what a call does to its scores (attn_common.cuh)
+
 cudaError_t launch_kv_append(const DeviceInfo& dev, const void* k_new, const void* v_new,
                              void* k_cache, void* v_cache, const PagedArgs& a,
                              cudaStream_t stream);
@@ -150,12 +152,13 @@ size_t attn_workspace_bytes(int64_t total_q, int64_t hq, int64_t head_dim, int64
 
 // The split-KV chunk length (log2 of keys per work item) of a call: the fixed invariant
 // length when `invariant`, else the length a cost model picks from the call's sizes,
-// the SM count and the workspace.
-int attn_chunk_log2(const PagedArgs& a, size_t ws_bytes, int num_sms, bool invariant);
+// the SM count and the workspace.  window: how far back a token sees (0: to the start).
+int attn_chunk_log2(const PagedArgs& a, size_t ws_bytes, int num_sms, bool invariant,
+                    int64_t window = 0);
 
 cudaError_t launch_attention(const DeviceInfo& dev, const void* q, const PagedArgs& a,
-                             float scale, void* out, float* lse, void* workspace,
-                             int chunk_log2, cudaStream_t stream);
+                             float scale, const Shape& shape, void* out, float* lse,
+                             void* workspace, int chunk_log2, cudaStream_t stream);
 
 // The log-sum-exp merge of the chunk partials in `workspace` (as the split-KV kernels
 // leave them for chunk length 2^chunk_log2) into out (and lse).  With `cnt` (the item
@@ -164,7 +167,7 @@ cudaError_t launch_attention(const DeviceInfo& dev, const void* q, const PagedAr
 // it waits for the whole previous grid.  Timeouts are latched in `err`.
 cudaError_t launch_attn_merge(const PagedArgs& a, void* workspace, int chunk_log2, void* out,
                               float* lse, const unsigned int* cnt, unsigned int* err,
-                              cudaStream_t stream);
+                              cudaStream_t stream, const Shape& shape);
 
 // The item counters' place in a call's workspace, one per (sequence, KV head), and the kernel
 // that zeroes n of them before the partial kernel (which must be the next launch) counts.
@@ -174,8 +177,8 @@ cudaError_t launch_attn_count_reset(unsigned int* cnt, int n, cudaStream_t strea
 // Chunked prefill (prefill.cu): blocks of any width, each query reduced exactly as the
 // decode / verify kernels reduce it (invariant chunk length), then the same merge.
 cudaError_t launch_prefill(const DeviceInfo& dev, const void* q, const PagedArgs& a,
-                           float scale, void* out, float* lse, void* workspace,
-                           cudaStream_t stream);
+                           float scale, const Shape& shape, void* out, float* lse,
+                           void* workspace, cudaStream_t stream);
 
 // -------------------------------------- 8-bit cache (kv_q8.cu, attention_q8.cu)
 // The caches in `a` hold e4m3 codes; k_scale and v_scale their E8M0 bytes.

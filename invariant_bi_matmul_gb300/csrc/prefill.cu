@@ -84,7 +84,34 @@ struct PCfg {
     static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
-template <int D>
+// First key that any token of each query tile sees (block_low), for a call with first_key: entry
+// t0 + qt of `lows` for tile qt of the sequence whose first token is t0 (tiles hold a token at
+// least, so the entries are distinct).  A warp per tile slot; TQ tokens per tile.
+__global__ void __launch_bounds__(256)
+tile_low_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ cu_q, int B,
+                int total_q, int max_q, int max_seq_len, int TQ, const Shape sh, int* lows) {
+    pdl_wait();
+    pdl_trigger();
+    const int slot = int(blockIdx.x) * 8 + int(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (slot >= total_q) return;
+    int lo = 0, hi = B;  // largest b with cu_q[b] <= slot
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu_q[mid] <= slot) lo = mid; else hi = mid;
+    }
+    const SeqInfo si = seq_info(seq_lens, cu_q, lo);
+    const int qt = slot - si.t0;
+    if (!seq_ok(si, max_q, max_seq_len, total_q) || qt < 0 || int64_t(qt) * TQ >= si.qb) return;
+    const int j0 = qt * TQ, n = min(TQ, si.qb - j0), pos0 = si.L - si.qb + j0;
+    int low = pos0 + n - 1;
+    for (int j = lane; j < n; j += 32) low = min(low, row_low(sh, si.t0 + j0 + j, pos0 + j));
+    low = __reduce_min_sync(0xffffffffu, low);
+    if (lane == 0) lows[slot] = low;
+}
+
+// MODE: what the call does to its scores (kRange, kCap, kBias of attn_common.cuh; 0: nothing);
+// tile_lows: tile_low_kernel's, or null where no first_key is given.
+template <int D, int MODE>
 __global__ void __launch_bounds__(P_THREADS, 1)
 attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v,
@@ -93,7 +120,8 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ cu_q,
                     int B, int total_q, int max_q, int max_seq_len, int Hq, int Hkv,
                     float scale_log2, float* __restrict__ ws_o, float* __restrict__ ws_ml,
-                    int maxC, unsigned int* err) {
+                    int maxC, unsigned int* err, const Shape sh,
+                    const int* __restrict__ tile_lows) {
     using C = PCfg<D>;
     constexpr int NST = C::NST;
     constexpr int chunk_pages = CHUNK / PAGE;
@@ -159,13 +187,40 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
         *abort_flag = 0;
         fence_barrier_init();
     }
-    // chunks a query tile reduces: through the chunk of its last token's position
+    // chunks a query tile reduces: through the chunk of its last token's position ...
     auto tile_chunks = [&](int L, int qb, int qt) {
         const int last = min(qb, (qt + 1) * TQ) - 1;
         return ((L - qb + last) >> CHUNK_LOG2) + 1;
     };
+    // ... from that of the first key that any of its tokens sees
+    auto tile_low = [&](int L, int t0, int qb, int qt) {
+        if (!MODE) return 0;
+        return tile_lows ? tile_lows[t0 + qt]
+                         : block_low(sh, t0 + qt * TQ, L - qb + qt * TQ, min(TQ, qb - qt * TQ));
+    };
     // work items per sequence: sum over its query tiles of chunks x KV heads
-    for (int b = tid; b < B; b += P_THREADS) {
+    if (MODE) {  // (a warp per sequence: a tile's first key may be a load)
+        for (int b = warp; b < B; b += P_THREADS / 32) {
+            const SeqInfo si = seq_info(seq_lens, cu_q, b);
+            const bool ok = seq_ok(si, max_q, max_seq_len, total_q);
+            if (!ok && lane == 0) latch_error(err, kErrDeviceArg);
+            int n = 0;
+            if (ok) {
+                const int nqt = (si.qb + TQ - 1) / TQ;
+                for (int qt = lane; qt < nqt; qt += 32)
+                    n += tile_chunks(si.L, si.qb, qt) -
+                         (tile_low(si.L, si.t0, si.qb, qt) >> CHUNK_LOG2);
+            }
+            n = __reduce_add_sync(0xffffffffu, n);
+            if (lane == 0) {
+                prefix[b + 1] = n * Hkv;
+                seq_len[b] = si.L;
+                seq_t0[b] = si.t0;
+                seq_qb[b] = ok ? si.qb : 0;
+            }
+        }
+    }
+    for (int b = tid; !MODE && b < B; b += P_THREADS) {
         const SeqInfo si = seq_info(seq_lens, cu_q, b);
         const bool ok = seq_ok(si, max_q, max_seq_len, total_q);
         if (!ok) latch_error(err, kErrDeviceArg);
@@ -205,12 +260,20 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
     const int w_end = int(int64_t(blockIdx.x + 1) * total / gridDim.x);
 
     // Item cursor (every warp walks the same run): sequence b, query tile qt, KV head h,
-    // chunk c (fastest), and the tile's chunk count nch.
+    // chunk c (fastest), and the tile's chunk count nch, first key low and its chunk c0.
     struct Cursor {
-        int b, qt, h, c, nch;
+        int b, qt, h, c, nch, low, c0;
+    };
+    auto set_tile = [&](Cursor& k) {
+        k.nch = tile_chunks(seq_len[k.b], seq_qb[k.b], k.qt);
+        if (MODE) {
+            k.low = tile_low(seq_len[k.b], seq_t0[k.b], seq_qb[k.b], k.qt);
+            k.c0 = k.low >> CHUNK_LOG2;
+            k.nch -= k.c0;
+        }
     };
     auto seek = [&](int w) {
-        Cursor k{B, 0, 0, 0, 1};
+        Cursor k{B, 0, 0, 0, 1, 0, 0};
         if (w >= total) return k;  // an empty run
         // sequence b with prefix[b] <= w < prefix[b+1]: a valid one (it has items), so
         // its tiles' chunk counts are >= 1 and the walk below ends inside its tiles
@@ -223,8 +286,36 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
         int r = w - prefix[k.b];
         k.qt = 0;
         const int nqt = (seq_qb[k.b] + TQ - 1) / TQ;
+        if (MODE) {  // 32 tiles at a time, one per lane
+            const int L = seq_len[k.b], qb = seq_qb[k.b], t0 = seq_t0[k.b];
+            for (; k.qt < nqt; k.qt += 32) {
+                const int qt = k.qt + lane;
+                int n = 0;
+                if (qt < nqt)
+                    n = (tile_chunks(L, qb, qt) - (tile_low(L, t0, qb, qt) >> CHUNK_LOG2)) * Hkv;
+                int to = n;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int u = __shfl_up_sync(0xffffffffu, to, off);
+                    if (lane >= off) to += u;
+                }
+                const unsigned past = __ballot_sync(0xffffffffu, r < to);
+                if (past) {
+                    const int at = __ffs(past) - 1;
+                    r -= __shfl_sync(0xffffffffu, to - n, at);
+                    k.qt += at;
+                    break;
+                }
+                r -= __shfl_sync(0xffffffffu, to, 31);
+            }
+            if (k.qt >= nqt) k.qt = nqt - 1;  // (not reached: w < total)
+            set_tile(k);
+            k.h = min(r / k.nch, Hkv - 1);
+            k.c = k.c0 + r - k.h * k.nch;
+            return k;
+        }
         for (;;) {
-            k.nch = tile_chunks(seq_len[k.b], seq_qb[k.b], k.qt);
+            set_tile(k);
             if (r < k.nch * Hkv || k.qt + 1 >= nqt) break;
             r -= k.nch * Hkv;
             ++k.qt;
@@ -234,8 +325,8 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
         return k;
     };
     auto advance = [&](Cursor& k) {
-        if (++k.c < k.nch) return;
-        k.c = 0;
+        if (++k.c < k.c0 + k.nch) return;
+        k.c = k.c0;
         if (++k.h < Hkv) return;
         k.h = 0;
         if (++k.qt * TQ >= seq_qb[k.b]) {
@@ -244,13 +335,21 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 ++k.b;
             } while (k.b < B && prefix[k.b + 1] == prefix[k.b]);
         }
-        if (k.b < B) k.nch = tile_chunks(seq_len[k.b], seq_qb[k.b], k.qt);
+        if (k.b < B) {
+            set_tile(k);
+            k.c = k.c0;
+        }
     };
     // pages of chunk c: those the decode kernel reduces for the chunk, up to the
     // sequence's end (pages past a row's position are masked for it and add +0 to its O
     // and sums; processing the same pages keeps even the signs of zeros identical)
+    // (from the page of the tile's first key; what lies in front of it is masked likewise)
+    auto first_page = [&](const Cursor& k) {
+        return MODE ? max(k.c * chunk_pages, k.low / PAGE) : k.c * chunk_pages;
+    };
     auto item_pages = [&](const Cursor& k) {
-        return min(chunk_pages, (seq_len[k.b] - k.c * CHUNK + PAGE - 1) / PAGE);
+        const int n = min(chunk_pages, (seq_len[k.b] - k.c * CHUNK + PAGE - 1) / PAGE);
+        return MODE ? n - (first_page(k) - k.c * chunk_pages) : n;
     };
     auto give_up = [&]() {
         if (!*abort_flag) {
@@ -276,7 +375,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const int npages = item_pages(k);  // <= chunk_pages = 8
             // the item's block-table entries, one per lane, read before the first wait for
             // a free stage: no dependent global load between a stage freeing and its copy
-            const int pidx_l = k.c * chunk_pages + lane;
+            const int pidx_l = first_page(k) + lane;
             const int phys_l = (lane < npages && pidx_l < max_pages)
                                    ? block_table[int64_t(k.b) * max_pages + pidx_l]
                                    : -1;
@@ -326,7 +425,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
         Cursor k = seek(w_begin);
         for (int w = w_begin; ok && w < w_end; ++w, advance(k)) {
             const int npages = item_pages(k);
-            if (w == w_begin || k.c == 0) {
+            if (w == w_begin || k.c == k.c0) {
                 // a new Q tile: rows r = token (r / G) of the tile x head r mod G
                 if (qgen > 0) {
                     if (elect_one()) tc_commit(q_free);
@@ -492,18 +591,25 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
             // whether each page of the item is in the cache, from the block table (the
             // producer's test on the same entries), one page per lane: the softmax needs
             // no stage's landing for it, only for the pages whose V rows it zeroes
-            const int pidx_l = k.c * chunk_pages + lane;
+            const int pidx_l = first_page(k) + lane;
             const int phys_l = (lane < npages && pidx_l < max_pages)
                                    ? block_table[int64_t(k.b) * max_pages + pidx_l]
                                    : -1;
             const bool valid_l = phys_l >= 0 && phys_l < num_pages;
+            // the row's first key and slope (a row past the block: all masked by pos)
+            int low = 0;
+            float slope_log2 = 0.f;
+            if (MODE) {
+                if (j < qb) low = row_low(sh, seq_t0[k.b] + j, pos);
+                if (MODE & kBias) slope_log2 = sh.slopes[k.h * G + r % G] * kLog2e;
+            }
             float m_ref = -INFINITY;
             float l_run[4] = {0.f, 0.f, 0.f, 0.f};  // running sums of the four 16-key slices
             for (int i = 0; i < npages && ok; ++i) {
                 const uint32_t gi = g + uint32_t(i);
                 const int s = int(gi % NST), sb = int(gi & 1u);
                 const uint32_t par = (gi >> 1) & 1u;
-                const int page0 = k.c * CHUNK + i * PAGE;
+                const int page0 = (first_page(k) + i) * PAGE;
                 if (!wait(&s_full[sb], par)) break;
                 tc_fence_after_sync();
                 uint32_t sv[PAGE];
@@ -514,14 +620,26 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 if (lane == 0) mbar_arrive(&s_empty[sb]);
                 const bool valid = __shfl_sync(0xffffffffu, valid_l ? 1 : 0, i) != 0;
                 float sl[PAGE];
-                if (__all_sync(0xffffffffu, valid && page0 + PAGE - 1 <= pos)) {
+                if (MODE & kBias) {
+                    float v[PAGE];
+#pragma unroll
+                    for (int kk = 0; kk < PAGE; ++kk) v[kk] = __uint_as_float(sv[kk]);
+                    shape_scores<MODE>(v, sh, scale_log2, slope_log2, float(page0 - pos));
+#pragma unroll
+                    for (int kk = 0; kk < PAGE; ++kk) sv[kk] = __float_as_uint(v[kk]);
+                }
+                const bool all_seen = __all_sync(
+                    0xffffffffu, valid && page0 + PAGE - 1 <= pos && (!MODE || page0 >= low));
+                if (all_seen) {
                     // every key of the page is visible to every row of the warp
 #pragma unroll
                     for (int kk = 0; kk < PAGE; ++kk) sl[kk] = __uint_as_float(sv[kk]);
                 } else {
 #pragma unroll
                     for (int kk = 0; kk < PAGE; ++kk)
-                        sl[kk] = (valid && page0 + kk <= pos) ? __uint_as_float(sv[kk]) : -INFINITY;
+                        sl[kk] = (valid && page0 + kk <= pos && (!MODE || page0 + kk >= low))
+                                     ? __uint_as_float(sv[kk])
+                                     : -INFINITY;
                 }
                 // the exact row max of the page (max does not round: any order), by
                 // three-input maxima: 31 instructions instead of 63
@@ -539,7 +657,14 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     mt[0] = fmax3(fmax3(t2[0], t2[1], t2[2]), fmax3(t2[3], t2[4], t2[5]),
                                   fmaxf(t2[6], t2[7]));
                 }
-                const float m_page = mt[0] * scale_log2;
+                float m_page = mt[0] * scale_log2;
+                if (MODE & kBias) {
+                    m_page = mt[0];
+                } else if (MODE & kCap) {  // (the maximum of capped scores is the maximum's)
+                    float one[1] = {mt[0]};
+                    shape_scores<MODE>(one, sh, scale_log2, 0.f, 0.f);
+                    m_page = mt[0] == -INFINITY ? -INFINITY : one[0];
+                }
                 const bool raise = m_page > m_ref + kRescaleLog2 ||
                                    (m_ref == -INFINITY && m_page != -INFINITY);
                 const float factor = raise ? ex2(m_ref - m_page) : 1.f;
@@ -572,9 +697,28 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
                 for (int q4 = 0; q4 < 4; ++q4) {  // 16-key slice q4
                     float pv[16];
+                    if (MODE & kBias) {
 #pragma unroll
-                    for (int kk = 0; kk < 16; ++kk)
-                        pv[kk] = ex2(fmaf(sl[16 * q4 + kk], scale_log2, -m_use));
+                        for (int kk = 0; kk < 16; ++kk) pv[kk] = ex2(sl[16 * q4 + kk] - m_use);
+                    } else if (MODE & kCap) {
+                        float v[16];
+#pragma unroll
+                        for (int kk = 0; kk < 16; ++kk) v[kk] = __uint_as_float(sv[16 * q4 + kk]);
+                        shape_scores<MODE>(v, sh, scale_log2, 0.f, 0.f);
+#pragma unroll
+                        for (int kk = 0; kk < 16; ++kk) pv[kk] = ex2(v[kk] - m_use);
+                        if (!all_seen) {
+#pragma unroll
+                            for (int kk = 0; kk < 16; ++kk) {
+                                const int key = page0 + 16 * q4 + kk;
+                                if (!valid || key > pos || key < low) pv[kk] = 0.f;
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < 16; ++kk)
+                            pv[kk] = ex2(fmaf(sl[16 * q4 + kk], scale_log2, -m_use));
+                    }
 #pragma unroll
                     for (int kk = 0; kk < 16; kk += 2)
                         pk[8 * q4 + kk / 2] = pack_bf16x2(pv[kk], pv[kk + 1]);
@@ -604,6 +748,18 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     }
                     fence_proxy_async_smem();  // the zeroed V rows, read by the MMA
                 }
+                // ... and those in front of the first key that any row of the tile sees
+                if (MODE && k.low - page0 > sw * 16) {
+                    if (!wait(&full[s], (gi / NST) & 1u)) break;
+                    const int r0 = sw * 16, r1 = min(k.low - page0, r0 + 16);
+                    uint8_t* vst = sStage + s * C::STAGE_BYTES + C::PAGE_BYTES;
+                    for (int idx = lane; idx < C::BOXES * (r1 - r0) * 8; idx += 32) {
+                        const int bx = idx / ((r1 - r0) * 8), rem = idx - bx * ((r1 - r0) * 8);
+                        *reinterpret_cast<uint4*>(vst + bx * C::BOX_BYTES + r0 * 128 + rem * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
                 tc_fence_before_sync();    // the P stores, before the arrival
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[pb]);
@@ -628,10 +784,10 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
 }
 
-template <int D>
+template <int D, int MODE>
 cudaError_t launch_prefill_t(const DeviceInfo& dev, const void* q, const PagedArgs& a,
-                             float scale, void* out, float* lse, void* workspace,
-                             cudaStream_t stream) {
+                             float scale, const Shape& shape, void* out, float* lse,
+                             void* workspace, cudaStream_t stream) {
     using Cf = PCfg<D>;
     const uint64_t rows = uint64_t(a.num_pages) * uint64_t(a.hkv) * PAGE;
     const int G = int(a.hq / a.hkv);
@@ -641,7 +797,7 @@ cudaError_t launch_prefill_t(const DeviceInfo& dev, const void* q, const PagedAr
         !tmap_3d_bf16(&tq, q, D, uint64_t(a.hq), uint64_t(a.total_q), D, uint64_t(a.hq) * D, 64,
                       uint32_t(G), uint32_t(P_ROWS / G)))
         return cudaErrorNotSupported;
-    auto kern = attn_prefill_kernel<D>;
+    auto kern = attn_prefill_kernel<D, MODE>;
     static bool attr_done[64] = {};
     if (dev.device >= 0 && dev.device < 64 && !attr_done[dev.device]) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -657,23 +813,46 @@ cudaError_t launch_prefill_t(const DeviceInfo& dev, const void* q, const PagedAr
     const int grid = int(items_bound < dev.num_sms ? items_bound : dev.num_sms);
     float* ws_o = static_cast<float*>(workspace);
     float* ws_ml = ws_o + a.total_q * a.hq * int64_t(maxC) * D;
-    cudaError_t e = launch_pdl(kern, dim3(grid), dim3(P_THREADS), Cf::SMEM, stream, tk, tv, tq,
+    cudaError_t e = cudaSuccess;
+    int* tile_lows = nullptr;
+    if (MODE && shape.first_key) {
+        // (the workspace's item counters, one word per token and query head, are not used here)
+        tile_lows = reinterpret_cast<int*>(attn_item_counters(a, workspace, CHUNK_LOG2));
+        e = launch_pdl(tile_low_kernel, dim3(unsigned((a.total_q + 7) / 8)), dim3(256), 0, stream,
+                       a.seq_lens, a.cu_q, int(a.batch), int(a.total_q), int(a.max_q),
+                       int(a.max_seq_len), P_ROWS / G, shape, tile_lows);
+        if (e != cudaSuccess) return e;
+    }
+    e = launch_pdl(kern, dim3(grid), dim3(P_THREADS), Cf::SMEM, stream, tk, tv, tq,
                                a.block_table, int(a.max_pages), int(a.num_pages), a.seq_lens,
                                a.cu_q, int(a.batch), int(a.total_q), int(a.max_q),
                                int(a.max_seq_len), int(a.hq), int(a.hkv), scale * kLog2e, ws_o,
-                               ws_ml, maxC, dev.err_word);
+                               ws_ml, maxC, dev.err_word, shape,
+                               static_cast<const int*>(tile_lows));
     if (e != cudaSuccess) return e;
-    return launch_attn_merge(a, workspace, CHUNK_LOG2, out, lse, nullptr, dev.err_word, stream);
+    return launch_attn_merge(a, workspace, CHUNK_LOG2, out, lse, nullptr, dev.err_word, stream,
+                             shape);
+}
+
+template <int D>
+cudaError_t launch_prefill_d(const DeviceInfo& dev, const void* q, const PagedArgs& a,
+                             float scale, const Shape& shape, void* out, float* lse,
+                             void* workspace, cudaStream_t stream) {
+    auto run = shape.mode == 0                  ? launch_prefill_t<D, 0>
+               : shape.mode == kRange           ? launch_prefill_t<D, kRange>
+               : shape.mode == (kRange | kCap)  ? launch_prefill_t<D, kRange | kCap>
+               : shape.mode == (kRange | kBias) ? launch_prefill_t<D, kRange | kBias>
+                                                : launch_prefill_t<D, kRange | kCap | kBias>;
+    return run(dev, q, a, scale, shape, out, lse, workspace, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_prefill(const DeviceInfo& dev, const void* q, const PagedArgs& a,
-                           float scale, void* out, float* lse, void* workspace,
-                           cudaStream_t stream) {
-    return a.head_dim == 64
-               ? launch_prefill_t<64>(dev, q, a, scale, out, lse, workspace, stream)
-               : launch_prefill_t<128>(dev, q, a, scale, out, lse, workspace, stream);
+                           float scale, const Shape& shape, void* out, float* lse,
+                           void* workspace, cudaStream_t stream) {
+    auto run = a.head_dim == 64 ? launch_prefill_d<64> : launch_prefill_d<128>;
+    return run(dev, q, a, scale, shape, out, lse, workspace, stream);
 }
 
 }  // namespace bi
