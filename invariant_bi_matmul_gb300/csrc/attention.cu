@@ -532,6 +532,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
 
             float m_ref = -INFINITY, l_run = 0.f;
+            Reference<MODE> ref;
             for (int i = 0; i < npages && ok; ++i) {
                 const uint32_t gi = g + uint32_t(i);
                 const int s = int(gi % NST), sb = int(gi & 1u);
@@ -577,7 +578,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         for (int k = 0; k < PAGE; ++k) sa[k] = __float_as_uint(v[k]);
 #pragma unroll
                         for (int k = 0; k < KSL; ++k) sv[k] = __float_as_uint(w[k]);
-                    } else if (MODE & kCap) {  // (its maximum is the maximum's)
+                    } else if (MODE & kCap) {  // (the maximum is taken before the cap)
                         float w[KSL];
 #pragma unroll
                         for (int k = 0; k < KSL; ++k) w[k] = __uint_as_float(sv[k]);
@@ -613,22 +614,20 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     m_raw = fmax3(fmax3(t2[0], t2[1], t2[2]), fmax3(t2[3], t2[4], t2[5]),
                                   fmaxf(t2[6], t2[7]));
                 }
-                float m_page = m_raw * scale_log2;
-                if (MODE & kBias) {
-                    m_page = m_raw;
-                } else if (MODE & kCap) {
-                    float one[1] = {m_raw};
-                    shape_scores<MODE>(one, sh, scale_log2, 0.f, 0.f);
-                    m_page = m_raw == -INFINITY ? -INFINITY : one[0];
-                }
-
                 // reference max: raised (and O, l rescaled) only when the page max exceeds
                 // it by more than 2^8, so p = exp2(s - m_ref) <= 2^8
-                const bool raise = m_page > m_ref + kRescaleLog2 ||
-                                   (m_ref == -INFINITY && m_page != -INFINITY);
-                const float factor = raise ? ex2(m_ref - m_page) : 1.f;  // 0 on the first
-                if (raise) m_ref = m_page;
-                l_run *= factor;
+                bool raise;
+                float factor;
+                if (MODE & (kCap | kBias)) {
+                    raise = ref.raise(m_raw, sh, scale_log2, factor);
+                    m_ref = ref.m;
+                } else {
+                    const float m_page = m_raw * scale_log2;
+                    raise = m_page > m_ref + kRescaleLog2 ||
+                            (m_ref == -INFINITY && m_page != -INFINITY);
+                    factor = raise ? ex2(m_ref - m_page) : 1.f;  // 0 on the first
+                    if (raise) m_ref = m_page;
+                }
                 // this warp's 16 keys; a masked key (-inf) gives p = +0
                 // p = exp2(s * scale_log2 - m), the row-slice sum by a fixed pairwise tree
                 float pv[KSL];
@@ -636,7 +635,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
 #pragma unroll
                     for (int k = 0; k < KSL; ++k)
-                        pv[k] = (MODE & (kCap | kBias)) ? ex2(sl[k] - m_use)
+                        pv[k] = (MODE & (kCap | kBias)) ? ex2(__fadd_rn(sl[k], -m_use))
                                                         : ex2(fmaf(sl[k], scale_log2, -m_use));
                 }
                 uint32_t pk[KSL / 2];
@@ -647,7 +646,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
                     for (int k = 0; k < width; ++k) pv[k] = pv[k] + pv[k + width];
                 const float ps = pv[0];
-                l_run = l_run + ps;
+                l_run = fmaf(l_run, factor, ps);  // (spelled out: the prefill kernel's bits)
                 // P buffer sb is free once P V of page gi-2 has completed
                 if (!wait(&p_empty[sb], par ^ 1u)) break;
                 if (sw == 0 && i > 0 && __any_sync(0xffffffffu, raise)) {

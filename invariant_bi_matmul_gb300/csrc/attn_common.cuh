@@ -91,52 +91,107 @@ __device__ __forceinline__ int block_low(const Shape& sh, int t, int pos, int n)
     return low;
 }
 
-// v := cap_log2 * tanh(v * cap_in).  Up to |y| = 1 an odd polynomial (2^-24 off; with its fp32
-// evaluation 2^-22.5), which needs neither of the two special functions of the other branch,
-// 1 - 2 / (1 + e^2y); a warp takes that one for all its scores when one of them is beyond, and
-// each score keeps the value of its own range, so a value does not depend on its neighbours.
-// tanh.approx, off by 2^-11, would move a score near a cap of 50 by 0.02.
+// cap_log2 * tanh(s * cap_in) of a warp's scores.  Up to |y| = 1 an odd polynomial (2^-24 off;
+// with its fp32 evaluation 2^-22.5), which needs neither of the two special functions of the other
+// branch, 1 - 2 / (1 + e^2y), and goes two scores to an instruction; a warp takes the other one for
+// all its scores when one of them is beyond, and each score keeps the value of its own range, so a
+// value does not depend on its neighbours.  (tanh.approx, off by 2^-11, would move a score near a
+// cap of 50 by 0.02.)  Every operation is one that the compiler joins with no other: the kernels
+// that call this have the same bits.
+__device__ __forceinline__ float far_tanh(float y) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.f, ex2(__fmul_rn(y, 2.f * kLog2e)))));
+    return fmaf(-2.f, r, 1.f);
+}
 template <int N>
 __device__ __forceinline__ void cap_scores(float (&v)[N], float cap_in, float cap_log2) {
+    static_assert(N % 2 == 0, "pairs");
+    constexpr float c1 = -0.333329856f, c2 = 0.133264095f, c3 = -0.0534987077f,
+                    c4 = 0.0203597602f, c5 = -0.0062593394f, c6 = 0.00105826475f;
+    auto both = [](float x) { return make_float2(x, x); };
+    float2 t[N / 2];
     float most = 0.f;
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        v[k] *= cap_in;
-        most = fmaxf(most, fabsf(v[k]));
+    for (int k = 0; k < N / 2; ++k) {
+        const float2 y = mul2(make_float2(v[2 * k], v[2 * k + 1]), both(cap_in));
+        v[2 * k] = y.x;
+        v[2 * k + 1] = y.y;
+        most = fmax3(most, fabsf(y.x), fabsf(y.y));
+        const float2 z = mul2(y, y);
+        float2 p = fma2(z, both(c6), both(c5));
+        p = fma2(z, p, both(c4));
+        p = fma2(z, p, both(c3));
+        p = fma2(z, p, both(c2));
+        p = fma2(z, p, both(c1));
+        t[k] = fma2(mul2(z, p), y, y);
     }
-    const bool far = __any_sync(0xffffffffu, most > 1.f);
+    if (__any_sync(0xffffffffu, most > 1.f)) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const float y = v[k], z = y * y;
-        float p = fmaf(z, 0.00105826475f, -0.0062593394f);
-        p = fmaf(z, p, 0.0203597602f);
-        p = fmaf(z, p, -0.0534987077f);
-        p = fmaf(z, p, 0.133264095f);
-        p = fmaf(z, p, -0.333329856f);
-        float t = fmaf(z * p, y, y);
-        if (far) {
-            float r;
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(y * (2.f * kLog2e))));
-            t = fabsf(y) > 1.f ? fmaf(-2.f, r, 1.f) : t;
+        for (int k = 0; k < N / 2; ++k) {
+            if (fabsf(v[2 * k]) > 1.f) t[k].x = far_tanh(v[2 * k]);
+            if (fabsf(v[2 * k + 1]) > 1.f) t[k].y = far_tanh(v[2 * k + 1]);
         }
-        v[k] = __fmul_rn(cap_log2, t);  // (not joined with what the caller adds: one value)
+    }
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) {
+        const float2 x = mul2(both(cap_log2), t[k]);
+        v[2 * k] = x.x;
+        v[2 * k + 1] = x.y;
+    }
+}
+__device__ __forceinline__ float cap_score(float s, float cap_in, float cap_log2) {
+    float v[2] = {s, s};
+    cap_scores(v, cap_in, cap_log2);
+    return v[0];
+}
+
+// Scores of N consecutive keys, in log2 units; slope: the row's, times log2 e, and dist: how far
+// the first key is from the row's position (j - pos; whole numbers below 2^24 are exact, and so is
+// their sum with k: a bias at a short distance is not the difference of two long ones).
+template <int MODE, int N>
+__device__ __forceinline__ void shape_scores(float (&v)[N], const Shape& sh, float scale_log2,
+                                             float slope, float dist) {
+    if (MODE & kCap) cap_scores(v, sh.cap_in, sh.cap_log2);
+    if (MODE & kBias) {
+        auto both = [](float x) { return make_float2(x, x); };
+#pragma unroll
+        for (int k = 0; k < N; k += 2) {
+            float2 s = make_float2(v[k], v[k + 1]);
+            if (!(MODE & kCap)) s = mul2(s, both(scale_log2));
+            s = fma2(both(slope), add2(both(dist), make_float2(float(k), float(k + 1))), s);
+            v[k] = s.x;
+            v[k + 1] = s.y;
+        }
     }
 }
 
-// Scores of N consecutive keys of a row, the first at distance `dist` (j - pos), in log2 units.
-template <int MODE, int N>
-__device__ __forceinline__ void shape_scores(float (&v)[N], const Shape& sh, float scale_log2,
-                                             float slope_log2, float dist) {
-    if (MODE & kCap) {
-        cap_scores(v, sh.cap_in, sh.cap_log2);
-    } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = __fmul_rn(v[k], scale_log2);
+// The running reference of a row's softmax (log2 units) and its raises: by a page's largest score
+// where that exceeds it by more than 2^8.  With a cap the reference is the capped score of the
+// largest one at its last raise, and a raise is judged by the scores before the cap, of which it
+// takes no more than their difference: so a page that raises nothing forms no capped maximum.
+template <int MODE>
+struct Reference {
+    float m = -INFINITY;    // scores are taken relative to it
+    float seen = -INFINITY; // what raises are judged by
+    // page: the page's largest score as the MMA left it, or shaped with a bias; returns whether
+    // the reference was raised, and by which factor sums and O shrink
+    __device__ __forceinline__ bool raise(float page, const Shape& sh, float scale_log2,
+                                          float& factor) {
+        const float now = (MODE & kBias) ? page : __fmul_rn(page, scale_log2);
+        const bool up = now > __fadd_rn(seen, kRescaleLog2) || (seen == -INFINITY && now != -INFINITY);
+        factor = 1.f;
+        if (__any_sync(0xffffffffu, up)) {
+            const float to = ((MODE & kCap) && !(MODE & kBias))
+                                 ? cap_score(page, sh.cap_in, sh.cap_log2)
+                                 : now;
+            if (up) {
+                factor = ex2(__fadd_rn(m, -to));
+                m = to;
+                seen = now;
+            }
+        }
+        return up;
     }
-    if (MODE & kBias) {
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = fmaf(slope_log2, dist + float(k), v[k]);
-    }
-}
+};
 
 }  // namespace bi

@@ -604,6 +604,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 if (MODE & kBias) slope_log2 = sh.slopes[k.h * G + r % G] * kLog2e;
             }
             float m_ref = -INFINITY;
+            Reference<MODE> ref;
             float l_run[4] = {0.f, 0.f, 0.f, 0.f};  // running sums of the four 16-key slices
             for (int i = 0; i < npages && ok; ++i) {
                 const uint32_t gi = g + uint32_t(i);
@@ -620,57 +621,64 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 if (lane == 0) mbar_arrive(&s_empty[sb]);
                 const bool valid = __shfl_sync(0xffffffffu, valid_l ? 1 : 0, i) != 0;
                 float sl[PAGE];
-                if (MODE & kBias) {
-                    float v[PAGE];
 #pragma unroll
-                    for (int kk = 0; kk < PAGE; ++kk) v[kk] = __uint_as_float(sv[kk]);
-                    shape_scores<MODE>(v, sh, scale_log2, slope_log2, float(page0 - pos));
-#pragma unroll
-                    for (int kk = 0; kk < PAGE; ++kk) sv[kk] = __float_as_uint(v[kk]);
-                }
+                for (int kk = 0; kk < PAGE; ++kk) sl[kk] = __uint_as_float(sv[kk]);
+                if (MODE & kBias)  // (a score's size depends on its place: all are shaped)
+                    shape_scores<MODE>(sl, sh, scale_log2, slope_log2, float(page0 - pos));
+                // whether every key of the page is visible to every row of the warp
                 const bool all_seen = __all_sync(
                     0xffffffffu, valid && page0 + PAGE - 1 <= pos && (!MODE || page0 >= low));
-                if (all_seen) {
-                    // every key of the page is visible to every row of the warp
+                const int lim = valid ? pos - page0 : -1;  // the row's last visible key
+                const int fst = MODE ? low - page0 : 0;    // ... and its first
+                auto hide = [&](float (&to)[PAGE]) {
+                    if (!all_seen) {
 #pragma unroll
-                    for (int kk = 0; kk < PAGE; ++kk) sl[kk] = __uint_as_float(sv[kk]);
-                } else {
-#pragma unroll
-                    for (int kk = 0; kk < PAGE; ++kk)
-                        sl[kk] = (valid && page0 + kk <= pos && (!MODE || page0 + kk >= low))
-                                     ? __uint_as_float(sv[kk])
-                                     : -INFINITY;
-                }
+                        for (int kk = 0; kk < PAGE; ++kk)
+                            to[kk] = kk <= lim && (!MODE || kk >= fst) ? sl[kk] : -INFINITY;
+                    }
+                };
+                // (a cap is put on once the maximum, which needs none, is known)
+                constexpr bool CAP_LAST = (MODE & kCap) && !(MODE & kBias);
+                if (!CAP_LAST) hide(sl);
                 // the exact row max of the page (max does not round: any order), by
                 // three-input maxima: 31 instructions instead of 63
-                float mt[1];
-                {
+                auto max_of = [](const float (&a)[PAGE]) {
                     float t1[22], t2[8];
 #pragma unroll
                     for (int kk = 0; kk < 21; ++kk)
-                        t1[kk] = fmax3(sl[3 * kk], sl[3 * kk + 1], sl[3 * kk + 2]);
-                    t1[21] = sl[63];
+                        t1[kk] = fmax3(a[3 * kk], a[3 * kk + 1], a[3 * kk + 2]);
+                    t1[21] = a[63];
 #pragma unroll
                     for (int kk = 0; kk < 7; ++kk)
                         t2[kk] = fmax3(t1[3 * kk], t1[3 * kk + 1], t1[3 * kk + 2]);
                     t2[7] = t1[21];
-                    mt[0] = fmax3(fmax3(t2[0], t2[1], t2[2]), fmax3(t2[3], t2[4], t2[5]),
-                                  fmaxf(t2[6], t2[7]));
+                    return fmax3(fmax3(t2[0], t2[1], t2[2]), fmax3(t2[3], t2[4], t2[5]),
+                                 fmaxf(t2[6], t2[7]));
+                };
+                float m_raw;
+                if (CAP_LAST && !all_seen) {
+                    float shown[PAGE];
+                    hide(shown);
+                    m_raw = max_of(shown);
+                } else {
+                    m_raw = max_of(sl);
                 }
-                float m_page = mt[0] * scale_log2;
-                if (MODE & kBias) {
-                    m_page = mt[0];
-                } else if (MODE & kCap) {  // (the maximum of capped scores is the maximum's)
-                    float one[1] = {mt[0]};
-                    shape_scores<MODE>(one, sh, scale_log2, 0.f, 0.f);
-                    m_page = mt[0] == -INFINITY ? -INFINITY : one[0];
+                bool raise;
+                float factor;
+                if (MODE & (kCap | kBias)) {
+                    raise = ref.raise(m_raw, sh, scale_log2, factor);
+                    m_ref = ref.m;
+                    if (CAP_LAST) {
+                        shape_scores<MODE>(sl, sh, scale_log2, 0.f, 0.f);
+                        hide(sl);
+                    }
+                } else {
+                    const float m_page = m_raw * scale_log2;
+                    raise = m_page > m_ref + kRescaleLog2 ||
+                            (m_ref == -INFINITY && m_page != -INFINITY);
+                    factor = raise ? ex2(m_ref - m_page) : 1.f;
+                    if (raise) m_ref = m_page;
                 }
-                const bool raise = m_page > m_ref + kRescaleLog2 ||
-                                   (m_ref == -INFINITY && m_page != -INFINITY);
-                const float factor = raise ? ex2(m_ref - m_page) : 1.f;
-                if (raise) m_ref = m_page;
-#pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) l_run[q4] *= factor;
                 const int pb = int(gi % P_NPB);
                 if (!wait(&p_empty[pb], ((gi / P_NPB) & 1u) ^ 1u)) break;
                 tc_fence_after_sync();  // P V of page gi-4 read this P buffer: now rewritten
@@ -697,28 +705,11 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
                 for (int q4 = 0; q4 < 4; ++q4) {  // 16-key slice q4
                     float pv[16];
-                    if (MODE & kBias) {
 #pragma unroll
-                        for (int kk = 0; kk < 16; ++kk) pv[kk] = ex2(sl[16 * q4 + kk] - m_use);
-                    } else if (MODE & kCap) {
-                        float v[16];
-#pragma unroll
-                        for (int kk = 0; kk < 16; ++kk) v[kk] = __uint_as_float(sv[16 * q4 + kk]);
-                        shape_scores<MODE>(v, sh, scale_log2, 0.f, 0.f);
-#pragma unroll
-                        for (int kk = 0; kk < 16; ++kk) pv[kk] = ex2(v[kk] - m_use);
-                        if (!all_seen) {
-#pragma unroll
-                            for (int kk = 0; kk < 16; ++kk) {
-                                const int key = page0 + 16 * q4 + kk;
-                                if (!valid || key > pos || key < low) pv[kk] = 0.f;
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int kk = 0; kk < 16; ++kk)
-                            pv[kk] = ex2(fmaf(sl[16 * q4 + kk], scale_log2, -m_use));
-                    }
+                    for (int kk = 0; kk < 16; ++kk)
+                        pv[kk] = (MODE & (kCap | kBias))
+                                     ? ex2(__fadd_rn(sl[16 * q4 + kk], -m_use))
+                                     : ex2(fmaf(sl[16 * q4 + kk], scale_log2, -m_use));
 #pragma unroll
                     for (int kk = 0; kk < 16; kk += 2)
                         pk[8 * q4 + kk / 2] = pack_bf16x2(pv[kk], pv[kk + 1]);
@@ -726,7 +717,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     for (int width = 8; width >= 1; width /= 2)
 #pragma unroll
                         for (int kk = 0; kk < width; ++kk) pv[kk] = pv[kk] + pv[kk + width];
-                    l_run[q4] = l_run[q4] + pv[0];
+                    l_run[q4] = fmaf(l_run[q4], factor, pv[0]);  // (the decode kernel's bits)
                 }
                 // P into this quarter's lanes of the page's P buffer in tensor memory (the
                 // P V MMA reads it from there)

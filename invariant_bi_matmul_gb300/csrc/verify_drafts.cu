@@ -5,24 +5,26 @@
 // u q(token) < p(token); the block's last token is drawn by inverting the cumulative sums of
 // D_i = max(p_i - q_i, 0) (behind a refused draft) or of p_i.  Two launches:
 //
-// Statistics.  A CTA takes one part of one row (kBatch vectors a thread, all requested before
-// any is used) and leaves the part's maximum, sum of 2^((x - m) log2 e / T) in fp32 and, for a
-// sequence at temperature 0, its largest entry.  Every target row and every draft row is read
-// once, which is what the call cannot do without.
+// Statistics.  A warp takes one part of a row (kBatch vectors a lane, all requested before any is
+// used) and leaves the part's maximum, sum of 2^((x - m) log2 e / T) in fp32 and, for a sequence
+// at temperature 0, its largest entry.  Every target row and every draft row is read once, which
+// is what the call cannot do without.  (Persistent warps that request the next part before they
+// use this one had fewer loads under way: 32 sequences of up to 5 rows 43 us, 29 as it is.)
 //
 // Decision and draw.  A cluster of CTAs per sequence joins the parts (lanes over the parts, a
 // butterfly), finds the first refused draft, and goes over that row, and the draft's, once more.
 // A drawn token must not depend on how sums round, or it would depend on the order in which they
 // are taken: near equal entries of 2^-17 of the mass, fp32 sums would choose a neighbour in one
 // row of a few hundred.  So each weight is a whole number, 2^60 p_i, from a product x c in two
-// floats and a table of 2^(j/512), off by at most 2^-30 of itself (fixed_exp), and sums of whole
+// floats and 2^(j/32) (fixed_exp), off by at most 2^-29 of itself, and sums of whole
 // numbers are exact in any order: the token is the same whatever the split, in one row in 10^5 or
-// so another than the definition's.  The fp32 statistics only scale the weights to a sum near
+// so another than the definition's.  The fp32 statistics only scale the weights to sums near
 // 2^60; what the sums come to, sp and sq, corrects that: D_i is proportional to
-// max(p_i sq/sp - q_i, 0), and with e = sq/sp - 1 (1e-6 at most) the sum of D over a block is
-// sum max(p_i - q_i, 0) + e * sum of p_i where p_i > q_i, but for entries whose p and q agree to
-// within e, which weigh e times as much.  One pass so gives the totals, the correction and the
-// sums of each block of 512; the block that holds the drawn share is taken again, entry by entry.
+// max(p_i sq/sp - q_i, 0), and with e = sq/sp - 1 = sum (q_i - p_i) / 2^60 (1e-6 at most) the sum
+// of D over a block is sum max(p_i - q_i, 0) + e * sum of p_i where p_i > q_i, but for entries
+// whose p and q agree to within e, which weigh e times as much.  One pass so gives the totals,
+// the correction and the sums of each block of 512; the block that holds the drawn share is taken
+// again, entry by entry.
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
@@ -42,14 +44,15 @@ void set_last_error_message(const char* msg);
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kStats = 128;                             // threads of a statistics CTA
+constexpr int kThreads = 256;                           // ... and of the others
 constexpr int kBlock = 512;                             // entries of a block: 16 for each lane
 constexpr int kMaxCtas = 8;                             // of a sequence's cluster
 constexpr int kMaxBlocks = (BI_DRAFTS_MAX_N + kBlock - 1) / kBlock;
 constexpr float kHot = 0x1p-64f;                        // temperatures below it are 0
 
 template <int DT>
-constexpr int kPartLen = kThreads * kBatch * (16 / kSize<DT>);  // entries of a part
+constexpr int kPartLen = 32 * kBatch * (16 / kSize<DT>);  // entries of a part
 
 struct PartStats {
     float m, s;
@@ -70,7 +73,7 @@ struct DraftArgs {
     float* logprobs;
     unsigned int* err;
     float temperature;
-    int B, total_q, num_drafts, max_q, n, nparts;
+    int B, total_q, num_drafts, max_q, n, nparts, items;  // items: parts of all rows
 };
 
 __device__ __forceinline__ float temperature_of(const DraftArgs& a, int b) {
@@ -78,179 +81,156 @@ __device__ __forceinline__ float temperature_of(const DraftArgs& a, int b) {
     return t < kHot ? (t >= 0.f ? 0.f : kNaN) : t <= 3.4e38f ? t : kNaN;  // NaN: refused
 }
 
+// log2 e / T in two floats, to 2^-46 of itself.
+struct Rate {
+    float hi, lo;
+};
+__device__ __noinline__ Rate rate_of(float T) {
+    if (T == 0.f) T = 1.f;
+    Rate c;
+    c.hi = kLog2e / T;
+    c.lo = (fmaf(-c.hi, T, kLog2e) + 1.925963033500e-8f) / T;  // (log2 e - float(log2 e))
+    return c;
+}
+
 // --------------------------------------------------------------------------- statistics
 
 template <int DT, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) draft_stats_kernel(const DraftArgs a) {
-    constexpr int VE = 16 / kSize<DT>;
-    __shared__ float sm[kThreads / 32], ss[kThreads / 32];
-    __shared__ unsigned long long sk[kThreads / 32];
+__global__ void __launch_bounds__(kStats, !ALIGNED ? 6 : DT == BI_F32 ? 9 : 8)
+draft_stats_kernel(const DraftArgs a) {
+    constexpr int VE = 16 / kSize<DT>, kLen = 32 * kBatch;  // vectors of a part
     pdl_wait();
     pdl_trigger();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int row = int(blockIdx.x / unsigned(a.nparts));
-    const int part = int(blockIdx.x - unsigned(row) * unsigned(a.nparts));
+    const int lane = threadIdx.x & 31, warp0 = threadIdx.x & ~31;
+    const int item = int(blockIdx.x) * (kStats / 32) + int(threadIdx.x >> 5);
+    if (item >= a.items) return;
+    const int row = int(unsigned(item) / unsigned(a.nparts)), part = item - row * a.nparts;
     const bool draft = row >= a.total_q;
     const int r = draft ? row - a.total_q : row;
     const char* xr = static_cast<const char*>(draft ? a.y : a.x) +
                      int64_t(r) * (draft ? a.ldy : a.ldx) * kSize<DT>;
     const uint32_t skew = ALIGNED ? 0u : uint32_t(reinterpret_cast<uintptr_t>(xr) & 15u);
-    const int v0 = part * (kThreads * kBatch);
     uint4 v[kBatch];
-    load_batch<DT, kThreads, ALIGNED>(v, xr, skew, v0,
-                                      min((a.n + VE - 1) / VE, v0 + kThreads * kBatch), a.n);
-    // the row's sequence, found while the loads are under way: target rows of b are
-    // cu_q[b] .., draft rows cu_q[b] - b ..
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu_q[mid] - (draft ? mid : 0) <= r) lo = mid; else hi = mid;
-    }
-    const int end = a.cu_q[lo + 1] - (draft ? lo + 1 : 0);
-    if (r >= end) return;                   // a row of no sequence
-    const float T = temperature_of(a, lo);
+    // (load_batch counts a CTA's threads: this warp's are 0 .. 31)
+    load_batch<DT, 32, ALIGNED>(v, xr, skew, part * kLen - warp0,
+                                min((a.n + VE - 1) / VE, (part + 1) * kLen), a.n);
+    // the row's sequence, found while the loads are under way: target rows of b are cu_q[b] ..,
+    // draft rows cu_q[b] - b ..  (By counting, a lane's loads all at once: a binary search waits
+    // for one after the other.)
+    int b = 0;
+    for (int i = lane; i < a.B; i += 32) b += a.cu_q[i] - (draft ? i : 0) <= r ? 1 : 0;
+    b = max(__reduce_add_sync(~0u, b) - 1, 0);
+    const float T = temperature_of(a, b);
     const bool greedy = T == 0.f;
-    if (isnan(T) || (greedy && draft)) return;
-    const float c = kLog2e / (greedy ? 1.f : T);
+    if (r >= a.cu_q[b + 1] - (draft ? b + 1 : 0) || isnan(T) || (greedy && draft)) return;
+    const float c = rate_of(T).hi;
 
     float m = vec_max<DT>(v[0]);
 #pragma unroll
     for (int k = 1; k < kBatch; ++k) m = fmaxf(m, vec_max<DT>(v[k]));
-    const float ref = ref_of(m);
-    float s0 = 0.f, s1 = 0.f;               // (entries past the row are -inf: they add 0)
+    const float ref = -ref_of(m);
+    float2 s2 = make_float2(0.f, 0.f);      // (entries past the row are -inf: they add 0)
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
         float e[VE];
         widen<DT>(v[k], e);
 #pragma unroll
         for (int q = 0; q < VE; q += 2) {
-            s0 += ex2((e[q] - ref) * c);
-            s1 += ex2((e[q + 1] - ref) * c);
+            const float2 t = mul2(add2(make_float2(e[q], e[q + 1]), make_float2(ref, ref)),
+                                  make_float2(c, c));
+            s2 = add2(s2, make_float2(ex2(t.x), ex2(t.y)));
         }
     }
-    float s = s0 + s1;
+    float s = s2.x + s2.y;
     unsigned long long best = 0;
-    if (greedy) {
-#pragma unroll
+    if (greedy) {  // (read again, one vector after the other: unrolled, this doubled the kernel)
+#pragma unroll 1
         for (int k = 0; k < kBatch; ++k) {
+            const int g = part * kLen + k * 32 + lane;
             float e[VE];
-            widen<DT>(v[k], e);
-            const int64_t i0 = int64_t(v0 + k * kThreads + tid) * VE;
+            widen<DT>(load_vec<DT>(xr, skew == 0, g, a.n), e);
 #pragma unroll
             for (int q = 0; q < VE; ++q) {
-                if (i0 + q < a.n) {
-                    const unsigned long long key = order_key(e[q], int(i0) + q);
+                if (g * VE + q < a.n) {
+                    const unsigned long long key = order_key(e[q], g * VE + q);
                     best = key > best ? key : best;
                 }
             }
         }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            const unsigned long long o = __shfl_xor_sync(~0u, best, off);
+            best = o > best ? o : best;
+        }
     }
     float M = m;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        M = fmaxf(M, __shfl_xor_sync(~0u, M, off));
-        const unsigned long long o = __shfl_xor_sync(~0u, best, off);
-        best = o > best ? o : best;
-    }
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, off));
     if (m != -INFINITY) s *= ex2((m - M) * c);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(~0u, s, off);
-    if (lane == 0) {
-        sm[warp] = M;
-        ss[warp] = s;
-        sk[warp] = best;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        float top = sm[0];
-#pragma unroll
-        for (int w = 1; w < kThreads / 32; ++w) top = fmaxf(top, sm[w]);
-        PartStats p{top, 0.f, 0ull};
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            p.s += sm[w] == -INFINITY ? ss[w] : ss[w] * ex2((sm[w] - top) * c);
-            p.best = sk[w] > p.best ? sk[w] : p.best;
-        }
-        a.parts[int64_t(row) * a.nparts + part] = p;
-    }
+    if (lane == 0) a.parts[int64_t(row) * a.nparts + part] = PartStats{M, s, best};
 }
 
 // ---------------------------------------------------------------- weights in whole numbers
 
-// Entry j stands for v = 2^62 * 2^(j/512): hi = v / 2^32, and adj = v - hi * 0x4b000000, so that
-// hi * (0x4b000000 + G) + adj = v (1 + G / 2^32).
-struct Power {
-    uint32_t hi, pad;
-    unsigned long long adj;
+// Lane j's register holds 2^31 * 2^(j/32), rounded; a lane takes the one it needs by a shuffle.
+// (A table of 512 in shared memory, with a shorter series, cost twelve cycles of its pipe for each
+// look-up of a warp, and bound the kernel.)
+__constant__ uint32_t kPowers[32] = {
+    0x80000000u, 0x82cd8699u, 0x85aac368u, 0x88980e81u, 0x8b95c1e4u, 0x8ea4398bu,
+    0x91c3d374u, 0x94f4efa9u, 0x9837f052u, 0x9b8d39bau, 0x9ef53261u, 0xa2704303u,
+    0xa5fed6aau, 0xa9a15ab5u, 0xad583eeau, 0xb123f582u, 0xb504f334u, 0xb8fbaf47u,
+    0xbd08a39fu, 0xc12c4ccau, 0xc5672a11u, 0xc9b9bd86u, 0xce248c15u, 0xd2a81d92u,
+    0xd744fccbu, 0xdbfbb798u, 0xe0ccdeecu, 0xe5b906e7u, 0xeac0c6e8u, 0xefe4b99cu,
+    0xf5257d15u, 0xfa83b2dbu,
 };
-struct Powers {
-    Power at[512];
-};
-constexpr unsigned long long mul62(unsigned long long x, unsigned long long y) {
-    const unsigned long long xh = x >> 32, xl = x & 0xffffffffull, yh = y >> 32,
-                             yl = y & 0xffffffffull;
-    const unsigned long long mid = xh * yl + ((xl * yl) >> 32), mid2 = xl * yh + (mid & 0xffffffffull);
-    const unsigned long long h = xh * yh + (mid >> 32) + (mid2 >> 32), l = mid2 & 0xffffffffull;
-    return (h << 2) | (l >> 30);
-}
-constexpr Powers powers() {
-    // 2^62 * 2^(1/2), 2^(1/4), ..., 2^(1/512)
-    const unsigned long long root[9] = {
-        0x5a827999fcef3242ull, 0x4c1bf828c6dc54b8ull, 0x45cae0f1f545eb73ull,
-        0x42d561b3e6243d8aull, 0x4166c34c5615d0ecull, 0x40b268f9de0183baull,
-        0x4058f6a7ecccd5b6ull, 0x402c6be96af2fb58ull, 0x4016321b687027a8ull};
-    Powers p{};
-    for (int j = 0; j < 512; ++j) {
-        unsigned long long v = 1ull << 62;
-        for (int k = 0; k < 9; ++k)
-            if ((j >> (8 - k)) & 1) v = mul62(v, root[k]);
-        p.at[j].hi = uint32_t(v >> 32);
-        p.at[j].adj = v - (v >> 32) * 0x4b000000ull;
-    }
-    return p;
-}
-__device__ const Powers kPowers = powers();
 
-// How a row's entries become weights 2^60 * 2^((x - m) c - L): c in two floats, L = i + f / 2^30.
+// How a row's entries become weights 2^60 * 2^(x c - K), K = m c + log2 s (about), as
+// 2^((x - m0) c - i - f / 2^30): c in two floats, and m0 = 0, so that x needs no subtraction, or m
+// where m c is large, when x - m is exact for every x near enough to m to have a weight.
 struct RowScale {
-    float m, ch, cl;
+    float m0, ch, cl, alive;  // alive: what (x - m0) c exceeds in an entry with a weight
     int i, f;
 };
 
+// All lanes of a warp call it together; power: the lane's entry of kPowers.
 __device__ __forceinline__ unsigned long long fixed_exp(float x, const RowScale& r,
-                                                        const Power* table) {
+                                                        uint32_t power) {
     constexpr float kMagic = 12582912.f;    // 1.5 * 2^23: adding it rounds to a whole number
-    constexpr int kMagicBits = 0x4b400000;
-    constexpr float kZ = 0.6931471805599453f / 512.f;
-    // d + dl = x - m exactly; t + tl = (x - m) c to 2^-46 of itself
-    const float d = x - r.m;
-    const float xs = d + r.m;
-    const float dl = (x - xs) + ((xs - d) - r.m);
+    constexpr uint32_t kMagicBits = 0x4b400000u;
+    // t + tl = (x - m0) c to 2^-46 of itself, |t| < 2^14
+    const float d = x - r.m0;
     const float t = d * r.ch;
-    const float tl = fmaf(dl, r.ch, fmaf(d, r.cl, fmaf(d, r.ch, -t)));
+    const float tl = fmaf(d, r.cl, fmaf(d, r.ch, -t));
     // whole part and fraction, in 2^-30: each of three terms is rounded to that
     const float whole = t + kMagic;
-    const int s = __float2int_rn((t - (whole - kMagic)) * 0x1p30f) +
-                  (__float_as_int(fmaf(tl, 0x1p30f, kMagic)) - kMagicBits) - r.f;
-    const int N = (__float_as_int(whole) - kMagicBits) - r.i + (s >> 30);
-    // 2^(fraction): the table at its first nine bits, a cubic of the other 21 (off by 2^-43), in
-    // units of 2^-32 as the low bits of 2^23 + ...
-    const float z = __uint_as_float((uint32_t(s) << 2 & 0x7fffffu) | 0x3f800000u) - 1.f;
-    constexpr float a1 = 0x1p32f * kZ, a2 = 0x1p32f * kZ * kZ / 2.f,
-                    a3 = 0x1p32f * kZ * kZ * kZ / 6.f;
-    const float g = fmaf(z, fmaf(z, fmaf(z, a3, a2), a1), 8388608.f);
-    const uint4 e = *reinterpret_cast<const uint4*>(&table[(s >> 21) & 511]);
-    const unsigned long long v =
-        static_cast<unsigned long long>(e.x) * __float_as_uint(g) +
-        ((static_cast<unsigned long long>(e.w) << 32) | e.z);
+    const uint32_t us = uint32_t(__float2int_rn((t - (whole - kMagic)) * 0x1p30f)) +
+                        (uint32_t(__float_as_int(fmaf(tl, 0x1p30f, kMagic))) - kMagicBits) -
+                        uint32_t(r.f);
+    const int s = int(us);
+    const int N = int(uint32_t(__float_as_int(whole)) - kMagicBits - uint32_t(r.i) +
+                      uint32_t(s >> 30));
+    // 2^(fraction): kPowers at its first five bits; of the other 25, z = (s mod 2^25) / 2^30, the
+    // linear term of 2^z - 1 in whole numbers (2^-32) and the rest, at most 2^-12, in fp32, as the
+    // low bits of 2^23 + ...
+    const uint32_t hi = __shfl_sync(~0u, power, s >> 25);
+    const uint32_t z = us << 7;
+    constexpr float kZ = 0.6931471805599453f / 32.f;  // y = 32 z
+    constexpr float b2 = 0x1p32f * kZ * kZ / 2.f, b3 = 0x1p32f * kZ * kZ * kZ / 6.f,
+                    b4 = 0x1p32f * kZ * kZ * kZ * kZ / 24.f;
+    const float y = __uint_as_float((z >> 9) | 0x3f800000u) - 1.f;
+    const float g = fmaf(y * y, fmaf(y, fmaf(y, b4, b3), b2), 8388608.f);
+    const uint32_t G = __umulhi(z, 93032640u) + (__float_as_uint(g) - 0x4b000000u);  // ln 2 * 2^27
     // (t is -inf or NaN where an entry is -inf, or far below the maximum: no weight)
-    return t > -64.f ? v >> min(max(2 - N, 0), 63) : 0ull;
+    const uint32_t w = t > r.alive ? hi + __umulhi(hi, G) : 0u;
+    return (static_cast<unsigned long long>(w) << 32) >> min(uint32_t(3 - N) & 0xffu, 63u);
 }
 
-// 2^60 p_i (1 + e): what a weight is after the correction, e in 2^-46.
-__device__ __forceinline__ unsigned long long corrected(unsigned long long d, unsigned long long p,
-                                                        long long e) {
-    return d + static_cast<unsigned long long>((static_cast<long long>(p >> 28) * e) >> 18);
+// A sum of max(p - q, 0), with p raised by e of itself (e in 2^-46); p: the sum of the upper words
+// of p where p > q.
+__device__ __forceinline__ unsigned long long corrected(unsigned long long d, uint32_t p, int e) {
+    return d + static_cast<unsigned long long>((static_cast<long long>(p) * e) >> 14);
 }
 
 // ------------------------------------------------------------------------ decision and draw
@@ -261,22 +241,30 @@ struct RowStats {
 };
 
 // The parts of a row together, the same in every lane of a warp.
-__device__ __forceinline__ RowStats join_parts(const PartStats* p, int nparts, float c) {
+__device__ __noinline__ RowStats join_parts(const PartStats* p, int nparts, float c) {
     const int lane = threadIdx.x & 31;
-    RowStats r{-INFINITY, 0.f, 0ull};
-    for (int i = lane; i < nparts; i += 32) r.m = fmaxf(r.m, p[i].m);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) r.m = fmaxf(r.m, __shfl_xor_sync(~0u, r.m, off));
-    for (int i = lane; i < nparts; i += 32) {
-        r.s += p[i].m == -INFINITY ? p[i].s : p[i].s * ex2((p[i].m - r.m) * c);
+    // (a lane's first part is kept: for up to 32 parts they are read once)
+    const PartStats none{-INFINITY, 0.f, 0ull}, own = lane < nparts ? p[lane] : none;
+    RowStats r{own.m, 0.f, own.best};
+#pragma unroll 1
+    for (int i = lane + 32; i < nparts; i += 32) {
+        r.m = fmaxf(r.m, p[i].m);
         r.best = p[i].best > r.best ? p[i].best : r.best;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
-        r.s += __shfl_xor_sync(~0u, r.s, off);
+        r.m = fmaxf(r.m, __shfl_xor_sync(~0u, r.m, off));
         const unsigned long long o = __shfl_xor_sync(~0u, r.best, off);
         r.best = o > r.best ? o : r.best;
     }
+    auto scaled = [&](const PartStats& q) {
+        return q.m == -INFINITY ? q.s : q.s * ex2((q.m - r.m) * c);
+    };
+    r.s = scaled(own);
+#pragma unroll 1
+    for (int i = lane + 32; i < nparts; i += 32) r.s += scaled(p[i]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) r.s += __shfl_xor_sync(~0u, r.s, off);
     return r;
 }
 
@@ -284,20 +272,42 @@ __device__ __forceinline__ bool has_distribution(const RowStats& r) {
     return isfinite(r.m) && isfinite(r.s);  // (a NaN or +inf in the row makes s NaN)
 }
 
-__device__ __forceinline__ RowScale scale_of(const RowStats& r, double c) {
+__device__ __noinline__ RowScale scale_of(const RowStats& r, const Rate& c) {
     RowScale k;
-    k.m = r.m;
-    k.ch = float(c);
-    k.cl = float(c - double(k.ch));
-    const float L = log2f(r.s), i = rintf(L);
-    k.i = int(i);
-    k.f = __float2int_rn((L - i) * 0x1p30f);
+    k.ch = c.hi;
+    k.cl = c.lo;
+    k.m0 = fabsf(r.m) * c.hi < 8192.f ? 0.f : r.m;
+    const float d = r.m - k.m0, t = d * c.hi, tl = fmaf(d, c.lo, fmaf(d, c.hi, -t));
+    const float L = log2f(r.s), i = rintf(L), whole = rintf(t);
+    const int f = __float2int_rn((t - whole) * 0x1p30f) + __float2int_rn(tl * 0x1p30f) +
+                  __float2int_rn((L - i) * 0x1p30f);
+    k.i = int(whole) + int(i) + (f >> 30);
+    k.f = f & 0x3fffffff;
+    k.alive = float(k.i - 62);
     return k;
 }
 
-// log p of an entry: (x - m) c is formed in fp64, once per emitted token.
-__device__ __forceinline__ float logp_of(float x, const RowStats& r, double c) {
-    return float((double(x) - double(r.m)) * c * 0.6931471805599453 - double(logf(r.s)));
+// (x - m) c in two floats.
+__device__ __forceinline__ float2 exponent_of(float x, const RowStats& r, const Rate& c) {
+    const float d = x - r.m, xs = d + r.m, dl = (x - xs) + ((xs - d) - r.m), t = d * c.hi;
+    return make_float2(t, fmaf(dl, c.hi, fmaf(d, c.lo, fmaf(d, c.hi, -t))));
+}
+
+// (not inlined: it stands at several places of a kernel that runs from a cold cache)
+__device__ __noinline__ float logp_of(float x, const RowStats& r, const Rate& c) {
+    const float2 t = exponent_of(x, r, c);
+    return fmaf(t.x, kLn2, t.y * kLn2) - logf(r.s);
+}
+
+// floor(u * Z) for 0 <= u < 1.
+__device__ __forceinline__ unsigned long long share_of(float u, unsigned long long Z) {
+    const uint32_t bits = __float_as_uint(u);
+    const int e = int(bits >> 23);
+    const unsigned long long m = e ? (bits & 0x7fffffu) | 0x800000u : bits;  // u = m / 2^(150 - e)
+    const int shift = 150 - max(e, 1);                                       // 24 .. 149
+    const unsigned long long lo = m * Z, hi = __umul64hi(m, Z);
+    return shift >= 128 ? 0ull : shift >= 64 ? hi >> (shift - 64)
+                                             : (hi << (64 - shift)) | (lo >> shift);
 }
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
@@ -316,38 +326,45 @@ __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v) { 
 }
 
 struct Sums {
-    unsigned long long d, p;  // of max(p - q, 0), and of p where p > q
+    unsigned long long d;  // of max(p - q, 0)
+    uint32_t p;            // of p's upper words where p > q
 };
 
 template <int DT>
 __global__ void __launch_bounds__(kThreads)
 draft_draw_kernel(const DraftArgs a, int ctas) {
-    constexpr int kWarps = kThreads / 32;
-    __shared__ __align__(16) Power table[512];
-    __shared__ Sums block_sums[kMaxBlocks / kMaxCtas];
-    __shared__ unsigned long long warp_sums[kWarps][4];
-    __shared__ unsigned long long cta_sums[kMaxCtas][4];  // every CTA's: p, q, d, p where p > q
-    __shared__ int first_refused;
+    constexpr int kWarps = kThreads / 32, kGroups = kBlock / 32;
+    constexpr int kAtOnce = 4, kSteps = kGroups / kAtOnce;  // entries of a block per lane
+    __shared__ Sums block_sums[kMaxBlocks];
+    __shared__ unsigned long long warp_sums[kWarps][3];
+    __shared__ unsigned long long cta_sums[kMaxCtas][3];  // every CTA's: p - q, and Sums
+    __shared__ RowStats last[2];                          // of the row that ends the block: p, q
+    __shared__ int first_refused, the_block;
+    __shared__ Sums the_start;
+    __shared__ unsigned long long weights[kGroups][32], group_sums[kGroups];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int b = int(blockIdx.x / unsigned(ctas)), rank = int(blockIdx.x - unsigned(b) * ctas);
-    for (int i = tid; i < 512; i += kThreads)
-        *reinterpret_cast<uint4*>(&table[i]) = *reinterpret_cast<const uint4*>(&kPowers.at[i]);
+    const uint32_t power = kPowers[lane];
     if (tid == 0) first_refused = 0x7fffffff;
     pdl_wait();
     pdl_trigger();
     // the offsets of the whole batch: a call with malformed ones decides nothing
     bool bad = tid == 0 && (a.cu_q[0] != 0 || a.cu_q[a.B] > a.total_q ||
                             a.cu_q[a.B] - a.B > a.num_drafts);
+#pragma unroll 1
     for (int i = tid; i < a.B; i += kThreads) {
         const int w = int(uint32_t(a.cu_q[i + 1]) - uint32_t(a.cu_q[i]));
         bad |= w < 1 || w > a.max_q || a.cu_q[i] < 0;
     }
+    const float T0 = temperature_of(a, b);
+    const int t0 = a.cu_q[b], drafts = a.cu_q[b + 1] - t0 - 1;
     bad = __syncthreads_or(bad) != 0;
-    const float T = bad ? kNaN : temperature_of(a, b);
+    const float T = bad ? kNaN : T0;
     int32_t* out = a.tokens + int64_t(b) * a.max_q;
     float* out_logp = a.logprobs ? a.logprobs + int64_t(b) * a.max_q : nullptr;
     if (isnan(T)) {
         if (rank == 0) {
+#pragma unroll 1
             for (int j = tid; j < a.max_q; j += kThreads) {
                 out[j] = -1;
                 if (out_logp) out_logp[j] = 0.f;
@@ -360,73 +377,78 @@ draft_draw_kernel(const DraftArgs a, int ctas) {
         return;
     }
     const bool greedy = T == 0.f;
-    const double c = greedy ? 1.4426950408889634 : 1.4426950408889634 / double(T);
-    const int t0 = a.cu_q[b], drafts = a.cu_q[b + 1] - t0 - 1;
+    const Rate c = rate_of(T);
     const int d0 = t0 - b;                  // the sequence's first draft
-    auto target = [&](int j) {
-        return join_parts(a.parts + int64_t(t0 + j) * a.nparts, a.nparts, float(c));
-    };
-    auto drafted = [&](int j) {
-        return join_parts(a.parts + (int64_t(a.total_q) + d0 + j) * a.nparts, a.nparts, float(c));
-    };
-    const int64_t xs = kSize<DT>;
+    const int64_t es = kSize<DT>;
     auto target_row = [&](int j) {
-        return static_cast<const char*>(a.x) + int64_t(t0 + j) * a.ldx * xs;
+        return static_cast<const char*>(a.x) + int64_t(t0 + j) * a.ldx * es;
     };
     auto draft_row = [&](int j) {
-        return static_cast<const char*>(a.y) + int64_t(d0 + j) * a.ldy * xs;
+        return static_cast<const char*>(a.y) + int64_t(d0 + j) * a.ldy * es;
     };
 
-    // a warp per draft; the row of a warp's lanes is the same
-    for (int j = warp; j < drafts; j += kWarps) {
-        const RowStats p = target(j);
-        const int token = a.draft_tokens[d0 + j];
+    // a warp per draft, and one for the row behind the last; a warp stops at its first refusal,
+    // since no later row of its own ends the block
+    RowStats P{0.f, 1.f, 0ull}, Q{0.f, 1.f, 0ull};
+    int mine = -1;
+#pragma unroll 1
+    for (int j = warp; j <= drafts && mine < 0; j += kWarps) {
+        const int token = j < drafts ? a.draft_tokens[d0 + j] : -1;
+        const bool inside = token >= 0 && token < a.n;
+        const bool with_q = inside && a.y && !greedy;
+        float x = 0.f, y = 0.f, u = 0.f;
+        if (inside) x = load1<DT>(target_row(j), token);
+        if (with_q) y = load1<DT>(draft_row(j), token);
+        if (inside) u = a.uniforms[t0 + j];
+        P = join_parts(a.parts + int64_t(t0 + j) * a.nparts, a.nparts, c.hi);
+        if (with_q)
+            Q = join_parts(a.parts + (int64_t(a.total_q) + d0 + j) * a.nparts, a.nparts, c.hi);
         bool take = false;
-        float x = 0.f;
-        if (token >= 0 && token < a.n) {
-            x = load1<DT>(target_row(j), token);
-            if (greedy) {
-                take = p.best != 0ull && 0x7fffffff - int(uint32_t(p.best)) == token;
-            } else if (has_distribution(p) && x != -INFINITY) {
-                // u 2^tq / sq < 2^tp / sp
-                double t = -(double(x) - double(p.m)) * c;
-                float sq = 1.f;
-                bool fine = true;
-                if (a.y) {
-                    const RowStats q = drafted(j);
-                    fine = has_distribution(q);
-                    sq = q.s;
-                    t += (double(load1<DT>(draft_row(j), token)) - double(q.m)) * c;
-                }
-                const float th = float(t);
-                const float e =
-                    isfinite(th) ? exp2f(th) * fmaf(float(t - double(th)), kLn2, 1.f) : exp2f(th);
-                const float u = a.uniforms[t0 + j];
-                take = fine && (u == 0.f || double(u) * double(e) * double(p.s) < double(sq));
+        if (inside && greedy) {
+            take = 0x7fffffff - int(uint32_t(P.best)) == token;
+        } else if (inside && has_distribution(P) && x != -INFINITY) {
+            // u 2^tq / sq < 2^tp / sp
+            const float2 tp = exponent_of(x, P, c);
+            float2 tq = make_float2(0.f, 0.f);
+            bool fine = true;
+            if (with_q) {
+                fine = has_distribution(Q);
+                tq = exponent_of(y, Q, c);
             }
-        } else if (token != -1 && lane == 0 && rank == 0) {
+            const float t = tq.x - tp.x, back = t + tp.x;
+            const float tl = ((tq.x - back) + ((back - t) - tp.x)) + (tq.y - tp.y);
+            const float e = exp2f(t) * (isfinite(t) ? fmaf(tl, kLn2, 1.f) : 1.f);
+            take = fine && (u == 0.f || u * e * P.s < (with_q ? Q.s : 1.f));
+        } else if (!inside && token != -1 && lane == 0 && rank == 0) {
             latch_error(a.err, kErrDeviceArg);
         }
-        if (lane == 0) {
-            if (!take) atomicMin(&first_refused, j);
-            if (rank == 0 && take) {
-                out[j] = token;
-                if (out_logp) out_logp[j] = logp_of(x, p, c);
-            }
+        if (!take) {
+            mine = j;
+            if (lane == 0) atomicMin(&first_refused, j);
+        } else if (rank == 0 && lane == 0) {
+            out[j] = token;
+            if (out_logp) out_logp[j] = logp_of(x, P, c);
         }
     }
     __syncthreads();
-    const int kept = min(drafts, first_refused);
+    const int kept = first_refused;         // (at most `drafts`)
+    if (mine == kept && lane == 0) {
+        last[0] = P;
+        last[1] = Q;
+    }
     const int refused = kept < drafts ? a.draft_tokens[d0 + kept] : -1;  // -1: drawn from p
     const bool behind = refused >= 0 && refused < a.n;
+    const float u_last = a.uniforms[t0 + drafts];
     if (rank == 0) {
+#pragma unroll 1
         for (int j = kept + 1 + tid; j < a.max_q; j += kThreads) {
             out[j] = -1;
             if (out_logp) out_logp[j] = 0.f;
         }
         if (tid == 0) a.accepted[b] = kept;
     }
-    const RowStats P = target(kept);
+    __syncthreads();
+    P = last[0];
     const char* xr = target_row(kept);
     auto emit = [&](int token) {
         out[kept] = token;
@@ -437,8 +459,7 @@ draft_draw_kernel(const DraftArgs a, int ctas) {
         return;
     }
     bool both = behind && a.y;              // subtract the draft's probabilities
-    RowStats Q{0.f, 1.f, 0ull};
-    if (both) Q = drafted(kept);
+    Q = last[1];
     if (!has_distribution(P) || (both && !has_distribution(Q))) {
         if (rank == 0 && tid == 0) emit(-1);
         return;
@@ -447,144 +468,188 @@ draft_draw_kernel(const DraftArgs a, int ctas) {
     const char* yr = both ? draft_row(kept) : nullptr;
     const RowScale kp = scale_of(P, c), kq = both ? scale_of(Q, c) : kp;
     const int blocks = (a.n + kBlock - 1) / kBlock;
-    const int k0 = int(int64_t(rank) * blocks / ctas), k1 = int(int64_t(rank + 1) * blocks / ctas);
+    // (at most 2^11 blocks and 8 CTAs)
+    const int k0 = rank * blocks / ctas, k1 = (rank + 1) * blocks / ctas;
 
     if (ctas > 1) cluster_sync_all();       // (the others have started)
     unsigned long long Z = 0;
-    long long e = 0;
+    int e = 0;
     Sums before{0, 0};                      // of the CTAs in front of the one that holds the share
     int holder = 0;
     unsigned long long share = 0;
     for (;;) {
-        unsigned long long sp = 0, sq = 0, sd = 0, sdp = 0;
+        unsigned long long diff = 0, sd = 0;
+        uint32_t sp = 0;
+        // (rolled loops: the code runs from a cold instruction cache, and unrolled over a block
+        // it was 180 KB, which took longer to fetch than to run)
         auto pass = [&](auto subtracts) {
             constexpr bool BOTH = decltype(subtracts)::value;
-            for (int k = k0 + warp; k < k1; k += kWarps) {
-                Sums s{0, 0};
+            float x[kAtOnce], y[kAtOnce];
+            auto fetch = [&](int it) {
+                const int i0 = (k0 + warp + it / kSteps * kWarps) * kBlock +
+                               it % kSteps * (kAtOnce * 32) + lane;
+                if (i0 - lane + kAtOnce * 32 <= a.n) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x[8], y[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const int i = k * kBlock + (8 * h + q) * 32 + lane;
-                        x[q] = i < a.n && i != without ? load1<DT>(xr, i) : -INFINITY;
-                        if (BOTH) y[q] = i < a.n ? load1<DT>(yr, i) : -INFINITY;
+                    for (int q = 0; q < kAtOnce; ++q) {
+                        x[q] = load1<DT>(xr, i0 + q * 32);
+                        if (BOTH) y[q] = load1<DT>(yr, i0 + q * 32);
                     }
+                } else {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const unsigned long long p = fixed_exp(x[q], kp, table);
-                        if (BOTH) {
-                            const unsigned long long w = fixed_exp(y[q], kq, table);
-                            sp += p;
-                            sq += w;
-                            if (p > w) {
-                                s.d += p - w;
-                                s.p += p;
-                            }
-                        } else {
-                            s.d += p;
-                        }
+                    for (int q = 0; q < kAtOnce; ++q) {
+                        const bool in = i0 + q * 32 < a.n;
+                        x[q] = in ? load1<DT>(xr, i0 + q * 32) : -INFINITY;
+                        if (BOTH) y[q] = in ? load1<DT>(yr, i0 + q * 32) : -INFINITY;
                     }
                 }
-                s.d = warp_sum(s.d);
-                if (BOTH) s.p = warp_sum(s.p);
-                if (lane == 0) block_sums[k - k0] = s;
-                sd += s.d;
-                sdp += s.p;
+            };
+            const int its = (max(0, k1 - k0 - warp) + kWarps - 1) / kWarps * kSteps;
+            if (its > 0) fetch(0);
+            Sums s{0, 0};
+#pragma unroll 1
+            for (int it = 0; it < its; ++it) {
+                float xn[kAtOnce], yn[kAtOnce];
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q) {
+                    xn[q] = x[q];
+                    if (BOTH) yn[q] = y[q];
+                }
+                if (it + 1 < its) fetch(it + 1);
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q) {
+                    const unsigned long long p = fixed_exp(xn[q], kp, power);
+                    if (BOTH) {
+                        const unsigned long long over = p - fixed_exp(yn[q], kq, power);
+                        diff += over;
+                        if (static_cast<long long>(over) > 0) {
+                            s.d += over;
+                            s.p += uint32_t(p >> 32);
+                        }
+                    } else {
+                        s.d += p;
+                    }
+                }
+                if (it % kSteps == kSteps - 1) {
+                    const int k = warp + it / kSteps * kWarps;
+                    s.d = warp_sum(s.d);
+                    if (BOTH) s.p = __reduce_add_sync(~0u, s.p);
+                    if (!BOTH && without >= 0 && without / kBlock == k0 + k)
+                        s.d -= fixed_exp(load1<DT>(xr, without), kp, power);
+                    if (lane == 0) block_sums[k] = s;
+                    sd += s.d;
+                    sp += s.p;
+                    s = Sums{0, 0};
+                }
             }
-            if (BOTH) {
-                sp = warp_sum(sp);
-                sq = warp_sum(sq);
-            }
+            if (BOTH) diff = warp_sum(diff);
         };
         if (both) pass(std::true_type()); else pass(std::false_type());
         if (lane == 0) {
-            warp_sums[warp][0] = sp;
-            warp_sums[warp][1] = sq;
-            warp_sums[warp][2] = sd;
-            warp_sums[warp][3] = sdp;
+            warp_sums[warp][0] = diff;
+            warp_sums[warp][1] = sd;
+            warp_sums[warp][2] = sp;
         }
         __syncthreads();
-        if (tid < 4) {
+        if (tid < 4 * ctas && (tid & 3) < 3) {  // a thread per sum and CTA to tell it to
+            const int i = tid & 3, to = tid >> 2;
             unsigned long long v = 0;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) v += warp_sums[w][tid];
-            cta_sums[rank][tid] = v;
-            for (int r = 0; r < ctas; ++r)
-                if (r != rank) st_cluster_b64(cluster_map(smem_addr(&cta_sums[rank][tid]), r), v);
+            for (int w = 0; w < kWarps; ++w) v += warp_sums[w][i];
+            if (to == rank)
+                cta_sums[rank][i] = v;
+            else
+                st_cluster_b64(cluster_map(smem_addr(&cta_sums[rank][i]), to), v);
         }
         if (ctas > 1) cluster_sync_all(); else __syncthreads();
         // every thread of the cluster comes to the same numbers
-        unsigned long long all[4] = {0, 0, 0, 0};
+        unsigned long long all[3] = {0, 0, 0};
+#pragma unroll 1
         for (int r = 0; r < ctas; ++r)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) all[i] += cta_sums[r][i];
-        e = both ? __double2ll_rn((double(all[1]) / double(all[0]) - 1.0) * 0x1p46) : 0;
-        e = max(-(1ll << 30), min(1ll << 30, e));
-        Z = corrected(all[2], all[3], e);
-        if (static_cast<long long>(Z) <= 0) {
-            if (!both && without < 0) break;  // (p has a sum near 2^60: not reached)
-            // nothing is left of p: the two distributions are one.  Drawn from p.
-            both = false;
-            without = -1;
-            if (ctas > 1) cluster_sync_all(); else __syncthreads();
-            continue;
-        }
-        const float u = a.uniforms[t0 + drafts];
-        const double part = double(u >= 0.f ? fminf(u, 0.99999994f) : 0.f) * double(Z);
-        share = min(static_cast<unsigned long long>(part), Z - 1);
-        // the first CTA whose sums reach past the share
-        for (holder = 0; holder < ctas - 1; ++holder) {
-            const Sums next{before.d + cta_sums[holder][2], before.p + cta_sums[holder][3]};
-            const unsigned long long F = corrected(next.d, next.p, e);
-            if (static_cast<long long>(F) > static_cast<long long>(share)) break;
-            before = next;
-        }
-        break;
+            for (int i = 0; i < 3; ++i) all[i] += cta_sums[r][i];
+        // e = sum (q - p) / 2^60, in 2^-46
+        if (both)
+            e = int(max(-(1ll << 30), min(1ll << 30, -static_cast<long long>(all[0]) >> 14)));
+        Z = corrected(all[1], uint32_t(all[2]), e);
+        if (static_cast<long long>(Z) > 0) break;
+        if (!both && without < 0) break;    // (p has a sum near 2^60: not reached)
+        // nothing is left of p: the two distributions are one.  Drawn from p.
+        both = false;
+        without = -1;
+        e = 0;
+        if (ctas > 1) cluster_sync_all(); else __syncthreads();
     }
-    if (rank != holder || warp != 0) return;
+    share = min(share_of(u_last >= 0.f ? fminf(u_last, 0.99999994f) : 0.f, Z), Z - 1);
+    // the first CTA whose sums reach past the share
+#pragma unroll 1
+    for (holder = 0; holder < ctas - 1; ++holder) {
+        const Sums next{before.d + cta_sums[holder][1],
+                        before.p + uint32_t(cta_sums[holder][2])};
+        if (static_cast<long long>(corrected(next.d, next.p, e)) > static_cast<long long>(share))
+            break;
+        before = next;
+    }
+    if (rank != holder) return;
 
     // the first block that does (a warp's lanes take 32 blocks at a time)
-    int block = k1 - 1;
-    for (int k = k0; k < k1; k += 32) {
-        const Sums s = k + lane < k1 ? block_sums[k - k0 + lane] : Sums{0, 0};
-        const Sums to{before.d + warp_scan(s.d), before.p + warp_scan(s.p)};
-        const bool past = k + lane < k1 && static_cast<long long>(corrected(to.d, to.p, e)) >
-                                               static_cast<long long>(share);
-        const uint32_t who = __ballot_sync(~0u, past);
-        const int at = who ? __ffs(who) - 1 : 31;
-        if (who || k + 32 >= k1) {
-            const int last = who ? at : min(31, k1 - 1 - k);
-            block = k + last;
-            before.d = __shfl_sync(~0u, to.d - s.d, last);
-            before.p = __shfl_sync(~0u, to.p - s.p, last);
-            break;
+    if (warp == 0) {
+        int block = k1 - 1;
+#pragma unroll 1
+        for (int k = k0; k < k1; k += 32) {
+            const Sums s = k + lane < k1 ? block_sums[k - k0 + lane] : Sums{0, 0};
+            const Sums to{before.d + warp_scan(s.d), before.p + uint32_t(warp_scan(s.p))};
+            const bool past = k + lane < k1 && static_cast<long long>(corrected(to.d, to.p, e)) >
+                                                   static_cast<long long>(share);
+            const uint32_t who = __ballot_sync(~0u, past);
+            if (who || k + 32 >= k1) {
+                const int at = who ? __ffs(who) - 1 : min(31, k1 - 1 - k);
+                block = k + at;
+                before.d = __shfl_sync(~0u, to.d - s.d, at);
+                before.p = __shfl_sync(~0u, to.p - s.p, at);
+                break;
+            }
+            before.d = __shfl_sync(~0u, to.d, 31);
+            before.p = __shfl_sync(~0u, to.p, 31);
         }
-        before.d = __shfl_sync(~0u, to.d, 31);
-        before.p = __shfl_sync(~0u, to.p, 31);
-    }
-    // ... and its first entry (the last one with a weight, should the sums of rounded
-    // corrections end below the share)
-    long long sum = static_cast<long long>(corrected(before.d, before.p, e));
-    int token = -1;
-    for (int q = 0; q < kBlock / 32; ++q) {
-        const int i = block * kBlock + q * 32 + lane;
-        long long w = 0;
-        if (i < a.n && i != without) {
-            const unsigned long long p = fixed_exp(load1<DT>(xr, i), kp, table);
-            w = static_cast<long long>(corrected(p, p, e));
-            if (both) w -= static_cast<long long>(fixed_exp(load1<DT>(yr, i), kq, table));
-            w = max(w, 0ll);
+        if (lane == 0) {
+            the_block = block;
+            the_start = before;
         }
-        const long long to =
-            sum + static_cast<long long>(warp_scan(static_cast<unsigned long long>(w)));
-        const uint32_t some = __ballot_sync(~0u, w > 0);
-        const uint32_t past = __ballot_sync(~0u, w > 0 && to > static_cast<long long>(share));
-        if (some) token = block * kBlock + q * 32 + (past ? __ffs(past) - 1 : 31 - __clz(some));
-        if (past) break;
-        sum = __shfl_sync(~0u, to, 31);
     }
-    if (lane == 0) emit(token);
+    __syncthreads();
+    // ... its entries' weights, 32 at a time
+#pragma unroll 1
+    for (int g = warp; g < kGroups; g += kWarps) {
+        const int i = the_block * kBlock + g * 32 + lane;
+        const float x = i < a.n && i != without ? load1<DT>(xr, i) : -INFINITY;
+        const float y = both && i < a.n ? load1<DT>(yr, i) : -INFINITY;
+        const unsigned long long p = fixed_exp(x, kp, power);
+        long long w = static_cast<long long>(corrected(p, uint32_t(p >> 32), e));
+        if (both) w = max(0ll, w - static_cast<long long>(fixed_exp(y, kq, power)));
+        weights[g][lane] = static_cast<unsigned long long>(w);
+        const unsigned long long s = warp_sum(static_cast<unsigned long long>(w));
+        if (lane == 0) group_sums[g] = s;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    // ... and the first that reaches past the share (the last one with a weight, should the sums
+    // of rounded corrections end below it).  (The sum in front may be below 0 by such roundings.)
+    const long long over = static_cast<long long>(share) -
+                           static_cast<long long>(corrected(the_start.d, the_start.p, e));
+    const unsigned long long s = lane < kGroups ? group_sums[lane] : 0ull, to = warp_scan(s);
+    uint32_t who = __ballot_sync(~0u, s > 0 && static_cast<long long>(to) > over);
+    const uint32_t any = __ballot_sync(~0u, s > 0);
+    if (!any) {  // (not reached: a block is chosen for its sum)
+        if (lane == 0) emit(-1);
+        return;
+    }
+    const int g = who ? __ffs(who) - 1 : 31 - __clz(any);
+    const unsigned long long w = weights[g][lane];
+    const long long reach = static_cast<long long>(__shfl_sync(~0u, to - s, g) + warp_scan(w));
+    who = __ballot_sync(~0u, w > 0 && reach > over);
+    const uint32_t some = __ballot_sync(~0u, w > 0);
+    if (lane == 0)
+        emit(the_block * kBlock + g * 32 + (who ? __ffs(who) - 1 : 31 - __clz(some)));
 }
 
 // ------------------------------------------------------------------------ host side
@@ -609,19 +674,33 @@ constexpr int64_t kI32Max = 0x7fffffffLL;
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 template <int DT>
-cudaError_t launch(DraftArgs& a, bool rows_aligned, cudaStream_t stream) {
+cudaError_t launch(const DeviceInfo& dev, DraftArgs& a, bool rows_aligned, cudaStream_t stream) {
     a.nparts = (a.n + kPartLen<DT> - 1) / kPartLen<DT>;
-    const int64_t rows = int64_t(a.total_q) + (a.y ? a.num_drafts : 0);
-    if (rows * a.nparts > kI32Max) return cudaErrorNotSupported;
+    const int64_t items = (int64_t(a.total_q) + (a.y ? a.num_drafts : 0)) * a.nparts;
+    if (items > kI32Max) return cudaErrorNotSupported;
+    a.items = int(items);
     auto stats = rows_aligned ? draft_stats_kernel<DT, true> : draft_stats_kernel<DT, false>;
-    cudaError_t e = launch_pdl(stats, dim3(unsigned(rows * a.nparts)), dim3(kThreads), 0, stream, a);
+    const int64_t grid = (items + kStats / 32 - 1) / (kStats / 32);
+    cudaError_t e = launch_pdl(stats, dim3(unsigned(grid)), dim3(kStats), 0, stream, a);
     if (e != cudaSuccess) return e;
-    // eight blocks (one for each warp) are worth a CTA
+    // CTAs of a sequence: one for every eight blocks (a block for each warp), while the
+    // multiprocessors hold them all at once (three each).  The batch is spread over them: left to
+    // itself the hardware puts the clusters of a small one on half of them.
     const int blocks = (a.n + kBlock - 1) / kBlock;
-    int ctas = 1;
-    while (ctas < kMaxCtas && blocks > ctas * 8) ctas *= 2;
-    return launch_pdl_cluster(draft_draw_kernel<DT>, dim3(unsigned(a.B) * unsigned(ctas)),
-                              dim3(kThreads), 0, stream, unsigned(ctas), a, ctas);
+    const int64_t sms = dev.num_sms;
+    const int ctas = int(std::max<int64_t>(
+        1, std::min<int64_t>({int64_t(kMaxCtas), (blocks + 7) / 8, 3 * sms / a.B})));
+    const int64_t total = int64_t(a.B) * ctas;
+    const size_t apart = total <= sms ? 120 * 1024 : total <= 2 * sms ? 48 * 1024 : 0;
+    auto draw = draft_draw_kernel<DT>;
+    static bool attr_done[64] = {};
+    if (dev.device >= 0 && dev.device < 64 && !attr_done[dev.device]) {
+        e = cudaFuncSetAttribute(draw, cudaFuncAttributeMaxDynamicSharedMemorySize, 120 * 1024);
+        if (e != cudaSuccess) return e;
+        attr_done[dev.device] = true;
+    }
+    return launch_pdl_cluster(draw, dim3(unsigned(total)), dim3(kThreads), apart, stream,
+                              unsigned(ctas), a, ctas);
 }
 
 }  // namespace
@@ -702,9 +781,9 @@ BI_EXPORT bi_status bi_verify_drafts(const void* logits, int64_t ldl, const void
     const bool al = aligned(logits, 16) && ldl * int64_t(es) % 16 == 0 &&
                     (!a.y || (aligned(a.y, 16) && ldd * int64_t(es) % 16 == 0));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = dtype == BI_F32   ? launch<BI_F32>(a, al, st)
-                    : dtype == BI_F16 ? launch<BI_F16>(a, al, st)
-                                      : launch<BI_BF16>(a, al, st);
+    cudaError_t e = dtype == BI_F32   ? launch<BI_F32>(*dev, a, al, st)
+                    : dtype == BI_F16 ? launch<BI_F16>(*dev, a, al, st)
+                                      : launch<BI_BF16>(*dev, a, al, st);
     if (e == cudaErrorNotSupported) return fail(BI_ERR_UNSUPPORTED, "%s: too many rows", fn);
     return launched(e, fn);
 }
