@@ -392,11 +392,57 @@ def _shape(softcap, slopes, window, first_key, hq, T):
     for name, t, dtype, n in (("slopes", slopes, torch.float32, hq),
                               ("first_key", first_key, torch.int32, T)):
         if t is not None:
-            _need(t, dtype, name, 1)
-            _on_current_device(**{name: t})
-            if t.shape[0] != n or not t.is_contiguous():
+            if not _all(_device_of(t), (t, dtype, 1)) or t.shape[0] != n:
+                _need(t, dtype, name, 1)
+                _on_current_device(**{name: t})
                 raise ValueError(f"{name} must be a contiguous [{n}] tensor")
-    return float(softcap), _ptr(slopes), int(window), _ptr(first_key)
+    return softcap, _ptr(slopes), window, _ptr(first_key)
+
+
+def _attend(fn, q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q, max_seq_len, scale, out,
+            lse, want_lse, workspace, stream, softcap, slopes, window, first_key):
+    torch = _torch()
+    bf16, i32 = torch.bfloat16, torch.int32
+    decode = fn == "bi_decode_attn"
+    dev = _device_of(q)
+    if not (_all(dev, (q, bf16, 3), (k_cache, bf16, 4), (v_cache, bf16, 4), (block_table, i32, 2),
+                 (seq_lens, i32, 1)) and (decode or _all(dev, (cu_q, i32, 1)))
+            and k_cache.shape == v_cache.shape):
+        _paged_common(k_cache, v_cache, block_table, seq_lens)
+        _need(q, bf16, "q", 3)
+        if not decode:
+            _need(cu_q, i32, "cu_q", 1)
+        if not q.is_contiguous() or not (decode or cu_q.is_contiguous()):
+            raise ValueError("q must be contiguous" if decode else "q and cu_q must be contiguous")
+    num_pages, hkv, page, d = k_cache.shape
+    T, hq, dq = q.shape
+    shape = _shape(softcap, slopes, window, first_key, hq, T)
+    if out is not None or lse is not None:
+        _attn_out(q, q if out is None else out, lse, False)  # (checks what the caller gave)
+    with _allocating_for(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None and want_lse:
+            lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            ws_bytes = max(16, lib().bi_attn_workspace_size(T, hq, d, max_seq_len))
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        else:
+            ws_bytes = workspace.numel() * workspace.element_size()
+    batch, max_pages = seq_lens.shape[0], block_table.shape[1]
+    sizes = (batch,) if decode else (cu_q.data_ptr(), batch, T, max_q)
+    head = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), num_pages,
+            block_table.data_ptr(), max_pages, seq_lens.data_ptr(), *sizes, max_seq_len, hq, hkv,
+            d, page, scale)
+    tail = (out.data_ptr(), _ptr(lse), workspace.data_ptr(), ws_bytes,
+            _stream_on(stream, dev) if dev >= 0 else _stream(stream))
+    if shape is None:
+        _check(getattr(lib(), fn)(*head, *tail))
+    else:
+        if dq != d:
+            raise ValueError("q must have the cache's D")
+        _check(getattr(lib(), fn + "_ex")(*head, *shape, *tail))
+    return out, lse
 
 
 def verify_block(q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q: int, max_seq_len: int,
@@ -405,25 +451,9 @@ def verify_block(q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q: int, m
     """Causal attention of each sequence's new block (q bf16 [T,Hq,D]) over its paged cache.
     softcap, slopes (fp32 [Hq]), window and first_key (int32 [T]) shape the scores before the
     softmax and limit the keys that a token sees (include/bi.h, Shaped scores)."""
-    torch = _torch()
-    num_pages, hkv, page, d = _paged_common(k_cache, v_cache, block_table, seq_lens)
-    _need(q, torch.bfloat16, "q", 3)
-    _need(cu_q, torch.int32, "cu_q", 1)
-    if not q.is_contiguous() or not cu_q.is_contiguous():
-        raise ValueError("q and cu_q must be contiguous")
-    T, hq, _ = q.shape
-    out, lse = _attn_out(q, out, lse, want_lse)
-    ws, ws_bytes = _workspace(workspace, attn_workspace_size(T, hq, d, max_seq_len), q.device)
-    shape = _shape(softcap, slopes, window, first_key, hq, T)
-    head = (_ptr(q), _ptr(k_cache), _ptr(v_cache), num_pages, _ptr(block_table),
-            block_table.shape[1], _ptr(seq_lens), _ptr(cu_q), seq_lens.shape[0], T, int(max_q),
-            int(max_seq_len), hq, hkv, d, page, float(scale))
-    tail = (_ptr(out), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream))
-    if shape is None:
-        _check(lib().bi_verify_block(*head, *tail))
-    else:
-        _check(lib().bi_verify_block_ex(*head, *shape, *tail))
-    return out, lse
+    return _attend("bi_verify_block", q, k_cache, v_cache, block_table, seq_lens, cu_q, int(max_q),
+                   int(max_seq_len), float(scale), out, lse, want_lse, workspace, stream,
+                   float(softcap), slopes, int(window), first_key)
 
 
 def prefill_attn(q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q: int, max_seq_len: int,
@@ -431,25 +461,9 @@ def prefill_attn(q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q: int, m
                  softcap: float = 0.0, slopes=None, window: int = 0, first_key=None):
     """verify_block for blocks of any width (chunked prefill, prefix caching): every query
     reduced exactly as verify_block / decode_attn reduce it, shaped scores included."""
-    torch = _torch()
-    num_pages, hkv, page, d = _paged_common(k_cache, v_cache, block_table, seq_lens)
-    _need(q, torch.bfloat16, "q", 3)
-    _need(cu_q, torch.int32, "cu_q", 1)
-    if not q.is_contiguous() or not cu_q.is_contiguous():
-        raise ValueError("q and cu_q must be contiguous")
-    T, hq, _ = q.shape
-    out, lse = _attn_out(q, out, lse, want_lse)
-    ws, ws_bytes = _workspace(workspace, attn_workspace_size(T, hq, d, max_seq_len), q.device)
-    shape = _shape(softcap, slopes, window, first_key, hq, T)
-    head = (_ptr(q), _ptr(k_cache), _ptr(v_cache), num_pages, _ptr(block_table),
-            block_table.shape[1], _ptr(seq_lens), _ptr(cu_q), seq_lens.shape[0], T, int(max_q),
-            int(max_seq_len), hq, hkv, d, page, float(scale))
-    tail = (_ptr(out), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream))
-    if shape is None:
-        _check(lib().bi_prefill_attn(*head, *tail))
-    else:
-        _check(lib().bi_prefill_attn_ex(*head, *shape, *tail))
-    return out, lse
+    return _attend("bi_prefill_attn", q, k_cache, v_cache, block_table, seq_lens, cu_q, int(max_q),
+                   int(max_seq_len), float(scale), out, lse, want_lse, workspace, stream,
+                   float(softcap), slopes, int(window), first_key)
 
 
 def verify_block_static_ws(q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q: int,
@@ -479,24 +493,9 @@ def decode_attn(q, k_cache, v_cache, block_table, seq_lens, max_seq_len: int, sc
                 softcap: float = 0.0, slopes=None, window: int = 0, first_key=None):
     """One new token per sequence: q bf16 [B,Hq,D]; token b is the last position of b.
     Shaped scores as in verify_block (first_key int32 [B])."""
-    torch = _torch()
-    num_pages, hkv, page, d = _paged_common(k_cache, v_cache, block_table, seq_lens)
-    _need(q, torch.bfloat16, "q", 3)
-    if not q.is_contiguous():
-        raise ValueError("q must be contiguous")
-    B, hq, _ = q.shape
-    out, lse = _attn_out(q, out, lse, want_lse)
-    ws, ws_bytes = _workspace(workspace, attn_workspace_size(B, hq, d, max_seq_len), q.device)
-    shape = _shape(softcap, slopes, window, first_key, hq, B)
-    head = (_ptr(q), _ptr(k_cache), _ptr(v_cache), num_pages, _ptr(block_table),
-            block_table.shape[1], _ptr(seq_lens), B, int(max_seq_len), hq, hkv, d, page,
-            float(scale))
-    tail = (_ptr(out), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream))
-    if shape is None:
-        _check(lib().bi_decode_attn(*head, *tail))
-    else:
-        _check(lib().bi_decode_attn_ex(*head, *shape, *tail))
-    return out, lse
+    return _attend("bi_decode_attn", q, k_cache, v_cache, block_table, seq_lens, None, 1,
+                   int(max_seq_len), float(scale), out, lse, want_lse, workspace, stream,
+                   float(softcap), slopes, int(window), first_key)
 
 
 # ------------------------------------------------------------------------ 8-bit cache
@@ -684,22 +683,21 @@ def decode_attn_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
 
 # -------------------------------------------------------------------- rotating append
 
-def _token_rows(t, dev, d, name):
+def _token_rows(t, dev, dtype, d, name):
     """(tokens, heads, row stride) of a bf16 [T, H, D] tensor on CUDA device dev whose heads are
     contiguous within a token."""
-    torch = _torch()
     try:
-        fine = t.get_device() == dev and t.dtype is torch.bfloat16 and t.dim() == 3
+        fine = t.get_device() == dev and t.dtype is dtype and t.dim() == 3
     except AttributeError:
         fine = False
     if not fine or dev < 0:
-        _need(t, torch.bfloat16, name, 3)
+        _need(t, dtype, name, 3)
         _on_current_device(**{name: t})
     T, h, dt = t.shape
-    st = t.stride()
-    if dt != d or st[2] != 1 or (st[1] != d and h > 1):
+    row, head, one = t.stride()
+    if dt != d or one != 1 or (head != d and h > 1):
         raise ValueError(f"{name} must have contiguous heads of the cache's D within a token")
-    return T, h, st[0] if T > 1 else h * d
+    return T, h, row if T > 1 else h * d
 
 
 def _rope_kv_append(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
@@ -720,9 +718,9 @@ def _rope_kv_append(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_t
         B, max_pages = block_table.shape
         if seq_lens.shape[0] != B:
             raise ValueError("block_table and seq_lens disagree on the batch")
-    T, hq, ldq = _token_rows(q, dev, d, "q")
-    Tk, hk, ldk = _token_rows(k_new, dev, d, "k_new")
-    Tv, hv, ldv = _token_rows(v_new, dev, d, "v_new")
+    T, hq, ldq = _token_rows(q, dev, bf16, d, "q")
+    Tk, hk, ldk = _token_rows(k_new, dev, bf16, d, "k_new")
+    Tv, hv, ldv = _token_rows(v_new, dev, bf16, d, "v_new")
     if not T == Tk == Tv or not hk == hv == hkv:
         raise ValueError("q, k_new and v_new must have one number of tokens, and k_new and v_new "
                          "the cache's Hkv")
@@ -755,7 +753,7 @@ def _rope_kv_append(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_t
             out = torch.empty((T, hq, d), dtype=bf16, device=q.device)
         ldo = hq * d
     else:
-        To, ho, ldo = _token_rows(out, dev, d, "out")
+        To, ho, ldo = _token_rows(out, dev, bf16, d, "out")
         if (To, ho) != (T, hq):
             raise ValueError("out must have the shape of q")
     head = (q.data_ptr(), ldq, k_new.data_ptr(), ldk, v_new.data_ptr(), ldv, out.data_ptr(), ldo,
@@ -1085,14 +1083,14 @@ def verify_drafts(logits, draft_tokens, uniforms, cu_q, max_q: int, draft_logits
     torch = _torch()
     i32, f32 = torch.int32, torch.float32
     dev = _device_of(logits)
-    per_row = isinstance(temperature, torch.Tensor)
-    given = [("draft_tokens", draft_tokens, i32), ("uniforms", uniforms, f32), ("cu_q", cu_q, i32)]
-    if per_row:
-        given.append(("temperature", temperature, f32))
-    if not _all(dev, *[(t, dtype, 1) for _, t, dtype in given]) or logits.dim() != 2:
+    hot = None if type(temperature) in (float, int) else temperature
+    given = ((draft_tokens, i32, 1), (uniforms, f32, 1), (cu_q, i32, 1))
+    if hot is not None:
+        given += ((hot, f32, 1),)
+    if not _all(dev, *given) or logits.dim() != 2:
         _need(logits, getattr(logits, "dtype", None), "logits", 2)
         _on_current_device(logits=logits)
-        for name, t, dtype in given:
+        for name, (t, dtype, _) in zip(("draft_tokens", "uniforms", "cu_q", "temperature"), given):
             _need(t, dtype, name, 1)
             _on_current_device(**{name: t})
             if not t.is_contiguous():
@@ -1102,15 +1100,16 @@ def verify_drafts(logits, draft_tokens, uniforms, cu_q, max_q: int, draft_logits
     B, N = cu_q.shape[0] - 1, draft_tokens.shape[0]
     if B < 0 or uniforms.shape[0] != T:
         raise ValueError("cu_q must have batch + 1 entries, and uniforms one per row of logits")
-    if per_row and temperature.shape[0] != B:
+    if hot is not None and hot.shape[0] != B:
         raise ValueError("temperature must have one entry per sequence")
-    ldl, ldd = _row_major_2d(logits, "logits"), 0
+    ldl, ldd, rows = _row_major_2d(logits, "logits"), 0, 0
     if draft_logits is not None:
-        _need(draft_logits, logits.dtype, "draft_logits", 2)
-        _on_current_device(draft_logits=draft_logits)
-        if tuple(draft_logits.shape) != (N, n):
+        if draft_logits.get_device() != dev or draft_logits.dtype is not logits.dtype:
+            _need(draft_logits, logits.dtype, "draft_logits", 2)
+            _on_current_device(draft_logits=draft_logits)
+        if draft_logits.shape != (N, n):
             raise ValueError("draft_logits must have one row of n entries per drafted token")
-        ldd = _row_major_2d(draft_logits, "draft_logits")
+        ldd, rows = _row_major_2d(draft_logits, "draft_logits"), N
     L = lib()
     max_q = int(max_q)
     if workspace is not None:
@@ -1123,12 +1122,13 @@ def verify_drafts(logits, draft_tokens, uniforms, cu_q, max_q: int, draft_logits
         logprobs = torch.empty((B, max(max_q, 0)), dtype=f32, device=device)
         accepted = torch.empty(B, dtype=i32, device=device)
         if workspace is None:
-            size = L.bi_verify_drafts_workspace_size(T, 0 if draft_logits is None else N, n)
-            workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=device)
+            size = max(16, L.bi_verify_drafts_workspace_size(T, rows, n))
+            workspace = torch.empty(size, dtype=torch.uint8, device=device)
+        else:
+            size = workspace.numel() * workspace.element_size()
     _check(L.bi_verify_drafts(
         logits.data_ptr(), ldl, _ptr(draft_logits), ldd, dt, draft_tokens.data_ptr(), N,
-        uniforms.data_ptr(), temperature.data_ptr() if per_row else None,
-        0.0 if per_row else float(temperature), cu_q.data_ptr(), B, T, max_q, n,
-        tokens.data_ptr(), accepted.data_ptr(), logprobs.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream_on(stream, dev)))
+        uniforms.data_ptr(), _ptr(hot), float(temperature) if hot is None else 0.0,
+        cu_q.data_ptr(), B, T, max_q, n, tokens.data_ptr(), accepted.data_ptr(),
+        logprobs.data_ptr(), workspace.data_ptr(), size, _stream_on(stream, dev)))
     return VerifiedDrafts(tokens, accepted, logprobs)

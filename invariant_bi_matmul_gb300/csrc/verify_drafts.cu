@@ -240,31 +240,41 @@ struct RowStats {
     unsigned long long best;
 };
 
-// The parts of a row together, the same in every lane of a warp.
+// The parts of a row together, the same in every lane of a warp: each lane's in ascending order,
+// four of them requested at a time, then a butterfly.
 __device__ __noinline__ RowStats join_parts(const PartStats* p, int nparts, float c) {
     const int lane = threadIdx.x & 31;
-    // (a lane's first part is kept: for up to 32 parts they are read once)
-    const PartStats none{-INFINITY, 0.f, 0ull}, own = lane < nparts ? p[lane] : none;
-    RowStats r{own.m, 0.f, own.best};
+    RowStats r{-INFINITY, 0.f, 0ull};
+    auto add = [&](float m, float s) {      // (a part of nothing but -inf and NaN has s = 0 or NaN)
+        const float M = fmaxf(r.m, m);
+        if (M != -INFINITY) {
+            r.s = r.m == -INFINITY ? r.s : r.s * ex2((r.m - M) * c);
+            s = m == -INFINITY ? s : s * ex2((m - M) * c);
+        }
+        r.s += s;
+        r.m = M;
+    };
 #pragma unroll 1
-    for (int i = lane + 32; i < nparts; i += 32) {
-        r.m = fmaxf(r.m, p[i].m);
-        r.best = p[i].best > r.best ? p[i].best : r.best;
+    for (int i0 = 0; i0 < nparts; i0 += 128) {
+        PartStats q[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + 32 * k + lane;
+            q[k] = PartStats{-INFINITY, 0.f, 0ull};
+            if (i < nparts) q[k] = p[i];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            add(q[k].m, q[k].s);
+            r.best = q[k].best > r.best ? q[k].best : r.best;
+        }
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
-        r.m = fmaxf(r.m, __shfl_xor_sync(~0u, r.m, off));
+        add(__shfl_xor_sync(~0u, r.m, off), __shfl_xor_sync(~0u, r.s, off));
         const unsigned long long o = __shfl_xor_sync(~0u, r.best, off);
         r.best = o > r.best ? o : r.best;
     }
-    auto scaled = [&](const PartStats& q) {
-        return q.m == -INFINITY ? q.s : q.s * ex2((q.m - r.m) * c);
-    };
-    r.s = scaled(own);
-#pragma unroll 1
-    for (int i = lane + 32; i < nparts; i += 32) r.s += scaled(p[i]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) r.s += __shfl_xor_sync(~0u, r.s, off);
     return r;
 }
 
@@ -330,8 +340,11 @@ struct Sums {
     uint32_t p;            // of p's upper words where p > q
 };
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads)
+// AHEAD: iterations whose entries are under way.  With one CTA or two on a multiprocessor a warp
+// waits for its own loads (a row of 128,256 entries over eight CTAs: AHEADTIME);
+// with three the others fill the time, and the registers are better spent on them.
+template <int DT, int AHEAD>
+__global__ void __launch_bounds__(kThreads, AHEAD > 1 ? 2 : 3)
 draft_draw_kernel(const DraftArgs a, int ctas) {
     constexpr int kWarps = kThreads / 32, kGroups = kBlock / 32;
     constexpr int kAtOnce = 4, kSteps = kGroups / kAtOnce;  // entries of a block per lane
@@ -484,42 +497,40 @@ draft_draw_kernel(const DraftArgs a, int ctas) {
         // it was 180 KB, which took longer to fetch than to run)
         auto pass = [&](auto subtracts) {
             constexpr bool BOTH = decltype(subtracts)::value;
-            float x[kAtOnce], y[kAtOnce];
-            auto fetch = [&](int it) {
+            constexpr int N = BOTH ? 2 * kAtOnce : kAtOnce;  // target entries, then draft's
+            float x[AHEAD][N];                               // of this iteration and the next ones
+            auto fetch = [&](float (&to)[N], int it) {
                 const int i0 = (k0 + warp + it / kSteps * kWarps) * kBlock +
                                it % kSteps * (kAtOnce * 32) + lane;
-                if (i0 - lane + kAtOnce * 32 <= a.n) {
+                const bool all = i0 - lane + kAtOnce * 32 <= a.n;
 #pragma unroll
-                    for (int q = 0; q < kAtOnce; ++q) {
-                        x[q] = load1<DT>(xr, i0 + q * 32);
-                        if (BOTH) y[q] = load1<DT>(yr, i0 + q * 32);
-                    }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < kAtOnce; ++q) {
-                        const bool in = i0 + q * 32 < a.n;
-                        x[q] = in ? load1<DT>(xr, i0 + q * 32) : -INFINITY;
-                        if (BOTH) y[q] = in ? load1<DT>(yr, i0 + q * 32) : -INFINITY;
-                    }
+                for (int q = 0; q < N; ++q) {
+                    const int i = i0 + q % kAtOnce * 32;
+                    to[q] = -INFINITY;
+                    if (all || i < a.n) to[q] = load1<DT>(q < kAtOnce ? xr : yr, i);
                 }
             };
             const int its = (max(0, k1 - k0 - warp) + kWarps - 1) / kWarps * kSteps;
-            if (its > 0) fetch(0);
+#pragma unroll
+            for (int f = 0; f < AHEAD; ++f)
+                if (f < its) fetch(x[f], f);
             Sums s{0, 0};
 #pragma unroll 1
             for (int it = 0; it < its; ++it) {
-                float xn[kAtOnce], yn[kAtOnce];
+                float now[N];
 #pragma unroll
-                for (int q = 0; q < kAtOnce; ++q) {
-                    xn[q] = x[q];
-                    if (BOTH) yn[q] = y[q];
+                for (int q = 0; q < N; ++q) {
+                    now[q] = x[0][q];
+#pragma unroll
+                    for (int f = 1; f < AHEAD; ++f) x[f - 1][q] = x[f][q];
                 }
-                if (it + 1 < its) fetch(it + 1);
+                if (it + AHEAD < its) fetch(x[AHEAD - 1], it + AHEAD);
 #pragma unroll
                 for (int q = 0; q < kAtOnce; ++q) {
-                    const unsigned long long p = fixed_exp(xn[q], kp, power);
+                    const unsigned long long p = fixed_exp(now[q], kp, power);
                     if (BOTH) {
-                        const unsigned long long over = p - fixed_exp(yn[q], kq, power);
+                        const unsigned long long over =
+                            p - fixed_exp(now[(q + kAtOnce) % N], kq, power);
                         diff += over;
                         if (static_cast<long long>(over) > 0) {
                             s.d += over;
@@ -692,10 +703,11 @@ cudaError_t launch(const DeviceInfo& dev, DraftArgs& a, bool rows_aligned, cudaS
         1, std::min<int64_t>({int64_t(kMaxCtas), (blocks + 7) / 8, 3 * sms / a.B})));
     const int64_t total = int64_t(a.B) * ctas;
     const size_t apart = total <= sms ? 120 * 1024 : total <= 2 * sms ? 48 * 1024 : 0;
-    auto draw = draft_draw_kernel<DT>;
+    auto few = draft_draw_kernel<DT, 4>;
+    auto draw = total <= 2 * sms ? few : draft_draw_kernel<DT, 1>;
     static bool attr_done[64] = {};
     if (dev.device >= 0 && dev.device < 64 && !attr_done[dev.device]) {
-        e = cudaFuncSetAttribute(draw, cudaFuncAttributeMaxDynamicSharedMemorySize, 120 * 1024);
+        e = cudaFuncSetAttribute(few, cudaFuncAttributeMaxDynamicSharedMemorySize, 120 * 1024);
         if (e != cudaSuccess) return e;
         attr_done[dev.device] = true;
     }
