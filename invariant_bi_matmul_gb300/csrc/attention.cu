@@ -134,8 +134,12 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
     int* seq_t0 = seq_len + MAX_BATCH;
     uint8_t* seq_qb = reinterpret_cast<uint8_t*>(seq_t0 + MAX_BATCH);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(seq_qb + MAX_BATCH);
-    // first key that any of a sequence's tokens sees (a call that shapes its scores)
+    // a call that shapes its scores: the first key that any of a sequence's tokens sees; with a
+    // bias the slices' maxima of each row, by page parity, and their barriers
     int* seq_lo = reinterpret_cast<int*>(seq_qb + MAX_BATCH) + 4;
+    float* slice_max = reinterpret_cast<float*>(seq_lo + MAX_BATCH);  // [2][NSM][MAXR]
+    uint64_t* max_bar = reinterpret_cast<uint64_t*>(  // (the lists in front end on 4 bytes)
+        (reinterpret_cast<uintptr_t>(slice_max + 2 * NSM * MAXR) + 7) & ~uintptr_t(7));
     const unsigned long long wait_ns = wait_budget_ns(err);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -164,6 +168,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             mbar_init(&o_full[i], 1);
             mbar_init(&o_empty[i], 1);
             mbar_init(&xs_bar[i], NSM);
+            if (MODE & kBias) mbar_init(&max_bar[i], NSM);
         }
         mbar_init(q_full, NSM);
         mbar_init(drain, 1);
@@ -545,7 +550,10 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 tc_fence_after_sync();
                 uint32_t sa[PAGE], sv[KSL];
                 const uint32_t s_tm = tmem_base + lane_base + uint32_t(C::S_COL + sb * PAGE);
-                tmem_load_x64_x16_sync(s_tm, s_tm + uint32_t(sw * KSL), sa, sv);
+                if (MODE & kBias)  // (the slices' maxima are exchanged, see below)
+                    tmem_load_32x32b_x16_sync(s_tm + uint32_t(sw * KSL), sv);
+                else
+                    tmem_load_x64_x16_sync(s_tm, s_tm + uint32_t(sw * KSL), sa, sv);
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_empty[sb]);
@@ -563,37 +571,52 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 // for the block's rows; the padding rows past R (zero Q, never stored) then
                 // see it too, which changes nothing in the other rows.
                 float sl[KSL], m_raw;
-                {
-                    float a[PAGE];
-                    if (MODE & kBias) {  // (a score's size depends on its place: all are shaped)
-                        float v[PAGE], w[KSL];
+                const bool all_seen =
+                    valid && page0 + PAGE - 1 <= L - qb && (!MODE || page0 >= all_low);
+                const int lim = valid ? pos - page0 : -1;  // the row's last visible key, or < 0
+                const int fst = MODE ? low - page0 : 0;    // ... and its first
+                if (MODE & (kCap | kBias)) {
+                    float w[KSL];
 #pragma unroll
-                        for (int k = 0; k < PAGE; ++k) v[k] = __uint_as_float(sa[k]);
+                    for (int k = 0; k < KSL; ++k) w[k] = __uint_as_float(sv[k]);
+                    shape_scores<MODE>(w, sh, scale_log2, slope_log2,
+                                       float(page0 + sw * KSL - pos));
 #pragma unroll
-                        for (int k = 0; k < KSL; ++k) w[k] = __uint_as_float(sv[k]);
-                        shape_scores<MODE>(v, sh, scale_log2, slope_log2, float(page0 - pos));
-                        shape_scores<MODE>(w, sh, scale_log2, slope_log2,
-                                           float(page0 + sw * KSL - pos));
+                    for (int k = 0; k < KSL; ++k) sv[k] = __float_as_uint(w[k]);
+                }
+                if (MODE & kBias) {
+                    // a biased score's size depends on its place, so the page's maximum is that of
+                    // the shaped scores: each warp takes its slice's, and they exchange them
+                    // (shaping all 64 keys in each warp, a cap and a bias over 64 sequences of up
+                    // to 16,388 keys took 1,004 us, 662 so)
 #pragma unroll
-                        for (int k = 0; k < PAGE; ++k) sa[k] = __float_as_uint(v[k]);
+                    for (int k = 0; k < KSL; ++k) sl[k] = __uint_as_float(sv[k]);
+                    if (!all_seen) {
 #pragma unroll
-                        for (int k = 0; k < KSL; ++k) sv[k] = __float_as_uint(w[k]);
-                    } else if (MODE & kCap) {  // (the maximum is taken before the cap)
-                        float w[KSL];
-#pragma unroll
-                        for (int k = 0; k < KSL; ++k) w[k] = __uint_as_float(sv[k]);
-                        shape_scores<MODE>(w, sh, scale_log2, 0.f, 0.f);
-#pragma unroll
-                        for (int k = 0; k < KSL; ++k) sv[k] = __float_as_uint(w[k]);
+                        for (int k = 0; k < KSL; ++k)
+                            sl[k] = sw * KSL + k <= lim && sw * KSL + k >= fst ? sl[k] : -INFINITY;
                     }
-                    if (valid && page0 + PAGE - 1 <= L - qb && (!MODE || page0 >= all_low)) {
+                    float t[KSL / 2];
+#pragma unroll
+                    for (int k = 0; k < KSL / 2; ++k) t[k] = fmaxf(sl[2 * k], sl[2 * k + 1]);
+                    const float mine = fmaxf(fmax3(fmax3(t[0], t[1], t[2]), t[3], t[4]),
+                                             fmax3(t[5], t[6], t[7]));
+                    float* slot = slice_max + sb * (NSM * MAXR);
+                    slot[sw * MAXR + r] = mine;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&max_bar[sb]);
+                    if (!wait(&max_bar[sb], par)) break;
+                    m_raw = fmaxf(fmaxf(slot[r], slot[MAXR + r]),
+                                  fmaxf(slot[2 * MAXR + r], slot[3 * MAXR + r]));
+                } else {
+                    // (a cap's maximum is taken before the cap, see Reference)
+                    float a[PAGE];
+                    if (all_seen) {
 #pragma unroll
                         for (int k = 0; k < PAGE; ++k) a[k] = __uint_as_float(sa[k]);
 #pragma unroll
                         for (int k = 0; k < KSL; ++k) sl[k] = __uint_as_float(sv[k]);
                     } else {
-                        const int lim = valid ? pos - page0 : -1;  // last visible key, or < 0
-                        const int fst = MODE ? low - page0 : 0;    // first
 #pragma unroll
                         for (int k = 0; k < PAGE; ++k)
                             a[k] = k <= lim && (!MODE || k >= fst) ? __uint_as_float(sa[k])
@@ -1160,7 +1183,9 @@ cudaError_t launch_attention_t(const DeviceInfo& dev, const void* q, const Paged
                                float scale, const Shape& shape, void* out, float* lse,
                                void* workspace, int chunk_log2, cudaStream_t stream) {
     using Cf = Cfg<D>;
-    constexpr size_t SMEM = Cf::SMEM + (MODE ? MAX_BATCH * 4 + 16 : 0);  // (and seq_lo)
+    // (and seq_lo, slice_max and its barriers)
+    constexpr size_t SMEM = Cf::SMEM + (MODE ? MAX_BATCH * 4 + 16 : 0) +
+                            ((MODE & kBias) ? 2 * NSM * MAXR * 4 + 24 : 0);
     static_assert(SMEM <= 232448, "shared memory per CTA");
     const uint64_t rows = uint64_t(a.num_pages) * uint64_t(a.hkv) * PAGE;
     CUtensorMap tk, tv;

@@ -75,17 +75,21 @@ struct Shape {
     int mode = 0;                       // kRange, kCap, kBias; 0: a call that shapes nothing
 };
 
+// The first key that the window leaves to position pos.
+__device__ __forceinline__ int window_low(const Shape& sh, int pos) {
+    return sh.window > 0 ? max(pos - sh.window + 1, 0) : 0;
+}
+
 // The first key that token t at position pos sees; past pos where it sees none.
 __device__ __forceinline__ int row_low(const Shape& sh, int t, int pos) {
-    int low = sh.window > 0 ? pos - sh.window + 1 : 0;
-    if (sh.first_key) low = max(low, sh.first_key[t]);
-    return max(low, 0);
+    const int low = window_low(sh, pos);
+    return sh.first_key ? max(low, sh.first_key[t]) : low;
 }
 
 // The first key that any of the tokens t .. t + n - 1 (positions pos ..) sees; a token that sees
 // none counts as if it saw itself, so that every block has a chunk and a page.
 __device__ __forceinline__ int block_low(const Shape& sh, int t, int pos, int n) {
-    if (!sh.first_key) return min(row_low(sh, t, pos), pos);  // (the window's rises with t)
+    if (!sh.first_key) return window_low(sh, pos);  // (it rises with the position)
     int low = pos + n - 1;
     for (int j = 0; j < n; ++j) low = min(low, row_low(sh, t + j, pos + j));
     return low;
@@ -125,7 +129,7 @@ __device__ __forceinline__ void cap_scores(float (&v)[N], float cap_in, float ca
         p = fma2(z, p, both(c1));
         t[k] = fma2(mul2(z, p), y, y);
     }
-    if (__any_sync(0xffffffffu, most > 1.f)) {
+    if (__builtin_expect(__any_sync(0xffffffffu, most > 1.f), 0)) {  // (out of the common line)
 #pragma unroll
         for (int k = 0; k < N / 2; ++k) {
             if (fabsf(v[2 * k]) > 1.f) t[k].x = far_tanh(v[2 * k]);

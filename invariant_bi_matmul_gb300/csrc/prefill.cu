@@ -43,8 +43,14 @@ namespace {
 
 constexpr int P_NSM = 4;                 // softmax warps
 constexpr int P_EPI = 4;                 // first epilogue warp (quarters 0..3)
-constexpr int P_PRODUCER = 8, P_MMA = 9, P_PV = 10;
-constexpr int P_THREADS = 11 * 32;
+constexpr int P_SHAPE = 8;               // first shaping warp, where scores are shaped
+// the other warps; MODE: see attn_prefill_kernel
+template <int MODE>
+struct PWarps {
+    static constexpr bool SHAPES = (MODE & (kCap | kBias)) != 0;
+    static constexpr int PRODUCER = SHAPES ? 12 : 8, MMA = PRODUCER + 1, PV = PRODUCER + 2;
+    static constexpr int THREADS = (PRODUCER + 3) * 32;
+};
 constexpr int P_NPB = 4;                 // P buffers in tensor memory (by page)
 static_assert(PAGE == 64, "the page max below is a three-input max tree over 64 keys");
 constexpr int P_ROWS = 128;              // query rows per tile, one per TMEM lane
@@ -63,12 +69,13 @@ struct PCfg {
     static constexpr int RING_OFF = Q_BYTES;             // (P lives in tensor memory)
     static constexpr int BAR_OFF = RING_OFF + NST * STAGE_BYTES;
     // ring (2 NST), s / o full and empty pairs, p full / empty per P buffer, the xs pair,
-    // q_full, q_free, and one drain per issuer
-    static constexpr int NBARS = 2 * NST + 4 + 2 * P_NPB + 4 + 2 + 4;
+    // q_full, q_free, one drain per issuer, and the shaped pair
+    static constexpr int NBARS = 2 * NST + 4 + 2 * P_NPB + 4 + 2 + 4 + 2;
     // the barriers, then the tensor-memory address slot (8 bytes), then the (m, l) rows
     static constexpr int XS_OFF = (BAR_OFF + NBARS * 8 + 8 + 15) / 16 * 16;
     static constexpr int XS_BYTES = 2 * P_ROWS * 8;       // per O buffer: (m, l) per row
-    static constexpr int MISC_OFF = XS_OFF + XS_BYTES;
+    static constexpr int PMAX_OFF = XS_OFF + XS_BYTES;    // per S buffer: the rows' page maxima
+    static constexpr int MISC_OFF = PMAX_OFF + 2 * P_ROWS * 4;
     static constexpr int MISC_BYTES = ((P_MAX_BATCH + 1) + 3 * P_MAX_BATCH + 4) * 4;
     // per epilogue warp: 32 O rows of 32 floats, staged for coalesced stores (rows padded
     // to 144 bytes: conflict-free both ways)
@@ -83,6 +90,44 @@ struct PCfg {
     static_assert(RING_OFF % 1024 == 0 && BAR_OFF % 1024 == 0, "1024-byte aligned buffers");
     static_assert(SMEM <= 232448, "shared memory per CTA");
 };
+
+// Whether every key of a page is visible to every row of the warp (pos: the row's last, low: its
+// first visible key), and -inf in place of the scores that a row does not see.
+template <int MODE>
+__device__ __forceinline__ bool page_seen(bool valid, int page0, int pos, int low) {
+    return __all_sync(0xffffffffu, valid && page0 + PAGE - 1 <= pos && (!MODE || page0 >= low));
+}
+template <int MODE, int N>
+__device__ __forceinline__ void hide_keys(float (&s)[N], bool valid, int first_of_s, int pos,
+                                          int low) {
+    const int last = valid ? pos - first_of_s : -1, first = MODE ? low - first_of_s : 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] = k <= last && (!MODE || k >= first) ? s[k] : -INFINITY;
+}
+
+// The exact maximum of a row's scores of a page (max does not round: any order), by three-input
+// maxima: 31 instructions instead of 63.
+__device__ __forceinline__ float page_max_of(const float (&s)[PAGE]) {
+    float t1[22], t2[8];
+#pragma unroll
+    for (int k = 0; k < 21; ++k) t1[k] = fmax3(s[3 * k], s[3 * k + 1], s[3 * k + 2]);
+    t1[21] = s[63];
+#pragma unroll
+    for (int k = 0; k < 7; ++k) t2[k] = fmax3(t1[3 * k], t1[3 * k + 1], t1[3 * k + 2]);
+    t2[7] = t1[21];
+    return fmax3(fmax3(t2[0], t2[1], t2[2]), fmax3(t2[3], t2[4], t2[5]), fmaxf(t2[6], t2[7]));
+}
+// ... and of half a page.
+__device__ __forceinline__ float half_max_of(const float (&s)[PAGE / 2]) {
+    float t1[11], t2[4];
+#pragma unroll
+    for (int k = 0; k < 10; ++k) t1[k] = fmax3(s[3 * k], s[3 * k + 1], s[3 * k + 2]);
+    t1[10] = fmaxf(s[30], s[31]);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) t2[k] = fmax3(t1[3 * k], t1[3 * k + 1], t1[3 * k + 2]);
+    t2[3] = fmaxf(t1[9], t1[10]);
+    return fmaxf(fmax3(t2[0], t2[1], t2[2]), t2[3]);
+}
 
 // First key that any token of each query tile sees (block_low), for a call with first_key: entry
 // t0 + qt of `lows` for tile qt of the sequence whose first token is t0 (tiles hold a token at
@@ -112,7 +157,7 @@ tile_low_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict_
 // MODE: what the call does to its scores (kRange, kCap, kBias of attn_common.cuh; 0: nothing);
 // tile_lows: tile_low_kernel's, or null where no first_key is given.
 template <int D, int MODE>
-__global__ void __launch_bounds__(P_THREADS, 1)
+__global__ void __launch_bounds__(PWarps<MODE>::THREADS, 1)
 attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v,
                     const __grid_constant__ CUtensorMap tmap_q,
@@ -123,6 +168,8 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     int maxC, unsigned int* err, const Shape sh,
                     const int* __restrict__ tile_lows) {
     using C = PCfg<D>;
+    using W = PWarps<MODE>;
+    constexpr int P_PRODUCER = W::PRODUCER, P_MMA = W::MMA, P_PV = W::PV, P_THREADS = W::THREADS;
     constexpr int NST = C::NST;
     constexpr int chunk_pages = CHUNK / PAGE;
     static_assert(chunk_pages <= 32, "an item's block-table entries are read one per lane");
@@ -143,9 +190,11 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
     uint64_t* q_full = xs_bar + 2;     // the Q tile has landed (TMA)
     uint64_t* q_free = q_full + 1;     // every MMA reading the previous Q tile is done
     uint64_t* drain = q_free + 1;      // [2]: S issuer, P V issuer
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
-    static_assert(C::XS_OFF >= C::BAR_OFF + (2 * NST + 4 + 2 * P_NPB + 4 + 2 + 4) * 8 + 8,
+    uint64_t* shaped = drain + 2;      // [2]: S buffer holds shaped scores (four shaping warps)
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(shaped + 2);
+    static_assert(C::XS_OFF >= C::BAR_OFF + (2 * NST + 4 + 2 * P_NPB + 4 + 2 + 4 + 2) * 8 + 8,
                   "barriers overlap xs");
+    float* page_max = reinterpret_cast<float*>(smem + C::PMAX_OFF);  // [2][P_ROWS]
     float2* xs = reinterpret_cast<float2*>(smem + C::XS_OFF);  // [2][P_ROWS]
     int* prefix = reinterpret_cast<int*>(smem + C::MISC_OFF);  // [B+1] items before sequence b
     int* seq_len = prefix + P_MAX_BATCH + 1;    // per sequence: length, first token, width
@@ -179,6 +228,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
             mbar_init(&o_full[i], 1);
             mbar_init(&o_empty[i], 4);
             mbar_init(&xs_bar[i], P_NSM);
+            mbar_init(&shaped[i], 4);
         }
         mbar_init(q_full, 1);
         mbar_init(q_free, 1);
@@ -195,8 +245,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // ... from that of the first key that any of its tokens sees
     auto tile_low = [&](int L, int t0, int qb, int qt) {
         if (!MODE) return 0;
-        return tile_lows ? tile_lows[t0 + qt]
-                         : block_low(sh, t0 + qt * TQ, L - qb + qt * TQ, min(TQ, qb - qt * TQ));
+        return tile_lows ? tile_lows[t0 + qt] : window_low(sh, L - qb + qt * TQ);
     };
     // work items per sequence: sum over its query tiles of chunks x KV heads
     if (MODE) {  // (a warp per sequence: a tile's first key may be a load)
@@ -312,18 +361,19 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
             set_tile(k);
             k.h = min(r / k.nch, Hkv - 1);
             k.c = k.c0 + r - k.h * k.nch;
-            return k;
+        } else {
+            for (;;) {
+                set_tile(k);
+                if (r < k.nch * Hkv || k.qt + 1 >= nqt) break;
+                r -= k.nch * Hkv;
+                ++k.qt;
+            }
+            k.h = r / k.nch;
+            k.c = r - k.h * k.nch;
         }
-        for (;;) {
-            set_tile(k);
-            if (r < k.nch * Hkv || k.qt + 1 >= nqt) break;
-            r -= k.nch * Hkv;
-            ++k.qt;
-        }
-        k.h = r / k.nch;
-        k.c = r - k.h * k.nch;
         return k;
     };
+    const Cursor start = seek(w_begin);
     auto advance = [&](Cursor& k) {
         if (++k.c < k.c0 + k.nch) return;
         k.c = k.c0;
@@ -363,6 +413,77 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
         return ok;
     };
 
+    // Shaping warps, one per quarter (calls that cap or bias their scores): read the scores of a
+    // page, take the rows' maximum (of the capped ones before the cap, see Reference), and write
+    // the shaped scores back for the softmax.  The softmax warps' chain of a page is what bounds
+    // this kernel; shaping on it, a prompt of 8,192 tokens with a cap took SHAPEDTIME.
+    auto shape_pages = [&]() {
+        const int quarter = warp & 3;
+        const int r = 32 * quarter + lane;
+        const uint32_t lane_base = uint32_t(32 * quarter) << 16;
+        uint32_t g = 0;
+        Cursor k = start;
+        for (int w = w_begin; ok && w < w_end; ++w, advance(k)) {
+            const int L = seq_len[k.b], qb = seq_qb[k.b];
+            const int npages = item_pages(k);
+            const int j = k.qt * TQ + r / G;
+            const int pos = j < qb ? L - qb + j : -1;
+            // (the producer's test of the pages, see the softmax)
+            const int pidx_l = first_page(k) + lane;
+            const int phys_l = (lane < npages && pidx_l < max_pages)
+                                   ? block_table[int64_t(k.b) * max_pages + pidx_l]
+                                   : -1;
+            const bool valid_l = phys_l >= 0 && phys_l < num_pages;
+            const int low = j < qb ? row_low(sh, seq_t0[k.b] + j, pos) : 0;
+            const float slope_log2 =
+                (MODE & kBias) ? sh.slopes[k.h * G + r % G] * kLog2e : 0.f;
+            for (int i = 0; i < npages && ok; ++i) {
+                const uint32_t gi = g + uint32_t(i);
+                const int sb = int(gi & 1u);
+                const int page0 = (first_page(k) + i) * PAGE;
+                if (!wait(&s_full[sb], (gi >> 1) & 1u)) break;
+                tc_fence_after_sync();
+                const uint32_t at = tmem_base + lane_base + uint32_t(C::S_COL + sb * PAGE);
+                const bool valid = __shfl_sync(0xffffffffu, valid_l ? 1 : 0, i) != 0;
+                const bool all_seen = page_seen<MODE>(valid, page0, pos, low);
+                float most = -INFINITY;
+#pragma unroll 1  // (the warps' roles share an instruction cache)
+                for (int half = 0; half < 2; ++half) {
+                    constexpr int N = PAGE / 2;
+                    const int key0 = page0 + half * N;
+                    uint32_t sv[N];
+                    tmem_load_32x32b_x32_sync(at + uint32_t(half * N), sv);
+                    float s[N];
+#pragma unroll
+                    for (int kk = 0; kk < N; ++kk) s[kk] = __uint_as_float(sv[kk]);
+                    auto take_max = [&]() {
+                        if (all_seen) {
+                            most = fmaxf(most, half_max_of(s));
+                        } else {
+                            float shown[N];
+#pragma unroll
+                            for (int kk = 0; kk < N; ++kk) shown[kk] = s[kk];
+                            hide_keys<MODE>(shown, valid, key0, pos, low);
+                            most = fmaxf(most, half_max_of(shown));
+                        }
+                    };
+                    if (!(MODE & kBias)) take_max();
+                    shape_scores<MODE>(s, sh, scale_log2, slope_log2, float(key0 - pos));
+                    if (MODE & kBias) take_max();
+#pragma unroll
+                    for (int kk = 0; kk < N; ++kk) sv[kk] = __float_as_uint(s[kk]);
+                    tmem_store_32x32b_x32_sync(at + uint32_t(half * N), sv);
+                }
+                page_max[sb * P_ROWS + r] = most;
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&shaped[sb]);
+            }
+            g += uint32_t(npages);
+        }
+        if (!ok && lane == 0) give_up();
+    };
+
     if (warp == P_PRODUCER) {
         // ------------------------------------------------------------------ producer
         if (lane == 0) {
@@ -370,7 +491,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
             tma_prefetch_desc(&tmap_v);
         }
         uint32_t g = 0;
-        Cursor k = seek(w_begin);
+        Cursor k = start;
         for (int w = w_begin; ok && w < w_end; ++w, advance(k)) {
             const int npages = item_pages(k);  // <= chunk_pages = 8
             // the item's block-table entries, one per lane, read before the first wait for
@@ -422,7 +543,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
         if (lane == 0) tma_prefetch_desc(&tmap_q);
         uint32_t g = 0, qgen = 0;
         bool q_in_flight = false;
-        Cursor k = seek(w_begin);
+        Cursor k = start;
         for (int w = w_begin; ok && w < w_end; ++w, advance(k)) {
             const int npages = item_pages(k);
             if (w == w_begin || k.c == k.c0) {
@@ -487,7 +608,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
             umma_smem_desc(smem_addr(sStage + C::PAGE_BYTES), C::BOX_BYTES, 1024, 2);
         uint32_t g = 0;
         int item = 0;
-        Cursor k = seek(w_begin);
+        Cursor k = start;
         for (int w = w_begin; ok && w < w_end; ++w, advance(k), ++item) {
             const int npages = item_pages(k);
             const int ob = item & 1;
@@ -518,6 +639,8 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
         if (elect_one()) tc_commit(&drain[1]);
         __syncwarp();
         mbar_wait(&drain[1], 0, nullptr, 100000000ull);
+    } else if (W::SHAPES && warp >= P_SHAPE) {
+        shape_pages();
     } else if (warp >= P_EPI) {
         // ------------------------------------------------------------------ epilogue
         // Quarter e = warp mod 4: rows 32e..32e+31 of item k's O (buffer k&1), written
@@ -526,7 +649,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const int r = 32 * e + lane;
         uint8_t* epi_stage = smem + C::EPI_OFF + e * (32 * C::EPI_STRIDE);
         int item = 0;
-        Cursor k = seek(w_begin);
+        Cursor k = start;
         for (int w = w_begin; ok && w < w_end; ++w, advance(k), ++item) {
             const int L = seq_len[k.b], qb = seq_qb[k.b];
             const int j = k.qt * TQ + r / G, gg = r - (r / G) * G;
@@ -581,7 +704,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const uint32_t lane_base = uint32_t(32 * sw) << 16;
         uint32_t g = 0;
         int item = 0;
-        Cursor k = seek(w_begin);
+        Cursor k = start;
         for (int w = w_begin; ok && w < w_end; ++w, advance(k), ++item) {
             const int L = seq_len[k.b], qb = seq_qb[k.b];
             const int npages = item_pages(k);
@@ -596,13 +719,8 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                    ? block_table[int64_t(k.b) * max_pages + pidx_l]
                                    : -1;
             const bool valid_l = phys_l >= 0 && phys_l < num_pages;
-            // the row's first key and slope (a row past the block: all masked by pos)
-            int low = 0;
-            float slope_log2 = 0.f;
-            if (MODE) {
-                if (j < qb) low = row_low(sh, seq_t0[k.b] + j, pos);
-                if (MODE & kBias) slope_log2 = sh.slopes[k.h * G + r % G] * kLog2e;
-            }
+            // the row's first key (a row past the block: all masked by pos)
+            const int low = MODE && j < qb ? row_low(sh, seq_t0[k.b] + j, pos) : 0;
             float m_ref = -INFINITY;
             Reference<MODE> ref;
             float l_run[4] = {0.f, 0.f, 0.f, 0.f};  // running sums of the four 16-key slices
@@ -611,11 +729,13 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const int s = int(gi % NST), sb = int(gi & 1u);
                 const uint32_t par = (gi >> 1) & 1u;
                 const int page0 = (first_page(k) + i) * PAGE;
-                if (!wait(&s_full[sb], par)) break;
+                if (!wait(W::SHAPES ? &shaped[sb] : &s_full[sb], par)) break;
                 tc_fence_after_sync();
                 uint32_t sv[PAGE];
                 tmem_load_32x32b_x64_sync(tmem_base + lane_base + uint32_t(C::S_COL + sb * PAGE),
                                           sv);
+                float m_raw = 0.f;
+                if (W::SHAPES) m_raw = page_max[sb * P_ROWS + r];
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_empty[sb]);
@@ -623,55 +743,14 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 float sl[PAGE];
 #pragma unroll
                 for (int kk = 0; kk < PAGE; ++kk) sl[kk] = __uint_as_float(sv[kk]);
-                if (MODE & kBias)  // (a score's size depends on its place: all are shaped)
-                    shape_scores<MODE>(sl, sh, scale_log2, slope_log2, float(page0 - pos));
-                // whether every key of the page is visible to every row of the warp
-                const bool all_seen = __all_sync(
-                    0xffffffffu, valid && page0 + PAGE - 1 <= pos && (!MODE || page0 >= low));
-                const int lim = valid ? pos - page0 : -1;  // the row's last visible key
-                const int fst = MODE ? low - page0 : 0;    // ... and its first
-                auto hide = [&](float (&to)[PAGE]) {
-                    if (!all_seen) {
-#pragma unroll
-                        for (int kk = 0; kk < PAGE; ++kk)
-                            to[kk] = kk <= lim && (!MODE || kk >= fst) ? sl[kk] : -INFINITY;
-                    }
-                };
-                // (a cap is put on once the maximum, which needs none, is known)
-                constexpr bool CAP_LAST = (MODE & kCap) && !(MODE & kBias);
-                if (!CAP_LAST) hide(sl);
-                // the exact row max of the page (max does not round: any order), by
-                // three-input maxima: 31 instructions instead of 63
-                auto max_of = [](const float (&a)[PAGE]) {
-                    float t1[22], t2[8];
-#pragma unroll
-                    for (int kk = 0; kk < 21; ++kk)
-                        t1[kk] = fmax3(a[3 * kk], a[3 * kk + 1], a[3 * kk + 2]);
-                    t1[21] = a[63];
-#pragma unroll
-                    for (int kk = 0; kk < 7; ++kk)
-                        t2[kk] = fmax3(t1[3 * kk], t1[3 * kk + 1], t1[3 * kk + 2]);
-                    t2[7] = t1[21];
-                    return fmax3(fmax3(t2[0], t2[1], t2[2]), fmax3(t2[3], t2[4], t2[5]),
-                                 fmaxf(t2[6], t2[7]));
-                };
-                float m_raw;
-                if (CAP_LAST && !all_seen) {
-                    float shown[PAGE];
-                    hide(shown);
-                    m_raw = max_of(shown);
-                } else {
-                    m_raw = max_of(sl);
-                }
+                const bool all_seen = page_seen<MODE>(valid, page0, pos, low);
+                if (!all_seen) hide_keys<MODE>(sl, valid, page0, pos, low);
+                if (!W::SHAPES) m_raw = page_max_of(sl);
                 bool raise;
                 float factor;
-                if (MODE & (kCap | kBias)) {
+                if (W::SHAPES) {
                     raise = ref.raise(m_raw, sh, scale_log2, factor);
                     m_ref = ref.m;
-                    if (CAP_LAST) {
-                        shape_scores<MODE>(sl, sh, scale_log2, 0.f, 0.f);
-                        hide(sl);
-                    }
                 } else {
                     const float m_page = m_raw * scale_log2;
                     raise = m_page > m_ref + kRescaleLog2 ||
@@ -707,7 +786,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     float pv[16];
 #pragma unroll
                     for (int kk = 0; kk < 16; ++kk)
-                        pv[kk] = (MODE & (kCap | kBias))
+                        pv[kk] = W::SHAPES
                                      ? ex2(__fadd_rn(sl[16 * q4 + kk], -m_use))
                                      : ex2(fmaf(sl[16 * q4 + kk], scale_log2, -m_use));
 #pragma unroll
@@ -814,7 +893,7 @@ cudaError_t launch_prefill_t(const DeviceInfo& dev, const void* q, const PagedAr
                        int(a.max_seq_len), P_ROWS / G, shape, tile_lows);
         if (e != cudaSuccess) return e;
     }
-    e = launch_pdl(kern, dim3(grid), dim3(P_THREADS), Cf::SMEM, stream, tk, tv, tq,
+    e = launch_pdl(kern, dim3(grid), dim3(PWarps<MODE>::THREADS), Cf::SMEM, stream, tk, tv, tq,
                                a.block_table, int(a.max_pages), int(a.num_pages), a.seq_lens,
                                a.cu_q, int(a.batch), int(a.total_q), int(a.max_q),
                                int(a.max_seq_len), int(a.hq), int(a.hkv), scale * kLog2e, ws_o,
