@@ -1117,9 +1117,9 @@ def verify_drafts(logits, draft_tokens, uniforms, cu_q, max_q: int, draft_logits
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
     with _allocating_for(stream):
-        device = logits.device
-        tokens = torch.empty((B, max(max_q, 0)), dtype=i32, device=device)
-        logprobs = torch.empty((B, max(max_q, 0)), dtype=f32, device=device)
+        device, wide = logits.device, (B, max(max_q, 0))
+        tokens = torch.empty(wide, dtype=i32, device=device)
+        logprobs = torch.empty(wide, dtype=f32, device=device)
         accepted = torch.empty(B, dtype=i32, device=device)
         if workspace is None:
             size = max(16, L.bi_verify_drafts_workspace_size(T, rows, n))

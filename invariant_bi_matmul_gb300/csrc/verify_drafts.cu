@@ -95,16 +95,13 @@ __device__ __noinline__ Rate rate_of(float T) {
 
 // --------------------------------------------------------------------------- statistics
 
-template <int DT, bool ALIGNED>
-__global__ void __launch_bounds__(kStats, !ALIGNED ? 6 : DT == BI_F32 ? 9 : 8)
-draft_stats_kernel(const DraftArgs a) {
+// The statistics of one part, by a warp; temperature(): the row's, asked for once the loads are
+// under way (NaN: nothing to do for this row).
+template <int DT, bool ALIGNED, class Temperature>
+__device__ __forceinline__ void part_stats(const DraftArgs& a, int row, int part,
+                                           Temperature temperature) {
     constexpr int VE = 16 / kSize<DT>, kLen = 32 * kBatch;  // vectors of a part
-    pdl_wait();
-    pdl_trigger();
     const int lane = threadIdx.x & 31, warp0 = threadIdx.x & ~31;
-    const int item = int(blockIdx.x) * (kStats / 32) + int(threadIdx.x >> 5);
-    if (item >= a.items) return;
-    const int row = int(unsigned(item) / unsigned(a.nparts)), part = item - row * a.nparts;
     const bool draft = row >= a.total_q;
     const int r = draft ? row - a.total_q : row;
     const char* xr = static_cast<const char*>(draft ? a.y : a.x) +
@@ -114,15 +111,9 @@ draft_stats_kernel(const DraftArgs a) {
     // (load_batch counts a CTA's threads: this warp's are 0 .. 31)
     load_batch<DT, 32, ALIGNED>(v, xr, skew, part * kLen - warp0,
                                 min((a.n + VE - 1) / VE, (part + 1) * kLen), a.n);
-    // the row's sequence, found while the loads are under way: target rows of b are cu_q[b] ..,
-    // draft rows cu_q[b] - b ..  (By counting, a lane's loads all at once: a binary search waits
-    // for one after the other.)
-    int b = 0;
-    for (int i = lane; i < a.B; i += 32) b += a.cu_q[i] - (draft ? i : 0) <= r ? 1 : 0;
-    b = max(__reduce_add_sync(~0u, b) - 1, 0);
-    const float T = temperature_of(a, b);
+    const float T = temperature();
     const bool greedy = T == 0.f;
-    if (r >= a.cu_q[b + 1] - (draft ? b + 1 : 0) || isnan(T) || (greedy && draft)) return;
+    if (isnan(T) || (greedy && draft)) return;
     const float c = rate_of(T).hi;
 
     float m = vec_max<DT>(v[0]);
@@ -170,6 +161,28 @@ draft_stats_kernel(const DraftArgs a) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(~0u, s, off);
     if (lane == 0) a.parts[int64_t(row) * a.nparts + part] = PartStats{M, s, best};
+}
+
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(kStats, !ALIGNED ? 6 : DT == BI_F32 ? 9 : 8)
+draft_stats_kernel(const DraftArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int item = int(blockIdx.x) * (kStats / 32) + int(threadIdx.x >> 5);
+    if (item >= a.items) return;
+    const int row = int(unsigned(item) / unsigned(a.nparts)), part = item - row * a.nparts;
+    part_stats<DT, ALIGNED>(a, row, part, [&]() {
+        // the row's sequence: target rows of b are cu_q[b] .., draft rows cu_q[b] - b ..  (By
+        // counting, a lane's loads all at once: a binary search waits for one after the other.)
+        const bool draft = row >= a.total_q;
+        const int r = draft ? row - a.total_q : row;
+        int b = 0;
+        for (int i = lane; i < a.B; i += 32) b += a.cu_q[i] - (draft ? i : 0) <= r ? 1 : 0;
+        b = max(__reduce_add_sync(~0u, b) - 1, 0);
+        const float T = temperature_of(a, b);
+        return r < a.cu_q[b + 1] - (draft ? b + 1 : 0) ? T : kNaN;
+    });
 }
 
 // ---------------------------------------------------------------- weights in whole numbers
@@ -341,9 +354,12 @@ struct Sums {
 };
 
 // AHEAD: iterations whose entries are under way.  With one CTA or two on a multiprocessor a warp
-// waits for its own loads (a row of 128,256 entries over eight CTAs: AHEADTIME);
-// with three the others fill the time, and the registers are better spent on them.
-template <int DT, int AHEAD>
+// waits for its own loads (a row of 128,256 entries over eight CTAs, the whole call 17.5 us with
+// one iteration, 15.3 with four); with three CTAs the others fill the time, and the registers are
+// better spent on them.
+// OWN: the cluster takes its sequence's statistics itself (1: rows aligned, 2: not), for blocks of
+// few parts: one launch less.
+template <int DT, int AHEAD, int OWN>
 __global__ void __launch_bounds__(kThreads, AHEAD > 1 ? 2 : 3)
 draft_draw_kernel(const DraftArgs a, int ctas) {
     constexpr int kWarps = kThreads / 32, kGroups = kBlock / 32;
@@ -400,6 +416,17 @@ draft_draw_kernel(const DraftArgs a, int ctas) {
         return static_cast<const char*>(a.y) + int64_t(d0 + j) * a.ldy * es;
     };
 
+    if (OWN) {
+        const int rows = drafts + 1 + (a.y && !greedy ? drafts : 0);
+#pragma unroll 1
+        for (int i = rank * kWarps + warp; i < rows * a.nparts; i += ctas * kWarps) {
+            const int r = i / a.nparts;
+            part_stats<DT, OWN == 1>(a, r <= drafts ? t0 + r : a.total_q + d0 + r - drafts - 1,
+                                     i - r * a.nparts, [&]() { return T; });
+        }
+        // (the barriers order the parts in global memory, too)
+        if (ctas > 1) cluster_sync_all(); else __syncthreads();
+    }
     // a warp per draft, and one for the row behind the last; a warp stops at its first refusal,
     // since no later row of its own ends the block
     RowStats P{0.f, 1.f, 0ull}, Q{0.f, 1.f, 0ull};
@@ -484,7 +511,7 @@ draft_draw_kernel(const DraftArgs a, int ctas) {
     // (at most 2^11 blocks and 8 CTAs)
     const int k0 = rank * blocks / ctas, k1 = (rank + 1) * blocks / ctas;
 
-    if (ctas > 1) cluster_sync_all();       // (the others have started)
+    if (!OWN && ctas > 1) cluster_sync_all();  // (the others have started)
     unsigned long long Z = 0;
     int e = 0;
     Sums before{0, 0};                      // of the CTAs in front of the one that holds the share
@@ -690,10 +717,6 @@ cudaError_t launch(const DeviceInfo& dev, DraftArgs& a, bool rows_aligned, cudaS
     const int64_t items = (int64_t(a.total_q) + (a.y ? a.num_drafts : 0)) * a.nparts;
     if (items > kI32Max) return cudaErrorNotSupported;
     a.items = int(items);
-    auto stats = rows_aligned ? draft_stats_kernel<DT, true> : draft_stats_kernel<DT, false>;
-    const int64_t grid = (items + kStats / 32 - 1) / (kStats / 32);
-    cudaError_t e = launch_pdl(stats, dim3(unsigned(grid)), dim3(kStats), 0, stream, a);
-    if (e != cudaSuccess) return e;
     // CTAs of a sequence: one for every eight blocks (a block for each warp), while the
     // multiprocessors hold them all at once (three each).  The batch is spread over them: left to
     // itself the hardware puts the clusters of a small one on half of them.
@@ -703,12 +726,29 @@ cudaError_t launch(const DeviceInfo& dev, DraftArgs& a, bool rows_aligned, cudaS
         1, std::min<int64_t>({int64_t(kMaxCtas), (blocks + 7) / 8, 3 * sms / a.B})));
     const int64_t total = int64_t(a.B) * ctas;
     const size_t apart = total <= sms ? 120 * 1024 : total <= 2 * sms ? 48 * 1024 : 0;
-    auto few = draft_draw_kernel<DT, 4>;
-    auto draw = total <= 2 * sms ? few : draft_draw_kernel<DT, 1>;
+    // statistics in the same launch where a warp gets no more than two parts of its sequence (7
+    // sequences of 999 entries 24.5 us with the host's time, 25.8 in two launches; 4 rows of
+    // 128,256, eight parts for each warp, 29 and 25)
+    const int64_t rows = a.y ? 2 * int64_t(a.max_q) - 1 : a.max_q;
+    const bool own = total <= 2 * sms && rows * a.nparts <= 2 * ctas * (kThreads / 32);
+    if (!own) {
+        auto stats = rows_aligned ? draft_stats_kernel<DT, true> : draft_stats_kernel<DT, false>;
+        const int64_t grid = (items + kStats / 32 - 1) / (kStats / 32);
+        cudaError_t e = launch_pdl(stats, dim3(unsigned(grid)), dim3(kStats), 0, stream, a);
+        if (e != cudaSuccess) return e;
+    }
+    auto draw = total > 2 * sms ? draft_draw_kernel<DT, 1, 0>
+                : !own          ? draft_draw_kernel<DT, 4, 0>
+                : rows_aligned  ? draft_draw_kernel<DT, 4, 1>
+                                : draft_draw_kernel<DT, 4, 2>;
     static bool attr_done[64] = {};
     if (dev.device >= 0 && dev.device < 64 && !attr_done[dev.device]) {
-        e = cudaFuncSetAttribute(few, cudaFuncAttributeMaxDynamicSharedMemorySize, 120 * 1024);
-        if (e != cudaSuccess) return e;
+        for (auto k : {draft_draw_kernel<DT, 4, 0>, draft_draw_kernel<DT, 4, 1>,
+                       draft_draw_kernel<DT, 4, 2>}) {
+            cudaError_t e =
+                cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 120 * 1024);
+            if (e != cudaSuccess) return e;
+        }
         attr_done[dev.device] = true;
     }
     return launch_pdl_cluster(draw, dim3(unsigned(total)), dim3(kThreads), apart, stream,

@@ -32,6 +32,13 @@ beside the traces (``trace_logprobs``): the same bits whether the token was deco
 accepted from a verify block.  ``fork`` continues one sequence as several: its full cache pages
 are shared, its open page is copied, and ``compact`` moves the pages in use together.
 
+``speculate_sampled`` is speculative decoding at a temperature: each block's drafts are verified
+on the device against the target's probabilities, from uniform numbers that each sequence draws
+from a generator of its own, so a sequence's trace does not depend on the batch it runs in.
+``softcap`` and ``window`` shape the attention scores (bf16 caches); ``fused_append=True`` turns
+queries and keys and appends keys and values in one launch, with angles that stay exact at far
+positions (other bits than the separate rotation's, which forms angles in fp32).
+
 The traces are batch invariant only while every call is inside the batch-invariant
 limit: matmuls of up to ``max_batch * max_width`` rows and verify blocks of up to
 ``max_width`` tokens.  An ``invariant=True`` decoder (the default) refuses to run a block
@@ -45,8 +52,9 @@ from typing import Callable, List, Optional, Sequence
 import torch
 
 from . import (ATTN_MAX_Q, add, argmax, attn_workspace_size, embedding, kv_append, kv_append_q8,
-               kv_copy_pages, matmul, prefill_attn, prefill_attn_q8, rmsnorm, rope, swiglu,
-               token_logprobs, verify_block, verify_block_q8, within_batch_invariant_limit)
+               kv_copy_pages, matmul, prefill_attn, prefill_attn_q8, rmsnorm, rope,
+               rope_kv_append, rope_kv_append_q8, swiglu, token_logprobs, verify_block,
+               verify_block_q8, verify_drafts, within_batch_invariant_limit)
 from .inputs import PAGE_SIZE, DecoderConfig, decoder_context, decoder_first_token, page_permutation
 from .pages import PagePool
 
@@ -61,10 +69,15 @@ class GreedyDecoder:
     def __init__(self, cfg: DecoderConfig, weights: dict, max_batch: int, max_len: int,
                  max_width: int = 4, device="cuda", page_seed: int = 0,
                  invariant: bool = True, prefill_width: int = 0, kv_cache: str = "bf16",
-                 logprobs: bool = False):
+                 logprobs: bool = False, softcap: float = 0.0, window: int = 0,
+                 fused_append: bool = False):
         if kv_cache not in ("bf16", "q8"):
             raise ValueError("kv_cache must be 'bf16' or 'q8'")
+        if kv_cache == "q8" and (softcap or window):
+            raise ValueError("softcap and window need a bf16 cache")
         self.kv_cache, self.want_logprobs = kv_cache, logprobs
+        self.shape = dict(softcap=softcap, window=window) if softcap or window else {}
+        self.fused_append = fused_append
         self.cfg, self.w = cfg, weights
         self.invariant = invariant
         self.dev = torch.device(device)
@@ -124,6 +137,18 @@ class GreedyDecoder:
         else:
             kv_append(k, v, self.k_cache[layer], self.v_cache[layer], bt, sl, cq)
 
+    def _turn_and_append(self, layer: int, q, k, v, bt, sl, cq) -> None:
+        """The block's queries and keys turned, its keys and values in the cache."""
+        if not self.fused_append:
+            rope(q, sl, cq, self.cfg.theta)
+            rope(k, sl, cq, self.cfg.theta)
+            self._append(layer, k, v, bt, sl, cq)
+            return
+        scales = (self.k_scale[layer], self.v_scale[layer]) if self.kv_cache == "q8" else ()
+        fn = rope_kv_append_q8 if self.kv_cache == "q8" else rope_kv_append
+        fn(q, k, v, self.k_cache[layer], self.v_cache[layer], *scales, bt, sl, cq,
+           theta=self.cfg.theta, out=q)
+
     def _attend(self, layer: int, q, bt, sl, cq, max_q: int, max_seq_len: int, out) -> None:
         # blocks wider than a verify block: the chunked-prefill attention (same bits)
         wide = max_q > ATTN_MAX_Q
@@ -135,7 +160,7 @@ class GreedyDecoder:
                    self.v_scale[layer], bt, sl, cq, **rest)
         else:
             attend = prefill_attn if wide else verify_block
-            attend(q, self.k_cache[layer], self.v_cache[layer], bt, sl, cq, **rest)
+            attend(q, self.k_cache[layer], self.v_cache[layer], bt, sl, cq, **rest, **self.shape)
 
     def _set_tables(self, tables: List[List[int]]) -> None:
         self.tables = [list(t) for t in tables]
@@ -257,9 +282,7 @@ class GreedyDecoder:
             matmul(x, w[p + "wq"], out=self.q[:T])
             matmul(x, w[p + "wk"], out=self.k[:T])
             matmul(x, w[p + "wv"], out=self.v[:T])
-            rope(q, sl, cq, c.theta)
-            rope(k, sl, cq, c.theta)
-            self._append(i, k, v, bt, sl, cq)
+            self._turn_and_append(i, q, k, v, bt, sl, cq)
             self._attend(i, q, bt, sl, cq, max(q_lens), max(lens), attn)
             matmul(attn.view(T, c.heads * c.head_dim), w[p + "wo"], out=o)
             add(h, o, out=h)
@@ -378,6 +401,52 @@ class GreedyDecoder:
                 history[b].extend(new)
                 self.cached[b] += n + 1
                 self.last[b] = gb[n]
+        self.trace_logprobs = [t[:steps] for t in self.trace_logprobs]
+        return [t[:steps] for t in traces], blocks, accepted
+
+
+    def speculate_sampled(self, steps: int, width: int, drafter: Drafter, temperature: float,
+                          seed: int = 0, seq_ids: Optional[Sequence[int]] = None):
+        """Speculative decoding at a temperature, with verify blocks of `width` tokens whose
+        drafts `drafter` chose without chance: each is kept with its probability under the
+        target, the first that is not is replaced by a draw from what is left of the
+        distribution, so the traces are distributed as token-by-token sampling's.  Sequence b
+        draws its uniform numbers from a generator seeded by seed and seq_ids[b] (default: b),
+        one per token of each of its blocks.  Returns what speculate returns, and keeps the
+        emitted tokens' log-probabilities (at the temperature) in trace_logprobs."""
+        if not 1 <= width <= self.max_width:
+            raise ValueError(f"width must be in [1, {self.max_width}]")
+        B = self.batch
+        ids_of = list(range(B)) if seq_ids is None else list(seq_ids)
+        if len(ids_of) != B:
+            raise ValueError("one id per sequence")
+        gens = [torch.Generator().manual_seed(seed * 1000003 + i) for i in ids_of]
+        history = [[self.last[b]] for b in range(B)]
+        traces: List[List[int]] = [[] for _ in range(B)]
+        self.trace_logprobs = [[] for _ in range(B)]
+        blocks = accepted = 0
+        while min(len(t) for t in traces) < steps:
+            q_lens = [width if len(traces[b]) < steps else 1 for b in range(B)]
+            drafts = [list(drafter(b, history[b], q_lens[b] - 1))[:q_lens[b] - 1]
+                      if q_lens[b] > 1 else [] for b in range(B)]
+            ids = [t for b in range(B) for t in [self.last[b]] + drafts[b]]
+            self.forward(ids, q_lens)
+            uniforms = torch.cat([torch.rand(n, generator=g) for n, g in zip(q_lens, gens)])
+            drafted = torch.tensor([t for d in drafts for t in d], dtype=torch.int32)
+            r = verify_drafts(self.logits[:len(ids)], drafted.to(self.dev),
+                              uniforms.to(self.dev), self.cu_q[:B + 1], max_q=max(q_lens),
+                              temperature=temperature)
+            kept, tokens, logps = r.accepted.tolist(), r.tokens.tolist(), r.logprobs.tolist()
+            blocks += 1
+            for b in range(B):
+                n = kept[b] + 1
+                new = tokens[b][:n]
+                accepted += kept[b]
+                traces[b].extend(new)
+                self.trace_logprobs[b].extend(logps[b][:n])
+                history[b].extend(new)
+                self.cached[b] += n
+                self.last[b] = new[-1]
         self.trace_logprobs = [t[:steps] for t in self.trace_logprobs]
         return [t[:steps] for t in traces], blocks, accepted
 
