@@ -385,7 +385,8 @@ bi_status bi_prefill_attn(const void* q, const void* k_cache, const void* v_cach
  * token of the block (bi_prefill_attn: of the tile of 128 / G tokens) sees are not part of
  * any sum, whatever they hold; those that one of them sees must be finite, as a value that
  * is not times a weight of 0 makes the others NaN.
- * Chunks, merge tree, workspace, limit and invariance as in the plain calls: a query's bits
+ * Chunks, merge tree, workspace, limit and invariance as in the plain calls (outside the
+ * limit the chosen chunk length follows the window, too): a query's bits
  * depend on it, its position, its limits, its head's slope, softcap, scale and the keys and
  * values it sees, and are the same from all three (inside the batch-invariant limit).
  * Scores are formed in fp32 (tanh within 2^-22 of itself).

@@ -123,7 +123,7 @@ bi_status bi_token_logprobs_backward(const void* x, int64_t ldx, int x_dtype,
  *                negative, infinite or NaN gets no tokens and sets BI_ERR_DEVICE_ARG.
  *   cu_q         int32 [batch + 1], cu_q[0] = 0, 1 to max_q rows each, cu_q[batch] <= total_q and
  *                cu_q[batch] - batch <= num_drafts; else the whole call emits nothing and sets
- *                BI_ERR_DEVICE_ARG.  Rows behind the last sequence are not read.
+ *                BI_ERR_DEVICE_ARG.  Rows behind the last sequence take no part.
  *   tokens       int32 [batch, max_q]: the kept drafts, then the drawn token, then -1.
  *   accepted     int32 [batch]: how many drafts were kept.
  *   logprobs     fp32 [batch, max_q] or NULL: log p of each emitted token (of the softmax at

@@ -439,8 +439,14 @@ def _attend(fn, q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q, max_seq
     if shape is None:
         _check(getattr(lib(), fn)(*head, *tail))
     else:
-        if dq != d:
-            raise ValueError("q must have the cache's D")
+        if dev < 0:
+            _on_current_device(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+                               seq_lens=seq_lens, cu_q=cu_q, out=out, lse=lse,
+                               workspace=workspace)
+        if dq != d or block_table.shape[0] != batch or (
+                T != batch if decode else cu_q.shape[0] != batch + 1):
+            raise ValueError("q must have the cache's D, block_table a row per sequence, and cu_q "
+                             "batch + 1 entries (decode: q a token per sequence)")
         _check(getattr(lib(), fn + "_ex")(*head, *shape, *tail))
     return out, lse
 
@@ -1083,7 +1089,7 @@ def verify_drafts(logits, draft_tokens, uniforms, cu_q, max_q: int, draft_logits
     torch = _torch()
     i32, f32 = torch.int32, torch.float32
     dev = _device_of(logits)
-    hot = None if type(temperature) in (float, int) else temperature
+    hot = temperature if isinstance(temperature, torch.Tensor) else None
     given = ((draft_tokens, i32, 1), (uniforms, f32, 1), (cu_q, i32, 1))
     if hot is not None:
         given += ((hot, f32, 1),)

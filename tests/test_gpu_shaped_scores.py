@@ -308,3 +308,31 @@ def test_refused_arguments(dev):
         p.run("prefill", first_key=torch.zeros(3, device=dev))
     with pytest.raises(ValueError, match="CUDA"):
         p.run("prefill", slopes=torch.zeros(8))
+
+
+@pytest.mark.parametrize("name", ["cap", "all", "some see nothing"])
+@pytest.mark.parametrize("hq,hkv", [(32, 1), (64, 1), (3, 3)])
+def test_wide_and_single_groups(dev, name, hq, hkv):
+    """32 and 64 query heads of one KV head (tiles of four and two tokens), and as many KV heads."""
+    p = make(dev, name, [300, 70, 9], [40, 70, 1], hq, hkv, 64, seed=12)
+    p.check(*p.run("prefill"))
+    if hq // hkv <= 32:
+        p = make(dev, name, [300, 70, 9], [1, 1, 1], hq, hkv, 64, seed=13)
+        p.check(*p.run("decode"))
+
+
+def test_mismatched_tensors_are_refused(dev):
+    p = Paged(dev, [100, 70], [3, 2], 8, 2, 64)
+    p.shape = dict(window=10)
+    p.table = p.table[:1]
+    with pytest.raises(ValueError, match="block_table"):
+        p.run("verify")
+    p = Paged(dev, [100, 70], [3, 2], 8, 2, 64)
+    p.shape = dict(window=10)
+    p.q = p.q.repeat(1, 1, 2)
+    with pytest.raises(ValueError, match="cache's D"):
+        p.run("prefill")
+    p = Paged(dev, [100, 70], [1, 1], 8, 2, 64)
+    p.q = p.q[:1]
+    with pytest.raises(ValueError, match="a token per sequence"):
+        p.run("decode", window=10)
