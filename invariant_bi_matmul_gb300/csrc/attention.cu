@@ -149,6 +149,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         tmem_alloc(tmem_slot, TMEM_COLS);
         tmem_relinquish();
     }
+    if (MODE && !cnt) pdl_wait();  // (a call without item counters has no reset in front)
     // No griddepcontrol.wait here.  The grid right before this one is always the call's
     // own counter reset, which waits for its predecessors before it lets this grid launch:
     // every kernel that wrote an input (Q, the cache, the block table, the lengths) or
@@ -458,14 +459,14 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if (store) *reinterpret_cast<float2*>(ws_ml + idx * 2) = make_float2(m_ref, l_tot);
             // the item's partials are written: count it for its (sequence, KV head), which
             // the merge waits on (every lane's stores are ordered before the count)
-            __threadfence();
+            if (!MODE || cnt) __threadfence();
             __syncwarp();
             if (!reset_done) {
                 pdl_wait();
                 pdl_trigger();
                 reset_done = true;
             }
-            if (lane == 0) atomicAdd(cnt + b * Hkv + h, 1u);
+            if (lane == 0 && (!MODE || cnt)) atomicAdd(cnt + b * Hkv + h, 1u);
         }
         if (!ok && lane == 0) give_up();
         // a CTA with no item (or one that gave up) still waits before it completes, so the
@@ -759,6 +760,11 @@ constexpr int MERGE_UNROLL = 17;  // partials requested per round trip (136 chun
 // the CTA per row does better early there (24 sequences of 1,028 keys 25.3 us, 26.4 with one).
 constexpr int kMergeApart = 40 * 1024;
 constexpr int64_t kMergeApartItems = 2048;
+// Calls with shaped scores of up to this many items go without counters: the merge waits for the
+// whole partial grid, and the reset's launch falls away (one sequence of 300 keys 13.0 -> 11.7 us, 28
+// -> 26 with the host's time; 8 of 2,048 keys 23.1 -> 21.6; 1,024 items 59.1 and 59.0; 2,304 items
+// 131.0 with counters, 132.5 without).
+constexpr int64_t kUncountedItems = 1024;
 
 // The merge tree of one (token, query head) row with nC = pos/chunk + 1 chunk partials:
 // range w = [w*nC/8, (w+1)*nC/8) is folded in ascending chunk order (its max first, then
@@ -1211,9 +1217,14 @@ cudaError_t launch_attention_t(const DeviceInfo& dev, const void* q, const Paged
         static_cast<uint8_t*>(workspace) + partials_bytes(a.total_q, a.hq, D, maxC));
     const int ncnt = int(a.batch * a.hkv);
     const float scale_log2 = scale * kLog2e;
-    cudaError_t e = launch_pdl(attn_count_reset_kernel, dim3((ncnt + 1023) / 1024), dim3(256), 0,
-                               stream, cnt, ncnt);
-    if (e != cudaSuccess) return e;
+    cudaError_t e = cudaSuccess;
+    if (MODE && items_bound <= kUncountedItems) {
+        cnt = nullptr;
+    } else {
+        e = launch_pdl(attn_count_reset_kernel, dim3((ncnt + 1023) / 1024), dim3(256), 0, stream,
+                       cnt, ncnt);
+        if (e != cudaSuccess) return e;
+    }
     e = launch_pdl(
         kern, dim3(grid), dim3(THREADS), SMEM, stream, tk, tv,
         static_cast<const __nv_bfloat16*>(q), a.block_table, int(a.max_pages), int(a.num_pages),

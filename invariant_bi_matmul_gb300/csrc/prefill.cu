@@ -56,6 +56,11 @@ static_assert(PAGE == 64, "the page max below is a three-input max tree over 64 
 constexpr int P_ROWS = 128;              // query rows per tile, one per TMEM lane
 constexpr int P_TMEM_COLS = 512;
 constexpr int P_MAX_BATCH = BI_ATTN_MAX_BATCH;
+// Calls with first_key and up to this many tokens find the tiles' first keys in the kernel itself
+// (shared memory, a word per token); longer ones in a launch of its own (tile_low_kernel).  Documents
+// in 3 blocks of up to 600 tokens, the wall time 31.4 -> 29.4 us by one launch less, the GPU's 25.5 ->
+// 26.4; one block of 2,000, where the GPU's counts, 67.2 and 68.2.
+constexpr int P_OWN_LOWS = 1536;
 
 template <int D>
 struct PCfg {
@@ -81,14 +86,15 @@ struct PCfg {
     // to 144 bytes: conflict-free both ways)
     static constexpr int EPI_STRIDE = 32 * 4 + 16;
     static constexpr int EPI_OFF = (MISC_OFF + MISC_BYTES + 15) / 16 * 16;
-    static constexpr size_t SMEM = 1024 + size_t(EPI_OFF) + size_t(4 * 32 * EPI_STRIDE);
+    static constexpr int LOWS_OFF = EPI_OFF + 4 * 32 * EPI_STRIDE;  // tile lows (shaped calls)
+    static constexpr size_t SMEM = 1024 + size_t(LOWS_OFF);
     static constexpr int S_COL = 0;                       // S buffers: columns [0,64), [64,128)
     static constexpr int O_COL = 2 * PAGE;                // O buffers (by item): D columns each
     // P buffers (by page): 128 rows x 64 keys of bf16, two keys per 32-bit column
     static constexpr int P_TCOL = O_COL + 2 * D;
     static_assert(P_TCOL + P_NPB * (PAGE / 2) <= P_TMEM_COLS, "tensor memory columns");
     static_assert(RING_OFF % 1024 == 0 && BAR_OFF % 1024 == 0, "1024-byte aligned buffers");
-    static_assert(SMEM <= 232448, "shared memory per CTA");
+    static_assert(SMEM + P_OWN_LOWS * 4 <= 232448, "shared memory per CTA");
 };
 
 // Whether every key of a page is visible to every row of the warp (pos: the row's last, low: its
@@ -155,7 +161,7 @@ tile_low_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict_
 }
 
 // MODE: what the call does to its scores (kRange, kCap, kBias of attn_common.cuh; 0: nothing);
-// tile_lows: tile_low_kernel's, or null where no first_key is given.
+// tile_lows: tile_low_kernel's, or null where no first_key is given or total_q <= P_OWN_LOWS.
 template <int D, int MODE>
 __global__ void __launch_bounds__(PWarps<MODE>::THREADS, 1)
 attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
@@ -195,6 +201,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
     static_assert(C::XS_OFF >= C::BAR_OFF + (2 * NST + 4 + 2 * P_NPB + 4 + 2 + 4 + 2) * 8 + 8,
                   "barriers overlap xs");
     float* page_max = reinterpret_cast<float*>(smem + C::PMAX_OFF);  // [2][P_ROWS]
+    int* own_lows = reinterpret_cast<int*>(smem + C::LOWS_OFF);      // [P_OWN_LOWS]
     float2* xs = reinterpret_cast<float2*>(smem + C::XS_OFF);  // [2][P_ROWS]
     int* prefix = reinterpret_cast<int*>(smem + C::MISC_OFF);  // [B+1] items before sequence b
     int* seq_len = prefix + P_MAX_BATCH + 1;    // per sequence: length, first token, width
@@ -245,8 +252,32 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // ... from that of the first key that any of its tokens sees
     auto tile_low = [&](int L, int t0, int qb, int qt) {
         if (!MODE) return 0;
-        return tile_lows ? tile_lows[t0 + qt] : window_low(sh, L - qb + qt * TQ);
+        if (!sh.first_key) return window_low(sh, L - qb + qt * TQ);
+        return tile_lows ? tile_lows[t0 + qt] : own_lows[t0 + qt];
     };
+    if (MODE && sh.first_key && !tile_lows) {
+        // the tiles' first keys as tile_low_kernel finds them, in shared memory: each tile's last
+        // position, then the smallest of its tokens' first keys
+        for (int b = warp; b < B; b += P_THREADS / 32) {
+            const SeqInfo si = seq_info(seq_lens, cu_q, b);
+            if (!seq_ok(si, max_q, max_seq_len, total_q)) continue;
+            for (int qt = lane; qt * TQ < si.qb; qt += 32)
+                own_lows[si.t0 + qt] = si.L - si.qb + min(si.qb, (qt + 1) * TQ) - 1;
+        }
+        __syncthreads();
+        for (int t = tid; t < total_q; t += P_THREADS) {
+            int lo = 0, hi = B;  // sequence of token t: largest b with cu_q[b] <= t
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (cu_q[mid] <= t) lo = mid; else hi = mid;
+            }
+            const SeqInfo si = seq_info(seq_lens, cu_q, lo);
+            const int j = t - si.t0;
+            if (!seq_ok(si, max_q, max_seq_len, total_q) || j < 0 || j >= si.qb) continue;
+            atomicMin(&own_lows[si.t0 + j / TQ], row_low(sh, t, si.L - si.qb + j));
+        }
+        __syncthreads();
+    }
     // work items per sequence: sum over its query tiles of chunks x KV heads
     if (MODE) {  // (a warp per sequence: a tile's first key may be a load)
         for (int b = warp; b < B; b += P_THREADS / 32) {
@@ -859,6 +890,7 @@ cudaError_t launch_prefill_t(const DeviceInfo& dev, const void* q, const PagedAr
                              float scale, const Shape& shape, void* out, float* lse,
                              void* workspace, cudaStream_t stream) {
     using Cf = PCfg<D>;
+    constexpr size_t SMEM = Cf::SMEM + (MODE ? P_OWN_LOWS * 4 : 0);
     const uint64_t rows = uint64_t(a.num_pages) * uint64_t(a.hkv) * PAGE;
     const int G = int(a.hq / a.hkv);
     CUtensorMap tk, tv, tq;
@@ -871,7 +903,7 @@ cudaError_t launch_prefill_t(const DeviceInfo& dev, const void* q, const PagedAr
     static bool attr_done[64] = {};
     if (dev.device >= 0 && dev.device < 64 && !attr_done[dev.device]) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             int(Cf::SMEM));
+                                             int(SMEM));
         if (e != cudaSuccess) return e;
         attr_done[dev.device] = true;
     }
@@ -885,7 +917,7 @@ cudaError_t launch_prefill_t(const DeviceInfo& dev, const void* q, const PagedAr
     float* ws_ml = ws_o + a.total_q * a.hq * int64_t(maxC) * D;
     cudaError_t e = cudaSuccess;
     int* tile_lows = nullptr;
-    if (MODE && shape.first_key) {
+    if (MODE && shape.first_key && a.total_q > P_OWN_LOWS) {
         // (the workspace's item counters, one word per token and query head, are not used here)
         tile_lows = reinterpret_cast<int*>(attn_item_counters(a, workspace, CHUNK_LOG2));
         e = launch_pdl(tile_low_kernel, dim3(unsigned((a.total_q + 7) / 8)), dim3(256), 0, stream,
@@ -893,7 +925,7 @@ cudaError_t launch_prefill_t(const DeviceInfo& dev, const void* q, const PagedAr
                        int(a.max_seq_len), P_ROWS / G, shape, tile_lows);
         if (e != cudaSuccess) return e;
     }
-    e = launch_pdl(kern, dim3(grid), dim3(PWarps<MODE>::THREADS), Cf::SMEM, stream, tk, tv, tq,
+    e = launch_pdl(kern, dim3(grid), dim3(PWarps<MODE>::THREADS), SMEM, stream, tk, tv, tq,
                                a.block_table, int(a.max_pages), int(a.num_pages), a.seq_lens,
                                a.cu_q, int(a.batch), int(a.total_q), int(a.max_q),
                                int(a.max_seq_len), int(a.hq), int(a.hkv), scale * kLog2e, ws_o,
