@@ -18,7 +18,11 @@
 // (behind R: two neighbouring pieces, copied).  The D/16 threads of a head are neighbours in a
 // warp; each keeps its eight sines and cosines for the HPT heads that it takes of its token.
 // The 8-bit cache's row maxima go by shuffles among them.  Bound by memory: every q row is read
-// and written, every k and v row read and written (2 bytes an element, or 1 + 1/D).
+// and written, every k and v row read and written (2 bytes an element, or 1 + 1/D).  8,192 tokens
+// of 32 + 8 heads of 128 take 31.9 us into an 8-bit cache (5.8 TB/s) and 33.5 into a bf16 one (6.0),
+// 32 tokens 3.4 us.  CTAs of 64 threads, so that the last ones of a call do not wait for large
+// ones: 512 tokens 4.6 us, 6.9 with 256 threads.  Two heads a thread were slower on long blocks
+// (40.7 us), eight too (37.0); streaming loads changed nothing.
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
@@ -35,7 +39,7 @@ void set_last_error_message(const char* msg);
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;
 constexpr int kMaxPairs = 64;  // head_dim 128
 
 // What the rotation of a call needs beside the tensors.
@@ -325,7 +329,9 @@ bi_status run(const char* fn, const void* q, int64_t ldq, const void* k_new, int
     const DeviceInfo* dev = current_device_info(&why);
     if (!dev) return launched(why, fn);
 
-    const bool wide = tiles * ((heads + 3) / 4) >= 4 * int64_t(dev->num_sms);
+    // four heads a thread once that leaves every multiprocessor a CTA (300 tokens of 32 + 8 heads
+    // 3.5 us, 6.1 with one head; 8 tokens 4.0 and 3.3)
+    const bool wide = tiles * ((heads + 3) / 4) >= int64_t(dev->num_sms);
     const int64_t groups = wide ? (heads + 3) / 4 : heads;
     const AppendArgs a{static_cast<const uint4*>(q), static_cast<const uint4*>(k_new),
                        static_cast<const uint4*>(v_new), static_cast<uint4*>(q_out), ldq / 8,
