@@ -253,7 +253,10 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
     auto tile_low = [&](int L, int t0, int qb, int qt) {
         if (!MODE) return 0;
         if (!sh.first_key) return window_low(sh, L - qb + qt * TQ);
-        return tile_lows ? tile_lows[t0 + qt] : own_lows[t0 + qt];
+        // (offsets that fall from one sequence to the next leave two of them one entry, or one of
+        // them none: held inside the tile, whatever stands there)
+        const int low = tile_lows ? tile_lows[t0 + qt] : own_lows[t0 + qt];
+        return min(max(low, 0), L - qb + min(qb, (qt + 1) * TQ) - 1);
     };
     if (MODE && sh.first_key && !tile_lows) {
         // the tiles' first keys as tile_low_kernel finds them, in shared memory: each tile's last

@@ -336,3 +336,23 @@ def test_mismatched_tensors_are_refused(dev):
     p.q = p.q[:1]
     with pytest.raises(ValueError, match="a token per sequence"):
         p.run("decode", window=10)
+
+
+@pytest.mark.parametrize("total,fill", [(100, 0x7f), (100, 0xff), (1700, 0x7f), (1700, 0xff)])
+def test_offsets_that_fall_in_a_long_block(dev, total, fill):
+    """Token offsets that fall: that sequence is skipped and reported, the one behind it shares
+    tokens with the one in front, and the sequences apart from these are as they should be."""
+    lens, cu = [300, 200, 64, 5000], [0, 20, 90, 50, total]
+    p = Paged(dev, lens, [20, 70, 1, total - 50], 8, 2, 64, seed=9)
+    first = torch.randint(0, 250, (p.T,), dtype=torch.int32).tolist()
+    args = (p.k, p.v, p.table.to(dev), i32(lens, dev))
+    kw = dict(max_seq_len=5000, scale=p.scale, max_q=total)
+    ws = torch.full((bi.attn_workspace_size(p.T, 8, 64, 5000),), fill, dtype=torch.uint8,
+                    device=dev)
+    want, lse = bi.prefill_attn(p.q[:20], *(x[:1] if x.dim() < 3 else x for x in args),
+                                i32([0, 20], dev), first_key=i32(first[:20], dev), **kw)
+    assert bi.device_status() == bi.BI_OK
+    got = bi.prefill_attn(p.q, *args, i32(cu, dev), first_key=i32(first, dev), workspace=ws, **kw)
+    assert bi.device_status() == bi.BI_ERR_DEVICE_ARG
+    assert torch.equal(got[0][:20].view(torch.int16), want.view(torch.int16))
+    assert torch.equal(got[1][:20], lse)
