@@ -405,7 +405,7 @@ draft_draw_kernel(const DraftArgs a, int ctas) {
 #pragma unroll 1
     for (int i = tid; i < a.B; i += kThreads) {
         const int w = int(uint32_t(a.cu_q[i + 1]) - uint32_t(a.cu_q[i]));
-        bad |= w < 1 || w > a.max_q || a.cu_q[i] < 0;
+        bad |= w < 1 || w > a.max_q || a.cu_q[i + 1] < 0;  // (so they rise: none wraps)
     }
     const float T0 = temperature_of(a, b);
     const int t0 = a.cu_q[b], drafts = a.cu_q[b + 1] - t0 - 1;
@@ -810,7 +810,7 @@ BI_EXPORT bi_status bi_verify_drafts(const void* logits, int64_t ldl, const void
                     "%s: need batch, total_q, num_drafts >= 0 and max_q, n >= 1", fn);
     if (n > BI_DRAFTS_MAX_N)
         return fail(BI_ERR_UNSUPPORTED, "%s: n must be at most %d", fn, BI_DRAFTS_MAX_N);
-    if (total_q > kI32Max / 2 || num_drafts > kI32Max / 2 || max_q > kI32Max ||
+    if (total_q > kI32Max / 2 || num_drafts > kI32Max / 2 || max_q > kI32Max / 2 ||
         batch > kI32Max / kMaxCtas)
         return fail(BI_ERR_UNSUPPORTED, "%s: a size is too large", fn);
     if (ldl < n || (draft_logits && ldd < n))

@@ -39,7 +39,7 @@ def verify(L, **kw):
     (dict(temps=None, temp=-1.0), INVALID), (dict(temps=None, temp=float("nan")), INVALID),
     (dict(temps=None, temp=float("inf")), INVALID), (dict(total=1 << 31), UNSUPPORTED),
     (dict(num=1 << 31), UNSUPPORTED), (dict(batch=1 << 30, total=1 << 30), UNSUPPORTED),
-    (dict(max_q=1 << 31), UNSUPPORTED), (dict(batch=0, x=None, tokens=None), OK)])
+    (dict(max_q=1 << 31), UNSUPPORTED), (dict(max_q=1 << 30), UNSUPPORTED), (dict(batch=0, x=None, tokens=None), OK)])
 def test_refusals(L, change, want):
     assert verify(L, **change) == want
     if want != OK:
