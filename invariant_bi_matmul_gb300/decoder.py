@@ -420,6 +420,8 @@ class GreedyDecoder:
         ids_of = list(range(B)) if seq_ids is None else list(seq_ids)
         if len(ids_of) != B:
             raise ValueError("one id per sequence")
+        if not 0.0 <= temperature < float("inf"):
+            raise ValueError("temperature must be finite and >= 0")
         gens = [torch.Generator().manual_seed(seed * 1000003 + i) for i in ids_of]
         history = [[self.last[b]] for b in range(B)]
         traces: List[List[int]] = [[] for _ in range(B)]
@@ -441,6 +443,8 @@ class GreedyDecoder:
             for b in range(B):
                 n = kept[b] + 1
                 new = tokens[b][:n]
+                if new[-1] < 0:
+                    raise RuntimeError(f"sequence {b}: the model's logits have no distribution")
                 accepted += kept[b]
                 traces[b].extend(new)
                 self.trace_logprobs[b].extend(logps[b][:n])

@@ -140,3 +140,15 @@ def test_refusals(dev, weights):
         with pytest.raises(ValueError):
             dec.speculate_sampled(3, **(dict(width=2, drafter=lookup_drafter, temperature=1.0)
                                         | bad))
+
+
+def test_a_temperature_and_logits_without_a_distribution_are_reported(dev, weights):
+    dec = decoder(dev, weights)
+    dec.prefill(prompts(2))
+    for bad in (-1.0, float("inf"), float("nan")):
+        with pytest.raises(ValueError, match="temperature"):
+            dec.speculate_sampled(3, 2, lookup_drafter, bad)
+    dec.w = {k: torch.full_like(v, float("nan")) if v.dim() == 1 else v
+             for k, v in weights.items()}
+    with pytest.raises(RuntimeError, match="no distribution"):
+        dec.speculate_sampled(3, 2, lookup_drafter, 1.0)
