@@ -132,7 +132,7 @@ bi_status bi_token_logprobs_backward(const void* x, int64_t ldx, int x_dtype,
  *   distribution: the block ends there with a token of -1 and a log-probability of NaN.
  *   workspace    bi_verify_drafts_workspace_size(total_q, num_drafts, n) bytes (num_drafts 0 where
  *                draft_logits is NULL), 16-byte aligned, contents scratch.
- *   Weights are whole numbers of 2^-60, within 2^-30 of themselves, so the drawn token does not
+ *   Weights are whole numbers of 2^-60, within 2^-29 of themselves, so the drawn token does not
  *   depend on the order of any sum.  A sequence's outputs depend on its own rows, drafts, uniforms
  *   and temperature alone: not on the batch, max_q, alignment or strides. */
 #define BI_DRAFTS_MAX_N (1 << 20)

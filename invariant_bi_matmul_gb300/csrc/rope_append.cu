@@ -273,8 +273,9 @@ bi_status run(const char* fn, const void* q, int64_t ldq, const void* k_new, int
     if (rotary_dim < 16 || rotary_dim > head_dim || rotary_dim % 16 != 0)
         return fail(BI_ERR_UNSUPPORTED, "%s: rotary_dim must be a multiple of 16 in [16, head_dim]",
                     fn);
-    if (!inv_freq && (!(theta > 0.0) || !std::isfinite(theta)))
-        return fail(BI_ERR_INVALID_ARG, "%s: theta must be finite and > 0", fn);
+    // (the powers of a subnormal one may be infinite)
+    if (!inv_freq && (!(theta > 0.0) || !std::isnormal(theta)))
+        return fail(BI_ERR_INVALID_ARG, "%s: theta must be finite, > 0 and no subnormal", fn);
     if (num_axes < 0 || num_axes > rotary_dim / 2 || (num_axes > 0 && !sections))
         return fail(BI_ERR_INVALID_ARG, "%s: need 0 <= num_axes <= rotary_dim / 2, and sections",
                     fn);

@@ -45,7 +45,7 @@ def append(L, q8, **kw):
     (dict(out=P, ldo=8192), INVALID),
     (dict(rd=0), UNSUPPORTED), (dict(rd=24), UNSUPPORTED), (dict(rd=144), UNSUPPORTED),
     (dict(theta=0.0), INVALID), (dict(theta=float("inf")), INVALID),
-    (dict(theta=float("nan")), INVALID), (dict(freq=[float("nan")] * 64), INVALID),
+    (dict(theta=float("nan")), INVALID), (dict(theta=5e-324), INVALID), (dict(freq=[float("nan")] * 64), INVALID),
     (dict(axes=-1), INVALID), (dict(axes=2), INVALID),
     (dict(axes=2, sections=[32, 31], pos=P, ldp=2), INVALID),
     (dict(axes=2, sections=[32, 33], pos=P, ldp=2), INVALID),
