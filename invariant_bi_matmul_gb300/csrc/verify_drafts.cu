@@ -745,11 +745,18 @@ cudaError_t launch(const DeviceInfo& dev, DraftArgs& a, bool rows_aligned, cudaS
     a.ahead = items <= 8 * wave ? int(wave) : 0;
     // CTAs of a sequence: one for every eight blocks (a block for each warp), while the
     // multiprocessors hold them all at once (three each).  The batch is spread over them: left to
-    // itself the hardware puts the clusters of a small one on half of them.
+    // itself the hardware puts the clusters of a small one on half of them.  Six where seven would
+    // fit: clusters of seven do not all find room at once (64 sequences of 128,256 bf16 82.9 us with
+    // seven, 72.4 with six).  Two where one each leaves three eighths of the room empty and rows
+    // are long (230 sequences of 2 rows of 128,256 bf16 211 us with one, 175 with two, 256 of 50,257
+    // 94.6 and 88.8; 300 of 2 fp32 rows 156 and 165, 300 of 32,000 63.9 and 65.6).
     const int blocks = (a.n + kBlock - 1) / kBlock;
-    const int64_t sms = dev.num_sms;
+    const int64_t sms = dev.num_sms, room = 3 * sms;
+    int64_t fit = room / a.B;
+    if (fit == 7) fit = 6;
+    if (fit == 1 && 8 * int64_t(a.B) <= 5 * room && blocks >= 64) fit = 2;
     const int ctas = int(std::max<int64_t>(
-        1, std::min<int64_t>({int64_t(kMaxCtas), (blocks + 7) / 8, 3 * sms / a.B})));
+        1, std::min<int64_t>({int64_t(kMaxCtas), (blocks + 7) / 8, fit})));
     const int64_t total = int64_t(a.B) * ctas;
     const size_t apart = total <= sms ? 120 * 1024 : total <= 2 * sms ? 48 * 1024 : 0;
     // statistics in the same launch where a warp gets no more than two parts of its sequence (7

@@ -298,6 +298,20 @@ def test_a_sequence_alone_in_a_batch_and_unaligned(dev, dtype, n, draft):
         assert all(torch.equal(x, y) for x, y in zip(r, whole))
 
 
+@pytest.mark.parametrize("batch", [40, 60, 65, 100, 240, 285, 300])
+def test_first_sequences_of_batches_of_any_size(dev, batch):
+    """However many multiprocessors a sequence gets: the outputs that it has in a batch of five."""
+    b = Batch([2] * batch, 33000, dtype="bf16", seed=batch)
+    whole = b.run(dev)
+    some = bi.verify_drafts(b.logits[:10].to(dev), b.drafts[:5].to(dev), b.u[:10].to(dev),
+                            torch.tensor(b.cu[:6], dtype=torch.int32, device=dev), max_q=2,
+                            draft_logits=b.near[:5].to(dev),
+                            temperature=torch.tensor(b.temps[:5], device=dev))
+    assert bi.device_status() == bi.BI_OK
+    for x, y in zip(whole, some):
+        assert torch.equal(x[:5], y)
+
+
 def test_malformed_batches_emit_nothing(dev):
     b = Batch([3, 2, 4], 500, seed=14)
 
