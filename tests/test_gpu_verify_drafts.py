@@ -64,7 +64,7 @@ def softmax(x, t):
 def check(batch, r, which=None):
     """Every sequence, in 64 bits.  A decision may fall the other way only where u q and p agree to
     2^-20 (fp32 sums of at most 2^20 entries, pairwise below 2^6 terms: 70 roundings of 2^-24), a
-    drawn token may be another only where the share lies within the weights' 2^-30, for p and q,
+    drawn token may be another only where the share lies within the weights' 2^-29, for p and q,
     of an entry's border."""
     tokens, accepted, logps = (x.cpu().numpy() for x in (r.tokens, r.accepted, r.logprobs))
     W = tokens.shape[1]
