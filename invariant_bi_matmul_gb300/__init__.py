@@ -416,6 +416,12 @@ def _attend(fn, q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q, max_seq
             raise ValueError("q must be contiguous" if decode else "q and cu_q must be contiguous")
     num_pages, hkv, page, d = k_cache.shape
     T, hq, dq = q.shape
+    # (a plain decode call serves the rows of q, whatever else the buffers could hold)
+    batch, max_pages = T if decode else seq_lens.shape[0], block_table.shape[1]
+    if dq != d or block_table.shape[0] < batch or (
+            seq_lens.shape[0] < batch if decode else batch > max(cu_q.shape[0] - 1, 0)):
+        raise ValueError("q must have the cache's D, block_table a row per sequence, and cu_q "
+                         "batch + 1 entries (decode: q a token per sequence)")
     shape = _shape(softcap, slopes, window, first_key, hq, T)
     if out is not None or lse is not None:
         _attn_out(q, q if out is None else out, lse, False)  # (checks what the caller gave)
@@ -429,7 +435,6 @@ def _attend(fn, q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q, max_seq
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
         else:
             ws_bytes = workspace.numel() * workspace.element_size()
-    batch, max_pages = seq_lens.shape[0], block_table.shape[1]
     sizes = (batch,) if decode else (cu_q.data_ptr(), batch, T, max_q)
     head = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), num_pages,
             block_table.data_ptr(), max_pages, seq_lens.data_ptr(), *sizes, max_seq_len, hq, hkv,
@@ -443,10 +448,10 @@ def _attend(fn, q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q, max_seq
             _on_current_device(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
                                seq_lens=seq_lens, cu_q=cu_q, out=out, lse=lse,
                                workspace=workspace)
-        if dq != d or block_table.shape[0] != batch or (
-                T != batch if decode else cu_q.shape[0] != batch + 1):
-            raise ValueError("q must have the cache's D, block_table a row per sequence, and cu_q "
-                             "batch + 1 entries (decode: q a token per sequence)")
+        if block_table.shape[0] != batch or (
+                seq_lens.shape[0] != batch if decode else cu_q.shape[0] != batch + 1):
+            raise ValueError("block_table must have a row per sequence, and cu_q batch + 1 "
+                             "entries (decode: q a token per sequence)")
         _check(getattr(lib(), fn + "_ex")(*head, *shape, *tail))
     return out, lse
 
