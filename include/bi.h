@@ -380,11 +380,12 @@ bi_status bi_prefill_attn(const void* q, const void* k_cache, const void* v_cach
  * scale must be in (0, 2^20] where any of them is given.  With none of them the call is the
  * plain one; with limits alone a token whose limits hide nothing gets the plain call's bits.
  *
- * Only the pages that a block's tokens see are read, the others may be gone (any
- * block-table entry): work follows the window, not the sequence.  Keys and values that no
- * token of the block (bi_prefill_attn: of the tile of 128 / G tokens) sees are not part of
- * any sum, whatever they hold; those that one of them sees must be finite, as a value that
- * is not times a weight of 0 makes the others NaN.
+ * Of a sequence's pages those of the block's own tokens are read and those from the first
+ * key on that one of its tokens sees; the ones in front of both may be gone (any block-table
+ * entry): work follows the window, not the sequence.  Keys and values that no token of the
+ * block (bi_prefill_attn: of the tile of 128 / G tokens) sees are not part of any sum,
+ * whatever they hold; those that one of them sees must be finite, as a value that is not
+ * times a weight of 0 makes the others NaN, and so must their products scale * q . k.
  * Chunks, merge tree, workspace, limit and invariance as in the plain calls (outside the
  * limit the chosen chunk length follows the window, too): a query's bits
  * depend on it, its position, its limits, its head's slope, softcap, scale and the keys and

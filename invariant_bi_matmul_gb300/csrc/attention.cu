@@ -699,7 +699,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 // V rows of this slice past the sequence end (or of an invalid page) are
                 // zeroed so unwritten cache slots cannot inject NaN/Inf through 0 * v
                 const int vend = valid ? L - page0 : 0;  // first row to zero
-                if (vend < (sw + 1) * KSL) {
+                if (!MODE && vend < (sw + 1) * KSL) {
                     const int r0 = max(vend, sw * KSL);
                     uint8_t* vst = sStage + s * C::STAGE_BYTES + C::PAGE_BYTES;
                     const int n16 = ((sw + 1) * KSL - r0) * 8;  // 16-byte pieces per box
@@ -709,15 +709,15 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             make_uint4(0, 0, 0, 0);
                     }
                 }
-                // ... and so are those in front of the first key that a row sees
-                if (MODE && seq_lo[b] - page0 > sw * KSL) {
-                    const int r0 = sw * KSL, r1 = min(seq_lo[b] - page0, r0 + KSL);
-                    uint8_t* vst = sStage + s * C::STAGE_BYTES + C::PAGE_BYTES;
-                    for (int idx = lane; idx < C::BOXES * (r1 - r0) * 8; idx += 32) {
-                        const int bx = idx / ((r1 - r0) * 8), rem = idx - bx * ((r1 - r0) * 8);
-                        *reinterpret_cast<uint4*>(vst + bx * C::BOX_BYTES + r0 * 128 + rem * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    }
+                // ... and with limits every row of it that no query of the block sees (in front
+                // of the first keys, past the end, at the places of queries that see nothing)
+                if (MODE && !all_seen &&
+                    !__any_sync(0xffffffffu,
+                                fst <= sw * KSL && lim >= (sw + 1) * KSL - 1)) {
+                    const uint32_t seen = __reduce_or_sync(
+                        0xffffffffu, keys_between(fst - sw * KSL, lim - sw * KSL));
+                    zero_unseen<C::BOXES, C::BOX_BYTES>(
+                        sStage + s * C::STAGE_BYTES + C::PAGE_BYTES, sw * KSL, seen);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();

@@ -95,6 +95,27 @@ __device__ __forceinline__ int block_low(const Shape& sh, int t, int pos, int n)
     return low;
 }
 
+// Which of 16 consecutive keys lie in low .. last (both counted from the first of them).
+__device__ __forceinline__ uint32_t keys_between(int low, int last) {
+    low = max(low, 0);
+    last = min(last, 15);
+    return last >= low ? ((2u << last) - 1u) & ~((1u << low) - 1u) : 0u;
+}
+
+// Zeroes those of the 16 value rows from row r0 on of a page in shared memory (BOXES boxes of 64
+// columns, BOX_BYTES apart) that no query sees: a weight of 0 times a value that is not finite
+// would be NaN.  A warp calls it together; the caller orders it before the product.
+template <int BOXES, int BOX_BYTES>
+__device__ __forceinline__ void zero_unseen(uint8_t* v, int r0, uint32_t seen) {
+#pragma unroll 1
+    for (int idx = int(threadIdx.x) & 31; idx < BOXES * 128; idx += 32) {
+        const int row = (idx >> 3) & 15;
+        if (!((seen >> row) & 1u))
+            *reinterpret_cast<uint4*>(v + (idx >> 7) * BOX_BYTES + (r0 + row) * 128 +
+                                      (idx & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
+}
+
 // cap_log2 * tanh(s * cap_in) of a warp's scores.  Up to |y| = 1 an odd polynomial (2^-24 off;
 // with its fp32 evaluation 2^-22.5), which needs neither of the two special functions of the other
 // branch, 1 - 2 / (1 + e^2y), and goes two scores to an instruction; a warp takes the other one for

@@ -343,9 +343,10 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
     const int w_end = int(int64_t(blockIdx.x + 1) * total / gridDim.x);
 
     // Item cursor (every warp walks the same run): sequence b, query tile qt, KV head h,
-    // chunk c (fastest), and the tile's chunk count nch, first key low and its chunk c0.
+    // chunk c (fastest), and the tile's chunk count nch, first key low and its chunk c0, and its
+    // last token's position.
     struct Cursor {
-        int b, qt, h, c, nch, low, c0;
+        int b, qt, h, c, nch, low, c0, last;
     };
     auto set_tile = [&](Cursor& k) {
         k.nch = tile_chunks(seq_len[k.b], seq_qb[k.b], k.qt);
@@ -353,10 +354,11 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
             k.low = tile_low(seq_len[k.b], seq_t0[k.b], seq_qb[k.b], k.qt);
             k.c0 = k.low >> CHUNK_LOG2;
             k.nch -= k.c0;
+            k.last = seq_len[k.b] - seq_qb[k.b] + min(seq_qb[k.b], (k.qt + 1) * TQ) - 1;
         }
     };
     auto seek = [&](int w) {
-        Cursor k{B, 0, 0, 0, 1, 0, 0};
+        Cursor k{B, 0, 0, 0, 1, 0, 0, 0};
         if (w >= total) return k;  // an empty run
         // sequence b with prefix[b] <= w < prefix[b+1]: a valid one (it has items), so
         // its tiles' chunk counts are >= 1 and the walk below ends inside its tiles
@@ -427,13 +429,26 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // pages of chunk c: those the decode kernel reduces for the chunk, up to the
     // sequence's end (pages past a row's position are masked for it and add +0 to its O
     // and sums; processing the same pages keeps even the signs of zeros identical)
-    // (from the page of the tile's first key; what lies in front of it is masked likewise)
+    // (with limits from the page of the tile's first key to that of its last token: what lies
+    // outside is masked likewise)
     auto first_page = [&](const Cursor& k) {
         return MODE ? max(k.c * chunk_pages, k.low / PAGE) : k.c * chunk_pages;
     };
     auto item_pages = [&](const Cursor& k) {
-        const int n = min(chunk_pages, (seq_len[k.b] - k.c * CHUNK + PAGE - 1) / PAGE);
+        const int end = MODE ? k.last + 1 : seq_len[k.b];
+        const int n = min(chunk_pages, (end - k.c * CHUNK + PAGE - 1) / PAGE);
         return MODE ? n - (first_page(k) - k.c * chunk_pages) : n;
+    };
+    // which of the 16 keys from `from` on any token of the tile sees (a warp together)
+    auto tile_sees = [&](const Cursor& k, int from) {
+        if (!sh.first_key) return keys_between(k.low - from, k.last - from);
+        const int j0 = k.qt * TQ, n = min(TQ, seq_qb[k.b] - j0);
+        uint32_t seen = 0;
+        for (int j = lane; j < n; j += 32) {
+            const int at = seq_len[k.b] - seq_qb[k.b] + j0 + j;
+            seen |= keys_between(row_low(sh, seq_t0[k.b] + j0 + j, at) - from, at - from);
+        }
+        return __reduce_or_sync(0xffffffffu, seen);
     };
     auto give_up = [&]() {
         if (!*abort_flag) {
@@ -839,7 +854,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 // V rows of this warp's 16 keys past the sequence end (or of an invalid
                 // page) are zeroed so unwritten cache slots cannot inject NaN/Inf via 0 * v
                 const int vend = valid ? L - page0 : 0;
-                if (vend < (sw + 1) * 16) {
+                if (!MODE && vend < (sw + 1) * 16) {
                     // after the stage's copies have landed (an invalid page's stage had none)
                     if (!wait(&full[s], (gi / NST) & 1u)) break;
                     const int r0 = max(vend, sw * 16);
@@ -852,17 +867,18 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     }
                     fence_proxy_async_smem();  // the zeroed V rows, read by the MMA
                 }
-                // ... and those in front of the first key that any row of the tile sees
-                if (MODE && k.low - page0 > sw * 16) {
-                    if (!wait(&full[s], (gi / NST) & 1u)) break;
-                    const int r0 = sw * 16, r1 = min(k.low - page0, r0 + 16);
-                    uint8_t* vst = sStage + s * C::STAGE_BYTES + C::PAGE_BYTES;
-                    for (int idx = lane; idx < C::BOXES * (r1 - r0) * 8; idx += 32) {
-                        const int bx = idx / ((r1 - r0) * 8), rem = idx - bx * ((r1 - r0) * 8);
-                        *reinterpret_cast<uint4*>(vst + bx * C::BOX_BYTES + r0 * 128 + rem * 16) =
-                            make_uint4(0, 0, 0, 0);
+                // ... and with limits every one of them that no row of the tile sees
+                if (MODE && !all_seen) {
+                    const int key0 = page0 + sw * 16;
+                    if (!__any_sync(0xffffffffu, valid && low <= key0 && pos >= key0 + 15)) {
+                        const uint32_t seen = valid ? tile_sees(k, key0) : 0u;
+                        if (seen != 0xffffu) {
+                            if (!wait(&full[s], (gi / NST) & 1u)) break;
+                            zero_unseen<C::BOXES, C::BOX_BYTES>(
+                                sStage + s * C::STAGE_BYTES + C::PAGE_BYTES, sw * 16, seen);
+                            fence_proxy_async_smem();
+                        }
                     }
-                    fence_proxy_async_smem();
                 }
                 tc_fence_before_sync();    // the P stores, before the arrival
                 __syncwarp();
