@@ -137,7 +137,8 @@ __device__ __forceinline__ float half_max_of(const float (&s)[PAGE / 2]) {
 
 // First key that any token of each query tile sees (block_low), for a call with first_key: entry
 // t0 + qt of `lows` for tile qt of the sequence whose first token is t0 (tiles hold a token at
-// least, so the entries are distinct).  A warp per tile slot; TQ tokens per tile.
+// least, so the entries are distinct), the largest int in the others.  A warp per tile slot; TQ
+// tokens per tile.
 __global__ void __launch_bounds__(256)
 tile_low_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ cu_q, int B,
                 int total_q, int max_q, int max_seq_len, int TQ, const Shape sh, int* lows) {
@@ -152,10 +153,11 @@ tile_low_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict_
     }
     const SeqInfo si = seq_info(seq_lens, cu_q, lo);
     const int qt = slot - si.t0;
-    if (!seq_ok(si, max_q, max_seq_len, total_q) || qt < 0 || int64_t(qt) * TQ >= si.qb) return;
-    const int j0 = qt * TQ, n = min(TQ, si.qb - j0), pos0 = si.L - si.qb + j0;
-    int low = pos0 + n - 1;
-    for (int j = lane; j < n; j += 32) low = min(low, row_low(sh, si.t0 + j0 + j, pos0 + j));
+    int low = 0x7fffffff;
+    if (seq_ok(si, max_q, max_seq_len, total_q) && qt >= 0 && int64_t(qt) * TQ < si.qb) {
+        const int j0 = qt * TQ, n = min(TQ, si.qb - j0), pos0 = si.L - si.qb + j0;
+        for (int j = lane; j < n; j += 32) low = min(low, row_low(sh, si.t0 + j0 + j, pos0 + j));
+    }
     low = __reduce_min_sync(0xffffffffu, low);
     if (lane == 0) lows[slot] = low;
 }
@@ -253,20 +255,16 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
     auto tile_low = [&](int L, int t0, int qb, int qt) {
         if (!MODE) return 0;
         if (!sh.first_key) return window_low(sh, L - qb + qt * TQ);
-        // (offsets that fall from one sequence to the next leave two of them one entry, or one of
-        // them none: held inside the tile, whatever stands there)
+        // (held inside the tile: none of its tokens may see a key, and offsets that fall from one
+        // sequence to the next leave two of them one entry, or one of them none)
         const int low = tile_lows ? tile_lows[t0 + qt] : own_lows[t0 + qt];
         return min(max(low, 0), L - qb + min(qb, (qt + 1) * TQ) - 1);
     };
     if (MODE && sh.first_key && !tile_lows) {
-        // the tiles' first keys as tile_low_kernel finds them, in shared memory: each tile's last
-        // position, then the smallest of its tokens' first keys
-        for (int b = warp; b < B; b += P_THREADS / 32) {
-            const SeqInfo si = seq_info(seq_lens, cu_q, b);
-            if (!seq_ok(si, max_q, max_seq_len, total_q)) continue;
-            for (int qt = lane; qt * TQ < si.qb; qt += 32)
-                own_lows[si.t0 + qt] = si.L - si.qb + min(si.qb, (qt + 1) * TQ) - 1;
-        }
+        // the tiles' first keys as tile_low_kernel finds them, in shared memory: the smallest of
+        // each tile's tokens' first keys.  (Minima alone, from one value: every CTA comes to the
+        // same entries, and so to the same runs of items, where falling offsets share some, too.)
+        for (int t = tid; t < total_q; t += P_THREADS) own_lows[t] = 0x7fffffff;
         __syncthreads();
         for (int t = tid; t < total_q; t += P_THREADS) {
             int lo = 0, hi = B;  // sequence of token t: largest b with cu_q[b] <= t
