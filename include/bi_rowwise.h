@@ -106,7 +106,7 @@ bi_status bi_token_logprobs_backward(const void* x, int64_t ldx, int x_dtype,
  *   - behind a block that is kept in full, the first i for which the sum of p_k exceeds u.
  *   The emitted tokens are distributed as p, whatever the drafts were.
  *   T = 0 (or below 2^-64): a draft is kept while it is the row's largest entry, and the largest
- *   entry is emitted at the end, ranked as bi_argmax ranks.
+ *   entry is emitted at the end, ranked as bi_argmax ranks; draft rows take no part.
  *
  *   logits       [total_q, n], dtype BI_BF16, BI_F16 or BI_F32, row stride ldl >= n, aligned to
  *                its element size.  1 <= n <= BI_DRAFTS_MAX_N.
@@ -129,7 +129,8 @@ bi_status bi_token_logprobs_backward(const void* x, int64_t ldx, int x_dtype,
  *   logprobs     fp32 [batch, max_q] or NULL: log p of each emitted token (of the softmax at
  *                temperature 1 where T is 0), 0 behind them.
  *   A row that the block comes to, target or draft, with a NaN, +inf or nothing but -inf has no
- *   distribution: the block ends there with a token of -1 and a log-probability of NaN.
+ *   distribution, at any temperature: the block ends there with a token of -1 and a
+ *   log-probability of NaN.
  *   workspace    bi_verify_drafts_workspace_size(total_q, num_drafts, n) bytes (num_drafts 0 where
  *                draft_logits is NULL), 16-byte aligned, contents scratch.
  *   Weights are whole numbers of 2^-60, within 2^-29 of themselves, so the drawn token does not

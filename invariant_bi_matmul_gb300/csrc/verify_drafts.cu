@@ -469,7 +469,7 @@ draft_draw_kernel(const DraftArgs a, int ctas) {
         if (with_q) Q = join_parts(qp, a.nparts, c.hi);
         bool take = false;
         if (inside && greedy) {
-            take = 0x7fffffff - int(uint32_t(P.best)) == token;
+            take = has_distribution(P) && 0x7fffffff - int(uint32_t(P.best)) == token;
         } else if (inside && has_distribution(P) && x != -INFINITY) {
             // u 2^tq / sq < 2^tp / sp
             const float2 tp = exponent_of(x, P, c);
@@ -519,7 +519,8 @@ draft_draw_kernel(const DraftArgs a, int ctas) {
         if (out_logp) out_logp[kept] = token < 0 ? kNaN : logp_of(load1<DT>(xr, token), P, c);
     };
     if (greedy) {
-        if (rank == 0 && tid == 0) emit(0x7fffffff - int(uint32_t(P.best)));
+        if (rank == 0 && tid == 0)
+            emit(has_distribution(P) ? 0x7fffffff - int(uint32_t(P.best)) : -1);
         return;
     }
     bool both = behind && a.y;              // subtract the draft's probabilities
