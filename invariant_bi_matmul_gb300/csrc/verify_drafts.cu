@@ -341,6 +341,8 @@ __device__ __forceinline__ float2 exponent_of(float x, const RowStats& r, const 
 // (not inlined: it stands at several places of a kernel that runs from a cold cache)
 __device__ __noinline__ float logp_of(float x, const RowStats& r, const Rate& c) {
     const float2 t = exponent_of(x, r, c);
+    // (the type's lowest value: times log2 e it is past fp32's range, by itself it need not be)
+    if (t.x == -INFINITY) return (x - r.m) * (c.hi * kLn2);
     return fmaf(t.x, kLn2, t.y * kLn2) - logf(r.s);
 }
 
