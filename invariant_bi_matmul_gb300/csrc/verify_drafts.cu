@@ -79,7 +79,7 @@ struct DraftArgs {
 
 __device__ __forceinline__ float temperature_of(const DraftArgs& a, int b) {
     const float t = a.temperatures ? a.temperatures[b] : a.temperature;
-    return t < kHot ? (t >= 0.f ? 0.f : kNaN) : t <= 3.4e38f ? t : kNaN;  // NaN: refused
+    return t < kHot ? (t >= 0.f ? 0.f : kNaN) : isfinite(t) ? t : kNaN;  // NaN: refused
 }
 
 // log2 e / T in two floats, to 2^-46 of itself.
