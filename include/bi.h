@@ -133,7 +133,9 @@ int bi_get_weight_prefetch(void);
  * sizes would run under the current limit, on a GPU with num_sms SMs.
  * bi_matmul_splits: CTAs per output tile along K (1 = the invariant single K loop).
  * bi_attn_chunk: split-KV chunk length in keys (BI_ATTN_CHUNK inside the limit);
- *   workspace_bytes is the workspace the call would be given.
+ *   workspace_bytes is the workspace the call would be given.  For calls without a window:
+ *   outside the limit a call with one picks by the window + max_q keys that a block sees,
+ *   which this does not know.
  * Both return 0 for invalid sizes. */
 int bi_matmul_splits(int64_t M, int64_t N, int64_t K, int w_layout, int num_sms);
 int64_t bi_attn_chunk(int64_t batch, int64_t total_q, int64_t max_q, int64_t max_seq_len,

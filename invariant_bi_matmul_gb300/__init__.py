@@ -220,8 +220,8 @@ def matmul_splits(M: int, N: int, K: int, w_layout: str = "nk", num_sms: int = 1
 def attn_chunk(batch: int, total_q: int, max_q: int, max_seq_len: int, num_q_heads: int,
                num_kv_heads: int, head_dim: int, workspace_bytes: int,
                num_sms: int = 152) -> int:
-    """The split-KV chunk length (keys) a verify/decode call with these sizes would use
-    under the current limit (ATTN_CHUNK inside it).  0 for invalid sizes."""
+    """The split-KV chunk length (keys) a verify/decode call with these sizes and no window would
+    use under the current limit (ATTN_CHUNK inside it, window or not).  0 for invalid sizes."""
     return int(lib().bi_attn_chunk(int(batch), int(total_q), int(max_q), int(max_seq_len),
                                    int(num_q_heads), int(num_kv_heads), int(head_dim),
                                    int(workspace_bytes), int(num_sms)))
@@ -503,7 +503,8 @@ def decode_attn(q, k_cache, v_cache, block_table, seq_lens, max_seq_len: int, sc
                 out=None, lse=None, want_lse=True, workspace=None, stream=None,
                 softcap: float = 0.0, slopes=None, window: int = 0, first_key=None):
     """One new token per sequence: q bf16 [B,Hq,D]; token b is the last position of b.
-    Shaped scores as in verify_block (first_key int32 [B])."""
+    block_table and seq_lens may have more rows than q, which are then left alone.
+    Shaped scores as in verify_block (first_key int32 [B]; block_table and seq_lens of q's rows)."""
     return _attend("bi_decode_attn", q, k_cache, v_cache, block_table, seq_lens, None, 1,
                    int(max_seq_len), float(scale), out, lse, want_lse, workspace, stream,
                    float(softcap), slopes, int(window), first_key)

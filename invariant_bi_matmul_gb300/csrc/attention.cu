@@ -589,7 +589,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     // a biased score's size depends on its place, so the page's maximum is that of
                     // the shaped scores: each warp takes its slice's, and they exchange them
                     // (shaping all 64 keys in each warp, a cap and a bias over 64 sequences of up
-                    // to 16,388 keys took 1,004 us, 662 so)
+                    // to 16,388 keys took 1,004 us, 662 so, 631 today)
 #pragma unroll
                     for (int k = 0; k < KSL; ++k) sl[k] = __uint_as_float(sv[k]);
                     if (!all_seen) {

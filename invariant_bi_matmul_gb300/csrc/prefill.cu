@@ -21,7 +21,9 @@
 //     same pairwise tree), added in ascending slice order at the end of the chunk;
 //   * the chunk partials (m, l, o) go to the same workspace and through the same merge
 //     kernel.
-// A chunk's pages run to the sequence's end, as in the decode kernel, whatever the tile.
+// A chunk's pages run to the sequence's end, as in the decode kernel, whatever the tile; where
+// scores are shaped or limited, to the tile's last token, as the decode kernel's do to its
+// block's (a capped prompt of 8,192 tokens 1.48 -> 1.33 ms).
 //
 // What differs from the decode kernel is the tile: 128 DIFFERENT query rows (128/G tokens
 // x the G query heads of one KV head), one per tensor-memory lane, instead of <= 32 rows
@@ -58,8 +60,9 @@ constexpr int P_TMEM_COLS = 512;
 constexpr int P_MAX_BATCH = BI_ATTN_MAX_BATCH;
 // Calls with first_key and up to this many tokens find the tiles' first keys in the kernel itself
 // (shared memory, a word per token); longer ones in a launch of its own (tile_low_kernel).  Documents
-// in 3 blocks of up to 600 tokens, the wall time 31.4 -> 29.4 us by one launch less, the GPU's 25.5 ->
-// 26.4; one block of 2,000, where the GPU's counts, 67.2 and 68.2.
+// in 3 blocks of up to 600 tokens: by one launch less the wall time 30.9 -> 29.2 us (medians of four
+// runs each, 29.7 to 32.8 and 27.5 to 30.1), the GPU's 20.2 -> 20.7, which is what a captured step
+// pays; one block of 2,000 of 32 + 8 heads, where the GPU's counts, 64.8 in two launches, 66.8 in one.
 constexpr int P_OWN_LOWS = 1536;
 
 template <int D>
@@ -463,7 +466,8 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // Shaping warps, one per quarter (calls that cap or bias their scores): read the scores of a
     // page, take the rows' maximum (of the capped ones before the cap, see Reference), and write
     // the shaped scores back for the softmax.  The softmax warps' chain of a page is what bounds
-    // this kernel: with the shaping on it a capped prompt of 8,192 tokens took 1.97 ms, so 1.48.
+    // this kernel: with the shaping on it a capped prompt of 8,192 tokens took 1.97 ms, 1.48 so (and
+    // 1.33 since a tile's pages end at its last token).
     auto shape_pages = [&]() {
         const int quarter = warp & 3;
         const int r = 32 * quarter + lane;

@@ -763,8 +763,8 @@ cudaError_t launch(const DeviceInfo& dev, DraftArgs& a, bool rows_aligned, cudaS
     const int64_t total = int64_t(a.B) * ctas;
     const size_t apart = total <= sms ? 120 * 1024 : total <= 2 * sms ? 48 * 1024 : 0;
     // statistics in the same launch where a warp gets no more than two parts of its sequence (7
-    // sequences of 999 entries 24.5 us with the host's time, 25.8 in two launches; 4 rows of
-    // 128,256, eight parts for each warp, 29 and 25)
+    // sequences of 999 entries 12.4 us on the GPU, 22 to 25 with the host's time; 15.2 and 26 in two
+    // launches; 4 rows of 128,256, eight parts for each warp, 29 and 25)
     const int64_t rows = a.y ? 2 * int64_t(a.max_q) - 1 : a.max_q;
     const bool own = total <= 2 * sms && rows * a.nparts <= 2 * ctas * (kThreads / 32);
     if (!own) {
