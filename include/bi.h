@@ -374,7 +374,8 @@ bi_status bi_prefill_attn(const void* q, const void* k_cache, const void* v_cach
  *   softcap    0: none; else in [2^-20, 2^20]:  x := softcap * tanh(x / softcap).
  *   slopes     fp32 [num_q_heads] (device) or NULL:  x := x + slopes[h] * (j - pos), a bias
  *              that falls with distance where the slope is positive.
- *   window     0: none; else a token sees the keys pos - window + 1 .. pos alone.
+ *   window     0 (or max_seq_len and above): none; else a token sees the keys
+ *              pos - window + 1 .. pos alone.
  *   first_key  int32 [total_q] (device; decode: [batch]) or NULL: a token sees no key in
  *              front of first_key[t] (a document's start in packed documents, for instance;
  *              negative: no limit).  Both limits hold together with j <= pos.  Where they
